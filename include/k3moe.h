@@ -69,7 +69,9 @@ enum {
   K3MOE_OP_SHARED_FFN = 3,
   K3MOE_OP_COMBINE = 4,
   K3MOE_OP_LAYER = 5,
-  K3MOE_OP_EXPERT_GATEUP = 6
+  K3MOE_OP_EXPERT_GATEUP = 6,
+  K3MOE_OP_SHARED_TRAIN = 7,
+  K3MOE_OP_SHARED_BACKWARD = 8
 };
 /* Router modes (k3moe_shape.router).
  *   SOFTMAX:      S_t = k largest logits; w = softmax of the chosen logits.
@@ -441,6 +443,112 @@ k3moe_status k3moe_cache_plan(k3moe_expert_cache* cache, const int32_t* ids, int
                               int32_t* slot_of);
 /* Counters since creation. */
 k3moe_status k3moe_cache_stats_get(const k3moe_expert_cache* cache, k3moe_cache_stats* stats);
+
+/* ---------------------------------------------------------------------------
+ * Training of the shared experts (the always-on bf16 ones; the routed 4-bit
+ * experts stay frozen).  Only T, d, n_shared, f_shared and out_dtype of the
+ * shape are used beside its checks; x_dtype must be K3MOE_BF16
+ * (EUNSUPPORTED), T <= 2^30 (ESHAPE).  With F = n_shared f_shared:
+ *   forward   g_s = Wg_s x, u_s = Wu_s x, h_s = silu(g_s) * u_s,
+ *             y = sum over the experts of Wd_s h_s
+ *   backward  of any loss, from dy = dL/dy:
+ *             dh_s = Wd_s^T dy, du_s = dh_s silu(g_s),
+ *             dg_s = dh_s u_s sigmoid(g_s) (1 + g_s (1 - sigmoid(g_s))),
+ *             dx = sum of Wg_s^T dg_s + Wu_s^T du_s,
+ *             dWg_s = dg_s^T x, dWu_s = du_s^T x, dWd_s = dy^T h_s (summed
+ *             over the tokens)
+ * Sums are fp32.  g, u (kept for the backward), h, dg, du and every gradient
+ * are rounded to bf16 once: they are bf16 operands of the next product (which
+ * is why this y is not the bits of k3moe_shared_ffn, whose h keeps 16 bits).
+ * The reference pages only run their model; a training pass over its
+ * always-on experts is this library's.
+ * ------------------------------------------------------------------------- */
+/* x [T][d] bf16 -> gu [T][n_shared][2 f_shared] bf16, the pre-activations
+ * (gate, then up, of every expert) for k3moe_shared_ffn_backward, and
+ * y [T][d] in out_dtype.  Errors: EINVAL (no shared experts, NULL pointers,
+ * bank not matching), EUNSUPPORTED (bank not BF16, x_dtype), ESHAPE, EALIGN,
+ * EWORKSPACE.  Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_SHARED_TRAIN). */
+k3moe_status k3moe_shared_ffn_train(const k3moe_shape* shape, const k3moe_expert_bank* bank,
+                                    const void* x, void* gu, void* y, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+/* x and gu of the forward and dy [T][d] bf16 -> dx [T][d], dw13 [n_shared][2
+ * f_shared][d] and dw2 [n_shared][d][f_shared], all bf16 and overwritten.  An
+ * output that is NULL is not computed (all three NULL: nothing is enqueued).
+ * T = 0 writes zeros to dw13 and dw2.  The outputs must not overlap the inputs
+ * or each other.  Errors: as for k3moe_shared_ffn_train.
+ * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_SHARED_BACKWARD). */
+k3moe_status k3moe_shared_ffn_backward(const k3moe_shape* shape, const k3moe_expert_bank* bank,
+                                       const void* x, const void* gu, const void* dy, void* dx,
+                                       void* dw13, void* dw2, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Products with 4-bit integer weights and group scales, for the few tokens of
+ * a decoding step (any T is computed; the weights are read again for every 64
+ * tokens, bf16, or 21, fp32).
+ *   W[r][j] = (q[r][j] - z[r][j / group]) * scale[r][j / group]
+ * codes [n][k / 2] u8: byte i of a row holds q of element 2i in its low
+ * nibble, of 2i + 1 in its high nibble; scale [n][k / group] bf16; zero
+ * [n][k / group] u8, NULL for 8 everywhere (symmetric codes).
+ * 1 <= n <= 2^24; group 32, 64 or a multiple of 128; group <= k <= 2^20 and
+ * k % group == 0 (ESHAPE); 0 <= T <= 2^18, T = 0 enqueues nothing.
+ * x [T][k] and the output in F32 or BF16 each (EUNSUPPORTED otherwise).  The
+ * sums are fp32 and follow IEEE rules for infinities and NaN in x and scale.
+ * The pages' engines run 4-bit weights without a dense copy (kimi-k3-in-c
+ * review page, "KDA/MLA/MoE" table); integer codes with group scales beside
+ * their MXFP4 are this library's.
+ * ------------------------------------------------------------------------- */
+typedef struct k3moe_w4_matrix {
+  int32_t n;       /* rows (outputs) */
+  int32_t k;       /* columns (contraction) */
+  int32_t group;   /* weights along a row that share a scale */
+  const void* codes;
+  const void* scale;
+  const void* zero;
+} k3moe_w4_matrix;
+
+/* out [T][n] = x W^T.  Errors: EINVAL (NULL pointers, negative sizes), ESHAPE,
+ * EUNSUPPORTED, EALIGN. */
+k3moe_status k3moe_w4_linear(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
+                             int32_t out_dtype, const void* x, void* out, void* stream);
+/* The gated form: rows 0 .. n/2 - 1 of W are the gate, the others the up
+ * projection (n even, ESHAPE): out [T][n / 2] = silu(x Wg^T) * (x Wu^T).
+ * Errors: as for k3moe_w4_linear. */
+k3moe_status k3moe_w4_glu(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
+                          int32_t out_dtype, const void* x, void* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The global norm of a training step's gradients, and clipping by it.  (The
+ * reference pages do not train; these belong to k3moe_shared_ffn_backward.)
+ * A gradient is any number of elements at any element-aligned address.
+ * ------------------------------------------------------------------------- */
+typedef struct k3moe_tensor {
+  const void* data;    /* device pointer, aligned to its element (NULL only if numel is 0) */
+  void* out;           /* k3moe_grad_clip's result; may be data itself with out_dtype == dtype */
+  int64_t numel;       /* 0 <= numel <= 2^40 */
+  int32_t dtype;       /* K3MOE_F32 or K3MOE_BF16 */
+  int32_t out_dtype;
+} k3moe_tensor;
+
+/* Workspace of the two calls below for n tensors (256-byte aligned; 0 if n < 0
+ * or n > 2^20). */
+size_t k3moe_grad_workspace_bytes(int32_t n);
+/* *norm (device fp32) = sqrt(sum over the tensors of the squares of their
+ * elements), summed in fp64 in a fixed order.  tensors is a HOST array (read
+ * before the call returns), `out` fields ignored; n = 0 gives 0.  The same
+ * tensor twice counts twice.  Errors: EINVAL (NULL, n < 0 or n > 2^20, sizes),
+ * EUNSUPPORTED (dtypes), EALIGN, EWORKSPACE. */
+k3moe_status k3moe_grad_norm(const k3moe_tensor* tensors, int32_t n, float* norm, void* workspace,
+                             size_t workspace_bytes, void* stream);
+/* The same norm, and out = data * min(1, max_norm / norm) for every tensor,
+ * rounded to out_dtype.  The factor comes from the fp64 norm (finite gradients
+ * are clipped even where *norm is past fp32's range); a norm of infinities or
+ * NaN scales nothing (out = data), and the caller sees it in *norm.  In place (out == data) a step that needs no
+ * clipping is left untouched.  Errors: as above; EINVAL also for a max_norm
+ * that is negative or NaN and for an out that overlaps any tensor but its own
+ * data. */
+k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_norm, float* norm,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* k3moe_status_str(k3moe_status status);

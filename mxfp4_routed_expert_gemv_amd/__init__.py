@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(HERE, "libk3moe.so")
 F32, BF16 = 0, 1
 FMT_MXFP4, FMT_BF16, FMT_RVQ3 = 0, 1, 2
 (OP_ROUTE, OP_PERMUTE, OP_EXPERT_FFN, OP_SHARED_FFN, OP_COMBINE, OP_LAYER,
- OP_EXPERT_GATEUP) = range(7)
+ OP_EXPERT_GATEUP, OP_SHARED_TRAIN, OP_SHARED_BACKWARD) = range(9)
 PATH_GEMV, PATH_MFMA = 0, 1
 ROUTER_SOFTMAX, ROUTER_SIGMOID, ROUTER_SIGMOID_NORM = 0, 1, 2
 ROUTERS = {"softmax": ROUTER_SOFTMAX, "sigmoid": ROUTER_SIGMOID,
@@ -38,7 +38,9 @@ EXPORTS = ["k3moe_workspace_bytes", "k3moe_mxfp4_bytes", "k3moe_path_class", "k3
            "k3moe_shared_ffn", "k3moe_combine", "k3moe_layer", "k3moe_layer_noalloc",
            "k3moe_status_str", "k3moe_last_error", "k3moe_cache_create", "k3moe_cache_destroy",
            "k3moe_cache_workspace_bytes", "k3moe_cache_layer", "k3moe_cache_prefetch",
-           "k3moe_cache_plan", "k3moe_cache_stats_get"]
+           "k3moe_cache_plan", "k3moe_cache_stats_get", "k3moe_shared_ffn_train",
+           "k3moe_shared_ffn_backward", "k3moe_w4_linear", "k3moe_w4_glu",
+           "k3moe_grad_workspace_bytes", "k3moe_grad_norm", "k3moe_grad_clip"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -65,6 +67,16 @@ class LayerWeights(ctypes.Structure):
 class CacheStats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("lookups", "hits", "misses", "prefetched",
                                               "prefetch_hits", "evictions", "bytes_copied")]
+
+
+class W4Matrix(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 class K3moeError(RuntimeError):
@@ -123,6 +135,20 @@ def _load():
     lib.k3moe_cache_plan.argtypes = [P, P, I32, P]
     lib.k3moe_cache_stats_get.restype = ctypes.c_int
     lib.k3moe_cache_stats_get.argtypes = [P, ctypes.POINTER(CacheStats)]
+    lib.k3moe_shared_ffn_train.restype = ctypes.c_int
+    lib.k3moe_shared_ffn_train.argtypes = [SP, BP, P, P, P, P, S, P]
+    lib.k3moe_shared_ffn_backward.restype = ctypes.c_int
+    lib.k3moe_shared_ffn_backward.argtypes = [SP, BP, P, P, P, P, P, P, P, S, P]
+    for f in (lib.k3moe_w4_linear, lib.k3moe_w4_glu):
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.POINTER(W4Matrix), I64, I32, I32, P, P, P]
+    lib.k3moe_grad_workspace_bytes.restype = S
+    lib.k3moe_grad_workspace_bytes.argtypes = [I32]
+    # (the list of tensors may come as any buffer of k3moe_tensor's layout)
+    lib.k3moe_grad_norm.restype = ctypes.c_int
+    lib.k3moe_grad_norm.argtypes = [P, I32, P, P, S, P]
+    lib.k3moe_grad_clip.restype = ctypes.c_int
+    lib.k3moe_grad_clip.argtypes = [P, I32, ctypes.c_float, P, P, S, P]
     lib.k3moe_status_str.restype = ctypes.c_char_p
     lib.k3moe_status_str.argtypes = [ctypes.c_int]
     lib.k3moe_last_error.restype = ctypes.c_char_p
@@ -238,6 +264,45 @@ def k3moe_layer_noalloc(shape, weights: LayerWeights, x, out, diag=None, stream=
                                    _addr(out), _addr(diag), _stream(stream)))
 
 
+def k3moe_shared_ffn_train(shape, bank: ExpertBank, x, gu, y, workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_shared_ffn_train(ctypes.byref(shape), ctypes.byref(bank), _addr(x),
+                                      _addr(gu), _addr(y), wp, wb, _stream(stream)))
+
+
+def k3moe_shared_ffn_backward(shape, bank: ExpertBank, x, gu, dy, dx, dw13, dw2, workspace=None,
+                              stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_shared_ffn_backward(ctypes.byref(shape), ctypes.byref(bank), _addr(x),
+                                         _addr(gu), _addr(dy), _addr(dx), _addr(dw13),
+                                         _addr(dw2), wp, wb, _stream(stream)))
+
+
+def k3moe_w4_linear(w: W4Matrix, T, x_dtype, out_dtype, x, out, stream=None):
+    _check(lib.k3moe_w4_linear(ctypes.byref(w), T, x_dtype, out_dtype, _addr(x), _addr(out),
+                               _stream(stream)))
+
+
+def k3moe_w4_glu(w: W4Matrix, T, x_dtype, out_dtype, x, out, stream=None):
+    _check(lib.k3moe_w4_glu(ctypes.byref(w), T, x_dtype, out_dtype, _addr(x), _addr(out),
+                            _stream(stream)))
+
+
+def k3moe_grad_workspace_bytes(n: int) -> int:
+    return lib.k3moe_grad_workspace_bytes(n)
+
+
+def k3moe_grad_norm(tensors, n, norm, workspace=None, stream=None):
+    """tensors: a ctypes array of Tensor, or the host address of such a list."""
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_grad_norm(tensors, n, _addr(norm), wp, wb, _stream(stream)))
+
+
+def k3moe_grad_clip(tensors, n, max_norm, norm, workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_grad_clip(tensors, n, max_norm, _addr(norm), wp, wb, _stream(stream)))
+
+
 class ExpertCache:
     """An HBM cache of host-resident routed experts (k3moe_cache_*): host_bank
     holds pinned host tensors, slot_bank device tensors of `slots` experts;
@@ -296,6 +361,10 @@ def make_shape(T, d, f, E, k, n_shared, f_shared, x_dtype, out_dtype, router=ROU
 
 def make_bank(fmt, n, d, f, w13, w13_scale, w2, w2_scale) -> ExpertBank:
     return ExpertBank(fmt, n, d, f, _addr(w13), _addr(w13_scale), _addr(w2), _addr(w2_scale))
+
+
+def make_w4(n, k, group, codes, scale, zero=None) -> W4Matrix:
+    return W4Matrix(n, k, group, _addr(codes), _addr(scale), _addr(zero))
 
 
 def make_weights(w_router, routed: ExpertBank, shared: ExpertBank,

@@ -4,8 +4,11 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
+#include <new>
 #include <string>
+#include <vector>
 
 #include "internal.h"
 
@@ -153,6 +156,97 @@ k3moe_status check_bias(const k3moe_shape& s, const float* bias) {
   return opt_ptr(bias, "router_bias");
 }
 
+// Checks of the shared experts' training calls (T = 0 included).
+k3moe_status check_train(const k3moe_shape* shape, const k3moe_expert_bank* bank) {
+  K3_CHECK(check_shape(shape));
+  K3_CHECK(check_shared_bank(*shape, bank));
+  if (shape->n_shared == 0) return fail(K3MOE_EINVAL, "shape has no shared experts");
+  if (shape->x_dtype != K3MOE_BF16)
+    return fail(K3MOE_EUNSUPPORTED, "the shared experts train on bf16 x");
+  if (shape->T > (int64_t(1) << 30))
+    return fail(K3MOE_ESHAPE, "T = %lld: need <= 2^30", (long long)shape->T);
+  return K3MOE_OK;
+}
+
+k3moe_status check_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_t out_dtype,
+                      bool glu) {
+  if (!w) return fail(K3MOE_EINVAL, "w is NULL");
+  if (T < 0 || w->n < 0 || w->k < 0 || w->group < 0) return fail(K3MOE_EINVAL, "negative size");
+  if (x_dtype != K3MOE_F32 && x_dtype != K3MOE_BF16)
+    return fail(K3MOE_EUNSUPPORTED, "x_dtype %d is not F32 or BF16", x_dtype);
+  if (out_dtype != K3MOE_F32 && out_dtype != K3MOE_BF16)
+    return fail(K3MOE_EUNSUPPORTED, "out_dtype %d is not F32 or BF16", out_dtype);
+  if (T > (1 << 18)) return fail(K3MOE_ESHAPE, "T = %lld: need <= 2^18", (long long)T);
+  if (w->n < 1 || w->n > (1 << 24)) return fail(K3MOE_ESHAPE, "n = %d: need 1 <= n <= 2^24", w->n);
+  if (glu && w->n % 2) return fail(K3MOE_ESHAPE, "n = %d: the gated form needs an even n", w->n);
+  if (w->group != 32 && w->group != 64 && (w->group < 128 || w->group % 128))
+    return fail(K3MOE_ESHAPE, "group = %d: need 32, 64 or a multiple of 128", w->group);
+  if (w->k < 1 || w->k > (1 << 20) || w->k % w->group)
+    return fail(K3MOE_ESHAPE, "k = %d: need group <= k <= 2^20, k %% group == 0", w->k);
+  return K3MOE_OK;
+}
+
+k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_t out_dtype,
+                    const void* x, void* out, void* stream, bool glu);
+
+constexpr int kMaxTensors = 1 << 20;
+
+struct Span {
+  uintptr_t lo, hi;
+  int32_t tensor;
+  bool out;
+};
+
+// No clipped tensor's output may touch another tensor, or its own data other
+// than exactly in place.
+k3moe_status check_overlap(const k3moe_tensor* ts, int32_t n) {
+  std::vector<Span> spans;
+  spans.reserve(2 * (size_t)n);
+  for (int32_t i = 0; i < n; ++i) {
+    const k3moe_tensor& t = ts[i];
+    if (t.numel == 0) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(t.data), b = reinterpret_cast<uintptr_t>(t.out);
+    const bool in_place = a == b && t.dtype == t.out_dtype;
+    if (!in_place) spans.push_back({a, a + t.numel * (t.dtype == K3MOE_F32 ? 4u : 2u), i, false});
+    spans.push_back({b, b + t.numel * (t.out_dtype == K3MOE_F32 ? 4u : 2u), i, true});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& p, const Span& q) { return p.lo < q.lo; });
+  // against the span that reaches furthest so far, and the output that does
+  uintptr_t any = 0, outs = 0;
+  int32_t any_t = 0, out_t = 0;
+  for (const Span& s : spans) {
+    const bool hit = s.out ? s.lo < any : s.lo < outs;
+    if (hit)
+      return fail(K3MOE_EINVAL, "the out of tensor %d overlaps tensor %d",
+                  s.out ? s.tensor : out_t, s.out ? any_t : s.tensor);
+    if (s.hi > any) any = s.hi, any_t = s.tensor;
+    if (s.out && s.hi > outs) outs = s.hi, out_t = s.tensor;
+  }
+  return K3MOE_OK;
+}
+
+k3moe_status check_grads(const k3moe_tensor* ts, int32_t n, const float* norm, bool clip) {
+  if (n < 0 || n > kMaxTensors) return fail(K3MOE_EINVAL, "n = %d: need 0 <= n <= 2^20", n);
+  if (n > 0 && !ts) return fail(K3MOE_EINVAL, "tensors is NULL");
+  if (!norm) return fail(K3MOE_EINVAL, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return fail(K3MOE_EALIGN, "norm is not 4-byte aligned");
+  for (int32_t i = 0; i < n; ++i) {
+    const k3moe_tensor& t = ts[i];
+    if (t.numel < 0 || t.numel > (int64_t(1) << 40))
+      return fail(K3MOE_EINVAL, "tensor %d has %lld elements", i, (long long)t.numel);
+    if (t.dtype != K3MOE_F32 && t.dtype != K3MOE_BF16)
+      return fail(K3MOE_EUNSUPPORTED, "tensor %d: dtype %d is not F32 or BF16", i, t.dtype);
+    if (clip && t.out_dtype != K3MOE_F32 && t.out_dtype != K3MOE_BF16)
+      return fail(K3MOE_EUNSUPPORTED, "tensor %d: out_dtype %d is not F32 or BF16", i, t.out_dtype);
+    if (t.numel == 0) continue;
+    if (!t.data || (clip && !t.out)) return fail(K3MOE_EINVAL, "tensor %d has a NULL pointer", i);
+    if ((reinterpret_cast<uintptr_t>(t.data) & (t.dtype == K3MOE_F32 ? 3u : 1u)) ||
+        (clip && (reinterpret_cast<uintptr_t>(t.out) & (t.out_dtype == K3MOE_F32 ? 3u : 1u))))
+      return fail(K3MOE_EALIGN, "tensor %d is not aligned to its elements", i);
+  }
+  return clip ? check_overlap(ts, n) : K3MOE_OK;
+}
+
 k3moe_status hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return ok();
   return fail(K3MOE_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
@@ -209,6 +303,25 @@ SharedWs carve_shared(const k3moe_shape& s, void* ws, size_t* bytes) {
   return r;
 }
 
+SharedTrainWs carve_shared_train(const k3moe_shape& s, bool backward, void* ws, size_t* bytes) {
+  Carver c(ws);
+  SharedTrainWs r;
+  const size_t n = (size_t)s.T * s.n_shared * s.f_shared;
+  r.h = c.take<uint16_t>(n);
+  r.dgu = backward ? c.take<uint16_t>(2 * n) : nullptr;
+  if (bytes) *bytes = c.off;
+  return r;
+}
+
+GradWs carve_grads(int n, void* ws, size_t* bytes) {
+  Carver c(ws);
+  GradWs r;
+  r.partial = c.take<double>(grad_partials(n));
+  r.scale = c.take<char>(256);
+  if (bytes) *bytes = c.off;
+  return r;
+}
+
 LayerWs carve_layer(const k3moe_shape& s, void* ws, size_t* bytes) {
   Carver c(ws);
   LayerWs r;
@@ -260,6 +373,39 @@ k3moe_status layer_validate(const k3moe_shape* shape, const k3moe_layer_weights*
   carve_layer(s, nullptr, need);
   return K3MOE_OK;
 }
+
+namespace {
+k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_t out_dtype,
+                    const void* x, void* out, void* stream, bool glu) {
+  K3_CHECK(check_w4(w, T, x_dtype, out_dtype, glu));
+  if (T == 0) return ok();
+  K3_CHECK(need_ptr(w->codes, "codes"));
+  K3_CHECK(need_ptr(w->scale, "scale"));
+  K3_CHECK(opt_ptr(w->zero, "zero"));
+  K3_CHECK(need_ptr(x, "x"));
+  K3_CHECK(need_ptr(out, "out"));
+  return hip_status(launch_w4(*w, T, x_dtype == K3MOE_F32, out_dtype == K3MOE_F32, glu, x, out,
+                              static_cast<hipStream_t>(stream)),
+                    glu ? "k3moe_w4_glu launch" : "k3moe_w4_linear launch");
+}
+k3moe_status run_grads(const k3moe_tensor* tensors, int32_t n, bool clip, float max_norm,
+                              float* norm, void* workspace, size_t workspace_bytes, void* stream,
+                              const char* what) {
+  try {
+    K3_CHECK(check_grads(tensors, n, norm, clip));
+  } catch (const std::bad_alloc&) {
+    return fail(K3MOE_EINVAL, "no host memory for the list of %d tensors", n);
+  }
+  size_t need = 0;
+  carve_grads(n, nullptr, &need);
+  K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  return hip_status(launch_grads(tensors, n, clip, max_norm, norm,
+                                 carve_grads(n, workspace, nullptr),
+                                 static_cast<hipStream_t>(stream)),
+                    what);
+}
+
+}  // namespace
 
 k3moe_status hip_failure(hipError_t e, const char* what) { return hip_status(e, what); }
 k3moe_status shape_status(const k3moe_shape* shape) { return check_shape(shape); }
@@ -371,6 +517,8 @@ size_t k3moe_workspace_bytes(const k3moe_shape* shape, int op) {
     case K3MOE_OP_SHARED_FFN: carve_shared(*shape, nullptr, &n); break;
     case K3MOE_OP_COMBINE: n = 0; break;
     case K3MOE_OP_LAYER: carve_layer(*shape, nullptr, &n); break;
+    case K3MOE_OP_SHARED_TRAIN: carve_shared_train(*shape, false, nullptr, &n); break;
+    case K3MOE_OP_SHARED_BACKWARD: carve_shared_train(*shape, true, nullptr, &n); break;
     default: return 0;
   }
   return n;
@@ -538,6 +686,81 @@ k3moe_status k3moe_layer(const k3moe_shape* shape, const k3moe_layer_weights* we
   if (shape->T == 0) return ok();
   K3_CHECK(check_ws(workspace, workspace_bytes, need));
   return layer_run(*shape, *weights, x, out, diag, workspace, static_cast<hipStream_t>(stream));
+}
+
+k3moe_status k3moe_shared_ffn_train(const k3moe_shape* shape, const k3moe_expert_bank* bank,
+                                    const void* x, void* gu, void* y, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  K3_CHECK(check_train(shape, bank));
+  const k3moe_shape& s = *shape;
+  if (s.T == 0) return ok();
+  K3_CHECK(need_ptr(x, "x"));
+  K3_CHECK(need_ptr(gu, "gu"));
+  K3_CHECK(need_ptr(y, "y"));
+  size_t need = 0;
+  carve_shared_train(s, false, nullptr, &need);
+  K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  return hip_status(launch_shared_train(s, *bank, x, gu, y,
+                                        carve_shared_train(s, false, workspace, nullptr),
+                                        static_cast<hipStream_t>(stream)),
+                    "k3moe_shared_ffn_train launch");
+}
+
+k3moe_status k3moe_shared_ffn_backward(const k3moe_shape* shape, const k3moe_expert_bank* bank,
+                                       const void* x, const void* gu, const void* dy, void* dx,
+                                       void* dw13, void* dw2, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  K3_CHECK(check_train(shape, bank));
+  const k3moe_shape& s = *shape;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  K3_CHECK(opt_ptr(dx, "dx"));
+  K3_CHECK(opt_ptr(dw13, "dw13"));
+  K3_CHECK(opt_ptr(dw2, "dw2"));
+  if (s.T == 0) {
+    const size_t w = (size_t)s.n_shared * s.f_shared * s.d * 2;
+    hipError_t e = launch_zero(dw13, 2 * w, st);
+    if (e == hipSuccess) e = launch_zero(dw2, w, st);
+    return hip_status(e, "k3moe_shared_ffn_backward launch");
+  }
+  K3_CHECK(need_ptr(x, "x"));
+  K3_CHECK(need_ptr(gu, "gu"));
+  K3_CHECK(need_ptr(dy, "dy"));
+  size_t need = 0;
+  carve_shared_train(s, true, nullptr, &need);
+  K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  return hip_status(launch_shared_backward(s, *bank, x, gu, dy, dx, dw13, dw2,
+                                           carve_shared_train(s, true, workspace, nullptr), st),
+                    "k3moe_shared_ffn_backward launch");
+}
+
+k3moe_status k3moe_w4_linear(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
+                             int32_t out_dtype, const void* x, void* out, void* stream) {
+  return run_w4(w, T, x_dtype, out_dtype, x, out, stream, false);
+}
+
+k3moe_status k3moe_w4_glu(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
+                          int32_t out_dtype, const void* x, void* out, void* stream) {
+  return run_w4(w, T, x_dtype, out_dtype, x, out, stream, true);
+}
+
+size_t k3moe_grad_workspace_bytes(int32_t n) {
+  if (n < 0 || n > kMaxTensors) return 0;
+  size_t need = 0;
+  carve_grads(n, nullptr, &need);
+  return need;
+}
+
+k3moe_status k3moe_grad_norm(const k3moe_tensor* tensors, int32_t n, float* norm, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return run_grads(tensors, n, false, 0.0f, norm, workspace, workspace_bytes, stream,
+                   "k3moe_grad_norm launch");
+}
+
+k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_norm, float* norm,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (!(max_norm >= 0.0f)) return fail(K3MOE_EINVAL, "max_norm is negative or NaN");
+  return run_grads(tensors, n, true, max_norm, norm, workspace, workspace_bytes, stream,
+                   "k3moe_grad_clip launch");
 }
 
 const char* k3moe_status_str(k3moe_status status) {

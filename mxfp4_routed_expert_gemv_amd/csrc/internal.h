@@ -172,6 +172,32 @@ hipError_t launch_shared_ffn(const k3moe_shape& s, const k3moe_expert_bank& bank
 hipError_t launch_combine(const k3moe_shape& s, const float* y_perm, const int32_t* pair_pos,
                           const float* topk_w, const float* shared_y, void* out, hipStream_t st);
 
+// The shared experts' training pass (dense_gemm.hip).
+struct SharedTrainWs {
+  uint16_t* h;     // [T][n_shared][f_shared] bf16
+  uint16_t* dgu;   // backward: [T][n_shared][2 f_shared] bf16; else nullptr
+};
+SharedTrainWs carve_shared_train(const k3moe_shape& s, bool backward, void* ws, size_t* bytes);
+hipError_t launch_shared_train(const k3moe_shape& s, const k3moe_expert_bank& b, const void* x,
+                               void* gu, void* y, const SharedTrainWs& ws, hipStream_t st);
+hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank& b, const void* x,
+                                  const void* gu, const void* dy, void* dx, void* dw13, void* dw2,
+                                  const SharedTrainWs& ws, hipStream_t st);
+// Zeros by a kernel (bytes a multiple of 16; p may be NULL).
+hipError_t launch_zero(void* p, size_t bytes, hipStream_t st);
+// Products with 4-bit weights and group scales (w4.hip), on checked arguments.
+hipError_t launch_w4(const k3moe_w4_matrix& w, int64_t T, bool x_f32, bool out_f32, bool glu,
+                     const void* x, void* out, hipStream_t st);
+// The gradients' norm and clipping (grads.hip).
+struct GradWs {
+  double* partial;   // partial sums of squares, grad_partials(n)
+  void* scale;       // the norm and the factor, 256 bytes
+};
+size_t grad_partials(int n);
+GradWs carve_grads(int n, void* ws, size_t* bytes);
+hipError_t launch_grads(const k3moe_tensor* ts, int n, bool clip, float max_norm, float* norm,
+                        const GradWs& ws, hipStream_t st);
+
 // Whole-layer entry points: the host-side validation (nothing enqueued; *need
 // = workspace bytes, 0 for an empty batch), the status of a workspace that is
 // too small, and the stages of a validated call on a workspace of at least
