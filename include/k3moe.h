@@ -448,7 +448,7 @@ k3moe_status k3moe_cache_stats_get(const k3moe_expert_cache* cache, k3moe_cache_
  * Training of the shared experts (the always-on bf16 ones; the routed 4-bit
  * experts stay frozen).  Only T, d, n_shared, f_shared and out_dtype of the
  * shape are used beside its checks; x_dtype must be K3MOE_BF16
- * (EUNSUPPORTED), T <= 2^30 (ESHAPE).  With F = n_shared f_shared:
+ * (EUNSUPPORTED), T <= 2^26 (ESHAPE).  With F = n_shared f_shared:
  *   forward   g_s = Wg_s x, u_s = Wu_s x, h_s = silu(g_s) * u_s,
  *             y = sum over the experts of Wd_s h_s
  *   backward  of any loss, from dy = dL/dy:

@@ -163,8 +163,8 @@ k3moe_status check_train(const k3moe_shape* shape, const k3moe_expert_bank* bank
   if (shape->n_shared == 0) return fail(K3MOE_EINVAL, "shape has no shared experts");
   if (shape->x_dtype != K3MOE_BF16)
     return fail(K3MOE_EUNSUPPORTED, "the shared experts train on bf16 x");
-  if (shape->T > (int64_t(1) << 30))
-    return fail(K3MOE_ESHAPE, "T = %lld: need <= 2^30", (long long)shape->T);
+  if (shape->T > (int64_t(1) << 26))
+    return fail(K3MOE_ESHAPE, "T = %lld: need <= 2^26", (long long)shape->T);
   return K3MOE_OK;
 }
 
@@ -309,6 +309,7 @@ SharedTrainWs carve_shared_train(const k3moe_shape& s, bool backward, void* ws, 
   const size_t n = (size_t)s.T * s.n_shared * s.f_shared;
   r.h = c.take<uint16_t>(n);
   r.dgu = backward ? c.take<uint16_t>(2 * n) : nullptr;
+  r.part = c.take<float>(shared_train_part_floats(s, backward));
   if (bytes) *bytes = c.off;
   return r;
 }

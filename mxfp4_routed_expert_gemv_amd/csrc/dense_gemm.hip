@@ -48,6 +48,8 @@ struct DenseArgs {
   uint16_t* o1;         // kGateUp, kDHid: h [T][F]
   int T, d, fs, S;
   int out_f32;          // kDown: y in fp32
+  float* part;          // split contraction: partial sums [splits][M][columns]
+  int splits, k_split;  // contraction elements per split (a multiple of kBK)
 };
 
 // A voffset past num_records: the copy writes zeros to LDS.  Every offset of
@@ -55,11 +57,11 @@ struct DenseArgs {
 constexpr uint32_t kRecords = 0x80000000u;
 constexpr uint32_t kOut = 0xFFFFFFF0u;
 
-__device__ __forceinline__ u32x4_t rsrc_of(const uint16_t* p) {
-  const uint64_t a = (uint64_t)(uintptr_t)p;
+// Buffer descriptor over base p (wave-uniform).
+__device__ __forceinline__ u32x4_t rsrc_of(uint64_t p) {
   u32x4_t r;
-  r.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  r.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xFFFFu);
+  r.x = __builtin_amdgcn_readfirstlane((uint32_t)p);
+  r.y = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));   // 48-bit address, stride 0
   r.z = kRecords;
   r.w = 0x00020000u;
   return r;
@@ -75,12 +77,19 @@ __device__ __forceinline__ void dma16_buf(u32x4_t rsrc, uint32_t voff, uint32_t 
 }
 #pragma clang diagnostic pop
 
-// Four bf16 roundings packed.
+// Four bf16 roundings (to nearest even, v_cvt_pk_bf16_f32) packed.
 __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
-  uint2 p;
-  p.x = (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
-  p.y = (uint32_t)f32_to_bf16(c) | ((uint32_t)f32_to_bf16(d) << 16);
-  return p;
+  typedef __attribute__((ext_vector_type(2))) float f2;
+  return make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf16x2_t)),
+                    __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{c, d}, bf16x2_t)));
+}
+
+// sigmoid(g) from the hardware's exp2 and reciprocal: off by about |g| 2^-24
+// of its value, far inside the bf16 rounding of everything made from it.  For g
+// below -88 the exponential is +inf and the result 0, so g sigmoid(g) is -0
+// there, never NaN.
+__device__ __forceinline__ float sigmoid_fast(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
 // An operand tile of R rows (of M or N) x 64 contraction elements in LDS.
@@ -144,9 +153,53 @@ struct Tile {
 // Column (row of w13) of hidden feature n's gate in [2 F]; its up is fs further.
 __device__ __forceinline__ int gate_col(int n, int fs) { return n + n / fs * fs; }
 
+// ---- epilogues: four consecutive columns n of row m from their fp32 sums
+__device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, f32x4_t ga, f32x4_t up) {
+  const int F = g.S * g.fs;
+  uint16_t* gu = static_cast<uint16_t*>(g.o0) + (size_t)m * 2 * F + gate_col(n, g.fs);
+  *reinterpret_cast<uint2*>(gu) = pack4(ga[0], ga[1], ga[2], ga[3]);
+  *reinterpret_cast<uint2*>(gu + g.fs) = pack4(up[0], up[1], up[2], up[3]);
+  *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) =
+      pack4(ga[0] * sigmoid_fast(ga[0]) * up[0], ga[1] * sigmoid_fast(ga[1]) * up[1],
+            ga[2] * sigmoid_fast(ga[2]) * up[2], ga[3] * sigmoid_fast(ga[3]) * up[3]);
+}
+// v = dh: dg, du and h from the kept g and u
+__device__ __forceinline__ void store_dhid(const DenseArgs& g, int m, int n, f32x4_t v) {
+  const int F = g.S * g.fs;
+  const size_t o = (size_t)m * 2 * F + gate_col(n, g.fs);
+  const uint2 gw = *reinterpret_cast<const uint2*>(g.gu + o);
+  const uint2 uw = *reinterpret_cast<const uint2*>(g.gu + o + g.fs);
+  const float ga[4] = {bf16_lo(gw.x), bf16_hi(gw.x), bf16_lo(gw.y), bf16_hi(gw.y)};
+  const float up[4] = {bf16_lo(uw.x), bf16_hi(uw.x), bf16_lo(uw.y), bf16_hi(uw.y)};
+  float dg[4], du[4], h[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float s = sigmoid_fast(ga[r]), gs = ga[r] * s;
+    h[r] = gs * up[r];
+    du[r] = v[r] * gs;
+    dg[r] = v[r] * up[r] * (s + gs * (1.0f - s));
+  }
+  uint16_t* o0 = static_cast<uint16_t*>(g.o0) + o;
+  *reinterpret_cast<uint2*>(o0) = pack4(dg[0], dg[1], dg[2], dg[3]);
+  *reinterpret_cast<uint2*>(o0 + g.fs) = pack4(du[0], du[1], du[2], du[3]);
+  *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) = pack4(h[0], h[1], h[2], h[3]);
+}
+template <int P>
+__device__ __forceinline__ void store_product(const DenseArgs& g, int m, int n, int N, f32x4_t v) {
+  if (P == kDown && g.out_f32) {
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.o0) + (size_t)m * N + n) = v;
+    return;
+  }
+  // dW2 [S][d][fs]: column n is feature n % fs of expert n / fs
+  const size_t o = P == kDW2 ? ((size_t)(n / g.fs) * g.d + m) * g.fs + n % g.fs : (size_t)m * N + n;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.o0) + o) = pack4(v[0], v[1], v[2], v[3]);
+}
+
 constexpr int kGM = 8;   // m-tiles per group of the item order
 
-template <int P, int BM, int BN, int WM, int WN>
+// SPLIT: an item is a tile and one of g.splits pieces of the contraction; its
+// sums go to g.part, and split_finish adds the pieces in order.
+template <int P, int BM, int BN, int WM, int WN, bool SPLIT = false>
 __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   using C = Tile<P, BM, BN, WM, WN>;
   using OA = typename C::A;
@@ -161,55 +214,57 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   const int M = P == kDW13 ? 2 * F : P == kDW2 ? d : T;
   const int N = P == kGateUp || P == kDHid || P == kDW2 ? F : d;
   const int K = P == kGateUp || P == kDHid ? d : P == kDown ? F : P == kDX ? 2 * F : T;
-  const int nst = (K + kBK - 1) / kBK;
   const int n_mt = (M + BM - 1) / BM, n_nt = (N + C::kN - 1) / C::kN;
-  const ItemRange ir = item_range((long)n_mt * n_nt);
+  const int n_cols = SPLIT ? n_nt * g.splits : n_nt;   // n-tiles, every split's in turn
+  const ItemRange ir = item_range((long)n_mt * n_cols);
+  const int it_first = (int)ir.first, it_end = (int)ir.end, it_step = (int)ir.step;
 
   // Items: groups of kGM m-tiles, the m-tile fastest, then the n-tile, so the
   // workgroups of an XCD share both operands through its L2.
-  auto item_tile = [&](long it, int& m0, int& n0) {
-    const long per = (long)kGM * n_nt;
-    const int grp = (int)(it / per), first = grp * kGM;
-    const int r = (int)(it - grp * per), gsz = min(n_mt - first, kGM);
-    const int nt = r / gsz;
-    n0 = nt * C::kN;
+  auto item_tile = [&](int it, int& m0, int& n0, int& k0, int& k1) {
+    const int per = kGM * n_cols, grp = it / per, first = grp * kGM;
+    const int r = it - grp * per, gsz = min(n_mt - first, kGM), nt = r / gsz;
+    const int sp = SPLIT ? nt / n_nt : 0;
+    n0 = (nt - sp * n_nt) * C::kN;
     m0 = (first + r - nt * gsz) * BM;
+    k0 = SPLIT ? sp * g.k_split : 0;
+    k1 = SPLIT ? min(k0 + g.k_split, K) : K;
+    return sp;
   };
 
   // ---- copies: this wave's units of both operands, as byte offsets from the
-  // tile's first element (kOut: outside the matrix), and the tile's base.
+  // tile's first element (kOut: outside the matrix), and that element's
+  // address, which advances with the stage.
   uint32_t va[C::NA], vb[C::NB];
-  int ka[C::NA], kb[C::NB];   // contraction element of each unit within the stage
-  const uint16_t *pa, *pb;
-  size_t sa, sb;              // elements a stage advances
-  long c_it = ir.first;
-  int c_st = 0;
+  const size_t lda = P == kGateUp || P == kDHid || P == kDW2 ? d : P == kDown ? F : 2 * F;
+  const size_t ldb = P == kGateUp || P == kDX || P == kDW13 ? d : P == kDW2 ? F : fs;
+  const uint32_t sa = C::A_KC ? kBK * 2 : kBK * 2 * (uint32_t)lda;   // bytes per stage
+  const uint32_t sb = C::B_KC ? kBK * 2 : kBK * 2 * (uint32_t)ldb;
+  uint64_t pa, pb;
+  int c_it = it_first, c_k, c_end;   // the copies' item, first contraction element, last but one
+  int c_ko = 0;                      // kDown: c_k within its expert's features
   auto setup = [&]() {
     int m0, n0;
-    item_tile(c_it, m0, n0);
-    const size_t lda = P == kGateUp || P == kDHid || P == kDW2 ? d : P == kDown ? F : 2 * F;
-    pa = g.a + (C::A_KC ? (size_t)m0 * lda : (size_t)m0);
-    sa = C::A_KC ? (size_t)kBK : kBK * lda;
+    item_tile(c_it, m0, n0, c_k, c_end);
+    pa = (uint64_t)(uintptr_t)(g.a + (C::A_KC ? (size_t)m0 * lda + c_k : (size_t)c_k * lda + m0));
 #pragma unroll
     for (int c = 0; c < C::NA; ++c) {
       int r, k;
       OA::unit((wv * C::NA + c) * 64 + lane, r, k);
-      ka[c] = k;
       const size_t e = C::A_KC ? (size_t)r * lda + k : (size_t)k * lda + r;
       va[c] = m0 + r < M ? (uint32_t)(e * 2) : kOut;
     }
     const int gc0 = gate_col(n0, fs);
-    const size_t ldb = P == kGateUp || P == kDX || P == kDW13 ? d : P == kDW2 ? F : fs;
-    pb = g.b + (P == kGateUp ? (size_t)gc0 * d
-                : P == kDHid ? (size_t)(n0 / fs) * d * fs + n0 % fs
-                : C::B_KC    ? (size_t)n0 * ldb
-                             : (size_t)n0);
-    sb = C::B_KC ? (size_t)kBK : kBK * ldb;
+    if (P == kDown) c_ko = c_k % fs;
+    pb = (uint64_t)(uintptr_t)(
+        g.b + (P == kGateUp ? (size_t)gc0 * d + c_k
+               : P == kDHid ? (size_t)(n0 / fs) * d * fs + n0 % fs + (size_t)c_k * fs
+               : P == kDown ? (size_t)(c_k / fs) * d * fs + (size_t)n0 * fs + c_ko
+                            : (size_t)c_k * ldb + n0));
 #pragma unroll
     for (int c = 0; c < C::NB; ++c) {
       int r, k;
       OB::unit((wv * C::NB + c) * 64 + lane, r, k);
-      kb[c] = k;
       if (P == kGateUp) {
         // each wave's NF fragments: NF / 2 of gate rows, then the matching up rows
         const int w = r / (16 * NF), f = (r >> 4) % NF;
@@ -222,138 +277,175 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
         const size_t e = (size_t)(n / fs - n0 / fs) * d * fs + n % fs + (size_t)k * fs;
         vb[c] = n < N ? (uint32_t)((e - n0 % fs) * 2) : kOut;
       } else {
-        // (kDown: the stage's expert and position are added in issue)
-        const size_t e = C::B_KC ? (size_t)r * ldb + (P == kDown ? 0 : k) : (size_t)k * ldb + r;
+        const size_t e = C::B_KC ? (size_t)r * ldb + k : (size_t)k * ldb + r;
         vb[c] = n0 + r < N ? (uint32_t)(e * 2) : kOut;
       }
     }
   };
-  auto issue = [&](int slot) {
-    if (c_it >= ir.end) return;
-    const int k0 = c_st * kBK;
-    const bool tail = k0 + kBK > K;
-    const u32x4_t ra = rsrc_of(pa + (size_t)c_st * sa);
-    const uint32_t la = lds_addr(sA) + (uint32_t)(slot * OA::kSlot + wv * (C::NA * 1024));
-#pragma unroll
-    for (int c = 0; c < C::NA; ++c)
-      dma16_buf(ra, tail && k0 + ka[c] >= K ? kOut : va[c], la + c * 1024);
-    const uint32_t lb = lds_addr(sB) + (uint32_t)(slot * OB::kSlot + wv * (C::NB * 1024));
-    if (P == kDown) {
-      // feature k0 + k is element (k0 + k) % fs of a row of expert (k0 + k) / fs
-      const int e0 = k0 / fs;
-      const u32x4_t rb = rsrc_of(pb + (size_t)e0 * d * fs);
-#pragma unroll
-      for (int c = 0; c < C::NB; ++c) {
-        const int k = k0 - e0 * fs + kb[c], e = k / fs;
-        const uint32_t o = (uint32_t)(((size_t)e * d * fs + (k - e * fs)) * 2);
-        dma16_buf(rb, vb[c] == kOut || k0 + kb[c] >= K ? kOut : vb[c] + o, lb + c * 1024);
-      }
-    } else {
-      const u32x4_t rb = rsrc_of(pb + (size_t)c_st * sb);
-#pragma unroll
-      for (int c = 0; c < C::NB; ++c)
-        dma16_buf(rb, tail && k0 + kb[c] >= K ? kOut : vb[c], lb + c * 1024);
+  // Copy c of the stage at c_k (A's units, then B's) into `slot`.
+  auto copy = [&](int slot, int c) {
+    const bool isa = c < C::NA;
+    const int q = isa ? c : c - C::NA, n = isa ? C::NA : C::NB;
+    const uint32_t to = lds_addr(isa ? sA : sB) +
+                        (uint32_t)(slot * (isa ? OA::kSlot : OB::kSlot) + (wv * n + q) * 1024);
+    int r, k;
+    if (isa) OA::unit((wv * n + q) * 64 + lane, r, k); else OB::unit((wv * n + q) * 64 + lane, r, k);
+    uint32_t v = isa ? va[q] : vb[q];
+    uint64_t p = isa ? pa : pb;
+    if (P == kDown && !isa) {
+      // units past the end of expert c_k / fs's rows (fs may be 32: two ends)
+      const uint32_t next = (uint32_t)(d - 1) * fs * 2;
+      v += (c_ko + k >= fs ? next : 0u) + (c_ko + k >= 2 * fs ? next : 0u);
+      v = vb[q] == kOut ? kOut : v;
     }
-    if (++c_st == nst) {
-      c_st = 0;
-      c_it += ir.step;
-      if (c_it < ir.end) setup();
+    dma16_buf(rsrc_of(p), c_k + kBK > c_end && c_k + k >= c_end ? kOut : v, to);
+  };
+  auto advance = [&]() {   // the copies' next stage
+    c_k += kBK;
+    pa += sa;
+    pb += sb;
+    if (P == kDown) {
+      c_ko += kBK;
+      while (c_ko >= fs) {   // into the next expert's matrix
+        c_ko -= fs;
+        pb += (uint64_t)(d - 1) * fs * 2;
+      }
+    }
+    if (c_k >= c_end) {
+      c_it += it_step;
+      if (c_it < it_end) {
+        setup();
+      } else {   // behind the last item: zeros, that nothing uses
+#pragma unroll
+        for (int c = 0; c < C::NA; ++c) va[c] = kOut;
+#pragma unroll
+        for (int c = 0; c < C::NB; ++c) vb[c] = kOut;
+      }
     }
   };
 
   const int wm = wv / WN, wn = wv - wm * WN;
-  if (c_it < ir.end) setup();
-  issue(0);
+  // Fragments of one 32-element half: a step's MFMAs use row block i of A and
+  // every block of B; the next half's reads are spread over all but the last
+  // two steps, so they have landed when its first MFMA issues.
+  bf16x8_t fa[MF], fb[NF], na[MF], nb[NF];
+  f32x4_t acc[MF][NF];
+  // MFMAs of fa, fb; reads of (slot, j) into na, nb; the copies into slot `to`
+  // spread over the steps (to < 0: none)
+  auto half = [&](int slot, int j, int to) {
+    const uint8_t* ba = sA + slot * OA::kSlot;
+    const uint8_t* bb = sB + slot * OB::kSlot;
+    constexpr int kCp = (C::NA + C::NB + MF - 1) / MF;
+    constexpr int kPer = (MF + NF + (MF > 2 ? MF - 2 : 1) - 1) / (MF > 2 ? MF - 2 : 1);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+#pragma unroll
+      for (int r = i * kPer; r < (i + 1) * kPer && r < MF + NF; ++r) {
+        if (r < NF) nb[r] = OB::frag(bb, wn * NF + r, j, ln, lg);
+        else na[r - NF] = OA::frag(ba, wm * MF + r - NF, j, ln, lg);
+      }
+#pragma unroll
+      for (int f = 0; f < NF; ++f)   // sums transposed: a lane holds 4 consecutive n of one m
+        acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[f], fa[i], acc[i][f], 0, 0, 0);
+      if (to >= 0) {
+#pragma unroll
+        for (int c = i * kCp; c < (i + 1) * kCp && c < C::NA + C::NB; ++c) copy(to, c);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) fa[i] = na[i];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) fb[f] = nb[f];
+  };
+  if (it_first >= it_end) return;
+  setup();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+#pragma unroll
+    for (int c = 0; c < C::NA + C::NB; ++c) copy(q, c);
+    advance();
+  }
+  wait_vmem<0>();
+  wg_barrier();
+#pragma unroll
+  for (int f = 0; f < NF; ++f) fb[f] = OB::frag(sB, wn * NF + f, 0, ln, lg);
+#pragma unroll
+  for (int i = 0; i < MF; ++i) fa[i] = OA::frag(sA, wm * MF + i, 0, ln, lg);
   int slot = 0;
-  for (long it = ir.first; it < ir.end; it += ir.step) {
-    int m0, n0;
-    item_tile(it, m0, n0);
-    f32x4_t acc[MF][NF];
+  for (int it = it_first; it < it_end; it += it_step) {
+    int m0, n0, k0, k1;
+    const int sp = item_tile(it, m0, n0, k0, k1);
+    const int nst = (k1 - k0 + kBK - 1) / kBK;
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[i][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int s = 0; s < nst; ++s, slot ^= 1) {
-      // this wave's copies of the stage have landed and its reads of the other
-      // slot are done; past the barrier both hold for every wave
-      wait_vmem<0>();
+      half(slot, 1, -1);
+      // this wave's reads of the slot are done and its copies of the next
+      // stage have landed; past the barrier both hold for every wave
       wait_lds();
+      wait_vmem<0>();
       wg_barrier();
-      issue(slot ^ 1);
-      const uint8_t* ba = sA + slot * OA::kSlot;
-      const uint8_t* bb = sB + slot * OB::kSlot;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        bf16x8_t b[NF], a[2];
-#pragma unroll
-        for (int f = 0; f < NF; ++f) b[f] = OB::frag(bb, wn * NF + f, j, ln, lg);
-        a[0] = OA::frag(ba, wm * MF, j, ln, lg);
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          if (i + 1 < MF) a[(i + 1) & 1] = OA::frag(ba, wm * MF + i + 1, j, ln, lg);
-#pragma unroll
-          for (int f = 0; f < NF; ++f)   // sums transposed: a lane holds 4 consecutive n of one m
-            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[f], a[i & 1], acc[i][f], 0, 0, 0);
-        }
-      }
+      half(slot ^ 1, 0, slot);   // and the stage after the next on its way
+      advance();
     }
     // ---- epilogue: lane (ln, lg) holds m = m0 + 16 (wm MF + i) + ln, four n
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       const int m = m0 + (wm * MF + i) * 16 + ln;
       if (m >= M) continue;
-      if constexpr (P == kGateUp) {
+      if constexpr (SPLIT) {
+        const int cols = P == kGateUp ? 2 * F : N;
+        float* row = g.part + ((size_t)sp * M + m) * cols;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const int n = P == kGateUp ? n0 + wn * (8 * NF) + (f % (NF / 2)) * 16 + lg * 4
+                                     : n0 + (wn * NF + f) * 16 + lg * 4;
+          if (n >= N) continue;
+          const int c = P == kGateUp ? gate_col(n, fs) + (f >= NF / 2 ? fs : 0) : n;
+          *reinterpret_cast<f32x4_t*>(row + c) = acc[i][f];
+        }
+      } else if constexpr (P == kGateUp) {
 #pragma unroll
         for (int f = 0; f < NF / 2; ++f) {
           const int n = n0 + wn * (8 * NF) + f * 16 + lg * 4;
           if (n >= N) continue;
-          const f32x4_t ga = acc[i][f], up = acc[i][f + NF / 2];
-          uint16_t* gu = static_cast<uint16_t*>(g.o0) + (size_t)m * 2 * F + gate_col(n, fs);
-          *reinterpret_cast<uint2*>(gu) = pack4(ga[0], ga[1], ga[2], ga[3]);
-          *reinterpret_cast<uint2*>(gu + fs) = pack4(up[0], up[1], up[2], up[3]);
-          *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) =
-              pack4(silu_mul(ga[0], up[0]), silu_mul(ga[1], up[1]), silu_mul(ga[2], up[2]),
-                    silu_mul(ga[3], up[3]));
+          store_gateup(g, m, n, acc[i][f], acc[i][f + NF / 2]);
         }
       } else {
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
           const int n = n0 + (wn * NF + f) * 16 + lg * 4;
           if (n >= N) continue;
-          const f32x4_t v = acc[i][f];
-          if constexpr (P == kDHid) {
-            const size_t o = (size_t)m * 2 * F + gate_col(n, fs);
-            const uint2 gw = *reinterpret_cast<const uint2*>(g.gu + o);
-            const uint2 uw = *reinterpret_cast<const uint2*>(g.gu + o + fs);
-            const float ga[4] = {bf16_lo(gw.x), bf16_hi(gw.x), bf16_lo(gw.y), bf16_hi(gw.y)};
-            const float up[4] = {bf16_lo(uw.x), bf16_hi(uw.x), bf16_lo(uw.y), bf16_hi(uw.y)};
-            float dg[4], du[4], h[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float s = 1.0f / (1.0f + expf(-ga[r]));
-              // g s: for g < -88 e^-g is +inf and s is 0, the product -0, never NaN
-              const float gs = ga[r] * s;
-              h[r] = gs * up[r];
-              du[r] = v[r] * gs;
-              dg[r] = v[r] * up[r] * (s + gs * (1.0f - s));
-            }
-            uint16_t* o0 = static_cast<uint16_t*>(g.o0) + o;
-            *reinterpret_cast<uint2*>(o0) = pack4(dg[0], dg[1], dg[2], dg[3]);
-            *reinterpret_cast<uint2*>(o0 + fs) = pack4(du[0], du[1], du[2], du[3]);
-            *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) = pack4(h[0], h[1], h[2], h[3]);
-          } else if (P == kDown && g.out_f32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(g.o0) + (size_t)m * N + n) =
-                make_float4(v[0], v[1], v[2], v[3]);
-          } else {
-            // dW2 [S][d][fs]: column n is feature n % fs of expert n / fs
-            const size_t o = P == kDW2 ? ((size_t)(n / fs) * d + m) * fs + n % fs : (size_t)m * N + n;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.o0) + o) = pack4(v[0], v[1], v[2], v[3]);
-          }
+          if constexpr (P == kDHid) store_dhid(g, m, n, acc[i][f]);
+          else store_product<P>(g, m, n, N, acc[i][f]);
         }
       }
     }
   }
+}
+
+// The pieces of a split contraction added in order, and the product's epilogue:
+// one thread per row and four columns.
+template <int P>
+__global__ __launch_bounds__(256) void split_finish(DenseArgs g) {
+  const int F = g.S * g.fs, M = g.T;
+  const int N = P == kGateUp || P == kDHid ? F : g.d, cols = P == kGateUp ? 2 * F : N;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(i / (N / 4)), n = (int)(i - (int64_t)m * (N / 4)) * 4;
+  if (m >= M) return;
+  const float* p = g.part + (size_t)m * cols + (P == kGateUp ? gate_col(n, g.fs) : n);
+  f32x4_t a = {0.f, 0.f, 0.f, 0.f}, b = a;
+  for (int s = 0; s < g.splits; ++s, p += (size_t)M * cols) {
+    a += *reinterpret_cast<const f32x4_t*>(p);
+    if (P == kGateUp) b += *reinterpret_cast<const f32x4_t*>(p + g.fs);
+  }
+  if constexpr (P == kGateUp) store_gateup(g, m, n, a, b);
+  else if constexpr (P == kDHid) store_dhid(g, m, n, a);
+  else store_product<P>(g, m, n, N, a);
 }
 
 __global__ __launch_bounds__(256) void zero_fill(uint4* p, size_t n16) {
@@ -361,9 +453,81 @@ __global__ __launch_bounds__(256) void zero_fill(uint4* p, size_t n16) {
     p[i] = make_uint4(0, 0, 0, 0);
 }
 
+// How a product runs: its tile and, for the smallest, the pieces its contraction
+// is split into.
+enum { kTile256, kTile128, kTile64 };
+struct Plan {
+  int tile, splits, k_split;
+};
+
+// The tile whose rounds cost least, by what a 64-element stage was measured to
+// take (us; d 7168, two experts of 2048):
+//   256 x 256, one workgroup a CU:  1.2 (a part round) to 1.6;  from T = 2048 on
+//     the fastest (gate/up 353 us at T = 4096 against 440 and 725)
+//   128 x 256, one workgroup a CU:  0.8 to 1.0;  fewer tiles than CUs at T = 517
+//     (gate/up 94 us against 132 and 136)
+//   64 x 64, four workgroups a CU:  0.5 to 0.8;  small T (58 us against 129 and
+//     94 at T = 200), where its contraction is also split (the outputs are few,
+//     the weights have to come from every CU's loads at once)
+Plan plan_product(int P, const k3moe_shape& s) {
+  const int64_t F = (int64_t)s.n_shared * s.f_shared, T = s.T, d = s.d;
+  const int64_t M = P == kDW13 ? 2 * F : P == kDW2 ? d : T;
+  const int64_t N = P == kGateUp || P == kDHid || P == kDW2 ? F : d;
+  const int64_t K = P == kGateUp || P == kDHid ? d : P == kDown ? F : P == kDX ? 2 * F : T;
+  const int64_t nst = (K + kBK - 1) / kBK, w = P == kGateUp ? 2 : 1;
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N * w + bn - 1) / bn); };
+  auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
+  const int64_t t64 = tiles(64, 64);
+  const double c256 = rounds(tiles(256, 256), 256) * 1.5 * nst;
+  const double c128 = rounds(tiles(128, 256), 256) * 0.95 * nst;
+  double c64 = (t64 <= 256 ? 0.5 : rounds(t64, 1024) * 0.8) * nst;
+  Plan p{kTile64, 1, 0};
+  if (P != kDW13 && P != kDW2 && t64 <= 512) {
+    int64_t n = std::min<int64_t>(1024 / t64, nst / 4);
+    if (n > 1) {
+      const int64_t per = (nst + n - 1) / n;
+      n = (nst + per - 1) / per;
+      const double c = 0.8 * per + 5.0;   // the second kernel
+      if (c < c64) {
+        c64 = c;
+        p.splits = (int)n;
+        p.k_split = (int)(per * kBK);
+      }
+    }
+  }
+  if (c256 <= c128 && c256 <= c64) return Plan{kTile256, 1, 0};
+  if (c128 <= c64) return Plan{kTile128, 1, 0};
+  return p;
+}
+
+// Floats of the partial sums of a split product (0 when it is not split).
+size_t part_floats(int P, const k3moe_shape& s) {
+  const Plan p = plan_product(P, s);
+  const size_t F = (size_t)s.n_shared * s.f_shared;
+  const size_t cols = P == kGateUp ? 2 * F : P == kDHid ? F : (size_t)s.d;
+  return p.splits > 1 ? (size_t)p.splits * s.T * cols : 0;
+}
+
 template <int P>
-hipError_t launch_product(const DenseArgs& g, hipStream_t st) {
-  dense_tile<P, 128, 128, 2, 2><<<grouped_grid() * 2, 256, 0, st>>>(g);
+hipError_t launch_product(const k3moe_shape& s, DenseArgs g, float* part, hipStream_t st) {
+  const Plan p = plan_product(P, s);
+  const int cus = grouped_grid();
+  if (p.tile == kTile256) {
+    dense_tile<P, 256, 256, 2, 4><<<cus, 512, 0, st>>>(g);
+  } else if (p.tile == kTile128) {
+    dense_tile<P, 128, 256, 2, 4><<<cus, 512, 0, st>>>(g);
+  } else if (p.splits == 1) {
+    dense_tile<P, 64, 64, 2, 2><<<cus * 4, 256, 0, st>>>(g);
+  } else if constexpr (P != kDW13 && P != kDW2) {
+    g.part = part;
+    g.splits = p.splits;
+    g.k_split = p.k_split;
+    dense_tile<P, 64, 64, 2, 2, true><<<cus * 4, 256, 0, st>>>(g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t n = s.T * (P == kGateUp || P == kDHid ? (int64_t)g.S * g.fs : g.d) / 4;
+    split_finish<P><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
+  }
   return hipGetLastError();
 }
 
@@ -378,6 +542,11 @@ DenseArgs dense_args(const k3moe_shape& s) {
 
 }  // namespace
 
+size_t shared_train_part_floats(const k3moe_shape& s, bool backward) {
+  return backward ? std::max(part_floats(kDHid, s), part_floats(kDX, s))
+                  : std::max(part_floats(kGateUp, s), part_floats(kDown, s));
+}
+
 hipError_t launch_shared_train(const k3moe_shape& s, const k3moe_expert_bank& b, const void* x,
                                void* gu, void* y, const SharedTrainWs& ws, hipStream_t st) {
   DenseArgs g = dense_args(s);
@@ -385,14 +554,14 @@ hipError_t launch_shared_train(const k3moe_shape& s, const k3moe_expert_bank& b,
   g.b = static_cast<const uint16_t*>(b.w13);
   g.o0 = gu;
   g.o1 = ws.h;
-  hipError_t e = launch_product<kGateUp>(g, st);
+  hipError_t e = launch_product<kGateUp>(s, g, ws.part, st);
   if (e != hipSuccess) return e;
   g = dense_args(s);
   g.a = ws.h;
   g.b = static_cast<const uint16_t*>(b.w2);
   g.o0 = y;
   g.out_f32 = s.out_dtype == K3MOE_F32;
-  return launch_product<kDown>(g, st);
+  return launch_product<kDown>(s, g, ws.part, st);
 }
 
 hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank& b, const void* x,
@@ -406,14 +575,14 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   g.gu = static_cast<const uint16_t*>(gu);
   g.o0 = ws.dgu;
   g.o1 = ws.h;
-  hipError_t e = launch_product<kDHid>(g, st);
+  hipError_t e = launch_product<kDHid>(s, g, ws.part, st);
   if (e != hipSuccess) return e;
   if (dx) {
     g = z;
     g.a = ws.dgu;
     g.b = static_cast<const uint16_t*>(b.w13);
     g.o0 = dx;
-    e = launch_product<kDX>(g, st);
+    e = launch_product<kDX>(s, g, ws.part, st);
     if (e != hipSuccess) return e;
   }
   if (dw13) {
@@ -421,7 +590,7 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
     g.a = ws.dgu;
     g.b = static_cast<const uint16_t*>(x);
     g.o0 = dw13;
-    e = launch_product<kDW13>(g, st);
+    e = launch_product<kDW13>(s, g, ws.part, st);
     if (e != hipSuccess) return e;
   }
   if (dw2) {
@@ -429,7 +598,7 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
     g.a = static_cast<const uint16_t*>(dy);
     g.b = ws.h;
     g.o0 = dw2;
-    e = launch_product<kDW2>(g, st);
+    e = launch_product<kDW2>(s, g, ws.part, st);
   }
   return e;
 }

@@ -176,7 +176,9 @@ hipError_t launch_combine(const k3moe_shape& s, const float* y_perm, const int32
 struct SharedTrainWs {
   uint16_t* h;     // [T][n_shared][f_shared] bf16
   uint16_t* dgu;   // backward: [T][n_shared][2 f_shared] bf16; else nullptr
+  float* part;     // partial sums of products whose contraction is split (small T)
 };
+size_t shared_train_part_floats(const k3moe_shape& s, bool backward);
 SharedTrainWs carve_shared_train(const k3moe_shape& s, bool backward, void* ws, size_t* bytes);
 hipError_t launch_shared_train(const k3moe_shape& s, const k3moe_expert_bank& b, const void* x,
                                void* gu, void* y, const SharedTrainWs& ws, hipStream_t st);
