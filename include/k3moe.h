@@ -485,13 +485,14 @@ k3moe_status k3moe_shared_ffn_backward(const k3moe_shape* shape, const k3moe_exp
 /* ---------------------------------------------------------------------------
  * Products with 4-bit integer weights and group scales, for the few tokens of
  * a decoding step (any T is computed; the weights are read again for every 64
- * tokens, bf16, or 21, fp32).
+ * tokens, bf16, or 32, fp32).
  *   W[r][j] = (q[r][j] - z[r][j / group]) * scale[r][j / group]
  * codes [n][k / 2] u8: byte i of a row holds q of element 2i in its low
  * nibble, of 2i + 1 in its high nibble; scale [n][k / group] bf16; zero
  * [n][k / group] u8, NULL for 8 everywhere (symmetric codes).
- * 1 <= n <= 2^24; group 32, 64 or a multiple of 128; group <= k <= 2^20 and
- * k % group == 0 (ESHAPE); 0 <= T <= 2^18, T = 0 enqueues nothing.
+ * 1 <= n <= 2^20; group 32, 64 or a multiple of 128; group <= k <= 2^20 and
+ * k % group == 0, n * k <= 2^36 (ESHAPE); 0 <= T <= 2^18, T = 0 enqueues
+ * nothing.
  * x [T][k] and the output in F32 or BF16 each (EUNSUPPORTED otherwise).  The
  * sums are fp32 and follow IEEE rules for infinities and NaN in x and scale.
  * The pages' engines run 4-bit weights without a dense copy (kimi-k3-in-c
@@ -507,15 +508,20 @@ typedef struct k3moe_w4_matrix {
   const void* zero;
 } k3moe_w4_matrix;
 
+/* Workspace of the two calls below (0, where NULL is accepted, up to 16 tokens,
+ * and for invalid arguments); 256-byte aligned. */
+size_t k3moe_w4_workspace_bytes(const k3moe_w4_matrix* w, int64_t T);
 /* out [T][n] = x W^T.  Errors: EINVAL (NULL pointers, negative sizes), ESHAPE,
- * EUNSUPPORTED, EALIGN. */
+ * EUNSUPPORTED, EALIGN, EWORKSPACE. */
 k3moe_status k3moe_w4_linear(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
-                             int32_t out_dtype, const void* x, void* out, void* stream);
+                             int32_t out_dtype, const void* x, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream);
 /* The gated form: rows 0 .. n/2 - 1 of W are the gate, the others the up
  * projection (n even, ESHAPE): out [T][n / 2] = silu(x Wg^T) * (x Wu^T).
  * Errors: as for k3moe_w4_linear. */
 k3moe_status k3moe_w4_glu(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
-                          int32_t out_dtype, const void* x, void* out, void* stream);
+                          int32_t out_dtype, const void* x, void* out, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * The global norm of a training step's gradients, and clipping by it.  (The

@@ -11,6 +11,7 @@ memory and streams only.
 If libk3moe.so is not built this module raises on import: there is no other
 implementation to fall back to.
 """
+import contextlib
 import ctypes
 import os
 
@@ -39,7 +40,7 @@ EXPORTS = ["k3moe_workspace_bytes", "k3moe_mxfp4_bytes", "k3moe_path_class", "k3
            "k3moe_status_str", "k3moe_last_error", "k3moe_cache_create", "k3moe_cache_destroy",
            "k3moe_cache_workspace_bytes", "k3moe_cache_layer", "k3moe_cache_prefetch",
            "k3moe_cache_plan", "k3moe_cache_stats_get", "k3moe_shared_ffn_train",
-           "k3moe_shared_ffn_backward", "k3moe_w4_linear", "k3moe_w4_glu",
+           "k3moe_shared_ffn_backward", "k3moe_w4_workspace_bytes", "k3moe_w4_linear", "k3moe_w4_glu",
            "k3moe_grad_workspace_bytes", "k3moe_grad_norm", "k3moe_grad_clip"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -141,7 +142,9 @@ def _load():
     lib.k3moe_shared_ffn_backward.argtypes = [SP, BP, P, P, P, P, P, P, P, S, P]
     for f in (lib.k3moe_w4_linear, lib.k3moe_w4_glu):
         f.restype = ctypes.c_int
-        f.argtypes = [ctypes.POINTER(W4Matrix), I64, I32, I32, P, P, P]
+        f.argtypes = [ctypes.POINTER(W4Matrix), I64, I32, I32, P, P, P, S, P]
+    lib.k3moe_w4_workspace_bytes.restype = S
+    lib.k3moe_w4_workspace_bytes.argtypes = [ctypes.POINTER(W4Matrix), I64]
     lib.k3moe_grad_workspace_bytes.restype = S
     lib.k3moe_grad_workspace_bytes.argtypes = [I32]
     # (the list of tensors may come as any buffer of k3moe_tensor's layout)
@@ -175,6 +178,25 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def current_stream(device) -> int:
+    """torch's current stream of `device` (a torch.device with an index) as a raw handle."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def on_device(device, stream=None):
+    """A context in which `device` is the current one and, if given, `stream` (a
+    torch stream or a raw handle) its current stream, so that what a call
+    allocates belongs to the stream that uses it."""
+    import torch
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device)
+        return torch.cuda.stream(stream)
+    return (contextlib.nullcontext() if torch.cuda.current_device() == device.index
+            else torch.cuda.device(device))
 
 
 def _ws(ws):
@@ -278,13 +300,19 @@ def k3moe_shared_ffn_backward(shape, bank: ExpertBank, x, gu, dy, dx, dw13, dw2,
                                          _addr(dw2), wp, wb, _stream(stream)))
 
 
-def k3moe_w4_linear(w: W4Matrix, T, x_dtype, out_dtype, x, out, stream=None):
-    _check(lib.k3moe_w4_linear(ctypes.byref(w), T, x_dtype, out_dtype, _addr(x), _addr(out),
+def k3moe_w4_workspace_bytes(w: W4Matrix, T: int) -> int:
+    return lib.k3moe_w4_workspace_bytes(ctypes.byref(w), T)
+
+
+def k3moe_w4_linear(w: W4Matrix, T, x_dtype, out_dtype, x, out, workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_w4_linear(ctypes.byref(w), T, x_dtype, out_dtype, _addr(x), _addr(out), wp, wb,
                                _stream(stream)))
 
 
-def k3moe_w4_glu(w: W4Matrix, T, x_dtype, out_dtype, x, out, stream=None):
-    _check(lib.k3moe_w4_glu(ctypes.byref(w), T, x_dtype, out_dtype, _addr(x), _addr(out),
+def k3moe_w4_glu(w: W4Matrix, T, x_dtype, out_dtype, x, out, workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_w4_glu(ctypes.byref(w), T, x_dtype, out_dtype, _addr(x), _addr(out), wp, wb,
                             _stream(stream)))
 
 

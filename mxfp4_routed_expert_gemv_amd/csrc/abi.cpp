@@ -177,17 +177,20 @@ k3moe_status check_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int3
   if (out_dtype != K3MOE_F32 && out_dtype != K3MOE_BF16)
     return fail(K3MOE_EUNSUPPORTED, "out_dtype %d is not F32 or BF16", out_dtype);
   if (T > (1 << 18)) return fail(K3MOE_ESHAPE, "T = %lld: need <= 2^18", (long long)T);
-  if (w->n < 1 || w->n > (1 << 24)) return fail(K3MOE_ESHAPE, "n = %d: need 1 <= n <= 2^24", w->n);
+  if (w->n < 1 || w->n > (1 << 20)) return fail(K3MOE_ESHAPE, "n = %d: need 1 <= n <= 2^20", w->n);
   if (glu && w->n % 2) return fail(K3MOE_ESHAPE, "n = %d: the gated form needs an even n", w->n);
   if (w->group != 32 && w->group != 64 && (w->group < 128 || w->group % 128))
     return fail(K3MOE_ESHAPE, "group = %d: need 32, 64 or a multiple of 128", w->group);
   if (w->k < 1 || w->k > (1 << 20) || w->k % w->group)
     return fail(K3MOE_ESHAPE, "k = %d: need group <= k <= 2^20, k %% group == 0", w->k);
+  if ((int64_t)w->n * w->k > (int64_t(1) << 36))
+    return fail(K3MOE_ESHAPE, "n = %d, k = %d: need n * k <= 2^36", w->n, w->k);
   return K3MOE_OK;
 }
 
 k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_t out_dtype,
-                    const void* x, void* out, void* stream, bool glu);
+                    const void* x, void* out, void* workspace, size_t workspace_bytes, void* stream,
+                    bool glu);
 
 constexpr int kMaxTensors = 1 << 20;
 
@@ -318,7 +321,7 @@ GradWs carve_grads(int n, void* ws, size_t* bytes) {
   Carver c(ws);
   GradWs r;
   r.partial = c.take<double>(grad_partials(n));
-  r.scale = c.take<char>(256);
+  r.total = c.take<double>(1);
   if (bytes) *bytes = c.off;
   return r;
 }
@@ -377,7 +380,8 @@ k3moe_status layer_validate(const k3moe_shape* shape, const k3moe_layer_weights*
 
 namespace {
 k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_t out_dtype,
-                    const void* x, void* out, void* stream, bool glu) {
+                    const void* x, void* out, void* workspace, size_t workspace_bytes, void* stream,
+                    bool glu) {
   K3_CHECK(check_w4(w, T, x_dtype, out_dtype, glu));
   if (T == 0) return ok();
   K3_CHECK(need_ptr(w->codes, "codes"));
@@ -385,8 +389,9 @@ k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_
   K3_CHECK(opt_ptr(w->zero, "zero"));
   K3_CHECK(need_ptr(x, "x"));
   K3_CHECK(need_ptr(out, "out"));
+  K3_CHECK(check_ws(workspace, workspace_bytes, align256(w4_part_floats(*w, T) * sizeof(float))));
   return hip_status(launch_w4(*w, T, x_dtype == K3MOE_F32, out_dtype == K3MOE_F32, glu, x, out,
-                              static_cast<hipStream_t>(stream)),
+                              static_cast<float*>(workspace), static_cast<hipStream_t>(stream)),
                     glu ? "k3moe_w4_glu launch" : "k3moe_w4_linear launch");
 }
 k3moe_status run_grads(const k3moe_tensor* tensors, int32_t n, bool clip, float max_norm,
@@ -734,14 +739,21 @@ k3moe_status k3moe_shared_ffn_backward(const k3moe_shape* shape, const k3moe_exp
                     "k3moe_shared_ffn_backward launch");
 }
 
+size_t k3moe_w4_workspace_bytes(const k3moe_w4_matrix* w, int64_t T) {
+  if (check_w4(w, T, K3MOE_BF16, K3MOE_BF16, false) != K3MOE_OK) return 0;
+  return align256(w4_part_floats(*w, T) * sizeof(float));
+}
+
 k3moe_status k3moe_w4_linear(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
-                             int32_t out_dtype, const void* x, void* out, void* stream) {
-  return run_w4(w, T, x_dtype, out_dtype, x, out, stream, false);
+                             int32_t out_dtype, const void* x, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return run_w4(w, T, x_dtype, out_dtype, x, out, workspace, workspace_bytes, stream, false);
 }
 
 k3moe_status k3moe_w4_glu(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
-                          int32_t out_dtype, const void* x, void* out, void* stream) {
-  return run_w4(w, T, x_dtype, out_dtype, x, out, stream, true);
+                             int32_t out_dtype, const void* x, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return run_w4(w, T, x_dtype, out_dtype, x, out, workspace, workspace_bytes, stream, true);
 }
 
 size_t k3moe_grad_workspace_bytes(int32_t n) {

@@ -11,10 +11,11 @@
 namespace k3 {
 namespace {
 
-constexpr int kPerLaunch = 96;      // tensors in one launch's arguments
+constexpr int kPerLaunch = 120;     // tensors in one launch's arguments (below 4 KB)
 constexpr int kUnit = 16384;        // elements per work item
 constexpr int kMaxGrid = 2048;      // workgroups of a launch: partial sums per launch
 constexpr int kVec = 8;             // elements per load
+constexpr int64_t kMaxUnits = int64_t(1) << 30;   // work items of a launch
 
 struct Entry {
   const void* in;
@@ -27,11 +28,7 @@ struct Table {
   Entry e[kPerLaunch];
   int count, units;
 };
-struct Scale {
-  double norm;
-  float factor;
-  int scaled;   // factor < 1
-};
+static_assert(sizeof(Table) <= 4000, "kernel arguments");
 
 // Gradients may start at any element: loads and stores of 8 elements are only
 // element-aligned.
@@ -93,31 +90,42 @@ __global__ __launch_bounds__(256) void sum_squares(Table t, double* __restrict__
   if (threadIdx.x == 0) partial[blockIdx.x] = (s_wave[0] + s_wave[1]) + (s_wave[2] + s_wave[3]);
 }
 
-__global__ __launch_bounds__(256) void finish_norm(const double* __restrict__ partial, int n,
-                                                   float max_norm, float* norm, Scale* scale) {
+// The norm from n partial sums, in one order whatever workgroup does it.
+__device__ __forceinline__ double norm_of(const double* __restrict__ partial, int n) {
   __shared__ double s_wave[4];
   double sum = 0.0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < n; i += 256) sum += partial[i];
   sum = wave_sum(sum);
+  __syncthreads();
   if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6] = sum;
   __syncthreads();
+  return sqrt((s_wave[0] + s_wave[1]) + (s_wave[2] + s_wave[3]));
+}
+
+// *norm, and the fp64 norm for scale_all.
+__global__ __launch_bounds__(256) void finish_norm(const double* __restrict__ partial, int n,
+                                                   float* norm, double* total) {
+  const double v = norm_of(partial, n);
   if (threadIdx.x == 0) {
-    const double v = sqrt((s_wave[0] + s_wave[1]) + (s_wave[2] + s_wave[3]));
     *norm = (float)v;
-    if (scale) {
-      // (a norm that is not finite leaves the gradients as they are)
-      const bool clip = v < (double)INFINITY && v > (double)max_norm;
-      scale->norm = v;
-      scale->factor = clip ? (float)((double)max_norm / v) : 1.0f;
-      scale->scaled = clip;
-    }
+    if (total) *total = v;
   }
 }
 
-__global__ __launch_bounds__(256) void scale_all(Table t, const Scale* __restrict__ scale) {
-  const float f = scale->factor;
-  const bool scaled = scale->scaled;
-  for (int u = blockIdx.x; u < t.units; u += gridDim.x) {
+// Scales the tensors; n > 0: every workgroup takes the norm from the n partial
+// sums itself (the first one writes it), which a launch of its own would take
+// longer for; n = 0: the norm is at partial[0].  The last items come first: the
+// norm's pass read them last, so a part of them is still in the last-level cache.
+__global__ __launch_bounds__(256) void scale_all(Table t, const double* __restrict__ partial, int n,
+                                                 float max_norm, float* norm) {
+  const double v = n > 0 ? norm_of(partial, n) : partial[0];
+  if (n > 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
+  // (a norm of infinities or NaN leaves the gradients as they are)
+  const bool scaled = v < (double)INFINITY && v > (double)max_norm;
+  const float f = scaled ? (float)((double)max_norm / v) : 1.0f;
+  for (int w = blockIdx.x; w < t.units; w += gridDim.x) {
+    const int u = t.units - 1 - w;
     const Entry& e = t.e[tensor_of(t, u)];
     if (!scaled && e.in == e.out) continue;   // in place and not clipped: nothing to do
     const int64_t a = (int64_t)(u - e.unit0) * kUnit, b = a + kUnit < e.n ? a + kUnit : e.n;
@@ -165,7 +173,7 @@ void fill_table(const k3moe_tensor* ts, int n, int i, Batch& b) {
     const k3moe_tensor& s = ts[i];
     if (s.numel == 0) continue;
     const int64_t u = (s.numel + kUnit - 1) / kUnit;
-    if (units + u > INT32_MAX) break;
+    if (units + u > kMaxUnits) break;
     Entry& e = b.t.e[b.t.count++];
     e.in = s.data;
     e.out = s.out;
@@ -182,7 +190,7 @@ void fill_table(const k3moe_tensor* ts, int n, int i, Batch& b) {
 }  // namespace
 
 // One launch takes kPerLaunch non-empty tensors, or fewer where their work
-// items would pass 2^31 (tensors are at most 2^40 elements: 2^26 items).
+// items would pass 2^30 (tensors are at most 2^40 elements: 2^26 items each).
 size_t grad_partials(int n) { return ((size_t)n / 16 + 2) * kMaxGrid; }
 
 hipError_t launch_grads(const k3moe_tensor* ts, int n, bool clip, float max_norm, float* norm,
@@ -198,16 +206,18 @@ hipError_t launch_grads(const k3moe_tensor* ts, int n, bool clip, float max_norm
     if (e != hipSuccess) return e;
     slots += grid;
   }
-  finish_norm<<<1, 256, 0, st>>>(ws.partial, slots, max_norm, norm,
-                                 clip ? static_cast<Scale*>(ws.scale) : nullptr);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !clip) return e;
+  const bool fused = clip && slots > 0 && slots <= kMaxGrid;
+  if (!fused) {
+    finish_norm<<<1, 256, 0, st>>>(ws.partial, slots, norm, ws.total);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !clip) return e;
+  }
   for (int i = 0; i < n; i = b.next) {
     fill_table(ts, n, i, b);
     if (b.t.units == 0) continue;
     scale_all<<<b.t.units < kMaxGrid ? b.t.units : kMaxGrid, 256, 0, st>>>(
-        b.t, static_cast<const Scale*>(ws.scale));
-    e = hipGetLastError();
+        b.t, fused ? ws.partial : ws.total, fused ? slots : 0, max_norm, norm);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -189,11 +189,12 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t st);
 // Products with 4-bit weights and group scales (w4.hip), on checked arguments.
 hipError_t launch_w4(const k3moe_w4_matrix& w, int64_t T, bool x_f32, bool out_f32, bool glu,
-                     const void* x, void* out, hipStream_t st);
+                     const void* x, void* out, float* part, hipStream_t st);
+size_t w4_part_floats(const k3moe_w4_matrix& w, int64_t T);
 // The gradients' norm and clipping (grads.hip).
 struct GradWs {
   double* partial;   // partial sums of squares, grad_partials(n)
-  void* scale;       // the norm and the factor, 256 bytes
+  double* total;     // the norm
 };
 size_t grad_partials(int n);
 GradWs carve_grads(int n, void* ws, size_t* bytes);

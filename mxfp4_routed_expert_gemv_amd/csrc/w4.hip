@@ -14,19 +14,24 @@
 // a wave whose sums are not finite repeats its slice with the weights (q - z) s
 // themselves, as two exact bf16 parts, which follows the definition.
 //
-// fp32 activations are three exact bf16 parts (the top 8 significant bits, the
-// next 8, the rest), each an activation row of its own, summed at the end.
+// fp32 activations enter as three exact bf16 parts (the top 8 significant bits,
+// the next 8, the rest), one instruction each into the same sums.
+#include <algorithm>
+
 #include "internal.h"
 #include "kern_common.h"
+#include "grouped.h"
 
 namespace k3 {
 namespace {
+
+using grouped::wait_lds;
+using grouped::wait_vmem;
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
 
-constexpr int kWaves = 8;   // waves per workgroup, splitting the contraction
 constexpr int kBlk = 128;   // contraction elements per 16-byte load of a lane
 
 struct W4Args {
@@ -35,8 +40,12 @@ struct W4Args {
   const uint8_t* zero;     // [n][k / group], or nullptr: 8
   const void* x;           // [T][k]
   void* out;
-  int T, n, k, group, f;   // f: gated form, rows of the gate half; else n
+  int T, n, k, f;          // f: gated form, rows of the gate half; else n
+  int groups;              // scales of a row
+  uint32_t per_group;      // blocks / (group / 128) = umulhi(blocks, per_group); 0: group 128
   int out_f32;
+  float* part;             // more than 16 tokens: partial sums [splits][T][n]
+  int splits, per_split;   // pieces of the contraction, blocks of a piece
 };
 
 // 4x4 transpose of dwords across the wave's four rows of 16 lanes: dword j of
@@ -49,16 +58,18 @@ __device__ __forceinline__ void transpose4(uint32_t (&v)[4]) {
   t = __builtin_amdgcn_permlane16_swap(v[2], v[3], false, false); v[2] = t.x; v[3] = t.y;
 }
 
-// The 8 codes of a dword as 16 + q, in the order 0 4 1 5 2 6 3 7.
+// The 8 codes of a dword as 16 + q, in order: of byte b, the low nibble sits at
+// bits 3 .. 6 of w << 3's byte b, the high one there in w >> 1's.
 __device__ __forceinline__ bf16x8_t codes_biased(uint32_t w) {
-  uint4 r;
-  r.x = ((w << 3) & 0x00780078u) | 0x41804180u;
-  r.y = ((w >> 1) & 0x00780078u) | 0x41804180u;
-  r.z = ((w >> 5) & 0x00780078u) | 0x41804180u;
-  r.w = ((w >> 9) & 0x00780078u) | 0x41804180u;
+  const uint32_t lo = w << 3, hi = w >> 1;
+  uint4 r;   // (0x0C selects a zero byte; the second operand's bytes are 0 .. 3)
+  r.x = (__builtin_amdgcn_perm(hi, lo, 0x0C040C00u) & 0x00780078u) | 0x41804180u;
+  r.y = (__builtin_amdgcn_perm(hi, lo, 0x0C050C01u) & 0x00780078u) | 0x41804180u;
+  r.z = (__builtin_amdgcn_perm(hi, lo, 0x0C060C02u) & 0x00780078u) | 0x41804180u;
+  r.w = (__builtin_amdgcn_perm(hi, lo, 0x0C070C03u) & 0x00780078u) | 0x41804180u;
   return __builtin_bit_cast(bf16x8_t, r);
 }
-// The weights (q - z) s themselves in the same order, as two bf16 parts of one
+// The weights (q - z) s themselves, as two bf16 parts of one
 // sign whose sum is exact: q - z has at most 8 significant bits, a bf16 scale 8,
 // so the product 16.  Neither part is zero unless the weight is (a weight of 8
 // bits is halved), and an infinite or NaN weight is both: a part times an
@@ -67,8 +78,7 @@ __device__ __forceinline__ void codes_exact(uint32_t w, int z, float s, bf16x8_t
   uint32_t h[8], l[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int shift = 4 * (i >> 1) + 16 * (i & 1);
-    const float v = (float)((int)((w >> shift) & 15u) - z) * s;
+    const float v = (float)((int)((w >> (4 * i)) & 15u) - z) * s;
     const float top = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
     const bool whole = !(fabsf(v - top) > 0.0f);   // 8 bits, or not finite
     const float a = whole ? 0.5f * v : top;
@@ -81,207 +91,615 @@ __device__ __forceinline__ void codes_exact(uint32_t w, int z, float s, bf16x8_t
                                                l[4] | l[5] << 16, l[6] | l[7] << 16));
 }
 
-// Part p (0, 1, 2) of an fp32 value as bf16 bits: the value is the sum of its
-// three parts (an infinity or NaN is its first part's).
-__device__ __forceinline__ uint32_t part_of(float v, int p) {
-  const uint32_t u = __float_as_uint(v);
-  const bool special = (u & 0x7F800000u) == 0x7F800000u;
-  // a NaN whose payload lies in the low bits alone would truncate to infinity
-  const uint32_t hi = special && (u & 0x007FFFFFu) ? u | 0x00400000u : u;
-  if (p == 0) return hi >> 16;
-  if (special) return 0;
-  const float r1 = v - __uint_as_float(u & 0xFFFF0000u);
-  const uint32_t u1 = __float_as_uint(r1);
-  if (p == 1) return u1 >> 16;
-  return __float_as_uint(r1 - __uint_as_float(u1 & 0xFFFF0000u)) >> 16;
+// Eight activations as fragments whose sum is exact: bf16 as they are; fp32 as the top 8 significant bits, the next 8 and the rest.
+// SPECIAL: an infinity or NaN is every part, and no part is zero unless the
+// value is, so that a part times an infinite weight is what the value times it
+// is (otherwise an infinity or NaN is the first part's alone or all of them).
+template <bool F32X, bool SPECIAL>
+__device__ __forceinline__ void x_frags(const uint4* x, bf16x8_t (&out)[F32X ? 3 : 1]) {
+  if constexpr (F32X) {
+    const uint4 a = x[0], b = x[1];
+    const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t p[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = __uint_as_float(in[i]);
+      const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), r1 = v - hi;
+      const float mid = __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u), lo = r1 - mid;
+      float q[3] = {hi, mid, lo};
+      if (SPECIAL) {
+        if (!(fabsf(v) < INFINITY)) {
+          q[0] = q[1] = q[2] = v != v ? __uint_as_float(0x7FC00000u) : v;
+        } else if (r1 == 0.0f) {
+          q[0] = 0.5f * v; q[1] = q[2] = 0.25f * v;
+        } else if (lo == 0.0f) {
+          q[1] = q[2] = 0.5f * r1;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) p[k][i] = __float_as_uint(q[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      out[k] = __builtin_bit_cast(
+          bf16x8_t, make_uint4(__builtin_amdgcn_perm(p[k][1], p[k][0], 0x07060302u),
+                               __builtin_amdgcn_perm(p[k][3], p[k][2], 0x07060302u),
+                               __builtin_amdgcn_perm(p[k][5], p[k][4], 0x07060302u),
+                               __builtin_amdgcn_perm(p[k][7], p[k][6], 0x07060302u)));
+  } else {
+    out[0] = __builtin_bit_cast(bf16x8_t, x[0]);
+  }
 }
 
-// Activation row r of the workgroup (bf16: token r; fp32: part r % 3 of token
-// r / 3), elements k .. k + 8, in the codes' order; zeros for rows past the
-// last token and elements past the contraction.
-template <bool F32X>
-__device__ __forceinline__ bf16x8_t x_frag(const W4Args& g, int t0, int r, int k) {
-  const int t = t0 + (F32X ? r / 3 : r);
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (t < g.T && k < g.k) {
-    if (F32X) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(g.x) + (size_t)t * g.k + k);
-      const float4 a = p[0], b = p[1];
-      const int q = r % 3;
-      v.x = part_of(a.x, q) | (part_of(b.x, q) << 16);
-      v.y = part_of(a.y, q) | (part_of(b.y, q) << 16);
-      v.z = part_of(a.z, q) | (part_of(b.z, q) << 16);
-      v.w = part_of(a.w, q) | (part_of(b.w, q) << 16);
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.x) + (size_t)t * g.k + k);
-      v.x = (w.x & 0xFFFFu) | (w.z << 16);
-      v.y = (w.x >> 16) | (w.z & 0xFFFF0000u);
-      v.z = (w.y & 0xFFFFu) | (w.w << 16);
-      v.w = (w.y >> 16) | (w.w & 0xFFFF0000u);
+// The weights' side of one 128-element block, as loaded.
+template <int NF, int SG>
+struct Codes {
+  uint4 c[NF];               // 32 codes per lane: elements 32 lg .. + 32 of row ln
+  uint16_t s[4 / SG][NF];    // a scale for every SG steps of 32 elements
+  uint8_t z[4 / SG][NF];
+};
+
+// A lane's rows: fragment f's weight row, and its token.
+template <int NF>
+struct Rows {
+  int row[NF], tok, lg;
+};
+
+// The scale of step group s (of SG steps) of block blk in a row's list.
+template <int SG>
+__device__ __forceinline__ int group_of(const W4Args& g, int blk, int s) {
+  return SG < 4 ? min(blk * (4 / SG) + s, g.groups - 1)
+                : (g.per_group ? (int)__umulhi((uint32_t)blk, g.per_group) : blk);
+}
+
+// (lanes past the contraction read its last 32 elements, which no step uses)
+template <int NF, int SG>
+__device__ __forceinline__ void load_codes(const W4Args& g, int blk, const Rows<NF>& r,
+                                           Codes<NF, SG>& b) {
+  const int kc = min(blk * kBlk + 32 * r.lg, g.k - 32);
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    b.c[f] = ldg16(g.codes + (size_t)r.row[f] * (g.k >> 1) + (kc >> 1));
+#pragma unroll
+    for (int s = 0; s < 4 / SG; ++s) {
+      const size_t o = (size_t)r.row[f] * g.groups + group_of<SG>(g, blk, s);
+      b.s[s][f] = g.scale[o];
+      b.z[s][f] = g.zero ? g.zero[o] : 8;
     }
   }
-  return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// One wave's slice of the contraction (blocks wv, wv + kWaves, ...) for MB x 16
-// activation rows and NF x 16 weight rows.  SG: 32-element steps per scale.
-template <int MB, int NF, int SG, bool F32X, bool EXACT>
-__device__ __forceinline__ void w4_slice(const W4Args& g, int t0, int wv, int ln, int lg,
-                                         const int (&row)[NF], f32x4_t (&acc)[MB][NF]) {
-  const f32x4_t nil = {0.f, 0.f, 0.f, 0.f};
-  const int groups = g.k / g.group;
+// The activations of one block: step j of lane (ln, lg) is row ln, elements
+// 32 j + 8 lg .. + 8.
+template <bool F32X>
+struct Acts {
+  uint4 v[4][F32X ? 2 : 1];
+};
+template <bool F32X, int NF>
+__device__ __forceinline__ void load_acts(const W4Args& g, int blk, const Rows<NF>& r, Acts<F32X>& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const size_t o = (size_t)r.tok * g.k + min(blk * kBlk + 32 * j, g.k - 32) + 8 * r.lg;
+    const uint8_t* p = static_cast<const uint8_t*>(g.x) + o * (F32X ? 4 : 2);
+    b.v[j][0] = ldg16(p);
+    if constexpr (F32X) b.v[j][1] = ldg16(p + 16);
+  }
+}
+
+// A wave's blocks (blk0, blk0 + step, ... below blk1) with the weights
+// themselves: for sums that are not finite.
+template <int NF, int SG, bool F32X>
+__device__ __noinline__ void w4_slice_exact(const W4Args g, int blk0, int blk1, int step,
+                                            const Rows<NF> rows, f32x4_t (&acc)[NF]) {
+  constexpr int XP = F32X ? 3 : 1;
+#pragma unroll
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int blk = blk0; blk < blk1; blk += step) {
+    Codes<NF, SG> c;
+    load_codes<NF, SG>(g, blk, rows, c);
+    uint32_t t[NF][4];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      t[f][0] = c.c[f].x; t[f][1] = c.c[f].y; t[f][2] = c.c[f].z; t[f][3] = c.c[f].w;
+      transpose4(t[f]);
+    }
+    Acts<F32X> x;
+    load_acts<F32X, NF>(g, blk, rows, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (blk * kBlk + 32 * j >= g.k) break;
+      bf16x8_t a[XP];
+      x_frags<F32X, true>(x.v[j], a);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        bf16x8_t hi, lo;
+        codes_exact(t[f][j], c.z[j / SG][f], bf16_lo(c.s[j / SG][f]), hi, lo);
+#pragma unroll
+        for (int p = 0; p < XP; ++p) {
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], lo, acc[f], 0, 0, 0);
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], hi, acc[f], 0, 0, 0);
+        }
+      }
+    }
+  }
+}
+
+// ---- the kernel.  A workgroup's W waves split the contraction in blocks of 128
+// (wave w takes blocks w, w + W, ...); a wave copies its blocks into a ring of D
+// slots of its own by LDS-DMA, so that D blocks of every wave are in flight
+// whatever the registers hold, and no wave waits for another before the sum at
+// the end.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// LDS-DMA copies from base + off: lane i's 16 bytes (two bytes, one byte, as a
+// dword) land at lds + 16 i (4 i).
+__device__ __forceinline__ void dma_b128(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_u16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ushort %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_u8(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Slot of a block, for RC tokens and 16 NF weight rows:
+//   codes  [16 NF rows][4 units of 16 bytes], unit u of row r at u ^ code_swz(r)
+//   x      [RC rows][16 (fp32: 32) units], unit u of row r at u ^ (r mod 16)
+//   scale  [4 / SG][16 NF] dwords, then zero the same
+// The permutations spread the 16 rows of a fragment read over the LDS banks.
+template <int RC, int NF, int SG, bool F32X>
+struct Slot {
+  static constexpr int kRow = F32X ? 512 : 256;             // bytes of x per token
+  static constexpr int kX = NF * 1024, kS = kX + RC * kRow;
+  static constexpr int kVals = 4 / SG * 16 * NF;            // scales
+  static constexpr int NS = (kVals + 63) / 64;              // copies of them
+  static constexpr int kZ = kS + NS * 256, kBytes = kZ + NS * 256;
+  static constexpr int NX = RC * kRow / 1024;               // copies of x
+  static constexpr int kCopies = NF + NX + 2 * NS;
+};
+__device__ __forceinline__ int code_swz(int r) { return ((r >> 1) & 2) ^ ((r >> 3) & 1) * 3; }
+
+// Workgroup (blockIdx.x, blockIdx.y): 16 NF weight rows (gated form: 8 NF gate
+// rows and the matching up rows) x RC tokens.
+template <int W, int D, int RC, int NF, int SG, bool F32X, bool GLU>
+__global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
+  using L = Slot<RC, NF, SG, F32X>;
+  constexpr int NB = GLU ? 8 * NF : 16 * NF;   // outputs per token
+  constexpr int XP = F32X ? 3 : 1;
+  static_assert(!GLU || NF % 2 == 0, "gate and up fragments come in pairs");
+  static_assert(RC * (16 * NF + 1) * 4 <= D * L::kBytes, "a wave's sums fit its ring");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[W][D * L::kBytes];
+  const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n_out = GLU ? g.f : g.n;
+  const int t0 = blockIdx.y * RC, n0 = blockIdx.x * NB, tn = min(RC, g.T - t0);
+  if (n0 >= n_out) return;
+  // row of the workgroup's row i (rows past the last are read as it, and not stored)
+  auto weight_row = [&](int i) {
+    const int f = i >> 4, first = n0 + (GLU ? f % (NF / 2) : f) * 16;
+    return min(first + (i & 15), n_out - 1) + (GLU && f >= NF / 2 ? g.f : 0);
+  };
+
+  // ---- copies: offsets from the wave's first block, in the arrays' rows
+  const int kb = g.k >> 1;   // bytes of a row of codes
+  uint32_t oc[NF], ox[L::NX], os[L::NS];
+  int kc[NF], kx[L::NX], vs[L::NS];
+  const int row_lo = weight_row(0);
+  const size_t up_rows = GLU ? (size_t)g.f : 0;   // fragments of the up half start there
+#pragma unroll
+  for (int c = 0; c < NF; ++c) {
+    const int r = lane >> 2;
+    kc[c] = ((lane & 3) ^ code_swz(r)) * 32;
+    oc[c] = (uint32_t)(weight_row(c * 16 + r) - row_lo - (GLU && c >= NF / 2 ? g.f : 0)) * (uint32_t)kb;
+  }
+#pragma unroll
+  for (int c = 0; c < L::NX; ++c) {
+    constexpr int U = L::kRow / 16;   // units per token
+    const int i = c * 64 + lane, r = i / U, u = (i % U) ^ (r & 15);
+    kx[c] = u * (F32X ? 4 : 8);
+    ox[c] = (uint32_t)min(r, tn - 1) * (uint32_t)g.k;
+  }
+#pragma unroll
+  for (int c = 0; c < L::NS; ++c) {
+    const int i = min(c * 64 + lane, L::kVals - 1);
+    vs[c] = i / (16 * NF);
+    const int f = i % (16 * NF) >> 4;
+    os[c] = (uint32_t)(weight_row(i % (16 * NF)) - row_lo - (GLU && f >= NF / 2 ? g.f : 0)) *
+            (uint32_t)g.groups;
+    if (GLU && f >= NF / 2) os[c] += (uint32_t)(up_rows * g.groups);
+  }
+  const uint32_t my = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring[wv];
+  const int nblk = (g.k + kBlk - 1) / kBlk;
+  const uint8_t* const zeros = g.zero ? g.zero : reinterpret_cast<const uint8_t*>(g.scale);
+  auto issue = [&](int b, int slot) {
+    if (b >= nblk) return;
+    const int k0 = b * kBlk;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(my + slot * L::kBytes);
+    const int left = g.k - 32 - k0;   // codes past the row's end: its last 32, not used
+#pragma unroll
+    for (int c = 0; c < NF; ++c)
+      dma_b128(g.codes + ((size_t)row_lo + (GLU && c >= NF / 2 ? up_rows : 0)) * kb + (k0 >> 1),
+               oc[c] + (uint32_t)(min(kc[c], left) >> 1), to + c * 1024);
+    const uint8_t* x = static_cast<const uint8_t*>(g.x) + ((size_t)t0 * g.k + k0) * (F32X ? 4 : 2);
+#pragma unroll
+    for (int c = 0; c < L::NX; ++c)
+      dma_b128(x, (ox[c] + (uint32_t)min(kx[c], g.k - (F32X ? 4 : 8) - k0)) * (F32X ? 4 : 2),
+               to + L::kX + c * 1024);
+#pragma unroll
+    for (int c = 0; c < L::NS; ++c) {
+      uint32_t o = os[c] + (uint32_t)(SG < 4 ? min(b * (4 / SG) + vs[c], g.groups - 1)
+                                             : group_of<SG>(g, b, 0));
+      dma_u16(g.scale + (size_t)row_lo * g.groups, o * 2, to + L::kS + c * 256);
+      dma_u8(zeros + (size_t)row_lo * g.groups, o, to + L::kZ + c * 256);
+    }
+  };
+
+  f32x4_t acc[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   bf16x8_t ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 #pragma unroll
-  for (int m = 0; m < MB; ++m)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) acc[m][f] = nil;
-  const int nblk = (g.k + kBlk - 1) / kBlk;
+  for (int q = 0; q < D; ++q) issue(wv + q * W, q);
+  int slot = 0;
 #pragma unroll 1
-  for (int blk = wv; blk < nblk; blk += kWaves) {
-    const int k0 = blk * kBlk;
+  for (int blk = wv; blk < nblk; blk += W) {
+    // (towards the end fewer are in flight: wait for all)
+    if (blk + (D - 1) * W < nblk) wait_vmem<(D - 1) * L::kCopies>();
+    else wait_vmem<0>();
+    const uint8_t* at = ring[wv] + slot * L::kBytes;
     uint32_t c[NF][4];
+    uint4 x[4][F32X ? 2 : 1];
+    float sc[4 / SG][NF], off[4 / SG][NF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      // (the last block may end inside: those lanes read the row's last 16
-      // bytes, against activations of zero)
-      const int kk = min(k0 + 32 * lg, g.k - 32);
-      const uint4 v = ldg16(g.codes + (size_t)row[f] * (g.k >> 1) + (kk >> 1));
+      const uint4 v = *reinterpret_cast<const uint4*>(at + f * 1024 + ln * 64 + ((lg ^ code_swz(ln)) << 4));
       c[f][0] = v.x; c[f][1] = v.y; c[f][2] = v.z; c[f][3] = v.w;
-      transpose4(c[f]);
+#pragma unroll
+      for (int s = 0; s < 4 / SG; ++s) {
+        const int i = ((s * NF + f) * 16 + ln) * 4;
+        sc[s][f] = bf16_lo(*reinterpret_cast<const uint32_t*>(at + L::kS + i));
+        const int z = g.zero ? *reinterpret_cast<const int*>(at + L::kZ + i) : 8;
+        off[s][f] = -(float)(16 + z);
+      }
     }
+    const int xr = ln & (RC - 1);   // (rows past RC repeat one of them)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < (F32X ? 2 : 1); ++h) {
+        const int u = F32X ? 8 * j + 2 * lg + h : 4 * j + lg;
+        x[j][h] = *reinterpret_cast<const uint4*>(at + L::kX + xr * L::kRow + ((u ^ xr) << 4));
+      }
+    // the slot is in registers: its next block may come
+    wait_lds();
+    issue(blk + D * W, slot);
+    slot = slot == D - 1 ? 0 : slot + 1;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) transpose4(c[f]);
 #pragma unroll
     for (int s = 0; s < 4 / SG; ++s) {
-      const int gi = min((k0 + s * SG * 32) / g.group, groups - 1);
-      float sc[NF];
-      int z[NF];
+      if (blk * kBlk + s * SG * 32 >= g.k) break;
+      f32x4_t sum = {0.f, 0.f, 0.f, 0.f}, dot[NF];
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const size_t o = (size_t)row[f] * groups + gi;
-        sc[f] = __uint_as_float((uint32_t)g.scale[o] << 16);
-        z[f] = g.zero ? g.zero[o] : 8;
-      }
-      f32x4_t dot[MB][NF], sum[MB];
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        sum[m] = nil;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) dot[m][f] = nil;
-      }
+      for (int f = 0; f < NF; ++f) dot[f] = sum;
 #pragma unroll
       for (int j = s * SG; j < (s + 1) * SG; ++j) {
-        bf16x8_t b[NF], b_lo[NF];
+        bf16x8_t a[XP];
+        x_frags<F32X, false>(x[j], a);
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          if (EXACT) codes_exact(c[f][j], z[f], sc[f], b[f], b_lo[f]);
-          else b[f] = codes_biased(c[f][j]);
-        }
+        for (int p = 0; p < XP; ++p) {
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], ones, sum, 0, 0, 0);
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          const bf16x8_t a = x_frag<F32X>(g, t0, m * 16 + ln, k0 + 32 * j + 8 * lg);
-          if (!EXACT) sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, sum[m], 0, 0, 0);
-#pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            if (EXACT) dot[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b_lo[f], dot[m][f], 0, 0, 0);
-            dot[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[f], dot[m][f], 0, 0, 0);
-          }
+          for (int f = 0; f < NF; ++f)
+            dot[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], codes_biased(c[f][j]), dot[f], 0, 0, 0);
         }
       }
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const float off = -(float)(16 + z[f]);
+      for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[m][f][r] = EXACT ? acc[m][f][r] + dot[m][f][r]
-                                 : __builtin_fmaf(sc[f], __builtin_fmaf(off, sum[m][r], dot[m][f][r]),
-                                                  acc[m][f][r]);
-      }
+        for (int r = 0; r < 4; ++r)
+          acc[f][r] = __builtin_fmaf(sc[s][f], __builtin_fmaf(off[s][f], sum[r], dot[f][r]), acc[f][r]);
     }
   }
-}
-
-// Workgroup (blockIdx.x, blockIdx.y): 16 NF weight rows (gated form: 8 NF gate
-// rows and the matching up rows) x the tokens of 16 MB activation rows.
-template <int MB, int NF, int SG, bool F32X, bool GLU>
-__global__ __launch_bounds__(64 * kWaves) void w4_kernel(W4Args g) {
-  constexpr int TOK = F32X ? 16 * MB / 3 : 16 * MB;   // tokens per workgroup
-  constexpr int NB = GLU ? 8 * NF : 16 * NF;          // outputs per token
-  static_assert(!GLU || NF % 2 == 0, "gate and up fragments come in pairs");
-  __shared__ float red[kWaves][16 * MB][16 * NF + 1];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
-  const int t0 = blockIdx.y * TOK, n0 = blockIdx.x * NB;
-  int row[NF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)   // (rows past the last are read as it, and not stored)
-    row[f] = GLU ? min(n0 + (f % (NF / 2)) * 16 + ln, g.f - 1) + (f >= NF / 2 ? g.f : 0)
-                 : min(n0 + f * 16 + ln, g.n - 1);
-  f32x4_t acc[MB][NF];
-  w4_slice<MB, NF, SG, F32X, false>(g, t0, wv, ln, lg, row, acc);
   bool bad = false;
 #pragma unroll
-  for (int m = 0; m < MB; ++m)
+  for (int f = 0; f < NF; ++f)
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
+    for (int r = 0; r < 4; ++r) bad |= lg * 4 + r < tn && !(fabsf(acc[f][r]) < INFINITY);
+  if (__any(bad)) {
+    Rows<NF> rows;
+    rows.lg = lg;
+    rows.tok = t0 + min(ln, tn - 1);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) bad |= !(fabsf(acc[m][f][r]) < INFINITY);
-  if (__any(bad)) w4_slice<MB, NF, SG, F32X, true>(g, t0, wv, ln, lg, row, acc);
+    for (int f = 0; f < NF; ++f) rows.row[f] = weight_row(f * 16 + ln);
+    f32x4_t again[NF];   // (acc's own address would keep it out of registers)
+    w4_slice_exact<NF, SG, F32X>(g, wv, nblk, W, rows, again);
 #pragma unroll
-  for (int m = 0; m < MB; ++m)
+    for (int f = 0; f < NF; ++f) acc[f] = again[f];
+  }
+  // ---- the waves' sums, each in its own ring (nothing is in flight to it any more)
+  float* red = reinterpret_cast<float*>(ring[wv]);
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
+  for (int f = 0; f < NF; ++f)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) red[wv][m * 16 + lg * 4 + r][f * 16 + ln] = acc[m][f][r];
+    for (int r = 0; r < 4; ++r)
+      if (lg * 4 + r < tn) red[(lg * 4 + r) * (16 * NF + 1) + f * 16 + ln] = acc[f][r];
   __syncthreads();
-  // sum over the waves in order (and over an fp32 value's parts, largest first)
-  const int tn = min(TOK, g.T - t0);
-  for (int i = threadIdx.x; i < tn * NB; i += 64 * kWaves) {
-    const int t = i / NB, c = i - t * NB;
-    if (n0 + c >= (GLU ? g.f : g.n)) continue;
+  for (int i = threadIdx.x; i < tn * NB; i += 64 * W) {
+    const int t = i / NB, col = i - t * NB;
+    if (n0 + col >= n_out) continue;
     float v[GLU ? 2 : 1];
 #pragma unroll
     for (int h = 0; h < (GLU ? 2 : 1); ++h) {
       float sum = 0.f;
 #pragma unroll
-      for (int p = 0; p < (F32X ? 3 : 1); ++p)
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += red[w][F32X ? t * 3 + p : t][c + h * NB];
+      for (int w = 0; w < W; ++w)
+        sum += reinterpret_cast<const float*>(ring[w])[t * (16 * NF + 1) + col + h * NB];
       v[h] = sum;
     }
     const float o = GLU ? silu_mul(v[0], v[GLU ? 1 : 0]) : v[0];
-    const size_t at = (size_t)(t0 + t) * (GLU ? g.f : g.n) + n0 + c;
+    const size_t at = (size_t)(t0 + t) * n_out + n0 + col;
     if (g.out_f32) static_cast<float*>(g.out)[at] = o;
     else static_cast<uint16_t*>(g.out)[at] = f32_to_bf16(o);
   }
 }
 
-template <int MB, int NF, int SG, bool F32X, bool GLU>
-hipError_t launch5(const W4Args& g, hipStream_t st) {
-  constexpr int TOK = F32X ? 16 * MB / 3 : 16 * MB, NB = GLU ? 8 * NF : 16 * NF;
-  const dim3 grid(((GLU ? g.f : g.n) + NB - 1) / NB, (g.T + TOK - 1) / TOK);
-  w4_kernel<MB, NF, SG, F32X, GLU><<<grid, 64 * kWaves, 0, st>>>(g);
+// ---- more than 16 tokens.  Here the activations are the larger operand of a
+// workgroup, so its 8 waves share them: wave w takes weight rows 16 w .. + 16 of
+// the workgroup's 128, for 16 MB tokens and one of g.splits pieces of the
+// contraction, whose fp32 sums w4_finish adds in order.  One ring of kStages slots
+// (x for all waves, each wave's codes and scales), one barrier a block.
+constexpr int kStages = 3;
+
+template <int MB, int SG, bool F32X>
+__global__ __launch_bounds__(512) void w4_tile(W4Args g) {
+  using L = Slot<16 * MB, 8, SG, F32X>;   // 8 fragments of rows: one a wave
+  constexpr int XC = L::NX / 8, XP = F32X ? 3 : 1, kCopies = XC + 3;
+  static_assert(XC * 8 == L::NX && L::kRow >= 256, "whole copies");
+  // (the scales of wave w: 4 / SG x 16 dwords at 256 w)
+  constexpr int kS = L::kS, kZ = kS + 2048, kBytes = kZ + 2048;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kStages * kBytes];
+  const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = blockIdx.z * (16 * MB), n0 = blockIdx.x * 128, tn = min(16 * MB, g.T - t0);
+  if (n0 >= g.n) return;
+  const int nblk = (g.k + kBlk - 1) / kBlk;
+  const int b0 = blockIdx.y * g.per_split, b1 = min(b0 + g.per_split, nblk);
+  const int row_lo = min(n0 + wv * 16, g.n - 1);   // rows past the last: read as it, not stored
+  const int kb = g.k >> 1;
+  const int cr = lane >> 2, ck = ((lane & 3) ^ code_swz(cr)) * 32;
+  const uint32_t oc = (uint32_t)(min(row_lo + cr, g.n - 1) - row_lo) * (uint32_t)kb;
+  uint32_t ox[XC];
+  int kx[XC];
+#pragma unroll
+  for (int c = 0; c < XC; ++c) {
+    constexpr int U = L::kRow / 16;
+    const int i = (wv * XC + c) * 64 + lane, r = i / U, u = (i % U) ^ (r & 15);
+    kx[c] = u * (F32X ? 4 : 8);
+    ox[c] = (uint32_t)min(r, tn - 1) * (uint32_t)g.k;
+  }
+  const int sv = min(lane >> 4, 4 / SG - 1);
+  const uint32_t os = (uint32_t)(min(row_lo + ln, g.n - 1) - row_lo) * (uint32_t)g.groups;
+  const uint8_t* const zeros = g.zero ? g.zero : reinterpret_cast<const uint8_t*>(g.scale);
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring;
+  auto issue = [&](int b, int slot) {
+    if (b >= b1) return;
+    const int k0 = b * kBlk;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(base + slot * kBytes);
+    dma_b128(g.codes + (size_t)row_lo * kb + (k0 >> 1), oc + (uint32_t)(min(ck, g.k - 32 - k0) >> 1),
+             to + wv * 1024);
+    const uint8_t* x = static_cast<const uint8_t*>(g.x) + ((size_t)t0 * g.k + k0) * (F32X ? 4 : 2);
+#pragma unroll
+    for (int c = 0; c < XC; ++c)
+      dma_b128(x, (ox[c] + (uint32_t)min(kx[c], g.k - (F32X ? 4 : 8) - k0)) * (F32X ? 4 : 2),
+               to + L::kX + (wv * XC + c) * 1024);
+    const uint32_t o = os + (uint32_t)(SG < 4 ? min(b * (4 / SG) + sv, g.groups - 1)
+                                              : group_of<SG>(g, b, 0));
+    dma_u16(g.scale + (size_t)row_lo * g.groups, o * 2, to + kS + wv * 256);
+    dma_u8(zeros + (size_t)row_lo * g.groups, o, to + kZ + wv * 256);
+  };
+  const f32x4_t nil = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[MB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m) acc[m] = nil;
+  bf16x8_t ones;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
+#pragma unroll
+  for (int q = 0; q < kStages - 1; ++q) issue(b0 + q, q);
+  int slot = 0;
+#pragma unroll 1
+  for (int blk = b0; blk < b1; ++blk) {
+    // this wave's copies of the block have landed and its reads of the one
+    // before are done; past the barrier both hold for every wave
+    wait_lds();
+    if (blk + kStages - 2 < b1) wait_vmem<(kStages - 2) * kCopies>();
+    else wait_vmem<0>();
+    grouped::wg_barrier();
+    issue(blk + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+    const uint8_t* at = ring + slot * kBytes;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    const uint4 v = *reinterpret_cast<const uint4*>(at + wv * 1024 + ln * 64 + ((lg ^ code_swz(ln)) << 4));
+    uint32_t c[4] = {v.x, v.y, v.z, v.w};
+    transpose4(c);
+#pragma unroll
+    for (int s = 0; s < 4 / SG; ++s) {
+      if (blk * kBlk + s * SG * 32 >= g.k) break;
+      const int i = wv * 256 + (s * 16 + ln) * 4;
+      const float sc = bf16_lo(*reinterpret_cast<const uint32_t*>(at + kS + i));
+      const float off = -(float)(16 + (g.zero ? *reinterpret_cast<const int*>(at + kZ + i) : 8));
+      f32x4_t sum[MB], dot[MB];
+#pragma unroll
+      for (int m = 0; m < MB; ++m) sum[m] = dot[m] = nil;
+#pragma unroll
+      for (int j = s * SG; j < (s + 1) * SG; ++j) {
+        const bf16x8_t w = codes_biased(c[j]);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+          uint4 xv[F32X ? 2 : 1];
+#pragma unroll
+          for (int h = 0; h < (F32X ? 2 : 1); ++h) {
+            const int u = F32X ? 8 * j + 2 * lg + h : 4 * j + lg;
+            xv[h] = *reinterpret_cast<const uint4*>(at + L::kX + (m * 16 + ln) * L::kRow + ((u ^ ln) << 4));
+          }
+          bf16x8_t a[XP];
+          x_frags<F32X, false>(xv, a);
+#pragma unroll
+          for (int p = 0; p < XP; ++p) {
+            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], ones, sum[m], 0, 0, 0);
+            dot[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w, dot[m], 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[m][r] = __builtin_fmaf(sc, __builtin_fmaf(off, sum[m][r], dot[m][r]), acc[m][r]);
+    }
+  }
+  bool bad = false;
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) bad |= m * 16 + lg * 4 + r < tn && !(fabsf(acc[m][r]) < INFINITY);
+  if (__any(bad)) {
+#pragma unroll 1
+    for (int m = 0; m < MB; ++m) {
+      Rows<1> rows;
+      rows.lg = lg;
+      rows.tok = t0 + min(m * 16 + ln, tn - 1);
+      rows.row[0] = min(row_lo + ln, g.n - 1);
+      f32x4_t again[1];
+      w4_slice_exact<1, SG, F32X>(g, b0, b1, 1, rows, again);
+#pragma unroll
+      for (int q = 0; q < MB; ++q)
+        if (q == m) acc[q] = again[0];
+    }
+  }
+  const int n = n0 + wv * 16 + ln;
+  if (n >= g.n) return;
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = m * 16 + lg * 4 + r;
+      if (t < tn) g.part[((size_t)blockIdx.y * g.T + t0 + t) * g.n + n] = acc[m][r];
+    }
+}
+
+// The pieces of a split contraction added in order, then the gated form's
+// activation: one workgroup row a token, V consecutive outputs a thread.
+template <bool GLU, int V>
+__global__ __launch_bounds__(256) void w4_finish(W4Args g) {
+  typedef __attribute__((ext_vector_type(V))) float vec_t;
+  const int n_out = GLU ? g.f : g.n, n = (blockIdx.x * 256 + threadIdx.x) * V;
+  const int64_t t = blockIdx.y;
+  if (n >= n_out) return;
+  const size_t piece = (size_t)g.T * g.n;
+  const float* p = g.part + t * g.n + n;
+  vec_t a = 0.f, b = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < g.splits; ++s) {
+    a += *reinterpret_cast<const vec_t*>(p + s * piece);
+    if (GLU) b += *reinterpret_cast<const vec_t*>(p + s * piece + g.f);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float o = GLU ? silu_mul(a[i], b[i]) : a[i];
+    if (g.out_f32) static_cast<float*>(g.out)[t * n_out + n + i] = o;
+    else static_cast<uint16_t*>(g.out)[t * n_out + n + i] = f32_to_bf16(o);
+  }
+}
+
+template <int W, int D, int RC, int NF, bool F32X, bool GLU>
+hipError_t launch(const W4Args& g, hipStream_t st) {
+  constexpr int NB = GLU ? 8 * NF : 16 * NF;
+  // (a multiple of 8 along the weights: the token blocks of one set of rows run
+  // on the same XCD, whose L2 then serves the codes)
+  const dim3 grid((((GLU ? g.f : g.n) + NB - 1) / NB + 7) / 8 * 8, (g.T + RC - 1) / RC);
+  const int group = g.k / g.groups;
+  if (group == 32) w4_kernel<W, D, RC, NF, 1, F32X, GLU><<<grid, 64 * W, 0, st>>>(g);
+  else if (group == 64) w4_kernel<W, D, RC, NF, 2, F32X, GLU><<<grid, 64 * W, 0, st>>>(g);
+  else w4_kernel<W, D, RC, NF, 4, F32X, GLU><<<grid, 64 * W, 0, st>>>(g);   // a multiple of 128
   return hipGetLastError();
 }
-template <int MB, int NF, bool F32X, bool GLU>
-hipError_t launch4(const W4Args& g, hipStream_t st) {
-  if (g.group == 32) return launch5<MB, NF, 1, F32X, GLU>(g, st);
-  if (g.group == 64) return launch5<MB, NF, 2, F32X, GLU>(g, st);
-  return launch5<MB, NF, 4, F32X, GLU>(g, st);   // a multiple of 128
+template <int MB, bool F32X, bool GLU>
+hipError_t launch_tile(const W4Args& g, hipStream_t st) {
+  const dim3 grid(((g.n + 127) / 128 + 7) / 8 * 8, g.splits, (g.T + 16 * MB - 1) / (16 * MB));
+  const int group = g.k / g.groups;
+  if (group == 32) w4_tile<MB, 1, F32X><<<grid, 512, 0, st>>>(g);
+  else if (group == 64) w4_tile<MB, 2, F32X><<<grid, 512, 0, st>>>(g);
+  else w4_tile<MB, 4, F32X><<<grid, 512, 0, st>>>(g);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int n_out = GLU ? g.f : g.n;
+  if (n_out % 4 == 0)   // (whole 16-byte pieces of every row)
+    w4_finish<GLU, 4><<<dim3((n_out + 1023) / 1024, g.T), 256, 0, st>>>(g);
+  else
+    w4_finish<GLU, 1><<<dim3((n_out + 255) / 256, g.T), 256, 0, st>>>(g);
+  return hipGetLastError();
 }
+
+// Up to 16 tokens a workgroup has all of them; beyond, the tiled kernel takes
+// kChunk tokens at a time (so that its partial sums stay bounded).
+constexpr int kFew = 16, kChunk = 256;
+
+// Pieces of the contraction for a chunk of T tokens: at most one workgroup a CU (a
+// second round of a few workgroups costs as much as the first), at least two
+// blocks a piece.
+int tile_splits(int n, int k, int T) {
+  const int64_t wgs = (int64_t)((n + 127) / 128) * ((T + 63) / 64);
+  const int nblk = (k + kBlk - 1) / kBlk;
+  const int64_t s = std::min<int64_t>(std::max<int64_t>(256 / wgs, 1), std::max(nblk / 2, 1));
+  const int per = (int)((nblk + s - 1) / s);
+  return (nblk + per - 1) / per;
+}
+
 template <bool F32X, bool GLU>
-hipError_t launch2(const W4Args& g, hipStream_t st) {
-  const long rows = (long)g.T * (F32X ? 3 : 1);
-  if (rows <= (F32X ? 15 : 16)) return launch4<1, 2, F32X, GLU>(g, st);
-  return launch4<4, 2, F32X, GLU>(g, st);
+hipError_t launch_t(W4Args g, hipStream_t st) {
+  if (g.T <= 4) return launch<8, F32X ? 3 : 4, 4, 2, F32X, GLU>(g, st);
+  if (g.T <= 8) return launch<8, 2, 8, 2, F32X, GLU>(g, st);
+  if (g.T <= kFew) return launch<F32X ? 4 : 8, 2, 16, 2, F32X, GLU>(g, st);
+  const int T = g.T, nblk = (g.k + kBlk - 1) / kBlk;
+  const size_t out = (size_t)(GLU ? g.f : g.n) * (g.out_f32 ? 4 : 2);
+  for (int t = 0; t < T; t += kChunk) {
+    W4Args c = g;
+    c.T = std::min(kChunk, T - t);
+    c.x = static_cast<const uint8_t*>(g.x) + (size_t)t * g.k * (F32X ? 4 : 2);
+    c.out = static_cast<uint8_t*>(g.out) + (size_t)t * out;
+    c.splits = tile_splits(g.n, g.k, c.T);
+    c.per_split = (nblk + c.splits - 1) / c.splits;
+    const hipError_t e = F32X || c.T <= 32 ? launch_tile<2, F32X, GLU>(c, st)
+                                           : launch_tile<F32X ? 2 : 4, F32X, GLU>(c, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
+// Floats of the partial sums: the largest of a chunk's and the last, smaller
+// chunk's.
+size_t w4_part_floats(const k3moe_w4_matrix& w, int64_t T) {
+  if (T <= kFew) return 0;
+  auto floats = [&](int64_t t) { return (size_t)tile_splits(w.n, w.k, (int)t) * t * w.n; };
+  const int64_t rest = T % kChunk;
+  return T < kChunk ? floats(T) : std::max(floats(kChunk), rest ? floats(rest) : 0);
+}
+
 hipError_t launch_w4(const k3moe_w4_matrix& w, int64_t T, bool x_f32, bool out_f32, bool glu,
-                     const void* x, void* out, hipStream_t st) {
-  W4Args g;
+                     const void* x, void* out, float* part, hipStream_t st) {
+  W4Args g{};
+  g.part = part;
   g.codes = static_cast<const uint8_t*>(w.codes);
   g.scale = static_cast<const uint16_t*>(w.scale);
   g.zero = static_cast<const uint8_t*>(w.zero);
@@ -290,11 +708,14 @@ hipError_t launch_w4(const k3moe_w4_matrix& w, int64_t T, bool x_f32, bool out_f
   g.T = (int)T;
   g.n = w.n;
   g.k = w.k;
-  g.group = w.group;
+  g.groups = w.k / w.group;
+  // (rounded up, exact for the at most 2^13 blocks of a row)
+  const uint32_t blocks = (uint32_t)w.group / kBlk;
+  g.per_group = blocks > 1 ? (uint32_t)(((uint64_t(1) << 32) + blocks - 1) / blocks) : 0;
   g.f = glu ? w.n / 2 : w.n;
   g.out_f32 = out_f32;
-  if (x_f32) return glu ? launch2<true, true>(g, st) : launch2<true, false>(g, st);
-  return glu ? launch2<false, true>(g, st) : launch2<false, false>(g, st);
+  if (x_f32) return glu ? launch_t<true, true>(g, st) : launch_t<true, false>(g, st);
+  return glu ? launch_t<false, true>(g, st) : launch_t<false, false>(g, st);
 }
 
 }  // namespace k3

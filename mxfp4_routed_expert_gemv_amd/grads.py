@@ -2,43 +2,54 @@
 lists of torch tensors.  Every computation happens in libk3moe's kernels; this
 file only marshals."""
 from array import array
+from itertools import chain
+from operator import attrgetter
 
 import torch
 
-from . import BF16, F32, k3moe_grad_clip, k3moe_grad_norm, k3moe_grad_workspace_bytes
+from . import (BF16, F32, current_stream, k3moe_grad_clip, k3moe_grad_norm,
+               k3moe_grad_workspace_bytes, on_device)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
+_dtype, _shape, _T = attrgetter("dtype"), attrgetter("shape"), torch.Tensor
 
 
-def _table(tensors, outs):
-    """The k3moe_tensor list: four words a tensor, the two types in the last."""
-    dev = tensors[0].device
+def _types(tensors):
     try:
-        words = array("q")
-        for t, o in zip(tensors, outs):
-            words.extend((t.data_ptr(), o.data_ptr(), t.numel(), _DT[t.dtype] | _DT[o.dtype] << 32))
-            if t.device != dev or o.device != dev or not (t.is_contiguous() and o.is_contiguous()):
-                raise ValueError("the tensors must be contiguous and on one device")
-            if o.shape != t.shape:
-                raise ValueError(f"an output of shape {tuple(o.shape)} for {tuple(t.shape)}")
+        return [_DT[t] for t in map(_dtype, tensors)]
     except KeyError as e:
         raise TypeError(f"gradients are float32 or bfloat16, not {e.args[0]}") from None
-    return words, dev
 
 
 def _call(run, tensors, outs, stream):
     tensors = list(tensors)
-    outs = tensors if outs is None else list(outs)
     if not tensors:
         raise ValueError("no tensors")
-    if len(outs) != len(tensors):
-        raise ValueError(f"{len(outs)} outputs for {len(tensors)} tensors")
-    words, dev = _table(tensors, outs)
+    dev = tensors[0].device
+    every = tensors
+    types = _types(tensors)
+    pointers = to = list(map(_T.data_ptr, tensors))
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != len(tensors):
+            raise ValueError(f"{len(outs)} outputs for {len(tensors)} tensors")
+        if list(map(_shape, outs)) != list(map(_shape, tensors)):
+            raise ValueError("the outputs' shapes are not the tensors'")
+        every = tensors + outs
+        to = list(map(_T.data_ptr, outs))
+        types = [t | o << 32 for t, o in zip(types, _types(outs))]
+    else:
+        types = [t | t << 32 for t in types]
+    if dev.type != "cuda" or set(map(_T.get_device, every)) != {dev.index} or \
+            not all(map(_T.is_contiguous, every)):
+        raise ValueError("the tensors must be contiguous and on one device")
+    # the k3moe_tensor list: four words a tensor, the two types in the last
+    words = array("q", chain.from_iterable(zip(pointers, to, map(_T.numel, tensors), types)))
     n = len(tensors)
-    with torch.cuda.device(dev):
+    with on_device(dev, stream):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         ws = torch.empty(k3moe_grad_workspace_bytes(n), dtype=torch.uint8, device=dev)
-        run(words.buffer_info()[0], n, norm, ws, stream)
+        run(words.buffer_info()[0], n, norm, ws, current_stream(dev))
     return norm
 
 
@@ -51,6 +62,6 @@ def grad_norm(tensors, stream=None):
 def clip_grads(tensors, max_norm, out=None, stream=None):
     """Scales the tensors by min(1, max_norm / norm), in place or into the tensors
     `out` (fp32 or bf16 each, of the same shapes), and returns the norm as
-    grad_norm does.  A norm that is not finite scales nothing."""
+    grad_norm does.  A norm of infinities or NaN scales nothing."""
     return _call(lambda ts, n, norm, ws, st: k3moe_grad_clip(ts, n, float(max_norm), norm, ws, st),
                  tensors, out, stream)

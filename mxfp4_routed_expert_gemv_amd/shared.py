@@ -6,9 +6,9 @@ enqueued on that device's current stream (or `stream`).  Every computation
 happens in libk3moe's kernels; this file only marshals."""
 import torch
 
-from . import (BF16, F32, FMT_BF16, OP_SHARED_BACKWARD, OP_SHARED_TRAIN,
+from . import (BF16, F32, FMT_BF16, OP_SHARED_BACKWARD, OP_SHARED_TRAIN, current_stream,
                k3moe_shared_ffn_backward, k3moe_shared_ffn_train, k3moe_workspace_bytes, make_bank,
-               make_shape)
+               make_shape, on_device)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -20,8 +20,8 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; {tuple(shape)} is needed")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the weights are on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    if not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} is not a contiguous tensor on a GPU")
 
 
 def _problem(x, w13, w2, out_dtype):
@@ -47,12 +47,12 @@ def shared_ffn_train(x, w13, w2, out_dtype=torch.bfloat16, workspace=None, strea
     [T][S][2 fs], the pre-activations that shared_ffn_backward takes.
     x [T][d], w13 [S][2 fs][d] (gate rows, then up rows), w2 [S][d][fs], bf16."""
     shape, bank, (T, d, fs, S, dev) = _problem(x, w13, w2, out_dtype)
-    with torch.cuda.device(dev):
+    with on_device(dev, stream):
         y = torch.empty((T, d), dtype=out_dtype, device=dev)
         gu = torch.empty((T, S, 2 * fs), dtype=torch.bfloat16, device=dev)
         if T:
             ws = _workspace(shape, OP_SHARED_TRAIN, dev) if workspace is None else workspace
-            k3moe_shared_ffn_train(shape, bank, x, gu, y, ws, stream)
+            k3moe_shared_ffn_train(shape, bank, x, gu, y, ws, current_stream(dev))
     return y, gu
 
 
@@ -62,13 +62,14 @@ def shared_ffn_backward(x, gu, dy, w13, w2, need=(True, True, True), workspace=N
     shape, bank, (T, d, fs, S, dev) = _problem(x, w13, w2, torch.bfloat16)
     _need(gu, "gu", torch.bfloat16, (T, S, 2 * fs), dev)
     _need(dy, "dy", torch.bfloat16, (T, d), dev)
-    with torch.cuda.device(dev):
+    with on_device(dev, stream):
         dx = torch.empty_like(x) if need[0] else None
         dw13 = torch.empty_like(w13) if need[1] else None
         dw2 = torch.empty_like(w2) if need[2] else None
         ws = _workspace(shape, OP_SHARED_BACKWARD, dev) if workspace is None else workspace
         # (an empty tensor's address may be NULL: for T = 0 nothing is read or written there)
-        k3moe_shared_ffn_backward(shape, bank, x, gu, dy, dx if T else None, dw13, dw2, ws, stream)
+        k3moe_shared_ffn_backward(shape, bank, x, gu, dy, dx if T else None, dw13, dw2, ws,
+                                  current_stream(dev))
     return dx, dw13, dw2
 
 

@@ -5,12 +5,12 @@ import ctypes
 
 import torch
 
-from . import BF16, F32, K3moeError, W4Matrix, lib
+from . import BF16, F32, K3moeError, W4Matrix, current_stream, lib, on_device
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _run(call, half, x, codes, scale, zero, out_dtype, out, stream):
+def _run(call, half, x, codes, scale, zero, out_dtype, out, workspace, stream):
     dev = x.device
     if codes.dim() != 2 or scale.dim() != 2 or x.dim() != 2:
         raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)} and scale "
@@ -31,37 +31,35 @@ def _run(call, half, x, codes, scale, zero, out_dtype, out, stream):
         raise ValueError(f"out must be {(T, cols)} {out_dtype}")
     if out.dtype not in _DT:
         raise TypeError(f"the output is float32 or bfloat16, not {out.dtype}")
-    for t in (x, codes, scale, out) if zero is None else (x, codes, scale, out, zero):
-        if not t.is_contiguous() or t.device != dev:
-            raise ValueError("the tensors must be contiguous and on one device")
+    same = dev == codes.device == scale.device == out.device and (zero is None or zero.device == dev)
+    if not same or dev.type != "cuda" or not (
+            x.is_contiguous() and codes.is_contiguous() and scale.is_contiguous()
+            and out.is_contiguous() and (zero is None or zero.is_contiguous())):
+        raise ValueError("the tensors must be contiguous and on one device")
     w = W4Matrix(n, k, k // groups, codes.data_ptr(), scale.data_ptr(),
                  None if zero is None else zero.data_ptr())
-    if torch.cuda.current_device() == dev.index:
-        st = _launch(call, w, T, x, out, dev, stream)
-    else:
-        with torch.cuda.device(dev):
-            st = _launch(call, w, T, x, out, dev, stream)
-    if st:
-        raise K3moeError(st, lib.k3moe_last_error().decode())
+    with on_device(dev, stream):
+        if workspace is None and T > 16:
+            workspace = torch.empty(lib.k3moe_w4_workspace_bytes(ctypes.byref(w), T),
+                                    dtype=torch.uint8, device=dev)
+        status = call(ctypes.byref(w), T, _DT[x.dtype], _DT[out.dtype], x.data_ptr(), out.data_ptr(),
+                      None if workspace is None else workspace.data_ptr(),
+                      0 if workspace is None else workspace.numel(), current_stream(dev))
+    if status:
+        raise K3moeError(status, lib.k3moe_last_error().decode())
     return out
 
 
-def _launch(call, w, T, x, out, dev, stream):
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    return call(ctypes.byref(w), T, _DT[x.dtype], _DT[out.dtype], x.data_ptr(), out.data_ptr(),
-                stream if isinstance(stream, int) else stream.cuda_stream)
-
-
-def w4_linear(x, codes, scale, zero=None, out_dtype=None, out=None, stream=None):
+def w4_linear(x, codes, scale, zero=None, out_dtype=None, out=None, workspace=None, stream=None):
     """out [T][n] = x W^T with W[r][j] = (q[r][j] - zero[r][j / g]) * scale[r][j / g]:
     x [T][k] (bf16 or fp32), codes [n][k / 2] uint8 (low nibble = even element),
     scale [n][k / g] bf16, zero [n][k / g] uint8 (None: 8 everywhere).
-    out_dtype: bf16 or fp32, x's by default."""
-    return _run(lib.k3moe_w4_linear, False, x, codes, scale, zero, out_dtype, out, stream)
+    out_dtype: bf16 or fp32, x's by default.  workspace: a uint8 tensor of
+    k3moe_w4_workspace_bytes (made when needed, above 16 tokens, if not given)."""
+    return _run(lib.k3moe_w4_linear, False, x, codes, scale, zero, out_dtype, out, workspace, stream)
 
 
-def w4_glu(x, codes, scale, zero=None, out_dtype=None, out=None, stream=None):
+def w4_glu(x, codes, scale, zero=None, out_dtype=None, out=None, workspace=None, stream=None):
     """The gated block's first half, silu(x Wg^T) * (x Wu^T) [T][n / 2]: the first
     n / 2 rows of W are the gate, the others the up projection."""
-    return _run(lib.k3moe_w4_glu, True, x, codes, scale, zero, out_dtype, out, stream)
+    return _run(lib.k3moe_w4_glu, True, x, codes, scale, zero, out_dtype, out, workspace, stream)

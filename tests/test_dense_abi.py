@@ -79,16 +79,17 @@ def w4(n=64, k=256, group=128, codes=FAKE, scale=FAKE, zero=None):
 def test_w4_refusals(glu):
     fn = k3.lib.k3moe_w4_glu if glu else k3.lib.k3moe_w4_linear
 
-    def call(w, T=1, xd=k3.BF16, od=k3.BF16, x=FAKE, out=FAKE):
-        return fn(ctypes.byref(w), T, xd, od, x, out, None)
-    assert fn(None, 1, k3.BF16, k3.BF16, FAKE, FAKE, None) == EINVAL
+    def call(w, T=1, xd=k3.BF16, od=k3.BF16, x=FAKE, out=FAKE, ws=(None, 0)):
+        return fn(ctypes.byref(w), T, xd, od, x, out, ws[0], ws[1], None)
+    assert fn(None, 1, k3.BF16, k3.BF16, FAKE, FAKE, None, 0, None) == EINVAL
     assert call(w4(), T=-1) == EINVAL
     assert call(w4(n=-2)) == EINVAL
     assert call(w4(n=0)) == ESHAPE
-    assert call(w4(n=(1 << 24) + 2)) == ESHAPE
+    assert call(w4(n=(1 << 20) + 2)) == ESHAPE
     assert call(w4(k=0)) == ESHAPE
     assert call(w4(k=200)) == ESHAPE
     assert call(w4(k=(1 << 20) + 128)) == ESHAPE
+    assert call(w4(n=1 << 20, k=1 << 17)) == ESHAPE   # 2^37 weights
     for g in (0, 16, 48, 96, 192):
         assert call(w4(k=g * 4 or 64, group=g)) == ESHAPE, g
     assert call(w4(group=512)) == ESHAPE          # longer than a row
@@ -103,6 +104,15 @@ def test_w4_refusals(glu):
     assert call(w4(codes=None), T=0, x=None, out=None) == 0
     if glu:
         assert call(w4(n=63)) == ESHAPE
+    # the workspace: none up to 16 tokens, then partial sums
+    assert k3.k3moe_w4_workspace_bytes(w4(), 16) == 0
+    assert k3.k3moe_w4_workspace_bytes(w4(n=0), 17) == 0
+    need = k3.k3moe_w4_workspace_bytes(w4(), 17)
+    assert need >= 17 * 64 * 4 and need % 256 == 0
+    assert k3.k3moe_w4_workspace_bytes(w4(n=7168, k=7168), 1 << 18) <= 1 << 28
+    assert call(w4(), T=17) == EWORKSPACE
+    assert call(w4(), T=17, ws=(FAKE, need - 256)) == EWORKSPACE
+    assert call(w4(), T=17, ws=(FAKE + 16, need)) == EALIGN
 
 
 def tensors(*rows):

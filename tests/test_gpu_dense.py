@@ -252,7 +252,7 @@ W4 = [(1, 64, 128, 128, False), (1, 17, 32, 32, True), (2, 100, 96, 32, False),
       (16, 130, 1024, 128, False), (17, 96, 1088, 64, True), (21, 66, 256, 256, False),
       (22, 1000, 512, 512, True), (33, 98, 2048, 128, True), (64, 514, 4096, 32, True),
       (65, 64, 384, 128, False), (131, 40, 224, 32, True), (1, 2050, 7168, 128, True),
-      (3, 7168, 2048, 64, False)]
+      (3, 7168, 2048, 64, False), (300, 130, 640, 64, True), (257, 66, 1280, 128, False)]
 
 
 @pytest.mark.parametrize("xd", [torch.bfloat16, torch.float32])
