@@ -216,8 +216,16 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   const int K = P == kGateUp || P == kDHid ? d : P == kDown ? F : P == kDX ? 2 * F : T;
   const int n_mt = (M + BM - 1) / BM, n_nt = (N + C::kN - 1) / C::kN;
   const int n_cols = SPLIT ? n_nt * g.splits : n_nt;   // n-tiles, every split's in turn
-  const ItemRange ir = item_range((long)n_mt * n_cols);
-  const int it_first = (int)ir.first, it_end = (int)ir.end, it_step = (int)ir.step;
+  const int n_items = n_mt * n_cols, G = gridDim.x, xcd = blockIdx.x & 7, wi = blockIdx.x >> 3;
+  // This workgroup's item of round r (n_items: none).  A round takes the next G
+  // items, its 8 contiguous pieces one to an XCD, the last round's shorter ones
+  // too: the XCDs work on neighbouring tiles at any time, so what they all read
+  // (a group's rows of A, all of B) stays in the last-level cache.
+  auto item_of = [&](int r) {
+    const int first = r * G, piece = (min(G, n_items - first) + 7) >> 3;
+    const int at = first + xcd * piece + wi;
+    return first < n_items && wi < piece && at < min(first + G, n_items) ? at : n_items;
+  };
 
   // Items: groups of kGM m-tiles, the m-tile fastest, then the n-tile, so the
   // workgroups of an XCD share both operands through its L2.
@@ -241,7 +249,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   const uint32_t sa = C::A_KC ? kBK * 2 : kBK * 2 * (uint32_t)lda;   // bytes per stage
   const uint32_t sb = C::B_KC ? kBK * 2 : kBK * 2 * (uint32_t)ldb;
   uint64_t pa, pb;
-  int c_it = it_first, c_k, c_end;   // the copies' item, first contraction element, last but one
+  int c_rd = 0, c_k, c_end;   // the copies' round, first contraction element and end
+  int c_it = item_of(0);
   int c_ko = 0;                      // kDown: c_k within its expert's features
   auto setup = [&]() {
     int m0, n0;
@@ -312,8 +321,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
       }
     }
     if (c_k >= c_end) {
-      c_it += it_step;
-      if (c_it < it_end) {
+      c_it = item_of(++c_rd);
+      if (c_it < n_items) {
         setup();
       } else {   // behind the last item: zeros, that nothing uses
 #pragma unroll
@@ -358,7 +367,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
 #pragma unroll
     for (int f = 0; f < NF; ++f) fb[f] = nb[f];
   };
-  if (it_first >= it_end) return;
+  if (c_it >= n_items) return;
   setup();
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -373,7 +382,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
 #pragma unroll
   for (int i = 0; i < MF; ++i) fa[i] = OA::frag(sA, wm * MF + i, 0, ln, lg);
   int slot = 0;
-  for (int it = it_first; it < it_end; it += it_step) {
+  for (int rd = 0, it; (it = item_of(rd)) < n_items; ++rd) {
     int m0, n0, k0, k1;
     const int sp = item_tile(it, m0, n0, k0, k1);
     const int nst = (k1 - k0 + kBK - 1) / kBK;

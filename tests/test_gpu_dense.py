@@ -207,11 +207,11 @@ def test_shared_rows_behind_the_batch_stay():
     from mxfp4_routed_expert_gemv_amd import shared
     T, d, fs, S = 37, 96, 32, 2
     x, w13, w2 = problem(T, d, fs, S, 60)
-    shape, bank, _ = shared._problem(x, w13, w2, torch.bfloat16)
+    shape, bank, nbytes, _ = shared._problem(x, w13, w2, torch.bfloat16, k3.OP_SHARED_BACKWARD)
     y = torch.full((T + 3, d), 7.0, dtype=torch.bfloat16, device="cuda")
     gu = torch.full((T + 3, S, 2 * fs), 7.0, dtype=torch.bfloat16, device="cuda")
     dx = y.clone()
-    ws = shared._workspace(shape, k3.OP_SHARED_BACKWARD, x.device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     k3.k3moe_shared_ffn_train(shape, bank, x, gu, y, ws)
     k3.k3moe_shared_ffn_backward(shape, bank, x, gu, x, dx, None, None, ws)
     torch.cuda.synchronize()
