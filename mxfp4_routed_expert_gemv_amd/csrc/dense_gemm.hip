@@ -197,16 +197,21 @@ __device__ __forceinline__ void store_product(const DenseArgs& g, int m, int n, 
 
 constexpr int kGM = 8;   // m-tiles per group of the item order
 
-// SPLIT: an item is a tile and one of g.splits pieces of the contraction; its
-// sums go to g.part, and split_finish adds the pieces in order.
-template <int P, int BM, int BN, int WM, int WN, bool SPLIT = false>
-__global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
+// Where a workgroup's items lie: rounds rd0 .. rd1 of G items each, of every
+// round the wi-th item of XCD xcd's piece.
+struct Items {
+  int G, xcd, wi, rd0, rd1;
+};
+
+// The tiles of one product that `at` names.  SPLIT: an item is a tile and one of
+// g.splits pieces of the contraction; its sums go to g.part, and split_finish adds
+// the pieces in order.
+template <int P, int BM, int BN, int WM, int WN, int RING, bool SPLIT>
+__device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, uint8_t* sA, uint8_t* sB) {
   using C = Tile<P, BM, BN, WM, WN>;
   using OA = typename C::A;
   using OB = typename C::B;
   constexpr int MF = C::MF, NF = C::NF;
-  __shared__ __attribute__((aligned(16))) uint8_t sA[2 * OA::kSlot];
-  __shared__ __attribute__((aligned(16))) uint8_t sB[2 * OB::kSlot];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ln = lane & 15, lg = lane >> 4;
@@ -216,15 +221,16 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   const int K = P == kGateUp || P == kDHid ? d : P == kDown ? F : P == kDX ? 2 * F : T;
   const int n_mt = (M + BM - 1) / BM, n_nt = (N + C::kN - 1) / C::kN;
   const int n_cols = SPLIT ? n_nt * g.splits : n_nt;   // n-tiles, every split's in turn
-  const int n_items = n_mt * n_cols, G = gridDim.x, xcd = blockIdx.x & 7, wi = blockIdx.x >> 3;
+  const int n_items = n_mt * n_cols;
   // This workgroup's item of round r (n_items: none).  A round takes the next G
   // items, its 8 contiguous pieces one to an XCD, the last round's shorter ones
   // too: the XCDs work on neighbouring tiles at any time, so what they all read
   // (a group's rows of A, all of B) stays in the last-level cache.
   auto item_of = [&](int r) {
-    const int first = r * G, piece = (min(G, n_items - first) + 7) >> 3;
-    const int at = first + xcd * piece + wi;
-    return first < n_items && wi < piece && at < min(first + G, n_items) ? at : n_items;
+    const int first = r * at.G, piece = (min(at.G, n_items - first) + 7) >> 3;
+    const int it = first + at.xcd * piece + at.wi;
+    return r < at.rd1 && first < n_items && at.wi < piece && it < min(first + at.G, n_items)
+               ? it : n_items;
   };
 
   // Items: groups of kGM m-tiles, the m-tile fastest, then the n-tile, so the
@@ -249,8 +255,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   const uint32_t sa = C::A_KC ? kBK * 2 : kBK * 2 * (uint32_t)lda;   // bytes per stage
   const uint32_t sb = C::B_KC ? kBK * 2 : kBK * 2 * (uint32_t)ldb;
   uint64_t pa, pb;
-  int c_rd = 0, c_k, c_end;   // the copies' round, first contraction element and end
-  int c_it = item_of(0);
+  int c_rd = at.rd0, c_k, c_end;   // the copies' round, first contraction element and end
+  int c_it = item_of(c_rd);
   int c_ko = 0;                      // kDown: c_k within its expert's features
   auto setup = [&]() {
     int m0, n0;
@@ -370,19 +376,19 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   if (c_it >= n_items) return;
   setup();
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < RING; ++q) {
 #pragma unroll
     for (int c = 0; c < C::NA + C::NB; ++c) copy(q, c);
     advance();
   }
-  wait_vmem<0>();
+  wait_vmem<(RING - 1) * (C::NA + C::NB)>();
   wg_barrier();
 #pragma unroll
   for (int f = 0; f < NF; ++f) fb[f] = OB::frag(sB, wn * NF + f, 0, ln, lg);
 #pragma unroll
   for (int i = 0; i < MF; ++i) fa[i] = OA::frag(sA, wm * MF + i, 0, ln, lg);
   int slot = 0;
-  for (int rd = 0, it; (it = item_of(rd)) < n_items; ++rd) {
+  for (int rd = at.rd0, it; (it = item_of(rd)) < n_items; ++rd) {
     int m0, n0, k0, k1;
     const int sp = item_tile(it, m0, n0, k0, k1);
     const int nst = (k1 - k0 + kBK - 1) / kBK;
@@ -391,15 +397,17 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[i][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int s = 0; s < nst; ++s, slot ^= 1) {
+    for (int s = 0; s < nst; ++s) {
       half(slot, 1, -1);
       // this wave's reads of the slot are done and its copies of the next
       // stage have landed; past the barrier both hold for every wave
       wait_lds();
-      wait_vmem<0>();
+      wait_vmem<(RING - 2) * (C::NA + C::NB)>();
       wg_barrier();
-      half(slot ^ 1, 0, slot);   // and the stage after the next on its way
+      const int next = RING == 2 ? slot ^ 1 : slot == RING - 1 ? 0 : slot + 1;
+      half(next, 0, slot);   // and the stage RING further on its way
       advance();
+      slot = next;
     }
     // ---- epilogue: lane (ln, lg) holds m = m0 + 16 (wm MF + i) + ln, four n
 #pragma unroll
@@ -437,6 +445,39 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   }
 }
 
+template <int P, int BM, int BN, int WM, int WN, int RING = 2, bool SPLIT = false>
+__global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
+  __shared__ __attribute__((aligned(16))) uint8_t sA[RING * BM * 2 * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sB[RING * BN * 2 * kBK];
+  const Items at{(int)gridDim.x, (int)blockIdx.x & 7, (int)blockIdx.x >> 3, 0, 1 << 30};
+  run_tiles<P, BM, BN, WM, WN, RING, SPLIT>(g, at, sA, sB);
+}
+
+// dx, dW13 and dW2 in one launch: none depends on another, and none's tiles fill
+// its last round of CUs.  kCUs workgroups for every n[p] rounds of product p, dx's
+// first (they are the longest); a CU that has no dx tile, or is done with it, takes
+// a workgroup of the next product.
+constexpr int kCUs = 256;
+struct GradArgs {
+  DenseArgs g[3];
+  int n[3], wgs[3];
+};
+template <int BM, int BN, int WM, int WN, int RING>
+__global__ __launch_bounds__(64 * WM * WN) void dense_grads(GradArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t sA[RING * BM * 2 * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sB[RING * BN * 2 * kBK];
+  int wg = blockIdx.x;   // (every product's first is a multiple of 8, so wg & 7 is the XCD)
+  auto items = [&](int p) {
+    const int w = wg >> 3, r = w / (kCUs / 8) * a.n[p];
+    return Items{kCUs, wg & 7, w % (kCUs / 8), r, r + a.n[p]};
+  };
+  if (wg < a.wgs[0]) return run_tiles<kDX, BM, BN, WM, WN, RING, false>(a.g[0], items(0), sA, sB);
+  wg -= a.wgs[0];
+  if (wg < a.wgs[1]) return run_tiles<kDW13, BM, BN, WM, WN, RING, false>(a.g[1], items(1), sA, sB);
+  wg -= a.wgs[1];
+  run_tiles<kDW2, BM, BN, WM, WN, RING, false>(a.g[2], items(2), sA, sB);
+}
+
 // The pieces of a split contraction added in order, and the product's epilogue:
 // one thread per row and four columns.
 template <int P>
@@ -464,20 +505,23 @@ __global__ __launch_bounds__(256) void zero_fill(uint4* p, size_t n16) {
 
 // How a product runs: its tile and, for the smallest, the pieces its contraction
 // is split into.
-enum { kTile256, kTile128, kTile64 };
+enum { kTile256, kTile128x256, kTile128, kTile64 };
 struct Plan {
   int tile, splits, k_split;
 };
 
 // The tile whose rounds cost least, by what a 64-element stage was measured to
-// take (us; d 7168, two experts of 2048):
-//   256 x 256, one workgroup a CU:  1.2 (a part round) to 1.6;  from T = 2048 on
-//     the fastest (gate/up 353 us at T = 4096 against 440 and 725)
-//   128 x 256, one workgroup a CU:  0.8 to 1.0;  fewer tiles than CUs at T = 517
-//     (gate/up 94 us against 132 and 136)
-//   64 x 64, four workgroups a CU:  0.5 to 0.8;  small T (58 us against 129 and
-//     94 at T = 200), where its contraction is also split (the outputs are few,
-//     the weights have to come from every CU's loads at once)
+// take (us; d 7168, two experts of 2048, weights from HBM):
+//   256 x 256, 2 slots, one workgroup a CU:    1.6;  the fastest from T = 2048 on
+//     (gate/up 185 us there, against 208 on 128 x 256)
+//   128 x 256, 3 slots, one workgroup a CU:    0.95;  gate/up 93 us at T = 517
+//     (167 on 256 x 256, 120 on 128 x 128; 132 with 2 slots)
+//   128 x 128, 3 slots, one workgroup a CU:    0.65;  dh 75 us at T = 1000 (108 on
+//     128 x 256, 122 on 64 x 64)
+//   64 x 64, 3 slots, three workgroups a CU:   0.43 (one a CU), 0.5 (two), 0.64;
+//     gate/up 57 us at T = 200 (66 on 128 x 128; 92 with 2 slots), and for fewer
+//     tokens with its contraction split: the outputs are few, the weights have to
+//     come by every CU's loads at once
 Plan plan_product(int P, const k3moe_shape& s) {
   const int64_t F = (int64_t)s.n_shared * s.f_shared, T = s.T, d = s.d;
   const int64_t M = P == kDW13 ? 2 * F : P == kDW2 ? d : T;
@@ -487,25 +531,27 @@ Plan plan_product(int P, const k3moe_shape& s) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N * w + bn - 1) / bn); };
   auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
   const int64_t t64 = tiles(64, 64);
-  const double c256 = rounds(tiles(256, 256), 256) * 1.5 * nst;
-  const double c128 = rounds(tiles(128, 256), 256) * 0.95 * nst;
-  double c64 = (t64 <= 256 ? 0.5 : rounds(t64, 1024) * 0.8) * nst;
+  double best = (t64 <= 256 ? 0.43 : t64 <= 512 ? 0.5 : rounds(t64, 768) * 0.64) * nst;
   Plan p{kTile64, 1, 0};
-  if (P != kDW13 && P != kDW2 && t64 <= 512) {
-    int64_t n = std::min<int64_t>(1024 / t64, nst / 4);
+  if (P != kDW13 && P != kDW2 && t64 <= 384) {
+    int64_t n = std::min<int64_t>(768 / t64, nst / 4);
     if (n > 1) {
       const int64_t per = (nst + n - 1) / n;
       n = (nst + per - 1) / per;
-      const double c = 0.8 * per + 5.0;   // the second kernel
-      if (c < c64) {
-        c64 = c;
+      const double c = 0.64 * per + 5.0;   // the second kernel
+      if (c < best) {
+        best = c;
         p.splits = (int)n;
         p.k_split = (int)(per * kBK);
       }
     }
   }
-  if (c256 <= c128 && c256 <= c64) return Plan{kTile256, 1, 0};
-  if (c128 <= c64) return Plan{kTile128, 1, 0};
+  const double c128 = rounds(tiles(128, 128), 256) * 0.65 * nst;
+  if (c128 < best) best = c128, p = Plan{kTile128, 1, 0};
+  const double c128x256 = rounds(tiles(128, 256), 256) * 0.95 * nst;
+  if (c128x256 < best) best = c128x256, p = Plan{kTile128x256, 1, 0};
+  const double c256 = rounds(tiles(256, 256), 256) * 1.6 * nst;
+  if (c256 <= best) p = Plan{kTile256, 1, 0};
   return p;
 }
 
@@ -522,21 +568,45 @@ hipError_t launch_product(const k3moe_shape& s, DenseArgs g, float* part, hipStr
   const Plan p = plan_product(P, s);
   const int cus = grouped_grid();
   if (p.tile == kTile256) {
-    dense_tile<P, 256, 256, 2, 4><<<cus, 512, 0, st>>>(g);
+    dense_tile<P, 256, 256, 2, 4, 2><<<cus, 512, 0, st>>>(g);
+  } else if (p.tile == kTile128x256) {
+    dense_tile<P, 128, 256, 2, 4, 3><<<cus, 512, 0, st>>>(g);
   } else if (p.tile == kTile128) {
-    dense_tile<P, 128, 256, 2, 4><<<cus, 512, 0, st>>>(g);
+    dense_tile<P, 128, 128, 2, 4, 3><<<cus, 512, 0, st>>>(g);
   } else if (p.splits == 1) {
-    dense_tile<P, 64, 64, 2, 2><<<cus * 4, 256, 0, st>>>(g);
+    dense_tile<P, 64, 64, 2, 2, 3><<<cus * 3, 256, 0, st>>>(g);
   } else if constexpr (P != kDW13 && P != kDW2) {
     g.part = part;
     g.splits = p.splits;
     g.k_split = p.k_split;
-    dense_tile<P, 64, 64, 2, 2, true><<<cus * 4, 256, 0, st>>>(g);
+    dense_tile<P, 64, 64, 2, 2, 3, true><<<cus * 3, 256, 0, st>>>(g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n = s.T * (P == kGateUp || P == kDHid ? (int64_t)g.S * g.fs : g.d) / 4;
     split_finish<P><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
   }
+  return hipGetLastError();
+}
+
+// The three gradients in one launch (g.o0 NULL: not wanted).  A workgroup takes as
+// many of the short tiles as 48 stages make, so that its start weighs little.
+template <int BM, int BN, int WM, int WN, int RING>
+hipError_t launch_grads_tile(const k3moe_shape& s, const DenseArgs (&g)[3], hipStream_t st) {
+  GradArgs a;
+  const int64_t F = (int64_t)s.n_shared * s.f_shared, T = s.T, d = s.d;
+  const int64_t M[3] = {T, 2 * F, d}, N[3] = {d, d, F}, K[3] = {2 * F, T, T};
+  int64_t total = 0;
+  for (int p = 0; p < 3; ++p) {
+    a.g[p] = g[p];
+    const int64_t items = (M[p] + BM - 1) / BM * ((N[p] + BN - 1) / BN);
+    const int64_t rounds = (items + kCUs - 1) / kCUs, nst = (K[p] + kBK - 1) / kBK;
+    const int64_t least = std::max<int64_t>(48 / nst, 1);
+    a.n[p] = (int)std::min(rounds, p == 0 ? rounds : p == 1 ? std::max(least, (rounds + 1) / 2) : least);
+    a.wgs[p] = g[p].o0 ? (int)((rounds + a.n[p] - 1) / a.n[p] * kCUs) : 0;
+    total += a.wgs[p];
+  }
+  if (total == 0) return hipSuccess;
+  dense_grads<BM, BN, WM, WN, RING><<<(unsigned)total, 64 * WM * WN, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -586,30 +656,27 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   g.o1 = ws.h;
   hipError_t e = launch_product<kDHid>(s, g, ws.part, st);
   if (e != hipSuccess) return e;
-  if (dx) {
-    g = z;
-    g.a = ws.dgu;
-    g.b = static_cast<const uint16_t*>(b.w13);
-    g.o0 = dx;
-    e = launch_product<kDX>(s, g, ws.part, st);
-    if (e != hipSuccess) return e;
-  }
-  if (dw13) {
-    g = z;
-    g.a = ws.dgu;
-    g.b = static_cast<const uint16_t*>(x);
-    g.o0 = dw13;
-    e = launch_product<kDW13>(s, g, ws.part, st);
-    if (e != hipSuccess) return e;
-  }
-  if (dw2) {
-    g = z;
-    g.a = static_cast<const uint16_t*>(dy);
-    g.b = ws.h;
-    g.o0 = dw2;
-    e = launch_product<kDW2>(s, g, ws.part, st);
-  }
-  return e;
+  DenseArgs grads[3] = {z, z, z};
+  grads[0].a = ws.dgu;
+  grads[0].b = static_cast<const uint16_t*>(b.w13);
+  grads[0].o0 = dx;
+  grads[1].a = ws.dgu;
+  grads[1].b = static_cast<const uint16_t*>(x);
+  grads[1].o0 = dw13;
+  grads[2].a = static_cast<const uint16_t*>(dy);
+  grads[2].b = ws.h;
+  grads[2].o0 = dw2;
+  // One launch for the three: 300 us in all at T = 517 (370 in three launches), 1195
+  // at 4096 (1235).  From four rounds of dx on a partly filled last round weighs
+  // less than what a workgroup saves by going from tile to tile: 4.70 ms in three
+  // launches at T = 16384 (4.74 in one).  With few tokens dx's contraction is split.
+  const int tile = plan_product(kDX, s).tile;
+  const int64_t dx_tiles = ((s.T + 255) / 256) * ((s.d + 255) / 256);
+  if (tile == kTile256 && dx_tiles < 4 * kCUs) return launch_grads_tile<256, 256, 2, 4, 2>(s, grads, st);
+  if (tile == kTile128 || tile == kTile128x256) return launch_grads_tile<128, 256, 2, 4, 3>(s, grads, st);
+  if (dx && (e = launch_product<kDX>(s, grads[0], ws.part, st)) != hipSuccess) return e;
+  if (dw13 && (e = launch_product<kDW13>(s, grads[1], ws.part, st)) != hipSuccess) return e;
+  return dw2 ? launch_product<kDW2>(s, grads[2], ws.part, st) : hipSuccess;
 }
 
 // The weight gradients of an empty batch.  (A fill kernel rather than a memset,
