@@ -589,7 +589,8 @@ hipError_t launch_product(const k3moe_shape& s, DenseArgs g, float* part, hipStr
 }
 
 // The three gradients in one launch (g.o0 NULL: not wanted).  A workgroup takes as
-// many of the short tiles as 48 stages make, so that its start weighs little.
+// many of the short tiles as 48 stages make (16 on the smallest tiles, three to a
+// CU), so that its start weighs little.
 template <int BM, int BN, int WM, int WN, int RING>
 hipError_t launch_grads_tile(const k3moe_shape& s, const DenseArgs (&g)[3], hipStream_t st) {
   GradArgs a;
@@ -600,7 +601,7 @@ hipError_t launch_grads_tile(const k3moe_shape& s, const DenseArgs (&g)[3], hipS
     a.g[p] = g[p];
     const int64_t items = (M[p] + BM - 1) / BM * ((N[p] + BN - 1) / BN);
     const int64_t rounds = (items + kCUs - 1) / kCUs, nst = (K[p] + kBK - 1) / kBK;
-    const int64_t least = std::max<int64_t>(48 / nst, 1);
+    const int64_t least = std::max<int64_t>((BM == 64 ? 16 : 48) / nst, 1);
     a.n[p] = (int)std::min(rounds, p == 0 ? rounds : p == 1 ? std::max(least, (rounds + 1) / 2) : least);
     a.wgs[p] = g[p].o0 ? (int)((rounds + a.n[p] - 1) / a.n[p] * kCUs) : 0;
     total += a.wgs[p];
@@ -669,11 +670,19 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   // One launch for the three: 300 us in all at T = 517 (370 in three launches), 1195
   // at 4096 (1235).  From four rounds of dx on a partly filled last round weighs
   // less than what a workgroup saves by going from tile to tile: 4.70 ms in three
-  // launches at T = 16384 (4.74 in one).  With few tokens dx's contraction is split.
+  // launches at T = 16384 (4.74 in one).
+  // On 64 x 64 tiles one launch is worth it for small layers (4 x 256 x 128: 10 us
+  // against 16; 163 x 2624 x 512, 1100 tiles: 25 against 34); where the weight
+  // gradients alone fill the chip they are faster on their own tiles, beside a dx
+  // whose contraction is split (64 x 7168 x 4096, 21600 tiles: 142 us against 150).
   const int tile = plan_product(kDX, s).tile;
   const int64_t dx_tiles = ((s.T + 255) / 256) * ((s.d + 255) / 256);
+  const int64_t t64 = (s.T + 63) / 64, d64 = (s.d + 63) / 64,
+                f64 = ((int64_t)s.n_shared * s.f_shared + 31) / 32;   // of 2 F
+  const int64_t tiles64 = t64 * d64 + f64 * d64 + (f64 + 1) / 2 * d64;
   if (tile == kTile256 && dx_tiles < 4 * kCUs) return launch_grads_tile<256, 256, 2, 4, 2>(s, grads, st);
   if (tile == kTile128 || tile == kTile128x256) return launch_grads_tile<128, 256, 2, 4, 3>(s, grads, st);
+  if (tile == kTile64 && tiles64 <= 4096) return launch_grads_tile<64, 64, 2, 2, 3>(s, grads, st);
   if (dx && (e = launch_product<kDX>(s, grads[0], ws.part, st)) != hipSuccess) return e;
   if (dw13 && (e = launch_product<kDW13>(s, grads[1], ws.part, st)) != hipSuccess) return e;
   return dw2 ? launch_product<kDW2>(s, grads[2], ws.part, st) : hipSuccess;
