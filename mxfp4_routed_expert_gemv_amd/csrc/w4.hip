@@ -265,7 +265,7 @@ struct Slot {
 };
 __device__ __forceinline__ int code_swz(int r) { return ((r >> 1) & 2) ^ ((r >> 3) & 1) * 3; }
 
-// Workgroup (blockIdx.x, blockIdx.y): 16 NF weight rows (gated form: 8 NF gate
+// Workgroup blockIdx.x: 16 NF weight rows (gated form: 8 NF gate
 // rows and the matching up rows) x RC tokens.
 template <int W, int D, int RC, int NF, int SG, bool F32X, bool GLU>
 __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
@@ -278,8 +278,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
   const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n_out = GLU ? g.f : g.n;
-  const int t0 = blockIdx.y * RC, n0 = blockIdx.x * NB, tn = min(RC, g.T - t0);
-  if (n0 >= n_out) return;
+  const int n0 = blockIdx.x * NB, tn = g.T;
   // row of the workgroup's row i (rows past the last are read as it, and not stored)
   auto weight_row = [&](int i) {
     const int f = i >> 4, first = n0 + (GLU ? f % (NF / 2) : f) * 16;
@@ -326,7 +325,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
     for (int c = 0; c < NF; ++c)
       dma_b128(g.codes + ((size_t)row_lo + (GLU && c >= NF / 2 ? up_rows : 0)) * kb + (k0 >> 1),
                oc[c] + (uint32_t)(min(kc[c], left) >> 1), to + c * 1024);
-    const uint8_t* x = static_cast<const uint8_t*>(g.x) + ((size_t)t0 * g.k + k0) * (F32X ? 4 : 2);
+    const uint8_t* x = static_cast<const uint8_t*>(g.x) + (size_t)k0 * (F32X ? 4 : 2);
 #pragma unroll
     for (int c = 0; c < L::NX; ++c)
       dma_b128(x, (ox[c] + (uint32_t)min(kx[c], g.k - (F32X ? 4 : 8) - k0)) * (F32X ? 4 : 2),
@@ -417,7 +416,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
   if (__any(bad)) {
     Rows<NF> rows;
     rows.lg = lg;
-    rows.tok = t0 + min(ln, tn - 1);
+    rows.tok = min(ln, tn - 1);
 #pragma unroll
     for (int f = 0; f < NF; ++f) rows.row[f] = weight_row(f * 16 + ln);
     f32x4_t again[NF];   // (acc's own address would keep it out of registers)
@@ -446,7 +445,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
       v[h] = sum;
     }
     const float o = GLU ? silu_mul(v[0], v[GLU ? 1 : 0]) : v[0];
-    const size_t at = (size_t)(t0 + t) * n_out + n0 + col;
+    const size_t at = (size_t)t * n_out + n0 + col;
     if (g.out_f32) static_cast<float*>(g.out)[at] = o;
     else static_cast<uint16_t*>(g.out)[at] = f32_to_bf16(o);
   }
@@ -620,20 +619,40 @@ __global__ __launch_bounds__(256) void w4_finish(W4Args g) {
   }
 }
 
-template <int W, int D, int RC, int NF, bool F32X, bool GLU>
-hipError_t launch(const W4Args& g, hipStream_t st) {
+// Slots of a wave's ring: as many as the 160 KB of a CU hold, at most 4.  What
+// counts is how many bytes a CU has in flight: one workgroup of 16 waves with a
+// slot or two each reads faster than 8 waves with up to four (n x k, group, us:
+// one token 7168 x 4096, 128: 6.7 against 7.4; gated 2 x 4096 x 7168: 10.5
+// against 11.4; 16 tokens 7168 x 4096, 64: 8.5 against 9.3; 5 fp32 tokens gated
+// 2 x 2049 x 7168, 64: 15.6 against 18.0), fp32 too, where the 16 waves' bound of
+// 128 registers puts five to nine of them in scratch; only 32 workgroups of a
+// short contraction lose (2 fp32 tokens 1024 x 1024, 32: 5.1 against 4.8).  16
+// fp32 tokens do not fit with 16 waves; 8 there against 4: 17.7, 22.2
+// (7168 x 7168).
+template <int W, int RC, int NF, int SG, bool F32X>
+constexpr int ring_depth() {
+  constexpr int n = (160 << 10) / (W * Slot<RC, NF, SG, F32X>::kBytes);
+  return n < 4 ? n : 4;
+}
+
+template <int W, int RC, int NF, int SG, bool F32X, bool GLU>
+hipError_t launch_sg(const W4Args& g, hipStream_t st) {
   constexpr int NB = GLU ? 8 * NF : 16 * NF;
-  // (a multiple of 8 along the weights: the token blocks of one set of rows run
-  // on the same XCD, whose L2 then serves the codes)
-  const dim3 grid((((GLU ? g.f : g.n) + NB - 1) / NB + 7) / 8 * 8, (g.T + RC - 1) / RC);
-  const int group = g.k / g.groups;
-  if (group == 32) w4_kernel<W, D, RC, NF, 1, F32X, GLU><<<grid, 64 * W, 0, st>>>(g);
-  else if (group == 64) w4_kernel<W, D, RC, NF, 2, F32X, GLU><<<grid, 64 * W, 0, st>>>(g);
-  else w4_kernel<W, D, RC, NF, 4, F32X, GLU><<<grid, 64 * W, 0, st>>>(g);   // a multiple of 128
+  w4_kernel<W, ring_depth<W, RC, NF, SG, F32X>(), RC, NF, SG, F32X, GLU>
+      <<<((GLU ? g.f : g.n) + NB - 1) / NB, 64 * W, 0, st>>>(g);
   return hipGetLastError();
+}
+template <int W, int RC, int NF, bool F32X, bool GLU>
+hipError_t launch(const W4Args& g, hipStream_t st) {
+  const int group = g.k / g.groups;
+  if (group == 32) return launch_sg<W, RC, NF, 1, F32X, GLU>(g, st);
+  if (group == 64) return launch_sg<W, RC, NF, 2, F32X, GLU>(g, st);
+  return launch_sg<W, RC, NF, 4, F32X, GLU>(g, st);   // a multiple of 128
 }
 template <int MB, bool F32X, bool GLU>
 hipError_t launch_tile(const W4Args& g, hipStream_t st) {
+  // (a multiple of 8 along the weights: the token blocks of one set of rows run
+  // on the same XCD, whose L2 then serves the codes)
   const dim3 grid(((g.n + 127) / 128 + 7) / 8 * 8, g.splits, (g.T + 16 * MB - 1) / (16 * MB));
   const int group = g.k / g.groups;
   if (group == 32) w4_tile<MB, 1, F32X><<<grid, 512, 0, st>>>(g);
@@ -666,9 +685,9 @@ int tile_splits(int n, int k, int T) {
 
 template <bool F32X, bool GLU>
 hipError_t launch_t(W4Args g, hipStream_t st) {
-  if (g.T <= 4) return launch<8, F32X ? 3 : 4, 4, 2, F32X, GLU>(g, st);
-  if (g.T <= 8) return launch<8, 2, 8, 2, F32X, GLU>(g, st);
-  if (g.T <= kFew) return launch<F32X ? 4 : 8, 2, 16, 2, F32X, GLU>(g, st);
+  if (g.T <= 4) return launch<16, 4, 2, F32X, GLU>(g, st);
+  if (g.T <= 8) return launch<16, 8, 2, F32X, GLU>(g, st);
+  if (g.T <= kFew) return launch<F32X ? 8 : 16, 16, 2, F32X, GLU>(g, st);
   const int T = g.T, nblk = (g.k + kBlk - 1) / kBlk;
   const size_t out = (size_t)(GLU ? g.f : g.n) * (g.out_f32 ? 4 : 2);
   for (int t = 0; t < T; t += kChunk) {

@@ -5,49 +5,66 @@ import ctypes
 
 import torch
 
-from . import BF16, F32, K3moeError, W4Matrix, current_stream, lib, on_device
+from . import BF16, F32, K3moeError, W4Matrix, lib, on_device
 
+_U8, _BF16 = torch.uint8, torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _run(call, half, x, codes, scale, zero, out_dtype, out, workspace, stream):
-    dev = x.device
-    if codes.dim() != 2 or scale.dim() != 2 or x.dim() != 2:
+    try:
+        (n, half_k), (T, k), (rows, groups) = codes.shape, x.shape, scale.shape
+    except ValueError:
+        n = half_k = T = k = rows = groups = 0
+    if 2 * half_k != k or rows != n or groups < 1 or k % groups:
         raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)} and scale "
-                         f"{tuple(scale.shape)} are [T][k], [n][k / 2] and [n][k / group]")
-    (n, bytes_), (T, k), groups = codes.shape, x.shape, scale.shape[1]
-    if 2 * bytes_ != k or scale.shape[0] != n or groups < 1 or k % groups:
-        raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)} and scale "
-                         f"{tuple(scale.shape)} do not fit each other")
-    if codes.dtype != torch.uint8 or scale.dtype != torch.bfloat16 or x.dtype not in _DT:
+                         f"{tuple(scale.shape)} are not [T][k], [n][k / 2] and [n][k / group]")
+    x_dtype = _DT.get(x.dtype)
+    if codes.dtype != _U8 or scale.dtype != _BF16 or x_dtype is None:
         raise TypeError(f"codes {codes.dtype}, scale {scale.dtype} and x {x.dtype} must be uint8, "
                         "bfloat16, and bfloat16 or float32")
-    if zero is not None and (zero.dtype != torch.uint8 or zero.shape != scale.shape):
+    if zero is not None and (zero.dtype != _U8 or zero.shape != scale.shape):
         raise TypeError(f"zero must be uint8 of scale's shape {tuple(scale.shape)}")
     cols = n // 2 if half else n
-    if out is None:
-        out = torch.empty((T, cols), dtype=x.dtype if out_dtype is None else out_dtype, device=dev)
-    elif tuple(out.shape) != (T, cols) or (out_dtype is not None and out.dtype != out_dtype):
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    o_dtype = _DT.get(out_dtype)
+    if o_dtype is None:
+        raise TypeError(f"the output is float32 or bfloat16, not {out_dtype}")
+    if out is not None and (out.shape != (T, cols) or out.dtype != out_dtype):
         raise ValueError(f"out must be {(T, cols)} {out_dtype}")
-    if out.dtype not in _DT:
-        raise TypeError(f"the output is float32 or bfloat16, not {out.dtype}")
-    same = dev == codes.device == scale.device == out.device and (zero is None or zero.device == dev)
-    if not same or dev.type != "cuda" or not (
-            x.is_contiguous() and codes.is_contiguous() and scale.is_contiguous()
-            and out.is_contiguous() and (zero is None or zero.is_contiguous())):
-        raise ValueError("the tensors must be contiguous and on one device")
+    index = x.get_device()
+    if index < 0 or codes.get_device() != index or scale.get_device() != index or not (
+            x.is_contiguous() and codes.is_contiguous() and scale.is_contiguous()) or \
+            not (zero is None or (zero.get_device() == index and zero.is_contiguous())) or \
+            not (out is None or (out.get_device() == index and out.is_contiguous())):
+        raise ValueError("the tensors must be contiguous and on one GPU")
     w = W4Matrix(n, k, k // groups, codes.data_ptr(), scale.data_ptr(),
                  None if zero is None else zero.data_ptr())
-    with on_device(dev, stream):
-        if workspace is None and T > 16:
-            workspace = torch.empty(lib.k3moe_w4_workspace_bytes(ctypes.byref(w), T),
-                                    dtype=torch.uint8, device=dev)
-        status = call(ctypes.byref(w), T, _DT[x.dtype], _DT[out.dtype], x.data_ptr(), out.data_ptr(),
-                      None if workspace is None else workspace.data_ptr(),
-                      0 if workspace is None else workspace.numel(), current_stream(dev))
+    if stream is None and torch.cuda.current_device() == index:
+        status, out = _launch(call, w, T, cols, x, x_dtype, out, out_dtype, o_dtype, workspace, index)
+    else:
+        with on_device(x.device, stream):
+            status, out = _launch(call, w, T, cols, x, x_dtype, out, out_dtype, o_dtype, workspace,
+                                  index)
     if status:
         raise K3moeError(status, lib.k3moe_last_error().decode())
     return out
+
+
+def _launch(call, w, T, cols, x, x_dtype, out, out_dtype, o_dtype, ws, index):
+    if out is None:
+        out = torch.empty((T, cols), dtype=out_dtype, device=x.device)
+    if T <= 16:
+        wp, wb = None, 0
+    else:
+        if ws is None:
+            ws = torch.empty(lib.k3moe_w4_workspace_bytes(ctypes.byref(w), T), dtype=_U8,
+                             device=x.device)
+        wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
+    return call(ctypes.byref(w), T, x_dtype, o_dtype, x.data_ptr(), out.data_ptr(), wp, wb,
+                _raw_stream(index)), out
 
 
 def w4_linear(x, codes, scale, zero=None, out_dtype=None, out=None, workspace=None, stream=None):
