@@ -225,7 +225,7 @@ __device__ __noinline__ void w4_slice_exact(const W4Args g, int blk0, int blk1, 
   }
 }
 
-// ---- the kernel.  A workgroup's W waves split the contraction in blocks of 128
+// ---- few tokens.  A workgroup's W waves split the contraction in blocks of 128
 // (wave w takes blocks w, w + W, ...); a wave copies its blocks into a ring of D
 // slots of its own by LDS-DMA, so that D blocks of every wave are in flight
 // whatever the registers hold, and no wave waits for another before the sum at
@@ -271,7 +271,7 @@ template <int W, int D, int RC, int NF, int SG, bool F32X, bool GLU>
 __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
   using L = Slot<RC, NF, SG, F32X>;
   constexpr int NB = GLU ? 8 * NF : 16 * NF;   // outputs per token
-  constexpr int XP = F32X ? 3 : 1;
+  constexpr int XP = F32X ? 3 : 1, MB = (RC + 15) / 16;   // fragments of tokens
   static_assert(!GLU || NF % 2 == 0, "gate and up fragments come in pairs");
   static_assert(RC * (16 * NF + 1) * 4 <= D * L::kBytes, "a wave's sums fit its ring");
   __shared__ __attribute__((aligned(16))) uint8_t ring[W][D * L::kBytes];
@@ -339,9 +339,12 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
     }
   };
 
-  f32x4_t acc[NF];
+  const f32x4_t nil = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[MB][NF];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[m][f] = nil;
   bf16x8_t ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
@@ -355,7 +358,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
     else wait_vmem<0>();
     const uint8_t* at = ring[wv] + slot * L::kBytes;
     uint32_t c[NF][4];
-    uint4 x[4][F32X ? 2 : 1];
+    uint4 x[MB][4][F32X ? 2 : 1];
     float sc[4 / SG][NF], off[4 / SG][NF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
@@ -371,12 +374,14 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
     }
     const int xr = ln & (RC - 1);   // (rows past RC repeat one of them)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int h = 0; h < (F32X ? 2 : 1); ++h) {
-        const int u = F32X ? 8 * j + 2 * lg + h : 4 * j + lg;
-        x[j][h] = *reinterpret_cast<const uint4*>(at + L::kX + xr * L::kRow + ((u ^ xr) << 4));
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < (F32X ? 2 : 1); ++h) {
+          const int u = F32X ? 8 * j + 2 * lg + h : 4 * j + lg;
+          x[m][j][h] = *reinterpret_cast<const uint4*>(at + L::kX + (m * 16 + xr) * L::kRow + ((u ^ xr) << 4));
+        }
     // the slot is in registers: its next block may come
     wait_lds();
     issue(blk + D * W, slot);
@@ -386,51 +391,78 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
 #pragma unroll
     for (int s = 0; s < 4 / SG; ++s) {
       if (blk * kBlk + s * SG * 32 >= g.k) break;
-      f32x4_t sum = {0.f, 0.f, 0.f, 0.f}, dot[NF];
+      f32x4_t sum[MB], dot[MB][NF];
 #pragma unroll
-      for (int f = 0; f < NF; ++f) dot[f] = sum;
+      for (int m = 0; m < MB; ++m) {
+        sum[m] = nil;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) dot[m][f] = nil;
+      }
 #pragma unroll
       for (int j = s * SG; j < (s + 1) * SG; ++j) {
-        bf16x8_t a[XP];
-        x_frags<F32X, false>(x[j], a);
+        bf16x8_t w[NF];
 #pragma unroll
-        for (int p = 0; p < XP; ++p) {
-          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], ones, sum, 0, 0, 0);
+        for (int f = 0; f < NF; ++f) w[f] = codes_biased(c[f][j]);
 #pragma unroll
-          for (int f = 0; f < NF; ++f)
-            dot[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], codes_biased(c[f][j]), dot[f], 0, 0, 0);
+        for (int m = 0; m < MB; ++m) {
+          bf16x8_t a[XP];
+          x_frags<F32X, false>(x[m][j], a);
+#pragma unroll
+          for (int p = 0; p < XP; ++p) {
+            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], ones, sum[m], 0, 0, 0);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+              dot[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w[f], dot[m][f], 0, 0, 0);
+          }
         }
       }
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
+      for (int m = 0; m < MB; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[f][r] = __builtin_fmaf(sc[s][f], __builtin_fmaf(off[s][f], sum[r], dot[f][r]), acc[f][r]);
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[m][f][r] = __builtin_fmaf(sc[s][f], __builtin_fmaf(off[s][f], sum[m][r], dot[m][f][r]),
+                                          acc[m][f][r]);
     }
   }
   bool bad = false;
 #pragma unroll
-  for (int f = 0; f < NF; ++f)
+  for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) bad |= lg * 4 + r < tn && !(fabsf(acc[f][r]) < INFINITY);
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        bad |= m * 16 + lg * 4 + r < tn && !(fabsf(acc[m][f][r]) < INFINITY);
   if (__any(bad)) {
     Rows<NF> rows;
     rows.lg = lg;
-    rows.tok = min(ln, tn - 1);
 #pragma unroll
     for (int f = 0; f < NF; ++f) rows.row[f] = weight_row(f * 16 + ln);
-    f32x4_t again[NF];   // (acc's own address would keep it out of registers)
-    w4_slice_exact<NF, SG, F32X>(g, wv, nblk, W, rows, again);
+#pragma unroll 1
+    for (int m = 0; m < MB; ++m) {
+      rows.tok = min(m * 16 + ln, tn - 1);
+      f32x4_t again[NF];   // (acc's own address would keep it out of registers)
+      w4_slice_exact<NF, SG, F32X>(g, wv, nblk, W, rows, again);
 #pragma unroll
-    for (int f = 0; f < NF; ++f) acc[f] = again[f];
+      for (int q = 0; q < MB; ++q)
+        if (q == m) {
+#pragma unroll
+          for (int f = 0; f < NF; ++f) acc[q][f] = again[f];
+        }
+    }
   }
   // ---- the waves' sums, each in its own ring (nothing is in flight to it any more)
   float* red = reinterpret_cast<float*>(ring[wv]);
 #pragma unroll
-  for (int f = 0; f < NF; ++f)
+  for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (lg * 4 + r < tn) red[(lg * 4 + r) * (16 * NF + 1) + f * 16 + ln] = acc[f][r];
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = m * 16 + lg * 4 + r;
+        if (t < tn) red[t * (16 * NF + 1) + f * 16 + ln] = acc[m][f][r];
+      }
   __syncthreads();
   for (int i = threadIdx.x; i < tn * NB; i += 64 * W) {
     const int t = i / NB, col = i - t * NB;
@@ -451,96 +483,142 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
   }
 }
 
-// ---- more than 16 tokens.  Here the activations are the larger operand of a
-// workgroup, so its 8 waves share them: wave w takes weight rows 16 w .. + 16 of
-// the workgroup's 128, for 16 MB tokens and one of g.splits pieces of the
-// contraction, whose fp32 sums w4_finish adds in order.  One ring of kStages slots
-// (x for all waves, each wave's codes and scales), one barrier a block.
-constexpr int kStages = 3;
+// ---- more tokens.  Here the activations are the larger operand of a workgroup, so
+// its 8 waves share them: 128 weight rows, 16 MB tokens and one of
+// g.splits pieces of the contraction, whose fp32 sums w4_finish adds in order.  A
+// step takes two blocks of 128: waves 0 .. 3 the first, 4 .. 7 the second, 32 rows
+// each, so that a fragment of x read from LDS and its sum serve two fragments of
+// weights; the two halves are added through LDS at the end.  One ring of steps, one
+// barrier a step.
+template <int MB, int SG, bool F32X>
+struct TileSlot {
+  static constexpr int kRow = F32X ? 512 : 256;        // bytes of x per token and block
+  static constexpr int XC = 16 * MB * kRow / 8192;     // copies of x per wave and block
+  static constexpr int kX = 8192, kBlock = kX + 16 * MB * kRow;   // codes, then x
+  // scales: [two blocks][4 / SG][128 rows] dwords, then zero the same
+  static constexpr int kVals = 2 * (4 / SG) * 128, kS = 2 * kBlock, kZ = kS + kVals * 4;
+  static constexpr int kBytes = kZ + kVals * 4;
+  static constexpr int kCopies = 2 * (1 + XC) + kVals / 256;
+  static constexpr int kStages = (160 << 10) / kBytes < 3 ? (160 << 10) / kBytes : 3;
+  static_assert(XC * 8192 == 16 * MB * kRow && kStages >= 2, "whole copies, two steps in LDS");
+};
 
 template <int MB, int SG, bool F32X>
 __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
-  using L = Slot<16 * MB, 8, SG, F32X>;   // 8 fragments of rows: one a wave
-  constexpr int XC = L::NX / 8, XP = F32X ? 3 : 1, kCopies = XC + 3;
-  static_assert(XC * 8 == L::NX && L::kRow >= 256, "whole copies");
-  // (the scales of wave w: 4 / SG x 16 dwords at 256 w)
-  constexpr int kS = L::kS, kZ = kS + 2048, kBytes = kZ + 2048;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[kStages * kBytes];
+  using L = TileSlot<MB, SG, F32X>;
+  constexpr int XP = F32X ? 3 : 1, kStages = L::kStages;
+  constexpr int kRed = 132;   // (a row of the sums; 4 rows apart: 16 banks)
+  static_assert(16 * MB * kRed * 4 <= kStages * L::kBytes, "the sums fit the ring");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kStages * L::kBytes];
   const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wk = wv >> 2, wn = wv & 3;
   const int t0 = blockIdx.z * (16 * MB), n0 = blockIdx.x * 128, tn = min(16 * MB, g.T - t0);
   if (n0 >= g.n) return;
   const int nblk = (g.k + kBlk - 1) / kBlk;
   const int b0 = blockIdx.y * g.per_split, b1 = min(b0 + g.per_split, nblk);
-  const int row_lo = min(n0 + wv * 16, g.n - 1);   // rows past the last: read as it, not stored
+  const int steps = (b1 - b0 + 1) >> 1;
+  const int last = g.n - 1 - n0;   // rows past it: read as it, not stored
   const int kb = g.k >> 1;
   const int cr = lane >> 2, ck = ((lane & 3) ^ code_swz(cr)) * 32;
-  const uint32_t oc = (uint32_t)(min(row_lo + cr, g.n - 1) - row_lo) * (uint32_t)kb;
-  uint32_t ox[XC];
-  int kx[XC];
+  const uint32_t oc = (uint32_t)min(wv * 16 + cr, last) * (uint32_t)kb;
+  uint32_t ox[L::XC];
+  int kx[L::XC];
 #pragma unroll
-  for (int c = 0; c < XC; ++c) {
+  for (int c = 0; c < L::XC; ++c) {
     constexpr int U = L::kRow / 16;
-    const int i = (wv * XC + c) * 64 + lane, r = i / U, u = (i % U) ^ (r & 15);
+    const int i = (wv * L::XC + c) * 64 + lane, r = i / U, u = (i % U) ^ (r & 15);
     kx[c] = u * (F32X ? 4 : 8);
     ox[c] = (uint32_t)min(r, tn - 1) * (uint32_t)g.k;
   }
-  const int sv = min(lane >> 4, 4 / SG - 1);
-  const uint32_t os = (uint32_t)(min(row_lo + ln, g.n - 1) - row_lo) * (uint32_t)g.groups;
-  const uint8_t* const zeros = g.zero ? g.zero : reinterpret_cast<const uint8_t*>(g.scale);
+  const uint8_t* const codes = g.codes + (size_t)n0 * kb;
+  const uint16_t* const scale = g.scale + (size_t)n0 * g.groups;
+  const uint8_t* const zero = g.zero ? g.zero + (size_t)n0 * g.groups
+                                     : reinterpret_cast<const uint8_t*>(scale);
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring;
-  auto issue = [&](int b, int slot) {
-    if (b >= b1) return;
-    const int k0 = b * kBlk;
-    const uint32_t to = __builtin_amdgcn_readfirstlane(base + slot * kBytes);
-    dma_b128(g.codes + (size_t)row_lo * kb + (k0 >> 1), oc + (uint32_t)(min(ck, g.k - 32 - k0) >> 1),
-             to + wv * 1024);
-    const uint8_t* x = static_cast<const uint8_t*>(g.x) + ((size_t)t0 * g.k + k0) * (F32X ? 4 : 2);
+  auto issue = [&](int step, int slot) {
+    if (step >= steps) return;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(base + slot * L::kBytes);
+    // (an odd piece's second block: its last again, which no wave uses)
+    auto block = [&](int h) { return min(b0 + 2 * step + h, b1 - 1); };
 #pragma unroll
-    for (int c = 0; c < XC; ++c)
-      dma_b128(x, (ox[c] + (uint32_t)min(kx[c], g.k - (F32X ? 4 : 8) - k0)) * (F32X ? 4 : 2),
-               to + L::kX + (wv * XC + c) * 1024);
-    const uint32_t o = os + (uint32_t)(SG < 4 ? min(b * (4 / SG) + sv, g.groups - 1)
-                                              : group_of<SG>(g, b, 0));
-    dma_u16(g.scale + (size_t)row_lo * g.groups, o * 2, to + kS + wv * 256);
-    dma_u8(zeros + (size_t)row_lo * g.groups, o, to + kZ + wv * 256);
+    for (int h = 0; h < 2; ++h) {
+      const int k0 = block(h) * kBlk;
+      dma_b128(codes + (k0 >> 1), oc + (uint32_t)(min(ck, g.k - 32 - k0) >> 1),
+               to + h * L::kBlock + wv * 1024);
+      const uint8_t* x = static_cast<const uint8_t*>(g.x) + ((size_t)t0 * g.k + k0) * (F32X ? 4 : 2);
+#pragma unroll
+      for (int c = 0; c < L::XC; ++c)
+        dma_b128(x, (ox[c] + (uint32_t)min(kx[c], g.k - (F32X ? 4 : 8) - k0)) * (F32X ? 4 : 2),
+                 to + h * L::kBlock + L::kX + (wv * L::XC + c) * 1024);
+    }
+    // scales and zeros, 64 of one block's and group's a copy: with 4 copies of each
+    // waves 0 .. 3 make the scales', the others the zeros'
+    auto value = [&](int c, bool z) {
+      const int q = c >> 1, b = block(q / (4 / SG)), s = q % (4 / SG);
+      const uint32_t o = (uint32_t)min((c & 1) * 64 + lane, last) * (uint32_t)g.groups +
+                         (uint32_t)group_of<SG>(g, b, s);
+      if (z) dma_u8(zero, o, to + L::kZ + c * 256);
+      else dma_u16(scale, o * 2, to + L::kS + c * 256);
+    };
+    if constexpr (L::kVals == 256) {
+      if (wv < 4) value(wv, false);
+      else value(wv - 4, true);
+    } else {
+#pragma unroll
+      for (int c = 0; c < L::kVals / 512; ++c) {
+        value(wv + 8 * c, false);
+        value(wv + 8 * c, true);
+      }
+    }
   };
   const f32x4_t nil = {0.f, 0.f, 0.f, 0.f};
-  f32x4_t acc[MB];
+  f32x4_t acc[2][MB];
 #pragma unroll
-  for (int m = 0; m < MB; ++m) acc[m] = nil;
+  for (int m = 0; m < MB; ++m) acc[0][m] = acc[1][m] = nil;
   bf16x8_t ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 #pragma unroll
-  for (int q = 0; q < kStages - 1; ++q) issue(b0 + q, q);
+  for (int q = 0; q < kStages - 1; ++q) issue(q, q);
   int slot = 0;
 #pragma unroll 1
-  for (int blk = b0; blk < b1; ++blk) {
-    // this wave's copies of the block have landed and its reads of the one
+  for (int step = 0; step < steps; ++step) {
+    // this wave's copies of the step have landed and its reads of the one
     // before are done; past the barrier both hold for every wave
     wait_lds();
-    if (blk + kStages - 2 < b1) wait_vmem<(kStages - 2) * kCopies>();
+    if (step + kStages - 2 < steps) wait_vmem<(kStages - 2) * L::kCopies>();
     else wait_vmem<0>();
     grouped::wg_barrier();
-    issue(blk + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
-    const uint8_t* at = ring + slot * kBytes;
+    issue(step + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+    const uint8_t* const vals = ring + slot * L::kBytes;
+    const uint8_t* const at = vals + wk * L::kBlock;
     slot = slot == kStages - 1 ? 0 : slot + 1;
-    const uint4 v = *reinterpret_cast<const uint4*>(at + wv * 1024 + ln * 64 + ((lg ^ code_swz(ln)) << 4));
-    uint32_t c[4] = {v.x, v.y, v.z, v.w};
-    transpose4(c);
+    const int blk = b0 + 2 * step + wk;
+    if (blk >= b1) continue;
+    uint32_t c[2][4];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const uint4 v = *reinterpret_cast<const uint4*>(at + (wn * 2 + f) * 1024 + ln * 64 +
+                                                      ((lg ^ code_swz(ln)) << 4));
+      c[f][0] = v.x; c[f][1] = v.y; c[f][2] = v.z; c[f][3] = v.w;
+      transpose4(c[f]);
+    }
 #pragma unroll
     for (int s = 0; s < 4 / SG; ++s) {
       if (blk * kBlk + s * SG * 32 >= g.k) break;
-      const int i = wv * 256 + (s * 16 + ln) * 4;
-      const float sc = bf16_lo(*reinterpret_cast<const uint32_t*>(at + kS + i));
-      const float off = -(float)(16 + (g.zero ? *reinterpret_cast<const int*>(at + kZ + i) : 8));
-      f32x4_t sum[MB], dot[MB];
+      float sc[2], off[2];
 #pragma unroll
-      for (int m = 0; m < MB; ++m) sum[m] = dot[m] = nil;
+      for (int f = 0; f < 2; ++f) {
+        const int i = ((wk * (4 / SG) + s) * 128 + wn * 32 + f * 16 + ln) * 4;
+        sc[f] = bf16_lo(*reinterpret_cast<const uint32_t*>(vals + L::kS + i));
+        off[f] = -(float)(16 + (g.zero ? *reinterpret_cast<const int*>(vals + L::kZ + i) : 8));
+      }
+      f32x4_t sum[MB], dot[2][MB];
+#pragma unroll
+      for (int m = 0; m < MB; ++m) sum[m] = dot[0][m] = dot[1][m] = nil;
 #pragma unroll
       for (int j = s * SG; j < (s + 1) * SG; ++j) {
-        const bf16x8_t w = codes_biased(c[j]);
+        const bf16x8_t w[2] = {codes_biased(c[0][j]), codes_biased(c[1][j])};
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
           uint4 xv[F32X ? 2 : 1];
@@ -554,44 +632,70 @@ __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
 #pragma unroll
           for (int p = 0; p < XP; ++p) {
             sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], ones, sum[m], 0, 0, 0);
-            dot[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w, dot[m], 0, 0, 0);
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+              dot[f][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], w[f], dot[f][m], 0, 0, 0);
           }
         }
       }
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+      for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[m][r] = __builtin_fmaf(sc, __builtin_fmaf(off, sum[m][r], dot[m][r]), acc[m][r]);
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[f][m][r] = __builtin_fmaf(sc[f], __builtin_fmaf(off[f], sum[m][r], dot[f][m][r]),
+                                          acc[f][m][r]);
     }
   }
   bool bad = false;
 #pragma unroll
-  for (int m = 0; m < MB; ++m)
+  for (int f = 0; f < 2; ++f)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) bad |= m * 16 + lg * 4 + r < tn && !(fabsf(acc[m][r]) < INFINITY);
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        bad |= m * 16 + lg * 4 + r < tn && !(fabsf(acc[f][m][r]) < INFINITY);
   if (__any(bad)) {
 #pragma unroll 1
     for (int m = 0; m < MB; ++m) {
-      Rows<1> rows;
+      Rows<2> rows;
       rows.lg = lg;
       rows.tok = t0 + min(m * 16 + ln, tn - 1);
-      rows.row[0] = min(row_lo + ln, g.n - 1);
-      f32x4_t again[1];
-      w4_slice_exact<1, SG, F32X>(g, b0, b1, 1, rows, again);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) rows.row[f] = n0 + min(wn * 32 + f * 16 + ln, last);
+      f32x4_t again[2];
+      w4_slice_exact<2, SG, F32X>(g, b0 + wk, b1, 2, rows, again);
 #pragma unroll
       for (int q = 0; q < MB; ++q)
-        if (q == m) acc[q] = again[0];
+        if (q == m) { acc[0][q] = again[0]; acc[1][q] = again[1]; }
     }
   }
-  const int n = n0 + wv * 16 + ln;
-  if (n >= g.n) return;
+  // ---- the two halves: each wave hands over half of its tokens' sums and adds the
+  // other's to the half it keeps (no copy is in flight into the ring any more)
+  float* const red = reinterpret_cast<float*>(ring);
+  __syncthreads();
 #pragma unroll
   for (int m = 0; m < MB; ++m)
+    if ((m < MB / 2) == (wk == 1)) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = m * 16 + lg * 4 + r;
-      if (t < tn) g.part[((size_t)blockIdx.y * g.T + t0 + t) * g.n + n] = acc[m][r];
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          red[(m * 16 + lg * 4 + r) * kRed + wn * 32 + f * 16 + ln] = acc[f][m][r];
+    }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+    if ((m < MB / 2) == (wk == 0)) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = m * 16 + lg * 4 + r, n = wn * 32 + f * 16 + ln;
+          if (t < tn && n <= last)
+            g.part[((size_t)blockIdx.y * g.T + t0 + t) * g.n + n0 + n] = acc[f][m][r] + red[t * kRed + n];
+        }
     }
 }
 
@@ -668,19 +772,33 @@ hipError_t launch_tile(const W4Args& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Up to 16 tokens a workgroup has all of them; beyond, the tiled kernel takes
-// kChunk tokens at a time (so that its partial sums stay bounded).
+// Up to 16 tokens a workgroup always has all of them; the tiled kernel takes kChunk
+// tokens at a time (so that its partial sums stay bounded).
 constexpr int kFew = 16, kChunk = 256;
 
-// Pieces of the contraction for a chunk of T tokens: at most one workgroup a CU (a
-// second round of a few workgroups costs as much as the first), at least two
-// blocks a piece.
-int tile_splits(int n, int k, int T) {
+// Blocks of a piece of the contraction for a chunk of T tokens, a whole number of
+// steps: at most one workgroup a CU (a second round of a few workgroups costs as
+// much as the first).
+int tile_piece(int n, int k, int T) {
   const int64_t wgs = (int64_t)((n + 127) / 128) * ((T + 63) / 64);
-  const int nblk = (k + kBlk - 1) / kBlk;
-  const int64_t s = std::min<int64_t>(std::max<int64_t>(256 / wgs, 1), std::max(nblk / 2, 1));
-  const int per = (int)((nblk + s - 1) / s);
-  return (nblk + per - 1) / per;
+  const int64_t pairs = (k + 2 * kBlk - 1) / (2 * kBlk), s = std::max<int64_t>(256 / wgs, 1);
+  return (int)((pairs + s - 1) / s * 2);
+}
+int tile_splits(int n, int k, int T) {
+  const int per = tile_piece(n, k, T) * kBlk;
+  return (k + per - 1) / per;
+}
+
+// Up to 64 tokens (fp32: 32) may still go without a split contraction, whose
+// partial sums and second launch cost 5 us: 32 weight rows a workgroup, which reads
+// all of x.  It pays where those workgroups run in one round of the 256 CUs and x
+// is short against what the split form writes, some n T sums (us, this form against
+// the split one; 32 tokens x 4096: n 512 7.7, 7.8; 8192 10.2, 14.1; 8448 17.6, 16.1;
+// 64 x 4096: n 512 11.6, 9.5; 3584 12.4, 14.1; 8192 15.2, 19.7; 64 x 7168: n 1024
+// 16.9, 13.2; 8192 23.3, 24.1; 32 fp32 x 4096: n 2048 15.1, 11.4; 8192 18.2, 21.0).
+bool one_round(const W4Args& g, bool x_f32) {
+  const int64_t T = g.T <= 32 ? 32 : 64, x = T * g.k * (x_f32 ? 4 : 2);
+  return g.T <= (x_f32 ? 32 : 64) && g.n <= 256 * 32 && x <= (256 << 10) + 64 * (int64_t)g.n;
 }
 
 template <bool F32X, bool GLU>
@@ -688,7 +806,11 @@ hipError_t launch_t(W4Args g, hipStream_t st) {
   if (g.T <= 4) return launch<16, 4, 2, F32X, GLU>(g, st);
   if (g.T <= 8) return launch<16, 8, 2, F32X, GLU>(g, st);
   if (g.T <= kFew) return launch<F32X ? 8 : 16, 16, 2, F32X, GLU>(g, st);
-  const int T = g.T, nblk = (g.k + kBlk - 1) / kBlk;
+  if (one_round(g, F32X)) {
+    if (g.T <= 32) return launch<8, 32, 2, F32X, GLU>(g, st);
+    if constexpr (!F32X) return launch<8, 64, 2, F32X, GLU>(g, st);
+  }
+  const int T = g.T;
   const size_t out = (size_t)(GLU ? g.f : g.n) * (g.out_f32 ? 4 : 2);
   for (int t = 0; t < T; t += kChunk) {
     W4Args c = g;
@@ -696,7 +818,7 @@ hipError_t launch_t(W4Args g, hipStream_t st) {
     c.x = static_cast<const uint8_t*>(g.x) + (size_t)t * g.k * (F32X ? 4 : 2);
     c.out = static_cast<uint8_t*>(g.out) + (size_t)t * out;
     c.splits = tile_splits(g.n, g.k, c.T);
-    c.per_split = (nblk + c.splits - 1) / c.splits;
+    c.per_split = tile_piece(g.n, g.k, c.T);
     const hipError_t e = F32X || c.T <= 32 ? launch_tile<2, F32X, GLU>(c, st)
                                            : launch_tile<F32X ? 2 : 4, F32X, GLU>(c, st);
     if (e != hipSuccess) return e;

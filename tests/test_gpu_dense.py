@@ -490,3 +490,131 @@ def test_captured_and_replayed_on_other_streams():
         want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want)), i
+
+
+# ------------------------------------------------------- where forms change
+@pytest.mark.parametrize("xd", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("T", [4, 8, 9, 16, 32, 64, 70, 128, 200])
+def test_w4_at_the_token_counts_where_the_form_changes(T, group, xd):
+    """Both sides of each change of kernel, with a last block and a last weight
+    row inside a tile and a contraction whose split pieces are uneven."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_linear
+    n, k = 131, 5 * 256 + group
+    for t in (T, T + 1):
+        x, codes, scale, z = w4_problem(t, n, k, group, group != 64, xd, 100 + t)
+        want, tol = w4_bounds(x, codes, scale, z)
+        log(f"case T={t} group={group} {xd}")
+        room = torch.full((t * n + 64,), 7.0, device="cuda")   # (out: 16-byte aligned)
+        out = room[32:-32].view(t, n)
+        w4_linear(x, codes, scale, z, out=out)
+        torch.cuda.synchronize()
+        within(out, want, rounded(want, tol, torch.float32), 0, "linear")
+        assert (room[:32] == 7).all() and (room[-32:] == 7).all()
+
+
+@pytest.mark.parametrize("n", [8192, 8224])
+def test_w4_on_both_sides_of_one_round_of_workgroups(n):
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_glu
+    x, codes, scale, z = w4_problem(40, n, 512, 128, True, torch.bfloat16, 120)
+    want, tol = w4_bounds(x, codes, scale, z)
+    f = n // 2
+    g, u, ge, ue = want[:, :f], want[:, f:], tol[:, :f], tol[:, f:]
+    sil = g * torch.sigmoid(g)
+    h = sil * u
+    e = 1.1 * ge * u.abs() + (sil.abs() + 1.1 * ge) * ue + 16 * S24 * h.abs()
+    got = w4_glu(x, codes, scale, z)
+    torch.cuda.synchronize()
+    within(got, h, rounded(h, e), 0, "glu")
+
+
+@pytest.mark.parametrize("xd", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,n,k", [(20, 48, 512), (50, 48, 512), (70, 48, 768), (140, 260, 768)])
+def test_w4_special_values_in_larger_batches(T, n, k, xd):
+    """As for few tokens: a value that is not finite reaches its own token's (or
+    weight row's) outputs alone."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_linear
+    x, codes, scale, z = w4_problem(T, n, k, 128, True, xd, 130)
+    codes[0, :], codes[1, :] = 0xFF, 0x00
+    z[:] = 8
+    x[T - 1, 10] = float("inf")
+    x[T - 2, k - 1] = float("-inf")
+    x[0, 300] = float("nan")
+    x[17, 7] = torch.finfo(xd).max    # finite, but 16 times it is not
+    x[17, 8:] = 0
+    scale[n - 1, 2] = float("inf")
+    scale[6, 1] = float("nan")
+    got = w4_linear(x, codes, scale, z, out_dtype=torch.float32).cpu()
+    w, _ = w4_dense(codes.cpu(), scale.cpu(), z.cpu())
+    want = torch.stack([(row.to(F8) * w).sum(1) for row in x.cpu()])
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert inf.any() and torch.equal(got[inf].to(F8), want[inf])
+    fine = torch.isfinite(want) & (want.abs() < 3e38)
+    mag = (x.cpu().to(F8).abs().nan_to_num(0, 0, 0) @ w.abs().nan_to_num(0, 0, 0).t())
+    assert ((got.to(F8) - want).abs()[fine] <= 1e-4 * mag[fine]).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F4])
+def test_clip_with_the_norm_joined_in_a_launch_of_its_own(dt):
+    """A list of so many pieces that the scaling does not join them itself."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.grads import clip_grads
+    ts = grad_list([60_000_000] + [129 + i for i in range(250)], [dt] * 251, 1, 140)
+    want = norm64(ts)
+    outs = [torch.empty_like(t) for t in ts]
+    got = clip_grads(ts, want / 4, out=outs)
+    assert abs(float(got) - want) <= S24 * want * 1.001
+    for t, o in zip(ts, outs):
+        exact = t.to(F8) * 0.25   # the factor's, the product's and the output's rounding
+        eps = 3 * S24 + (B if dt == BF else 0.0)
+        assert ((o.to(F8) - exact).abs() <= eps * exact.abs() * 1.001).all()
+
+
+def test_a_given_stream_and_workspaces_of_one_graph_beside_another():
+    """Calls on a stream that is not current, and two graphs whose calls were given
+    one workspace, replayed in turn."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.grads import clip_grads, grad_norm
+    from mxfp4_routed_expert_gemv_amd.shared import shared_ffn_backward, shared_ffn_train
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_glu, w4_linear
+    T, d, fs, S = 70, 256, 64, 1
+    x, w13, w2 = problem(T, d, fs, S, 150)
+    wx, codes, scale, z = w4_problem(T, 64, 2048, 64, True, torch.bfloat16, 155)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def step(workspace=None, stream=None):
+        y, gu = shared_ffn_train(x, w13, w2, workspace=workspace, stream=stream)
+        grads = shared_ffn_backward(x, gu, y, w13, w2, workspace=workspace, stream=stream)
+        more = [w4_linear(wx, codes, scale, z, workspace=workspace, stream=stream),
+                w4_glu(wx, codes, scale, z, workspace=workspace, stream=stream)]
+        outs = [torch.empty_like(g) for g in grads]
+        return [y, gu, *grads, *more, grad_norm(grads, stream=stream),
+                clip_grads(grads, 0.1, out=outs, stream=stream), *outs]
+
+    def same(a, b):
+        return all(torch.equal(p, q) for p, q in zip(a, b))
+    eager = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = step(stream=side)
+    side.synchronize()
+    assert same(eager, other)
+    graphs, held = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(step(ws))
+        graphs.append(g)
+    for i in range(3):
+        x.copy_(normal((T, d), 160 + i))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        assert same(held[0], want) and same(held[1], want), i
