@@ -194,6 +194,8 @@ def on_device(device, stream=None):
     if stream is not None:
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device)
+        if stream.device_index != device.index:
+            raise ValueError(f"a stream of GPU {stream.device_index} for tensors on {device}")
         return torch.cuda.stream(stream)
     return (contextlib.nullcontext() if torch.cuda.current_device() == device.index
             else torch.cuda.device(device))
@@ -321,7 +323,7 @@ def k3moe_grad_workspace_bytes(n: int) -> int:
 
 
 def k3moe_grad_norm(tensors, n, norm, workspace=None, stream=None):
-    """tensors: a ctypes array of Tensor, or the host address of such a list."""
+    """tensors: a ctypes array of Tensor, or bytes that hold such a list."""
     wp, wb = _ws(workspace)
     _check(lib.k3moe_grad_norm(tensors, n, _addr(norm), wp, wb, _stream(stream)))
 

@@ -1,9 +1,9 @@
 """The global gradient norm and clipping (k3moe_grad_norm, k3moe_grad_clip) on
 lists of torch tensors.  Every computation happens in libk3moe's kernels; this
 file only marshals."""
-from array import array
 from itertools import chain
 from operator import attrgetter
+from struct import pack
 
 import torch
 
@@ -15,10 +15,11 @@ _dtype, _shape, _T = attrgetter("dtype"), attrgetter("shape"), torch.Tensor
 
 
 def _types(tensors):
-    try:
-        return [_DT[t] for t in map(_dtype, tensors)]
-    except KeyError as e:
-        raise TypeError(f"gradients are float32 or bfloat16, not {e.args[0]}") from None
+    types = list(map(_DT.get, map(_dtype, tensors)))
+    if None in types:
+        raise TypeError("gradients are float32 or bfloat16, not "
+                        f"{tensors[types.index(None)].dtype}")
+    return types
 
 
 def _call(run, tensors, outs, stream):
@@ -44,12 +45,12 @@ def _call(run, tensors, outs, stream):
             not all(map(_T.is_contiguous, every)):
         raise ValueError("the tensors must be contiguous and on one device")
     # the k3moe_tensor list: four words a tensor, the two types in the last
-    words = array("q", chain.from_iterable(zip(pointers, to, map(_T.numel, tensors), types)))
     n = len(tensors)
+    words = pack(f"{4 * n}q", *chain.from_iterable(zip(pointers, to, map(_T.numel, tensors), types)))
     with on_device(dev, stream):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         ws = torch.empty(k3moe_grad_workspace_bytes(n), dtype=torch.uint8, device=dev)
-        run(words.buffer_info()[0], n, norm, ws, current_stream(dev))
+        run(words, n, norm, ws, current_stream(dev))
     return norm
 
 

@@ -217,3 +217,12 @@ def test_python_checks():
         grads.clip_grads([x], 1.0, out=[x, x])
     with pytest.raises(ValueError):
         grads.clip_grads([x], 1.0, out=[x[:2]])
+
+
+def test_a_stream_of_another_device_is_refused():
+    import types
+
+    import torch
+    from mxfp4_routed_expert_gemv_amd import on_device
+    with pytest.raises(ValueError, match="stream of GPU 1"):
+        on_device(torch.device("cuda", 0), types.SimpleNamespace(device_index=1))
