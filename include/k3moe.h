@@ -473,7 +473,9 @@ k3moe_status k3moe_shared_ffn_train(const k3moe_shape* shape, const k3moe_expert
                                     size_t workspace_bytes, void* stream);
 /* x and gu of the forward and dy [T][d] bf16 -> dx [T][d], dw13 [n_shared][2
  * f_shared][d] and dw2 [n_shared][d][f_shared], all bf16 and overwritten.  An
- * output that is NULL is not computed (all three NULL: nothing is enqueued).
+ * output that is NULL is not computed (all three NULL: nothing is enqueued), and
+ * which ones are asked for, or other tokens, can change the order of a sum and so
+ * its last bits; the same call gives the same bits.
  * T = 0 writes zeros to dw13 and dw2.  The outputs must not overlap the inputs
  * or each other.  Errors: as for k3moe_shared_ffn_train.
  * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_SHARED_BACKWARD). */
@@ -511,8 +513,10 @@ typedef struct k3moe_w4_matrix {
 /* Workspace of the two calls below (0, where NULL is accepted, up to 16 tokens,
  * and for invalid arguments); 256-byte aligned. */
 size_t k3moe_w4_workspace_bytes(const k3moe_w4_matrix* w, int64_t T);
-/* out [T][n] = x W^T.  Errors: EINVAL (NULL pointers, negative sizes), ESHAPE,
- * EUNSUPPORTED, EALIGN, EWORKSPACE. */
+/* out [T][n] = x W^T.  Errors: EINVAL (NULL pointers, negative sizes, an out that
+ * overlaps x or W), ESHAPE, EUNSUPPORTED, EALIGN (out is 16-byte aligned too),
+ * EWORKSPACE.  The order of a token's sums, and so its last bits, can depend on T;
+ * the same call gives the same bits. */
 k3moe_status k3moe_w4_linear(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
                              int32_t out_dtype, const void* x, void* out, void* workspace,
                              size_t workspace_bytes, void* stream);
@@ -549,8 +553,8 @@ k3moe_status k3moe_grad_norm(const k3moe_tensor* tensors, int32_t n, float* norm
 /* The same norm, and out = data * min(1, max_norm / norm) for every tensor,
  * rounded to out_dtype.  The factor comes from the fp64 norm (finite gradients
  * are clipped even where *norm is past fp32's range); a norm of infinities or
- * NaN scales nothing (out = data), and the caller sees it in *norm.  In place (out == data) a step that needs no
- * clipping is left untouched.  Errors: as above; EINVAL also for a max_norm
+ * NaN scales nothing (out = data), and the caller sees it in *norm.  In place
+ * (out == data) a step that needs no clipping is left untouched.  Errors: as above; EINVAL also for a max_norm
  * that is negative or NaN and for an out that overlaps any tensor but its own
  * data. */
 k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_norm, float* norm,

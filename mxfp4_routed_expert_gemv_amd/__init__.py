@@ -209,6 +209,12 @@ def _ws(ws):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def check_workspace(ws, device_index):
+    """Refuses a workspace tensor whose bytes a kernel on that device cannot use."""
+    if not isinstance(ws, tuple) and (ws.get_device() != device_index or not ws.is_contiguous()):
+        raise ValueError("the workspace must be a contiguous tensor on the operands' GPU")
+
+
 def _check(status):
     if status != 0:
         raise K3moeError(status, lib.k3moe_last_error().decode())

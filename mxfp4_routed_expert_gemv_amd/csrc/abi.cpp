@@ -192,6 +192,22 @@ k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_
                     const void* x, void* out, void* workspace, size_t workspace_bytes, void* stream,
                     bool glu);
 
+// out must not touch what other workgroups still read.
+k3moe_status check_w4_out(const k3moe_w4_matrix& w, size_t x_bytes, const void* x,
+                          const void* out, size_t out_bytes) {
+  const size_t scales = (size_t)w.n * (w.k / w.group);
+  const struct { const void* p; size_t bytes; const char* name; } in[] = {
+      {x, x_bytes, "x"}, {w.codes, (size_t)w.n * (w.k / 2), "codes"},
+      {w.scale, 2 * scales, "scale"}, {w.zero, w.zero ? scales : 0, "zero"}};
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out);
+  for (const auto& i : in) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(i.p);
+    if (i.bytes && o < a + i.bytes && a < o + out_bytes)
+      return fail(K3MOE_EINVAL, "out overlaps %s", i.name);
+  }
+  return K3MOE_OK;
+}
+
 constexpr int kMaxTensors = 1 << 20;
 
 struct Span {
@@ -390,6 +406,8 @@ k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_
   K3_CHECK(need_ptr(x, "x"));
   K3_CHECK(need_ptr(out, "out"));
   K3_CHECK(check_ws(workspace, workspace_bytes, align256(w4_part_floats(*w, T) * sizeof(float))));
+  K3_CHECK(check_w4_out(*w, (size_t)T * w->k * (x_dtype == K3MOE_F32 ? 4 : 2), x, out,
+                        (size_t)T * (glu ? w->n / 2 : w->n) * (out_dtype == K3MOE_F32 ? 4 : 2)));
   return hip_status(launch_w4(*w, T, x_dtype == K3MOE_F32, out_dtype == K3MOE_F32, glu, x, out,
                               static_cast<float*>(workspace), static_cast<hipStream_t>(stream)),
                     glu ? "k3moe_w4_glu launch" : "k3moe_w4_linear launch");

@@ -8,9 +8,9 @@ from functools import lru_cache
 
 import torch
 
-from . import (BF16, F32, FMT_BF16, OP_SHARED_BACKWARD, OP_SHARED_TRAIN, current_stream,
-               k3moe_shared_ffn_backward, k3moe_shared_ffn_train, k3moe_workspace_bytes, make_bank,
-               make_shape, on_device)
+from . import (BF16, F32, FMT_BF16, OP_SHARED_BACKWARD, OP_SHARED_TRAIN, check_workspace,
+               current_stream, k3moe_shared_ffn_backward, k3moe_shared_ffn_train,
+               k3moe_workspace_bytes, make_bank, make_shape, on_device)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -56,6 +56,8 @@ def shared_ffn_train(x, w13, w2, out_dtype=torch.bfloat16, workspace=None, strea
         if T:
             if workspace is None:
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            else:
+                check_workspace(workspace, dev.index)
             k3moe_shared_ffn_train(shape, bank, x, gu, y, workspace, current_stream(dev))
     return y, gu
 
@@ -73,6 +75,8 @@ def shared_ffn_backward(x, gu, dy, w13, w2, need=(True, True, True), workspace=N
         dw2 = torch.empty_like(w2) if need[2] else None
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:
+            check_workspace(workspace, dev.index)
         # (an empty tensor's address may be NULL: for T = 0 nothing is read or written there)
         k3moe_shared_ffn_backward(shape, bank, x, gu, dy, dx if T else None, dw13, dw2, workspace,
                                   current_stream(dev))

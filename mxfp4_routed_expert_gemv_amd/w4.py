@@ -5,7 +5,7 @@ import ctypes
 
 import torch
 
-from . import BF16, F32, K3moeError, W4Matrix, lib, on_device
+from . import BF16, F32, K3moeError, W4Matrix, check_workspace, lib, on_device
 
 _U8, _BF16 = torch.uint8, torch.bfloat16
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -62,6 +62,8 @@ def _launch(call, w, T, cols, x, x_dtype, out, out_dtype, o_dtype, ws, index):
         if ws is None:
             ws = torch.empty(lib.k3moe_w4_workspace_bytes(ctypes.byref(w), T), dtype=_U8,
                              device=x.device)
+        else:
+            check_workspace(ws, index)
         wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
     return call(ctypes.byref(w), T, x_dtype, o_dtype, x.data_ptr(), out.data_ptr(), wp, wb,
                 _raw_stream(index)), out

@@ -221,8 +221,29 @@ def test_python_checks():
 
 def test_a_stream_of_another_device_is_refused():
     import types
-
-    import torch
     from mxfp4_routed_expert_gemv_amd import on_device
     with pytest.raises(ValueError, match="stream of GPU 1"):
         on_device(torch.device("cuda", 0), types.SimpleNamespace(device_index=1))
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_w4_out_must_not_overlap_what_is_read(glu):
+    fn = k3.lib.k3moe_w4_glu if glu else k3.lib.k3moe_w4_linear
+    far = [FAKE + (i << 24) for i in range(5)]
+    T, n, k = 4, 64, 256
+
+    def call(x, codes, scale, zero, out, out_dtype):
+        w = k3.make_w4(n, k, 128, codes, scale, zero)
+        return fn(ctypes.byref(w), T, k3.BF16, out_dtype, x, out, None, 0, None)
+    for od, size in ((k3.BF16, 2), (k3.F32, 4)):
+        bytes_out = T * (n // 2 if glu else n) * size
+        for i, extent in enumerate((T * k * 2, n * k // 2, n * 2 * 2, n * 2)):
+            for at in (far[i], far[i] + extent - 16, far[i] - bytes_out + 16):
+                assert call(*far[:4], at, od) == EINVAL, (i, at)
+                assert b"overlaps" in k3.lib.k3moe_last_error()
+
+
+def test_a_workspace_kernels_cannot_use_is_refused():
+    from mxfp4_routed_expert_gemv_amd import check_workspace
+    with pytest.raises(ValueError, match="workspace"):
+        check_workspace(torch.zeros(256, dtype=torch.uint8), 0)   # host memory
