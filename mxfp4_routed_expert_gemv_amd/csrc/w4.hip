@@ -232,10 +232,14 @@ __device__ __noinline__ void w4_slice_exact(const W4Args g, int blk0, int blk1, 
 // the end.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// LDS-DMA copies from base + off: lane i's 16 bytes (two bytes, one byte, as a
-// dword) land at lds + 16 i (4 i).
+// LDS-DMA copies from base + off: lane i's 16 bytes (dword; two bytes, one byte, as
+// a dword) land at lds + 16 i (4 i).
 __device__ __forceinline__ void dma_b128(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_b32(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
 __device__ __forceinline__ void dma_u16(const void* base, uint32_t off, uint32_t lds) {
@@ -251,25 +255,39 @@ __device__ __forceinline__ void dma_u8(const void* base, uint32_t off, uint32_t 
 // Slot of a block, for RC tokens and 16 NF weight rows:
 //   codes  [16 NF rows][4 units of 16 bytes], unit u of row r at u ^ code_swz(r)
 //   x      [RC rows][16 (fp32: 32) units], unit u of row r at u ^ (r mod 16)
-//   scale  [4 / SG][16 NF] dwords, then zero the same
+//   scale  [4 / SG][16 NF] dwords, then zero the same; WIDE (groups of 32, four of
+//     them a block at a time, whose addresses are then whole dwords): scale [16 NF]
+//     [4] bf16, then zero [16 NF][4] bytes, half of the copies or less (64 tokens
+//     7168 x 4096: 16.9 us against 19.0; 32 tokens 16384 x 4096: 24.5, 27.3)
 // The permutations spread the 16 rows of a fragment read over the LDS banks.
-template <int RC, int NF, int SG, bool F32X>
+template <int RC, int NF, int SG, bool F32X, bool WIDE>
 struct Slot {
+  static_assert(!WIDE || SG == 1, "four scales a block");
   static constexpr int kRow = F32X ? 512 : 256;             // bytes of x per token
   static constexpr int kX = NF * 1024, kS = kX + RC * kRow;
-  static constexpr int kVals = 4 / SG * 16 * NF;            // scales
-  static constexpr int NS = (kVals + 63) / 64;              // copies of them
-  static constexpr int kZ = kS + NS * 256, kBytes = kZ + NS * 256;
+  static constexpr int kVals = WIDE ? 2 * 16 * NF : 4 / SG * 16 * NF;   // dwords of scales
+  static constexpr int kZeros = WIDE ? 16 * NF : kVals;
+  static constexpr int NS = (kVals + 63) / 64, NZ = (kZeros + 63) / 64;   // copies
+  static constexpr int kZ = kS + NS * 256, kBytes = kZ + NZ * 256;
   static constexpr int NX = RC * kRow / 1024;               // copies of x
-  static constexpr int kCopies = NF + NX + 2 * NS;
+  static constexpr int kCopies = NF + NX + NS + NZ;
 };
+// Scales, and 16 + zero points negated, of a row's four groups of 32.
+__device__ __forceinline__ void wide_values(const uint8_t* scale, const uint8_t* zero, bool has_zero,
+                                            float (&sc)[4], float (&off)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(scale);
+  const uint32_t z = has_zero ? *reinterpret_cast<const uint32_t*>(zero) : 0x08080808u;
+  sc[0] = bf16_lo(w.x); sc[1] = bf16_hi(w.x); sc[2] = bf16_lo(w.y); sc[3] = bf16_hi(w.y);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) off[s] = -(float)(16 + (z >> (8 * s) & 255u));
+}
 __device__ __forceinline__ int code_swz(int r) { return ((r >> 1) & 2) ^ ((r >> 3) & 1) * 3; }
 
 // Workgroup blockIdx.x: 16 NF weight rows (gated form: 8 NF gate
 // rows and the matching up rows) x RC tokens.
-template <int W, int D, int RC, int NF, int SG, bool F32X, bool GLU>
+template <int W, int D, int RC, int NF, int SG, bool F32X, bool WIDE, bool GLU>
 __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
-  using L = Slot<RC, NF, SG, F32X>;
+  using L = Slot<RC, NF, SG, F32X, WIDE>;
   constexpr int NB = GLU ? 8 * NF : 16 * NF;   // outputs per token
   constexpr int XP = F32X ? 3 : 1, MB = (RC + 15) / 16;   // fragments of tokens
   static_assert(!GLU || NF % 2 == 0, "gate and up fragments come in pairs");
@@ -287,7 +305,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
 
   // ---- copies: offsets from the wave's first block, in the arrays' rows
   const int kb = g.k >> 1;   // bytes of a row of codes
-  uint32_t oc[NF], ox[L::NX], os[L::NS];
+  uint32_t oc[NF], ox[L::NX], os[L::NS], oz[L::NZ];
   int kc[NF], kx[L::NX], vs[L::NS];
   const int row_lo = weight_row(0);
   const size_t up_rows = GLU ? (size_t)g.f : 0;   // fragments of the up half start there
@@ -304,15 +322,20 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
     kx[c] = u * (F32X ? 4 : 8);
     ox[c] = (uint32_t)min(r, tn - 1) * (uint32_t)g.k;
   }
+  // (in scales from the first row's; the up half's rows are further than the gate's)
+  auto scale_row = [&](int i) {
+    const uint32_t r = (uint32_t)(weight_row(i) - row_lo - (GLU && (i >> 4) >= NF / 2 ? g.f : 0));
+    return (r + (GLU && (i >> 4) >= NF / 2 ? (uint32_t)up_rows : 0u)) * (uint32_t)g.groups;
+  };
 #pragma unroll
   for (int c = 0; c < L::NS; ++c) {
     const int i = min(c * 64 + lane, L::kVals - 1);
-    vs[c] = i / (16 * NF);
-    const int f = i % (16 * NF) >> 4;
-    os[c] = (uint32_t)(weight_row(i % (16 * NF)) - row_lo - (GLU && f >= NF / 2 ? g.f : 0)) *
-            (uint32_t)g.groups;
-    if (GLU && f >= NF / 2) os[c] += (uint32_t)(up_rows * g.groups);
+    vs[c] = WIDE ? (i & 1) * 2 : i / (16 * NF);
+    os[c] = scale_row(WIDE ? i >> 1 : i % (16 * NF));
   }
+#pragma unroll
+  for (int c = 0; c < L::NZ; ++c)
+    oz[c] = WIDE ? scale_row(min(c * 64 + lane, 16 * NF - 1)) : os[c];
   const uint32_t my = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring[wv];
   const int nblk = (g.k + kBlk - 1) / kBlk;
   const uint8_t* const zeros = g.zero ? g.zero : reinterpret_cast<const uint8_t*>(g.scale);
@@ -330,12 +353,22 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
     for (int c = 0; c < L::NX; ++c)
       dma_b128(x, (ox[c] + (uint32_t)min(kx[c], g.k - (F32X ? 4 : 8) - k0)) * (F32X ? 4 : 2),
                to + L::kX + c * 1024);
+    const uint16_t* const s_lo = g.scale + (size_t)row_lo * g.groups;
+    const uint8_t* const z_lo = zeros + (size_t)row_lo * g.groups;
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int c = 0; c < L::NS; ++c) {
-      uint32_t o = os[c] + (uint32_t)(SG < 4 ? min(b * (4 / SG) + vs[c], g.groups - 1)
-                                             : group_of<SG>(g, b, 0));
-      dma_u16(g.scale + (size_t)row_lo * g.groups, o * 2, to + L::kS + c * 256);
-      dma_u8(zeros + (size_t)row_lo * g.groups, o, to + L::kZ + c * 256);
+      for (int c = 0; c < L::NS; ++c)
+        dma_b32(s_lo, (os[c] + (uint32_t)(b * 4 + vs[c])) * 2, to + L::kS + c * 256);
+#pragma unroll
+      for (int c = 0; c < L::NZ; ++c) dma_b32(z_lo, oz[c] + (uint32_t)(b * 4), to + L::kZ + c * 256);
+    } else {
+#pragma unroll
+      for (int c = 0; c < L::NS; ++c) {
+        const uint32_t o = os[c] + (uint32_t)(SG < 4 ? min(b * (4 / SG) + vs[c], g.groups - 1)
+                                                     : group_of<SG>(g, b, 0));
+        dma_u16(s_lo, o * 2, to + L::kS + c * 256);
+        dma_u8(z_lo, o, to + L::kZ + c * 256);
+      }
     }
   };
 
@@ -359,17 +392,22 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
     const uint8_t* at = ring[wv] + slot * L::kBytes;
     uint32_t c[NF][4];
     uint4 x[MB][4][F32X ? 2 : 1];
-    float sc[4 / SG][NF], off[4 / SG][NF];
+    float sc[NF][4 / SG], off[NF][4 / SG];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       const uint4 v = *reinterpret_cast<const uint4*>(at + f * 1024 + ln * 64 + ((lg ^ code_swz(ln)) << 4));
       c[f][0] = v.x; c[f][1] = v.y; c[f][2] = v.z; c[f][3] = v.w;
+      if constexpr (WIDE) {
+        const int r = f * 16 + ln;
+        wide_values(at + L::kS + r * 8, at + L::kZ + r * 4, g.zero, sc[f], off[f]);
+      } else {
 #pragma unroll
-      for (int s = 0; s < 4 / SG; ++s) {
-        const int i = ((s * NF + f) * 16 + ln) * 4;
-        sc[s][f] = bf16_lo(*reinterpret_cast<const uint32_t*>(at + L::kS + i));
-        const int z = g.zero ? *reinterpret_cast<const int*>(at + L::kZ + i) : 8;
-        off[s][f] = -(float)(16 + z);
+        for (int s = 0; s < 4 / SG; ++s) {
+          const int i = ((s * NF + f) * 16 + ln) * 4;
+          sc[f][s] = bf16_lo(*reinterpret_cast<const uint32_t*>(at + L::kS + i));
+          const int z = g.zero ? *reinterpret_cast<const int*>(at + L::kZ + i) : 8;
+          off[f][s] = -(float)(16 + z);
+        }
       }
     }
     const int xr = ln & (RC - 1);   // (rows past RC repeat one of them)
@@ -422,7 +460,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
         for (int f = 0; f < NF; ++f)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[m][f][r] = __builtin_fmaf(sc[s][f], __builtin_fmaf(off[s][f], sum[m][r], dot[m][f][r]),
+            acc[m][f][r] = __builtin_fmaf(sc[f][s], __builtin_fmaf(off[f][s], sum[m][r], dot[m][f][r]),
                                           acc[m][f][r]);
     }
   }
@@ -490,22 +528,23 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
 // each, so that a fragment of x read from LDS and its sum serve two fragments of
 // weights; the two halves are added through LDS at the end.  One ring of steps, one
 // barrier a step.
-template <int MB, int SG, bool F32X>
+template <int MB, int SG, bool F32X, bool WIDE>
 struct TileSlot {
   static constexpr int kRow = F32X ? 512 : 256;        // bytes of x per token and block
   static constexpr int XC = 16 * MB * kRow / 8192;     // copies of x per wave and block
   static constexpr int kX = 8192, kBlock = kX + 16 * MB * kRow;   // codes, then x
-  // scales: [two blocks][4 / SG][128 rows] dwords, then zero the same
-  static constexpr int kVals = 2 * (4 / SG) * 128, kS = 2 * kBlock, kZ = kS + kVals * 4;
-  static constexpr int kBytes = kZ + kVals * 4;
-  static constexpr int kCopies = 2 * (1 + XC) + kVals / 256;
+  // scales: [two blocks][4 / SG][128 rows] dwords, then zero the same; WIDE: [two
+  // blocks][128 rows][4] bf16, then zero [two blocks][128 rows][4] bytes
+  static constexpr int kVals = WIDE ? 512 : 2 * (4 / SG) * 128, kZeros = WIDE ? 256 : kVals;
+  static constexpr int kS = 2 * kBlock, kZ = kS + kVals * 4, kBytes = kZ + kZeros * 4;
+  static constexpr int kCopies = 2 * (1 + XC) + (WIDE ? 2 : kVals / 256);
   static constexpr int kStages = (160 << 10) / kBytes < 3 ? (160 << 10) / kBytes : 3;
   static_assert(XC * 8192 == 16 * MB * kRow && kStages >= 2, "whole copies, two steps in LDS");
 };
 
-template <int MB, int SG, bool F32X>
+template <int MB, int SG, bool F32X, bool WIDE>
 __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
-  using L = TileSlot<MB, SG, F32X>;
+  using L = TileSlot<MB, SG, F32X, WIDE>;
   constexpr int XP = F32X ? 3 : 1, kStages = L::kStages;
   constexpr int kRed = 132;   // (a row of the sums; 4 rows apart: 16 banks)
   static_assert(16 * MB * kRed * 4 <= kStages * L::kBytes, "the sums fit the ring");
@@ -560,7 +599,16 @@ __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
       if (z) dma_u8(zero, o, to + L::kZ + c * 256);
       else dma_u16(scale, o * 2, to + L::kS + c * 256);
     };
-    if constexpr (L::kVals == 256) {
+    if constexpr (WIDE) {
+      // wave w: scales 64 w .. + 64 (dwords) of the two blocks', zeros 64 (w mod 4)
+      // .. + 64 (every one twice, so that each wave has the same copies in flight)
+      const uint32_t r = (uint32_t)min((wv & 3) * 32 + (lane >> 1), last);
+      dma_b32(scale, (r * g.groups + (uint32_t)(block(wv >> 2) * 4 + (lane & 1) * 2)) * 2,
+              to + L::kS + wv * 256);
+      const int c = wv & 3;
+      dma_b32(zero, (uint32_t)min((c & 1) * 64 + lane, last) * (uint32_t)g.groups +
+                        (uint32_t)(block(c >> 1) * 4), to + L::kZ + c * 256);
+    } else if constexpr (L::kVals == 256) {
       if (wv < 4) value(wv, false);
       else value(wv - 4, true);
     } else {
@@ -596,12 +644,17 @@ __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
     const int blk = b0 + 2 * step + wk;
     if (blk >= b1) continue;
     uint32_t c[2][4];
+    float wsc[2][4], woff[2][4];   // WIDE: the block's four groups
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       const uint4 v = *reinterpret_cast<const uint4*>(at + (wn * 2 + f) * 1024 + ln * 64 +
                                                       ((lg ^ code_swz(ln)) << 4));
       c[f][0] = v.x; c[f][1] = v.y; c[f][2] = v.z; c[f][3] = v.w;
       transpose4(c[f]);
+      if constexpr (WIDE) {
+        const int r = wk * 128 + wn * 32 + f * 16 + ln;
+        wide_values(vals + L::kS + r * 8, vals + L::kZ + r * 4, g.zero, wsc[f], woff[f]);
+      }
     }
 #pragma unroll
     for (int s = 0; s < 4 / SG; ++s) {
@@ -609,6 +662,11 @@ __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
       float sc[2], off[2];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
+        if constexpr (WIDE) {
+          sc[f] = wsc[f][s];
+          off[f] = woff[f][s];
+          continue;
+        }
         const int i = ((wk * (4 / SG) + s) * 128 + wn * 32 + f * 16 + ln) * 4;
         sc[f] = bf16_lo(*reinterpret_cast<const uint32_t*>(vals + L::kS + i));
         off[f] = -(float)(16 + (g.zero ? *reinterpret_cast<const int*>(vals + L::kZ + i) : 8));
@@ -733,25 +791,26 @@ __global__ __launch_bounds__(256) void w4_finish(W4Args g) {
 // short contraction lose (2 fp32 tokens 1024 x 1024, 32: 5.1 against 4.8).  16
 // fp32 tokens do not fit with 16 waves; 8 there against 4: 17.7, 22.2
 // (7168 x 7168).
-template <int W, int RC, int NF, int SG, bool F32X>
+template <int W, int RC, int NF, int SG, bool F32X, bool WIDE>
 constexpr int ring_depth() {
-  constexpr int n = (160 << 10) / (W * Slot<RC, NF, SG, F32X>::kBytes);
+  constexpr int n = (160 << 10) / (W * Slot<RC, NF, SG, F32X, WIDE>::kBytes);
   return n < 4 ? n : 4;
 }
 
-template <int W, int RC, int NF, int SG, bool F32X, bool GLU>
+template <int W, int RC, int NF, int SG, bool F32X, bool WIDE, bool GLU>
 hipError_t launch_sg(const W4Args& g, hipStream_t st) {
   constexpr int NB = GLU ? 8 * NF : 16 * NF;
-  w4_kernel<W, ring_depth<W, RC, NF, SG, F32X>(), RC, NF, SG, F32X, GLU>
+  w4_kernel<W, ring_depth<W, RC, NF, SG, F32X, WIDE>(), RC, NF, SG, F32X, WIDE, GLU>
       <<<((GLU ? g.f : g.n) + NB - 1) / NB, 64 * W, 0, st>>>(g);
   return hipGetLastError();
 }
 template <int W, int RC, int NF, bool F32X, bool GLU>
 hipError_t launch(const W4Args& g, hipStream_t st) {
   const int group = g.k / g.groups;
-  if (group == 32) return launch_sg<W, RC, NF, 1, F32X, GLU>(g, st);
-  if (group == 64) return launch_sg<W, RC, NF, 2, F32X, GLU>(g, st);
-  return launch_sg<W, RC, NF, 4, F32X, GLU>(g, st);   // a multiple of 128
+  if (group == 32) return g.groups % 4 == 0 ? launch_sg<W, RC, NF, 1, F32X, true, GLU>(g, st)
+                                            : launch_sg<W, RC, NF, 1, F32X, false, GLU>(g, st);
+  if (group == 64) return launch_sg<W, RC, NF, 2, F32X, false, GLU>(g, st);
+  return launch_sg<W, RC, NF, 4, F32X, false, GLU>(g, st);   // a multiple of 128
 }
 template <int MB, bool F32X, bool GLU>
 hipError_t launch_tile(const W4Args& g, hipStream_t st) {
@@ -759,9 +818,10 @@ hipError_t launch_tile(const W4Args& g, hipStream_t st) {
   // on the same XCD, whose L2 then serves the codes)
   const dim3 grid(((g.n + 127) / 128 + 7) / 8 * 8, g.splits, (g.T + 16 * MB - 1) / (16 * MB));
   const int group = g.k / g.groups;
-  if (group == 32) w4_tile<MB, 1, F32X><<<grid, 512, 0, st>>>(g);
-  else if (group == 64) w4_tile<MB, 2, F32X><<<grid, 512, 0, st>>>(g);
-  else w4_tile<MB, 4, F32X><<<grid, 512, 0, st>>>(g);
+  if (group == 32 && g.groups % 4 == 0) w4_tile<MB, 1, F32X, true><<<grid, 512, 0, st>>>(g);
+  else if (group == 32) w4_tile<MB, 1, F32X, false><<<grid, 512, 0, st>>>(g);
+  else if (group == 64) w4_tile<MB, 2, F32X, false><<<grid, 512, 0, st>>>(g);
+  else w4_tile<MB, 4, F32X, false><<<grid, 512, 0, st>>>(g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int n_out = GLU ? g.f : g.n;
