@@ -26,6 +26,7 @@ using namespace grouped;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
@@ -77,11 +78,13 @@ __device__ __forceinline__ void dma16_buf(u32x4_t rsrc, uint32_t voff, uint32_t 
 }
 #pragma clang diagnostic pop
 
-// Four bf16 roundings (to nearest even, v_cvt_pk_bf16_f32) packed.
-__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+// bf16 roundings (to nearest even, v_cvt_pk_bf16_f32) packed.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
   typedef __attribute__((ext_vector_type(2))) float f2;
-  return make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf16x2_t)),
-                    __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{c, d}, bf16x2_t)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf16x2_t));
+}
+__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+  return make_uint2(pack2(a, b), pack2(c, d));
 }
 
 // sigmoid(g) from the hardware's exp2 and reciprocal: off by about |g| 2^-24
@@ -147,52 +150,115 @@ struct Tile {
   using A = Operand<A_KC, BM>;
   using B = Operand<B_KC, BN>;
   static_assert(NA * 64 * NW == BM * 8 && NB * 64 * NW == BN * 8 && MF >= 1 && NF >= 1, "whole copies");
-  static_assert(P != kGateUp || NF % 2 == 0, "gate and up fragments come in pairs");
+  static_assert(NF == 2 || NF % 4 == 0, "fragments (and pairs of gate and up) side by side");
 };
 
 // Column (row of w13) of hidden feature n's gate in [2 F]; its up is fs further.
 __device__ __forceinline__ int gate_col(int n, int fs) { return n + n / fs * fs; }
 
-// ---- epilogues: four consecutive columns n of row m from their fp32 sums
+// ---- epilogues.  A fragment's sums give a lane four consecutive columns of a row;
+// two fragments side by side, their odd and even groups of 16 lanes exchanged, give
+// it eight: lane group lg then has columns 8 (lg / 2) .. + 8 of fragment lg mod 2,
+// a store is 16 bytes and a row's part of it 64 (against stores of 8 and 32: the
+// backward at T = 64 131 us, 142; at 16384 4.54 ms, 4.67).
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+  const auto t = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = t[0];
+  b = t[1];
+}
+__device__ __forceinline__ uint4 pack8(f32x4_t a, f32x4_t b) {
+  uint2 p = pack4(a[0], a[1], a[2], a[3]), q = pack4(b[0], b[1], b[2], b[3]);
+  exchange(p.x, q.x);
+  exchange(p.y, q.y);
+  return make_uint4(p.x, p.y, q.x, q.y);
+}
+__device__ __forceinline__ f32x4_t gated(f32x4_t ga, f32x4_t up) {
+  f32x4_t h;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) h[r] = ga[r] * sigmoid_fast(ga[r]) * up[r];
+  return h;
+}
+// The forward's gate and up sums of row m: columns n .. + 4, or, of two
+// fragments, the lane's eight from n on.
 __device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, f32x4_t ga, f32x4_t up) {
   const int F = g.S * g.fs;
+  const f32x4_t h = gated(ga, up);
   uint16_t* gu = static_cast<uint16_t*>(g.o0) + (size_t)m * 2 * F + gate_col(n, g.fs);
   *reinterpret_cast<uint2*>(gu) = pack4(ga[0], ga[1], ga[2], ga[3]);
   *reinterpret_cast<uint2*>(gu + g.fs) = pack4(up[0], up[1], up[2], up[3]);
-  *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) =
-      pack4(ga[0] * sigmoid_fast(ga[0]) * up[0], ga[1] * sigmoid_fast(ga[1]) * up[1],
-            ga[2] * sigmoid_fast(ga[2]) * up[2], ga[3] * sigmoid_fast(ga[3]) * up[3]);
+  *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) = pack4(h[0], h[1], h[2], h[3]);
 }
-// v = dh: dg, du and h from the kept g and u
-__device__ __forceinline__ void store_dhid(const DenseArgs& g, int m, int n, f32x4_t v) {
+__device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, bool in, f32x4_t ga0,
+                                             f32x4_t up0, f32x4_t ga1, f32x4_t up1) {
+  const int F = g.S * g.fs;
+  const uint4 ga = pack8(ga0, ga1), up = pack8(up0, up1), h = pack8(gated(ga0, up0), gated(ga1, up1));
+  if (!in) return;
+  uint16_t* gu = static_cast<uint16_t*>(g.o0) + (size_t)m * 2 * F + gate_col(n, g.fs);
+  *reinterpret_cast<uint4*>(gu) = ga;
+  *reinterpret_cast<uint4*>(gu + g.fs) = up;
+  *reinterpret_cast<uint4*>(g.o1 + (size_t)m * F + n) = h;
+}
+// dh's sums v of row m: dg, du and h from the kept g and u (two bf16 values a word).
+__device__ __forceinline__ void gate_grads(const float* v, uint32_t gw, uint32_t uw, uint32_t& dg,
+                                           uint32_t& du, uint32_t& h) {
+  float d[2][3];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float ga = r ? bf16_hi(gw) : bf16_lo(gw), up = r ? bf16_hi(uw) : bf16_lo(uw);
+    const float s = sigmoid_fast(ga), gs = ga * s;
+    d[r][0] = v[r] * up * (s + gs * (1.0f - s));
+    d[r][1] = v[r] * gs;
+    d[r][2] = gs * up;
+  }
+  dg = pack2(d[0][0], d[1][0]);
+  du = pack2(d[0][1], d[1][1]);
+  h = pack2(d[0][2], d[1][2]);
+}
+template <int W, typename V>   // W words of two columns each
+__device__ __forceinline__ void store_dhid_words(const DenseArgs& g, int m, int n, const float* v) {
   const int F = g.S * g.fs;
   const size_t o = (size_t)m * 2 * F + gate_col(n, g.fs);
-  const uint2 gw = *reinterpret_cast<const uint2*>(g.gu + o);
-  const uint2 uw = *reinterpret_cast<const uint2*>(g.gu + o + g.fs);
-  const float ga[4] = {bf16_lo(gw.x), bf16_hi(gw.x), bf16_lo(gw.y), bf16_hi(gw.y)};
-  const float up[4] = {bf16_lo(uw.x), bf16_hi(uw.x), bf16_lo(uw.y), bf16_hi(uw.y)};
-  float dg[4], du[4], h[4];
+  const V gw = *reinterpret_cast<const V*>(g.gu + o), uw = *reinterpret_cast<const V*>(g.gu + o + g.fs);
+  V dg, du, h;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float s = sigmoid_fast(ga[r]), gs = ga[r] * s;
-    h[r] = gs * up[r];
-    du[r] = v[r] * gs;
-    dg[r] = v[r] * up[r] * (s + gs * (1.0f - s));
+  for (int w = 0; w < W; ++w) {
+    uint32_t a, b, c;
+    gate_grads(v + 2 * w, gw[w], uw[w], a, b, c);
+    dg[w] = a; du[w] = b; h[w] = c;
   }
   uint16_t* o0 = static_cast<uint16_t*>(g.o0) + o;
-  *reinterpret_cast<uint2*>(o0) = pack4(dg[0], dg[1], dg[2], dg[3]);
-  *reinterpret_cast<uint2*>(o0 + g.fs) = pack4(du[0], du[1], du[2], du[3]);
-  *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) = pack4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<V*>(o0) = dg;
+  *reinterpret_cast<V*>(o0 + g.fs) = du;
+  *reinterpret_cast<V*>(g.o1 + (size_t)m * F + n) = h;
+}
+__device__ __forceinline__ void store_dhid(const DenseArgs& g, int m, int n, f32x4_t v) {
+  const float a[4] = {v[0], v[1], v[2], v[3]};
+  store_dhid_words<2, u32x2_t>(g, m, n, a);
+}
+__device__ __forceinline__ void store_dhid(const DenseArgs& g, int m, int n, bool in, f32x4_t v0,
+                                           f32x4_t v1) {
+  float v[8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    uint32_t a = __float_as_uint(v0[r]), b = __float_as_uint(v1[r]);
+    exchange(a, b);
+    v[r] = __uint_as_float(a);
+    v[4 + r] = __uint_as_float(b);
+  }
+  if (in) store_dhid_words<4, u32x4_t>(g, m, n, v);
+}
+template <int P>
+__device__ __forceinline__ size_t product_at(const DenseArgs& g, int m, int n, int N) {
+  // dW2 [S][d][fs]: column n is feature n % fs of expert n / fs
+  return P == kDW2 ? ((size_t)(n / g.fs) * g.d + m) * g.fs + n % g.fs : (size_t)m * N + n;
 }
 template <int P>
 __device__ __forceinline__ void store_product(const DenseArgs& g, int m, int n, int N, f32x4_t v) {
-  if (P == kDown && g.out_f32) {
+  if (P == kDown && g.out_f32)
     *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.o0) + (size_t)m * N + n) = v;
-    return;
-  }
-  // dW2 [S][d][fs]: column n is feature n % fs of expert n / fs
-  const size_t o = P == kDW2 ? ((size_t)(n / g.fs) * g.d + m) * g.fs + n % g.fs : (size_t)m * N + n;
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.o0) + o) = pack4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.o0) + product_at<P>(g, m, n, N)) =
+        pack4(v[0], v[1], v[2], v[3]);
 }
 
 constexpr int kGM = 8;   // m-tiles per group of the item order
@@ -425,20 +491,33 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
           const int c = P == kGateUp ? gate_col(n, fs) + (f >= NF / 2 ? fs : 0) : n;
           *reinterpret_cast<f32x4_t*>(row + c) = acc[i][f];
         }
+      } else if constexpr (P == kGateUp && NF == 2) {
+        const int n = n0 + wn * 16 + lg * 4;
+        if (n < N) store_gateup(g, m, n, acc[i][0], acc[i][1]);
       } else if constexpr (P == kGateUp) {
 #pragma unroll
-        for (int f = 0; f < NF / 2; ++f) {
-          const int n = n0 + wn * (8 * NF) + f * 16 + lg * 4;
-          if (n >= N) continue;
-          store_gateup(g, m, n, acc[i][f], acc[i][f + NF / 2]);
+        for (int f = 0; f < NF / 2; f += 2) {
+          const int n = n0 + wn * (8 * NF) + (f + (lg & 1)) * 16 + (lg >> 1) * 8;
+          store_gateup(g, m, n, n < N, acc[i][f], acc[i][f + NF / 2], acc[i][f + 1],
+                       acc[i][f + 1 + NF / 2]);
         }
-      } else {
+      } else if (P == kDown && g.out_f32) {
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
           const int n = n0 + (wn * NF + f) * 16 + lg * 4;
-          if (n >= N) continue;
-          if constexpr (P == kDHid) store_dhid(g, m, n, acc[i][f]);
-          else store_product<P>(g, m, n, N, acc[i][f]);
+          if (n < N) store_product<P>(g, m, n, N, acc[i][f]);
+        }
+      } else {
+#pragma unroll
+        for (int f = 0; f < NF; f += 2) {
+          const int n = n0 + (wn * NF + f + (lg & 1)) * 16 + (lg >> 1) * 8;
+          if constexpr (P == kDHid) {
+            store_dhid(g, m, n, n < N, acc[i][f], acc[i][f + 1]);
+          } else {
+            const uint4 v = pack8(acc[i][f], acc[i][f + 1]);
+            if (n < N)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.o0) + product_at<P>(g, m, n, N)) = v;
+          }
         }
       }
     }
@@ -519,9 +598,13 @@ struct Plan {
 //   128 x 128, 3 slots, one workgroup a CU:    0.65;  dh 75 us at T = 1000 (108 on
 //     128 x 256, 122 on 64 x 64)
 //   64 x 64, 3 slots, three workgroups a CU:   0.43 (one a CU), 0.5 (two), 0.64;
-//     gate/up 57 us at T = 200 (66 on 128 x 128; 92 with 2 slots), and for fewer
-//     tokens with its contraction split: the outputs are few, the weights have to
-//     come by every CU's loads at once
+//     gate/up 57 us at T = 200 (66 on 128 x 128; 92 with 2 slots)
+// Where the outputs are few, the contraction is split, so that every CU loads a part
+// of the weights: on 64 x 64 tiles below about 100 tokens, on the larger ones up to
+// about 800 (forward at T = 128 60 us against 77 without a split on larger tiles,
+// T = 256 81, 109; backward at T = 512 237, 267).  The sums of a piece then cost
+// their way to memory and back, and a second kernel 5 us.
+constexpr double kPartUs = 1.6e-6;   // a partial sum written and read, 8 bytes
 Plan plan_product(int P, const k3moe_shape& s) {
   const int64_t F = (int64_t)s.n_shared * s.f_shared, T = s.T, d = s.d;
   const int64_t M = P == kDW13 ? 2 * F : P == kDW2 ? d : T;
@@ -538,7 +621,7 @@ Plan plan_product(int P, const k3moe_shape& s) {
     if (n > 1) {
       const int64_t per = (nst + n - 1) / n;
       n = (nst + per - 1) / per;
-      const double c = 0.64 * per + 5.0;   // the second kernel
+      const double c = 0.64 * per + 5.0 + kPartUs * n * M * N * w;
       if (c < best) {
         best = c;
         p.splits = (int)n;
@@ -546,10 +629,20 @@ Plan plan_product(int P, const k3moe_shape& s) {
       }
     }
   }
-  const double c128 = rounds(tiles(128, 128), 256) * 0.65 * nst;
-  if (c128 < best) best = c128, p = Plan{kTile128, 1, 0};
-  const double c128x256 = rounds(tiles(128, 256), 256) * 0.95 * nst;
-  if (c128x256 < best) best = c128x256, p = Plan{kTile128x256, 1, 0};
+  auto consider = [&](int tile, int64_t t, double stage) {
+    const double c = rounds(t, 256) * stage * nst;
+    if (c < best) best = c, p = Plan{tile, 1, 0};
+    // (dx shares its launch with the weight gradients, whose tiles fill its rounds)
+    if (P == kDX || P == kDW13 || P == kDW2 || t > 256) return;
+    for (int64_t n = 2; n <= 8 && 4 * n <= nst; ++n) {
+      const int64_t per = (nst + n - 1) / n;
+      if ((n - 1) * per >= nst) continue;
+      const double split = rounds(t * n, 256) * stage * per + 5.0 + kPartUs * n * M * N * w;
+      if (split < best) best = split, p = Plan{tile, (int)n, (int)(per * kBK)};
+    }
+  };
+  consider(kTile128, tiles(128, 128), 0.65);
+  consider(kTile128x256, tiles(128, 256), 0.95);
   const double c256 = rounds(tiles(256, 256), 256) * 1.6 * nst;
   if (c256 <= best) p = Plan{kTile256, 1, 0};
   return p;
@@ -567,23 +660,30 @@ template <int P>
 hipError_t launch_product(const k3moe_shape& s, DenseArgs g, float* part, hipStream_t st) {
   const Plan p = plan_product(P, s);
   const int cus = grouped_grid();
-  if (p.tile == kTile256) {
+  if (p.splits > 1) {
+    if constexpr (P != kDW13 && P != kDW2) {
+      g.part = part;
+      g.splits = p.splits;
+      g.k_split = p.k_split;
+      if (p.tile == kTile64) {
+        dense_tile<P, 64, 64, 2, 2, 3, true><<<cus * 3, 256, 0, st>>>(g);
+      } else if constexpr (P != kDX) {
+        if (p.tile == kTile128) dense_tile<P, 128, 128, 2, 4, 3, true><<<cus, 512, 0, st>>>(g);
+        else dense_tile<P, 128, 256, 2, 4, 3, true><<<cus, 512, 0, st>>>(g);
+      }
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      const int64_t n = s.T * (P == kGateUp || P == kDHid ? (int64_t)g.S * g.fs : g.d) / 4;
+      split_finish<P><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
+    }
+  } else if (p.tile == kTile256) {
     dense_tile<P, 256, 256, 2, 4, 2><<<cus, 512, 0, st>>>(g);
   } else if (p.tile == kTile128x256) {
     dense_tile<P, 128, 256, 2, 4, 3><<<cus, 512, 0, st>>>(g);
   } else if (p.tile == kTile128) {
     dense_tile<P, 128, 128, 2, 4, 3><<<cus, 512, 0, st>>>(g);
-  } else if (p.splits == 1) {
+  } else {
     dense_tile<P, 64, 64, 2, 2, 3><<<cus * 3, 256, 0, st>>>(g);
-  } else if constexpr (P != kDW13 && P != kDW2) {
-    g.part = part;
-    g.splits = p.splits;
-    g.k_split = p.k_split;
-    dense_tile<P, 64, 64, 2, 2, 3, true><<<cus * 3, 256, 0, st>>>(g);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int64_t n = s.T * (P == kGateUp || P == kDHid ? (int64_t)g.S * g.fs : g.d) / 4;
-    split_finish<P><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
   }
   return hipGetLastError();
 }
