@@ -604,6 +604,8 @@ struct Plan {
 // about 800 (forward at T = 128 60 us against 77 without a split on larger tiles,
 // T = 256 81, 109; backward at T = 512 237, 267).  The sums of a piece then cost
 // their way to memory and back, and a second kernel 5 us.
+// A weight gradient's contraction can be a few tokens: there a tile's way out counts
+// (us a round: 9, 4.6, 2.7, 1.9; both gradients at T = 64 65, 61, 63, 71).
 constexpr double kPartUs = 1.6e-6;   // a partial sum written and read, 8 bytes
 Plan plan_product(int P, const k3moe_shape& s) {
   const int64_t F = (int64_t)s.n_shared * s.f_shared, T = s.T, d = s.d;
@@ -614,9 +616,11 @@ Plan plan_product(int P, const k3moe_shape& s) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N * w + bn - 1) / bn); };
   auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
   const int64_t t64 = tiles(64, 64);
-  double best = (t64 <= 256 ? 0.43 : t64 <= 512 ? 0.5 : rounds(t64, 768) * 0.64) * nst;
+  const bool dw = P == kDW13 || P == kDW2;
+  double best = t64 <= 256 ? 0.43 * nst : t64 <= 512 ? 0.5 * nst
+                           : rounds(t64, 768) * (0.64 * nst + (dw ? 1.9 : 0.0));
   Plan p{kTile64, 1, 0};
-  if (P != kDW13 && P != kDW2 && t64 <= 384) {
+  if (!dw && t64 <= 384) {
     int64_t n = std::min<int64_t>(768 / t64, nst / 4);
     if (n > 1) {
       const int64_t per = (nst + n - 1) / n;
@@ -629,11 +633,11 @@ Plan plan_product(int P, const k3moe_shape& s) {
       }
     }
   }
-  auto consider = [&](int tile, int64_t t, double stage) {
-    const double c = rounds(t, 256) * stage * nst;
+  auto consider = [&](int tile, int64_t t, double stage, double out) {
+    const double c = rounds(t, 256) * (stage * nst + (dw ? out : 0.0));
     if (c < best) best = c, p = Plan{tile, 1, 0};
     // (dx shares its launch with the weight gradients, whose tiles fill its rounds)
-    if (P == kDX || P == kDW13 || P == kDW2 || t > 256) return;
+    if (P == kDX || dw || t > 256) return;
     for (int64_t n = 2; n <= 8 && 4 * n <= nst; ++n) {
       const int64_t per = (nst + n - 1) / n;
       if ((n - 1) * per >= nst) continue;
@@ -641,9 +645,9 @@ Plan plan_product(int P, const k3moe_shape& s) {
       if (split < best) best = split, p = Plan{tile, (int)n, (int)(per * kBK)};
     }
   };
-  consider(kTile128, tiles(128, 128), 0.65);
-  consider(kTile128x256, tiles(128, 256), 0.95);
-  const double c256 = rounds(tiles(256, 256), 256) * 1.6 * nst;
+  consider(kTile128, tiles(128, 128), 0.65, 2.7);
+  consider(kTile128x256, tiles(128, 256), 0.95, 4.6);
+  const double c256 = rounds(tiles(256, 256), 256) * (1.6 * nst + (dw ? 9.0 : 0.0));
   if (c256 <= best) p = Plan{kTile256, 1, 0};
   return p;
 }
