@@ -459,7 +459,8 @@ k3moe_status k3moe_cache_stats_get(const k3moe_expert_cache* cache, k3moe_cache_
  *             over the tokens)
  * Sums are fp32.  g, u (kept for the backward), h, dg, du and every gradient
  * are rounded to bf16 once: they are bf16 operands of the next product (which
- * is why this y is not the bits of k3moe_shared_ffn, whose h keeps 16 bits).
+ * is why this y is not the bits of k3moe_shared_ffn, whose h keeps 16 bits); up
+ * to 16 tokens h, dg and du keep 16 bits here too.
  * The reference pages only run their model; a training pass over its
  * always-on experts is this library's.
  * ------------------------------------------------------------------------- */
@@ -473,9 +474,9 @@ k3moe_status k3moe_shared_ffn_train(const k3moe_shape* shape, const k3moe_expert
                                     size_t workspace_bytes, void* stream);
 /* x and gu of the forward and dy [T][d] bf16 -> dx [T][d], dw13 [n_shared][2
  * f_shared][d] and dw2 [n_shared][d][f_shared], all bf16 and overwritten.  An
- * output that is NULL is not computed (all three NULL: nothing is enqueued), and
- * which ones are asked for, or other tokens, can change the order of a sum and so
- * its last bits; the same call gives the same bits.
+ * output that is NULL is not computed (all three NULL: nothing is enqueued).
+ * The number of tokens can change the order of a sum, and so the last bits of a
+ * token's values; the same call gives the same bits.
  * T = 0 writes zeros to dw13 and dw2.  The outputs must not overlap the inputs
  * or each other.  Errors: as for k3moe_shared_ffn_train.
  * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_SHARED_BACKWARD). */

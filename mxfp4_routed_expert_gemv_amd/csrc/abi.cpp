@@ -325,7 +325,7 @@ SharedWs carve_shared(const k3moe_shape& s, void* ws, size_t* bytes) {
 SharedTrainWs carve_shared_train(const k3moe_shape& s, bool backward, void* ws, size_t* bytes) {
   Carver c(ws);
   SharedTrainWs r;
-  const size_t n = (size_t)s.T * s.n_shared * s.f_shared;
+  const size_t n = (size_t)shared_train_rows(s) * s.n_shared * s.f_shared;
   r.h = c.take<uint16_t>(n);
   r.dgu = backward ? c.take<uint16_t>(2 * n) : nullptr;
   r.part = c.take<float>(shared_train_part_floats(s, backward));

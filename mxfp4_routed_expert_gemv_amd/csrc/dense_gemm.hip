@@ -11,7 +11,21 @@
 // the fp32 sums: the gated activation is taken in the forward's epilogue from
 // the gate and up sums of one wave, its derivative in the epilogue of dh.
 // g, u (for the backward), h, dg, du and every output are rounded to bf16
-// once, from fp32: they are operands of the next bf16 product.
+// once, from fp32: they are operands of the next bf16 product.  Up to kRows tokens
+// h, dg and du keep 16 bits, as two bf16 parts in two blocks of kRows rows: their
+// products read the weights' every byte whatever the rows, and a rounding to 8 bits
+// of so few values does not average out (an output's error of sqrt(2) of its own
+// rounding alone, but up to twice that for one token of a small layer).  That costs
+// nothing (T = 16 forward 46.5, backward 118 us; T = 17 46.3, 117).  Where the
+// parts are rows of a product, its sums of a row and of the one kRows further are
+// added; where they are contracted over, the other operand's rows are taken twice.
+// From about 2000 tokens the matrix cores bound all six (d 7168, two experts of 2048,
+// T = 16384: dx 1.35 ms = 1.42 PFLOP/s, dW13 1.27, dW2 1.21, dh 1.02, whose epilogue
+// moves 670 MB; the library's product of such sizes reaches 1.4 to 1.5): they are
+// busy 60 to 65 % of the time at the 1.95 GHz that this load leaves, what is missing
+// being LDS reads and copies between them.  Below about 300 tokens reading the
+// weights (backward: and writing their gradients) bounds them: T = 1 forward 46 us
+// for 176 MB, backward 116 us for 352 MB.
 #include <algorithm>
 
 #include "internal.h"
@@ -31,6 +45,7 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
 constexpr int kBK = 64;   // contraction elements per stage
+constexpr int kRows = 16; // up to so many tokens h, dg and du have two parts
 
 // The products.  M x N is the output, K the contraction:
 //   kGateUp  M = T   N = F  K = d    a = x       b = w13 (gate and up rows of N features)
@@ -49,6 +64,7 @@ struct DenseArgs {
   uint16_t* o1;         // kGateUp, kDHid: h [T][F]
   int T, d, fs, S;
   int out_f32;          // kDown: y in fp32
+  int parts;            // T <= kRows: h and dgu are [2 kRows] rows, second parts from kRows on
   float* part;          // split contraction: partial sums [splits][M][columns]
   int splits, k_split;  // contraction elements per split (a multiple of kBK)
 };
@@ -172,6 +188,14 @@ __device__ __forceinline__ uint4 pack8(f32x4_t a, f32x4_t b) {
   exchange(p.y, q.y);
   return make_uint4(p.x, p.y, q.x, q.y);
 }
+// What rounding to bf16 leaves of v (0 where that is not a number).
+__device__ __forceinline__ float rest(float v) {
+  const float d = v - bf16_lo(pack2(v, v));
+  return fabsf(d) < INFINITY ? d : 0.0f;
+}
+__device__ __forceinline__ f32x4_t rest(f32x4_t v) {
+  return f32x4_t{rest(v[0]), rest(v[1]), rest(v[2]), rest(v[3])};
+}
 __device__ __forceinline__ f32x4_t gated(f32x4_t ga, f32x4_t up) {
   f32x4_t h;
 #pragma unroll
@@ -179,7 +203,8 @@ __device__ __forceinline__ f32x4_t gated(f32x4_t ga, f32x4_t up) {
   return h;
 }
 // The forward's gate and up sums of row m: columns n .. + 4, or, of two
-// fragments, the lane's eight from n on.
+// fragments, the lane's eight from n on.  FEW: T may be at most kRows.
+template <bool FEW>
 __device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, f32x4_t ga, f32x4_t up) {
   const int F = g.S * g.fs;
   const f32x4_t h = gated(ga, up);
@@ -187,20 +212,31 @@ __device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, f
   *reinterpret_cast<uint2*>(gu) = pack4(ga[0], ga[1], ga[2], ga[3]);
   *reinterpret_cast<uint2*>(gu + g.fs) = pack4(up[0], up[1], up[2], up[3]);
   *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) = pack4(h[0], h[1], h[2], h[3]);
+  if (FEW && g.parts) {
+    const f32x4_t l = rest(h);
+    *reinterpret_cast<uint2*>(g.o1 + (size_t)(m + kRows) * F + n) = pack4(l[0], l[1], l[2], l[3]);
+  }
 }
+template <bool FEW>
 __device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, bool in, f32x4_t ga0,
                                              f32x4_t up0, f32x4_t ga1, f32x4_t up1) {
   const int F = g.S * g.fs;
-  const uint4 ga = pack8(ga0, ga1), up = pack8(up0, up1), h = pack8(gated(ga0, up0), gated(ga1, up1));
+  const f32x4_t h0 = gated(ga0, up0), h1 = gated(ga1, up1);
+  const uint4 ga = pack8(ga0, ga1), up = pack8(up0, up1), h = pack8(h0, h1);
+  uint4 l = h;
+  if (FEW && g.parts) l = pack8(rest(h0), rest(h1));
   if (!in) return;
   uint16_t* gu = static_cast<uint16_t*>(g.o0) + (size_t)m * 2 * F + gate_col(n, g.fs);
   *reinterpret_cast<uint4*>(gu) = ga;
   *reinterpret_cast<uint4*>(gu + g.fs) = up;
   *reinterpret_cast<uint4*>(g.o1 + (size_t)m * F + n) = h;
+  if (FEW && g.parts) *reinterpret_cast<uint4*>(g.o1 + (size_t)(m + kRows) * F + n) = l;
 }
-// dh's sums v of row m: dg, du and h from the kept g and u (two bf16 values a word).
-__device__ __forceinline__ void gate_grads(const float* v, uint32_t gw, uint32_t uw, uint32_t& dg,
-                                           uint32_t& du, uint32_t& h) {
+// dh's sums v of row m: dg, du and h from the kept g and u (two bf16 values a word),
+// and what their rounding leaves.
+template <bool REST>
+__device__ __forceinline__ void gate_grads(const float* v, uint32_t gw, uint32_t uw, uint32_t (&out)[3],
+                                           uint32_t (&low)[3]) {
   float d[2][3];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -210,31 +246,43 @@ __device__ __forceinline__ void gate_grads(const float* v, uint32_t gw, uint32_t
     d[r][1] = v[r] * gs;
     d[r][2] = gs * up;
   }
-  dg = pack2(d[0][0], d[1][0]);
-  du = pack2(d[0][1], d[1][1]);
-  h = pack2(d[0][2], d[1][2]);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    out[i] = pack2(d[0][i], d[1][i]);
+    if (REST) low[i] = pack2(rest(d[0][i]), rest(d[1][i]));
+  }
 }
-template <int W, typename V>   // W words of two columns each
+template <bool FEW, int W, typename V>   // W words of two columns each
 __device__ __forceinline__ void store_dhid_words(const DenseArgs& g, int m, int n, const float* v) {
   const int F = g.S * g.fs;
   const size_t o = (size_t)m * 2 * F + gate_col(n, g.fs);
   const V gw = *reinterpret_cast<const V*>(g.gu + o), uw = *reinterpret_cast<const V*>(g.gu + o + g.fs);
-  V dg, du, h;
+  V out[3], low[3];
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    uint32_t a, b, c;
-    gate_grads(v + 2 * w, gw[w], uw[w], a, b, c);
-    dg[w] = a; du[w] = b; h[w] = c;
+    uint32_t a[3], b[3];
+    gate_grads<FEW>(v + 2 * w, gw[w], uw[w], a, b);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      out[i][w] = a[i];
+      if (FEW) low[i][w] = b[i];
+    }
   }
-  uint16_t* o0 = static_cast<uint16_t*>(g.o0) + o;
-  *reinterpret_cast<V*>(o0) = dg;
-  *reinterpret_cast<V*>(o0 + g.fs) = du;
-  *reinterpret_cast<V*>(g.o1 + (size_t)m * F + n) = h;
+  auto put = [&](const V (&q)[3], int row) {
+    uint16_t* o0 = static_cast<uint16_t*>(g.o0) + o + (size_t)row * 2 * F;
+    *reinterpret_cast<V*>(o0) = q[0];
+    *reinterpret_cast<V*>(o0 + g.fs) = q[1];
+    *reinterpret_cast<V*>(g.o1 + (size_t)(m + row) * F + n) = q[2];
+  };
+  put(out, 0);
+  if (FEW && g.parts) put(low, kRows);
 }
+template <bool FEW>
 __device__ __forceinline__ void store_dhid(const DenseArgs& g, int m, int n, f32x4_t v) {
   const float a[4] = {v[0], v[1], v[2], v[3]};
-  store_dhid_words<2, u32x2_t>(g, m, n, a);
+  store_dhid_words<FEW, 2, u32x2_t>(g, m, n, a);
 }
+template <bool FEW>
 __device__ __forceinline__ void store_dhid(const DenseArgs& g, int m, int n, bool in, f32x4_t v0,
                                            f32x4_t v1) {
   float v[8];
@@ -245,7 +293,7 @@ __device__ __forceinline__ void store_dhid(const DenseArgs& g, int m, int n, boo
     v[r] = __uint_as_float(a);
     v[4 + r] = __uint_as_float(b);
   }
-  if (in) store_dhid_words<4, u32x4_t>(g, m, n, v);
+  if (in) store_dhid_words<FEW, 4, u32x4_t>(g, m, n, v);
 }
 template <int P>
 __device__ __forceinline__ size_t product_at(const DenseArgs& g, int m, int n, int N) {
@@ -284,7 +332,11 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
   const int T = g.T, d = g.d, fs = g.fs, F = g.S * g.fs;
   const int M = P == kDW13 ? 2 * F : P == kDW2 ? d : T;
   const int N = P == kGateUp || P == kDHid || P == kDW2 ? F : d;
-  const int K = P == kGateUp || P == kDHid ? d : P == kDown ? F : P == kDX ? 2 * F : T;
+  const int K = P == kGateUp || P == kDHid ? d : P == kDown ? F : P == kDX ? 2 * F
+                                               : g.parts ? 2 * kRows : T;
+  constexpr bool kFew = BM <= 128;   // (256 x 256 is no tile for the other products of few tokens)
+  constexpr bool kPartRows = kFew && (P == kDown || P == kDX), kPartK = P == kDW13 || P == kDW2;
+  const int a_rows = kPartRows && g.parts ? 2 * kRows : M;
   const int n_mt = (M + BM - 1) / BM, n_nt = (N + C::kN - 1) / C::kN;
   const int n_cols = SPLIT ? n_nt * g.splits : n_nt;   // n-tiles, every split's in turn
   const int n_items = n_mt * n_cols;
@@ -332,8 +384,13 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
     for (int c = 0; c < C::NA; ++c) {
       int r, k;
       OA::unit((wv * C::NA + c) * 64 + lane, r, k);
+      bool in = m0 + r < a_rows;
+      if (kPartK && g.parts) {   // (one stage: k is the row)
+        in = in && (k & (kRows - 1)) < T;
+        if (P == kDW2) k &= kRows - 1;
+      }
       const size_t e = C::A_KC ? (size_t)r * lda + k : (size_t)k * lda + r;
-      va[c] = m0 + r < M ? (uint32_t)(e * 2) : kOut;
+      va[c] = in ? (uint32_t)(e * 2) : kOut;
     }
     const int gc0 = gate_col(n0, fs);
     if (P == kDown) c_ko = c_k % fs;
@@ -358,8 +415,13 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
         const size_t e = (size_t)(n / fs - n0 / fs) * d * fs + n % fs + (size_t)k * fs;
         vb[c] = n < N ? (uint32_t)((e - n0 % fs) * 2) : kOut;
       } else {
+        bool in = n0 + r < N;
+        if (kPartK && g.parts) {
+          in = in && (k & (kRows - 1)) < T;
+          if (P == kDW13) k &= kRows - 1;
+        }
         const size_t e = C::B_KC ? (size_t)r * ldb + k : (size_t)k * ldb + r;
-        vb[c] = n0 + r < N ? (uint32_t)(e * 2) : kOut;
+        vb[c] = in ? (uint32_t)(e * 2) : kOut;
       }
     }
   };
@@ -476,6 +538,13 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
       slot = next;
     }
     // ---- epilogue: lane (ln, lg) holds m = m0 + 16 (wm MF + i) + ln, four n
+    if constexpr (kPartRows) {
+      static_assert(MF >= 2, "both parts of a row in one lane");
+      if (g.parts) {   // (the first wave's rows 0 .. 15 and 16 .. 31)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) acc[0][f] += acc[1][f];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       const int m = m0 + (wm * MF + i) * 16 + ln;
@@ -493,12 +562,12 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
         }
       } else if constexpr (P == kGateUp && NF == 2) {
         const int n = n0 + wn * 16 + lg * 4;
-        if (n < N) store_gateup(g, m, n, acc[i][0], acc[i][1]);
+        if (n < N) store_gateup<kFew>(g, m, n, acc[i][0], acc[i][1]);
       } else if constexpr (P == kGateUp) {
 #pragma unroll
         for (int f = 0; f < NF / 2; f += 2) {
           const int n = n0 + wn * (8 * NF) + (f + (lg & 1)) * 16 + (lg >> 1) * 8;
-          store_gateup(g, m, n, n < N, acc[i][f], acc[i][f + NF / 2], acc[i][f + 1],
+          store_gateup<kFew>(g, m, n, n < N, acc[i][f], acc[i][f + NF / 2], acc[i][f + 1],
                        acc[i][f + 1 + NF / 2]);
         }
       } else if (P == kDown && g.out_f32) {
@@ -512,7 +581,7 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
         for (int f = 0; f < NF; f += 2) {
           const int n = n0 + (wn * NF + f + (lg & 1)) * 16 + (lg >> 1) * 8;
           if constexpr (P == kDHid) {
-            store_dhid(g, m, n, n < N, acc[i][f], acc[i][f + 1]);
+            store_dhid<kFew>(g, m, n, n < N, acc[i][f], acc[i][f + 1]);
           } else {
             const uint4 v = pack8(acc[i][f], acc[i][f + 1]);
             if (n < N)
@@ -572,8 +641,8 @@ __global__ __launch_bounds__(256) void split_finish(DenseArgs g) {
     a += *reinterpret_cast<const f32x4_t*>(p);
     if (P == kGateUp) b += *reinterpret_cast<const f32x4_t*>(p + g.fs);
   }
-  if constexpr (P == kGateUp) store_gateup(g, m, n, a, b);
-  else if constexpr (P == kDHid) store_dhid(g, m, n, a);
+  if constexpr (P == kGateUp) store_gateup<true>(g, m, n, a, b);
+  else if constexpr (P == kDHid) store_dhid<true>(g, m, n, a);
   else store_product<P>(g, m, n, N, a);
 }
 
@@ -648,7 +717,7 @@ Plan plan_product(int P, const k3moe_shape& s) {
   consider(kTile128, tiles(128, 128), 0.65, 2.7);
   consider(kTile128x256, tiles(128, 256), 0.95, 4.6);
   const double c256 = rounds(tiles(256, 256), 256) * (1.6 * nst + (dw ? 9.0 : 0.0));
-  if (c256 <= best) p = Plan{kTile256, 1, 0};
+  if (c256 <= best && (dw || T > kRows)) p = Plan{kTile256, 1, 0};
   return p;
 }
 
@@ -721,10 +790,13 @@ DenseArgs dense_args(const k3moe_shape& s) {
   g.d = s.d;
   g.fs = s.f_shared;
   g.S = s.n_shared;
+  g.parts = s.T <= kRows;
   return g;
 }
 
 }  // namespace
+
+int64_t shared_train_rows(const k3moe_shape& s) { return s.T <= kRows ? 2 * kRows : s.T; }
 
 size_t shared_train_part_floats(const k3moe_shape& s, bool backward) {
   return backward ? std::max(part_floats(kDHid, s), part_floats(kDX, s))

@@ -174,10 +174,11 @@ hipError_t launch_combine(const k3moe_shape& s, const float* y_perm, const int32
 
 // The shared experts' training pass (dense_gemm.hip).
 struct SharedTrainWs {
-  uint16_t* h;     // [T][n_shared][f_shared] bf16
-  uint16_t* dgu;   // backward: [T][n_shared][2 f_shared] bf16; else nullptr
+  uint16_t* h;     // [rows][n_shared][f_shared] bf16
+  uint16_t* dgu;   // backward: [rows][n_shared][2 f_shared] bf16; else nullptr
   float* part;     // partial sums of products whose contraction is split (small T)
 };
+int64_t shared_train_rows(const k3moe_shape& s);   // T, or twice 16 for two parts
 size_t shared_train_part_floats(const k3moe_shape& s, bool backward);
 SharedTrainWs carve_shared_train(const k3moe_shape& s, bool backward, void* ws, size_t* bytes);
 hipError_t launch_shared_train(const k3moe_shape& s, const k3moe_expert_bank& b, const void* x,

@@ -618,3 +618,44 @@ def test_a_given_stream_and_workspaces_of_one_graph_beside_another():
         want = step()
         torch.cuda.synchronize()
         assert same(held[0], want) and same(held[1], want), i
+
+
+# tokens, d, fs, experts: every tile of each product, with its contraction whole and in
+# pieces, batches and features that end inside a tile
+TILES = [(65, 2048, 832, 2), (66, 3104, 2048, 1), (67, 2016, 1568, 2), (132, 3136, 1408, 3),
+         (131, 3392, 1472, 3), (1, 2048, 1984, 2), (402, 256, 1760, 2), (261, 256, 1856, 3),
+         (769, 256, 1280, 3), (662, 256, 1824, 3), (848, 3488, 128, 1), (1061, 3616, 128, 1),
+         (2, 2240, 960, 3), (3, 2912, 1440, 3)]
+
+
+@pytest.mark.parametrize("T,d,fs,S", TILES)
+def test_shared_tiles_and_splits(T, d, fs, S):
+    test_shared_train_and_backward(T, d, fs, S)
+
+
+@pytest.mark.parametrize("T,d,fs,S", [(1, 256, 128, 1), (2, 64, 32, 3), (4, 256, 128, 1), (15, 512, 64, 3),
+                                      (16, 320, 256, 2), (1, 2048, 1984, 2), (3, 4096, 512, 1)])
+def test_shared_values_of_few_tokens_keep_16_bits(T, d, fs, S, monkeypatch):
+    """Up to 16 tokens h, dg and du are two bf16 parts: the first leaves 2^-8 of a
+    value, the second 2^-8 of that.  So an fp32 y is off by 2^-16 of its terms, and a
+    bf16 output, as its rounding to the nearest moves by no more than its argument
+    does, by the exact value's own rounding and twice such a bound."""
+    require_gpu()
+    import sys
+    from mxfp4_routed_expert_gemv_amd.shared import shared_ffn_backward, shared_ffn_train
+    x, w13, w2 = problem(T, d, fs, S, 170)
+    y, gu = shared_ffn_train(x, w13, w2, out_dtype=torch.float32)
+    dy = normal((T, d), 175, 0.1)
+    grads = shared_ffn_backward(x, gu, dy, w13, w2)
+    torch.cuda.synchronize()
+    ref = Ref(x, w13, w2)
+    monkeypatch.setattr(sys.modules[__name__], "B", 2.0 ** -16)
+    want, tol = ref.forward()[:2]
+    back = ref.backward(gu, dy)
+    monkeypatch.undo()
+    within(y, want, rounded(want, tol, torch.float32), 0, "y")
+    for g, (want, tol), name in zip(grads, back, ("dx", "dw13", "dw2")):
+        own = float((want.bfloat16().to(F8) - want).norm())
+        err = float((g.to(F8) - want).norm())
+        log(f"  {name}: error {err:.3e}, its rounding alone {own:.3e}, parts {float(tol.norm()):.3e}")
+        assert err <= own + 2 * float(tol.norm()), name
