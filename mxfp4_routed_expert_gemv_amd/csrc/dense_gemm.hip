@@ -67,6 +67,7 @@ struct DenseArgs {
   int parts;            // T <= kRows: h and dgu are [2 kRows] rows, second parts from kRows on
   float* part;          // split contraction: partial sums [splits][M][columns]
   int splits, k_split;  // contraction elements per split (a multiple of kBK)
+  int m_lo, m_hi;       // kDW2: the rows of M taken (m_lo a multiple of the tile's)
 };
 
 // A voffset past num_records: the copy writes zeros to LDS.  Every offset of
@@ -330,14 +331,15 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ln = lane & 15, lg = lane >> 4;
   const int T = g.T, d = g.d, fs = g.fs, F = g.S * g.fs;
-  const int M = P == kDW13 ? 2 * F : P == kDW2 ? d : T;
+  const int M = P == kDW13 ? 2 * F : P == kDW2 ? g.m_hi : T;
+  const int m_lo = P == kDW2 ? g.m_lo : 0;
   const int N = P == kGateUp || P == kDHid || P == kDW2 ? F : d;
   const int K = P == kGateUp || P == kDHid ? d : P == kDown ? F : P == kDX ? 2 * F
                                                : g.parts ? 2 * kRows : T;
   constexpr bool kFew = BM <= 128;   // (256 x 256 is no tile for the other products of few tokens)
   constexpr bool kPartRows = kFew && (P == kDown || P == kDX), kPartK = P == kDW13 || P == kDW2;
   const int a_rows = kPartRows && g.parts ? 2 * kRows : M;
-  const int n_mt = (M + BM - 1) / BM, n_nt = (N + C::kN - 1) / C::kN;
+  const int n_mt = (M - m_lo + BM - 1) / BM, n_nt = (N + C::kN - 1) / C::kN;
   const int n_cols = SPLIT ? n_nt * g.splits : n_nt;   // n-tiles, every split's in turn
   const int n_items = n_mt * n_cols;
   // This workgroup's item of round r (n_items: none).  A round takes the next G
@@ -358,7 +360,7 @@ __device__ __forceinline__ void run_tiles(const DenseArgs& g, const Items at, ui
     const int r = it - grp * per, gsz = min(n_mt - first, kGM), nt = r / gsz;
     const int sp = SPLIT ? nt / n_nt : 0;
     n0 = (nt - sp * n_nt) * C::kN;
-    m0 = (first + r - nt * gsz) * BM;
+    m0 = m_lo + (first + r - nt * gsz) * BM;
     k0 = SPLIT ? sp * g.k_split : 0;
     k1 = SPLIT ? min(k0 + g.k_split, K) : K;
     return sp;
@@ -721,6 +723,25 @@ Plan plan_product(int P, const k3moe_shape& s) {
   return p;
 }
 
+// Both weight gradients on 256 x 256 tiles, in one launch whose rounds are all full:
+// the rows of dW2 that do not fit go to 128 x 128 tiles, four times as many, in a
+// launch of their own.  -1: two launches take no longer.  (T = 16384, d 7168, two
+// experts of 2048: 896 and 448 tiles, 4 and 2 rounds; here 5 and 1024 rows of dW2 in
+// one round of the small tiles: backward 4.44 ms against 4.55.)
+int64_t tail_rows(const k3moe_shape& s) {
+  if (plan_product(kDW13, s).tile != kTile256 || plan_product(kDW2, s).tile != kTile256) return -1;
+  const int64_t F = (int64_t)s.n_shared * s.f_shared;
+  const int64_t nd = (s.d + 255) / 256, nf = (F + 255) / 256, t13 = (2 * F + 255) / 256 * nd;
+  const int64_t total = t13 + nd * nf, over = (total % kCUs + nf - 1) / nf;   // tile rows of dW2
+  if (over >= nd) return -1;
+  const int64_t rows = over == 0 ? 0 : s.d - (nd - over) * 256;
+  auto rounds = [](int64_t n) { return (double)((n + kCUs - 1) / kCUs); };
+  const double two = 1.6 * (rounds(t13) + rounds(nd * nf));
+  const double one = 1.6 * (double)(total / kCUs) +
+                     0.65 * rounds((rows + 127) / 128 * ((F + 127) / 128));
+  return one < 0.98 * two ? rows : -1;
+}
+
 // Floats of the partial sums of a split product (0 when it is not split).
 size_t part_floats(int P, const k3moe_shape& s) {
   const Plan p = plan_product(P, s);
@@ -772,7 +793,8 @@ hipError_t launch_grads_tile(const k3moe_shape& s, const DenseArgs (&g)[3], hipS
   int64_t total = 0;
   for (int p = 0; p < 3; ++p) {
     a.g[p] = g[p];
-    const int64_t items = (M[p] + BM - 1) / BM * ((N[p] + BN - 1) / BN);
+    const int64_t rows = p == 2 ? g[p].m_hi : M[p];
+    const int64_t items = (rows + BM - 1) / BM * ((N[p] + BN - 1) / BN);
     const int64_t rounds = (items + kCUs - 1) / kCUs, nst = (K[p] + kBK - 1) / kBK;
     const int64_t least = std::max<int64_t>((BM == 64 ? 16 : 48) / nst, 1);
     a.n[p] = (int)std::min(rounds, p == 0 ? rounds : p == 1 ? std::max(least, (rounds + 1) / 2) : least);
@@ -791,6 +813,7 @@ DenseArgs dense_args(const k3moe_shape& s) {
   g.fs = s.f_shared;
   g.S = s.n_shared;
   g.parts = s.T <= kRows;
+  g.m_hi = s.d;
   return g;
 }
 
@@ -860,6 +883,15 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   if (tile == kTile128 || tile == kTile128x256) return launch_grads_tile<128, 256, 2, 4, 3>(s, grads, st);
   if (tile == kTile64 && tiles64 <= 4096) return launch_grads_tile<64, 64, 2, 2, 3>(s, grads, st);
   if (dx && (e = launch_product<kDX>(s, grads[0], ws.part, st)) != hipSuccess) return e;
+  if (const int64_t rows = dw13 && dw2 ? tail_rows(s) : -1; rows >= 0) {
+    grads[0].o0 = nullptr;
+    grads[2].m_hi = s.d - (int)rows;
+    if ((e = launch_grads_tile<256, 256, 2, 4, 2>(s, grads, st)) != hipSuccess || rows == 0) return e;
+    grads[2].m_lo = grads[2].m_hi;
+    grads[2].m_hi = s.d;
+    dense_tile<kDW2, 128, 128, 2, 4, 3><<<grouped_grid(), 512, 0, st>>>(grads[2]);
+    return hipGetLastError();
+  }
   if (dw13 && (e = launch_product<kDW13>(s, grads[1], ws.part, st)) != hipSuccess) return e;
   return dw2 ? launch_product<kDW2>(s, grads[2], ws.part, st) : hipSuccess;
 }

@@ -659,3 +659,33 @@ def test_shared_values_of_few_tokens_keep_16_bits(T, d, fs, S, monkeypatch):
         err = float((g.to(F8) - want).norm())
         log(f"  {name}: error {err:.3e}, its rounding alone {own:.3e}, parts {float(tol.norm()):.3e}")
         assert err <= own + 2 * float(tol.norm()), name
+
+
+@pytest.mark.parametrize("T,d,fs,S", [(10001, 7168, 2048, 2), (16385, 4096, 1504, 3), (12289, 6144, 4096, 1)])
+def test_shared_weight_gradients_of_large_batches(T, d, fs, S):
+    """Both weight gradients in one launch, the rows of dw2 behind its full rounds in
+    another: each row and column written, alone (in launches of their own) the same
+    bits, and sampled columns as defined."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.shared import shared_ffn_backward
+    x, w13, w2 = problem(T, d, fs, S, 180)
+    gu, dy = normal((T, S, 2 * fs), 185), normal((T, d), 186, 0.1)
+    dx, dw13, dw2 = shared_ffn_backward(x, gu, dy, w13, w2)
+    for i, got in ((0, dx), (1, dw13), (2, dw2)):
+        one = shared_ffn_backward(x, gu, dy, w13, w2, need=[j == i for j in range(3)])[i]
+        assert torch.equal(one, got), i
+    cols = torch.cat([torch.arange(0, fs, 301), torch.tensor([fs - 1])]).cuda()
+    few = S24 * T
+    for j in range(S):
+        g, u = gu[:, j, cols].to(F8), gu[:, j, fs + cols].to(F8)
+        h = g * torch.sigmoid(g) * u
+        want = dy.to(F8).t() @ h
+        tol = (B + 17 * S24 + few) * (dy.to(F8).abs().t() @ h.abs())
+        within(dw2[j][:, cols], want, rounded(want, tol), 2, f"dw2 of expert {j}")
+        dh = dy.to(F8) @ w2[j].to(F8)[:, cols]
+        du = dh * g * torch.sigmoid(g)
+        want = du.t() @ x.to(F8)
+        dh_e = d * S24 * (dy.to(F8).abs() @ w2[j].to(F8)[:, cols].abs())
+        e = B * du.abs() + 2 * (dh_e + 16 * S24 * dh.abs()) * (g * torch.sigmoid(g)).abs()
+        tol = (e + few * (du.abs() + e)).t() @ x.to(F8).abs()
+        within(dw13[j][fs + cols], want, rounded(want, tol), 2, f"dw13 (up) of expert {j}")
