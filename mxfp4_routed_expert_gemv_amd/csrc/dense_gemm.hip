@@ -20,12 +20,12 @@
 // parts are rows of a product, its sums of a row and of the one kRows further are
 // added; where they are contracted over, the other operand's rows are taken twice.
 // From about 2000 tokens the matrix cores bound all six (d 7168, two experts of 2048,
-// T = 16384: dx 1.35 ms = 1.42 PFLOP/s, dW13 1.27, dW2 1.21, dh 1.02, whose epilogue
-// moves 670 MB; the library's product of such sizes reaches 1.4 to 1.5): they are
-// busy 60 to 65 % of the time at the 1.95 GHz that this load leaves, what is missing
-// being LDS reads and copies between them.  Below about 300 tokens reading the
-// weights (backward: and writing their gradients) bounds them: T = 1 forward 46 us
-// for 176 MB, backward 116 us for 352 MB.
+// T = 16384: dx 1.36 ms = 1.41 PFLOP/s, dW13 and dW2 2.21 ms = 1.31, dh 0.85 ms =
+// 1.13, whose epilogue moves 670 MB; the library's product of such sizes reaches 1.4
+// to 1.5): they are busy 60 to 65 % of the time at the 1.95 GHz that this load
+// leaves, what is missing being LDS reads and copies between them.  Below about 300
+// tokens reading the weights (backward: and writing their gradients) bounds them:
+// T = 1 forward 46 us for 176 MB, backward 116 us for 352 MB.
 #include <algorithm>
 
 #include "internal.h"
@@ -866,22 +866,25 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   grads[2].a = static_cast<const uint16_t*>(dy);
   grads[2].b = ws.h;
   grads[2].o0 = dw2;
-  // One launch for the three: 300 us in all at T = 517 (370 in three launches), 1195
-  // at 4096 (1235).  From four rounds of dx on a partly filled last round weighs
-  // less than what a workgroup saves by going from tile to tile: 4.70 ms in three
-  // launches at T = 16384 (4.74 in one).
-  // On 64 x 64 tiles one launch is worth it for small layers (4 x 256 x 128: 10 us
-  // against 16; 163 x 2624 x 512, 1100 tiles: 25 against 34); where the weight
-  // gradients alone fill the chip they are faster on their own tiles, beside a dx
-  // whose contraction is split (64 x 7168 x 4096, 21600 tiles: 142 us against 150).
+  // One launch for the three: backward 257 us at T = 517 (279 in three launches), 1158
+  // at 4096 (1181).  From four rounds of dx on a partly filled last round weighs
+  // less than what a workgroup saves by going from tile to tile: 4.53 ms in launches
+  // of their own at T = 16384 (4.63 in one); and without dx there is nothing to fill
+  // the gaps with (T = 517 190 us against 201).
+  // On 64 x 64 tiles one launch is worth it for smaller layers (tokens x d x fs x
+  // experts: 4 x 256 x 128 16 us against 25; 128 x 4096 x 512 x 3, 4700 tiles: 44, 57;
+  // 64 x 4096 x 1024 x 3, 9300 tiles: 57, 63; without dx, 16 x 4096 x 512 x 3: 35, 34);
+  // where the weight gradients alone fill the chip they are faster on their own tiles,
+  // beside a dx whose contraction is split (64 x 7168 x 2048 x 2, 21600 tiles: 127 us
+  // against 140).
   const int tile = plan_product(kDX, s).tile;
   const int64_t dx_tiles = ((s.T + 255) / 256) * ((s.d + 255) / 256);
   const int64_t t64 = (s.T + 63) / 64, d64 = (s.d + 63) / 64,
                 f64 = ((int64_t)s.n_shared * s.f_shared + 31) / 32;   // of 2 F
   const int64_t tiles64 = t64 * d64 + f64 * d64 + (f64 + 1) / 2 * d64;
-  if (tile == kTile256 && dx_tiles < 4 * kCUs) return launch_grads_tile<256, 256, 2, 4, 2>(s, grads, st);
-  if (tile == kTile128 || tile == kTile128x256) return launch_grads_tile<128, 256, 2, 4, 3>(s, grads, st);
-  if (tile == kTile64 && tiles64 <= 4096) return launch_grads_tile<64, 64, 2, 2, 3>(s, grads, st);
+  if (dx && tile == kTile256 && dx_tiles < 4 * kCUs) return launch_grads_tile<256, 256, 2, 4, 2>(s, grads, st);
+  if (dx && (tile == kTile128 || tile == kTile128x256)) return launch_grads_tile<128, 256, 2, 4, 3>(s, grads, st);
+  if (tile == kTile64 && tiles64 <= (dx ? 10240 : 4096)) return launch_grads_tile<64, 64, 2, 2, 3>(s, grads, st);
   if (dx && (e = launch_product<kDX>(s, grads[0], ws.part, st)) != hipSuccess) return e;
   if (const int64_t rows = dw13 && dw2 ? tail_rows(s) : -1; rows >= 0) {
     grads[0].o0 = nullptr;
