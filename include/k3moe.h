@@ -460,7 +460,7 @@ k3moe_status k3moe_cache_stats_get(const k3moe_expert_cache* cache, k3moe_cache_
  * Sums are fp32.  g, u (kept for the backward), h, dg, du and every gradient
  * are rounded to bf16 once: they are bf16 operands of the next product (which
  * is why this y is not the bits of k3moe_shared_ffn, whose h keeps 16 bits); up
- * to 16 tokens h, dg and du keep 16 bits here too.
+ * to 16 tokens h, dg and du keep 15 bits or more, as two bf16 parts.
  * The reference pages only run their model; a training pass over its
  * always-on experts is this library's.
  * ------------------------------------------------------------------------- */

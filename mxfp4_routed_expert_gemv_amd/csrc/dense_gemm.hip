@@ -12,7 +12,7 @@
 // the gate and up sums of one wave, its derivative in the epilogue of dh.
 // g, u (for the backward), h, dg, du and every output are rounded to bf16
 // once, from fp32: they are operands of the next bf16 product.  Up to kRows tokens
-// h, dg and du keep 16 bits, as two bf16 parts in two blocks of kRows rows: their
+// h, dg and du keep 15 bits or more, as two bf16 parts in two blocks of kRows rows: their
 // products read the weights' every byte whatever the rows, and a rounding to 8 bits
 // of so few values does not average out (an output's error of sqrt(2) of its own
 // rounding alone, but up to twice that for one token of a small layer).  That costs
@@ -189,13 +189,24 @@ __device__ __forceinline__ uint4 pack8(f32x4_t a, f32x4_t b) {
   exchange(p.y, q.y);
   return make_uint4(p.x, p.y, q.x, q.y);
 }
-// What rounding to bf16 leaves of v (0 where that is not a number).
-__device__ __forceinline__ float rest(float v) {
-  const float d = v - bf16_lo(pack2(v, v));
-  return fabsf(d) < INFINITY ? d : 0.0f;
+// v as two bf16 parts (the second once rounded): its top 8 bits and the rest.  Both
+// have v's sign and neither is zero unless v is (a v of 8 bits is halved), and an
+// infinity or NaN is both: a part times an infinity is what v times it is.
+__device__ __forceinline__ float take_rest(float& v) {
+  const float top = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), d = v - top;
+  const bool whole = !(fabsf(d) > 0.0f);   // 8 bits, or not finite
+  v = whole ? 0.5f * v : top;
+  return whole ? v : d;
 }
-__device__ __forceinline__ f32x4_t rest(f32x4_t v) {
-  return f32x4_t{rest(v[0]), rest(v[1]), rest(v[2]), rest(v[3])};
+__device__ __forceinline__ f32x4_t take_rest(f32x4_t& v) {
+  f32x4_t l;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    float x = v[r];
+    l[r] = take_rest(x);
+    v[r] = x;
+  }
+  return l;
 }
 __device__ __forceinline__ f32x4_t gated(f32x4_t ga, f32x4_t up) {
   f32x4_t h;
@@ -208,24 +219,27 @@ __device__ __forceinline__ f32x4_t gated(f32x4_t ga, f32x4_t up) {
 template <bool FEW>
 __device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, f32x4_t ga, f32x4_t up) {
   const int F = g.S * g.fs;
-  const f32x4_t h = gated(ga, up);
+  f32x4_t h = gated(ga, up);
+  if (FEW && g.parts) {
+    const f32x4_t l = take_rest(h);
+    *reinterpret_cast<uint2*>(g.o1 + (size_t)(m + kRows) * F + n) = pack4(l[0], l[1], l[2], l[3]);
+  }
   uint16_t* gu = static_cast<uint16_t*>(g.o0) + (size_t)m * 2 * F + gate_col(n, g.fs);
   *reinterpret_cast<uint2*>(gu) = pack4(ga[0], ga[1], ga[2], ga[3]);
   *reinterpret_cast<uint2*>(gu + g.fs) = pack4(up[0], up[1], up[2], up[3]);
   *reinterpret_cast<uint2*>(g.o1 + (size_t)m * F + n) = pack4(h[0], h[1], h[2], h[3]);
-  if (FEW && g.parts) {
-    const f32x4_t l = rest(h);
-    *reinterpret_cast<uint2*>(g.o1 + (size_t)(m + kRows) * F + n) = pack4(l[0], l[1], l[2], l[3]);
-  }
 }
 template <bool FEW>
 __device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, bool in, f32x4_t ga0,
                                              f32x4_t up0, f32x4_t ga1, f32x4_t up1) {
   const int F = g.S * g.fs;
-  const f32x4_t h0 = gated(ga0, up0), h1 = gated(ga1, up1);
+  f32x4_t h0 = gated(ga0, up0), h1 = gated(ga1, up1);
+  uint4 l{};
+  if (FEW && g.parts) {
+    const f32x4_t l0 = take_rest(h0), l1 = take_rest(h1);
+    l = pack8(l0, l1);
+  }
   const uint4 ga = pack8(ga0, ga1), up = pack8(up0, up1), h = pack8(h0, h1);
-  uint4 l = h;
-  if (FEW && g.parts) l = pack8(rest(h0), rest(h1));
   if (!in) return;
   uint16_t* gu = static_cast<uint16_t*>(g.o0) + (size_t)m * 2 * F + gate_col(n, g.fs);
   *reinterpret_cast<uint4*>(gu) = ga;
@@ -234,10 +248,10 @@ __device__ __forceinline__ void store_gateup(const DenseArgs& g, int m, int n, b
   if (FEW && g.parts) *reinterpret_cast<uint4*>(g.o1 + (size_t)(m + kRows) * F + n) = l;
 }
 // dh's sums v of row m: dg, du and h from the kept g and u (two bf16 values a word),
-// and what their rounding leaves.
-template <bool REST>
-__device__ __forceinline__ void gate_grads(const float* v, uint32_t gw, uint32_t uw, uint32_t (&out)[3],
-                                           uint32_t (&low)[3]) {
+// or, of parts, their first and second parts.
+template <bool FEW>
+__device__ __forceinline__ void gate_grads(const float* v, uint32_t gw, uint32_t uw, bool parts,
+                                           uint32_t (&out)[3], uint32_t (&low)[3]) {
   float d[2][3];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -249,8 +263,11 @@ __device__ __forceinline__ void gate_grads(const float* v, uint32_t gw, uint32_t
   }
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
+    if (FEW && parts) {
+      const float l0 = take_rest(d[0][i]), l1 = take_rest(d[1][i]);
+      low[i] = pack2(l0, l1);
+    }
     out[i] = pack2(d[0][i], d[1][i]);
-    if (REST) low[i] = pack2(rest(d[0][i]), rest(d[1][i]));
   }
 }
 template <bool FEW, int W, typename V>   // W words of two columns each
@@ -261,8 +278,8 @@ __device__ __forceinline__ void store_dhid_words(const DenseArgs& g, int m, int 
   V out[3], low[3];
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    uint32_t a[3], b[3];
-    gate_grads<FEW>(v + 2 * w, gw[w], uw[w], a, b);
+    uint32_t a[3], b[3] = {0, 0, 0};
+    gate_grads<FEW>(v + 2 * w, gw[w], uw[w], g.parts, a, b);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       out[i][w] = a[i];

@@ -636,9 +636,9 @@ def test_shared_tiles_and_splits(T, d, fs, S):
 @pytest.mark.parametrize("T,d,fs,S", [(1, 256, 128, 1), (2, 64, 32, 3), (4, 256, 128, 1), (15, 512, 64, 3),
                                       (16, 320, 256, 2), (1, 2048, 1984, 2), (3, 4096, 512, 1)])
 def test_shared_values_of_few_tokens_keep_16_bits(T, d, fs, S, monkeypatch):
-    """Up to 16 tokens h, dg and du are two bf16 parts: the first leaves 2^-8 of a
-    value, the second 2^-8 of that.  So an fp32 y is off by 2^-16 of its terms, and a
-    bf16 output, as its rounding to the nearest moves by no more than its argument
+    """Up to 16 tokens h, dg and du are two bf16 parts: the first, cut off, leaves 2^-7
+    of a value, the second 2^-8 of that.  So an fp32 y is off by 2^-15 of its terms,
+    and a bf16 output, as its rounding to the nearest moves by no more than its argument
     does, by the exact value's own rounding and twice such a bound."""
     require_gpu()
     import sys
@@ -649,7 +649,7 @@ def test_shared_values_of_few_tokens_keep_16_bits(T, d, fs, S, monkeypatch):
     grads = shared_ffn_backward(x, gu, dy, w13, w2)
     torch.cuda.synchronize()
     ref = Ref(x, w13, w2)
-    monkeypatch.setattr(sys.modules[__name__], "B", 2.0 ** -16)
+    monkeypatch.setattr(sys.modules[__name__], "B", 2.0 ** -15)
     want, tol = ref.forward()[:2]
     back = ref.backward(gu, dy)
     monkeypatch.undo()
@@ -689,3 +689,39 @@ def test_shared_weight_gradients_of_large_batches(T, d, fs, S):
         e = B * du.abs() + 2 * (dh_e + 16 * S24 * dh.abs()) * (g * torch.sigmoid(g)).abs()
         tol = (e + few * (du.abs() + e)).t() @ x.to(F8).abs()
         within(dw13[j][fs + cols], want, rounded(want, tol), 2, f"dw13 (up) of expert {j}")
+
+
+@pytest.mark.parametrize("T", [3, 16, 17, 40])
+def test_shared_infinite_gradients_and_weights(T):
+    """An infinite dy or weight gives infinities and NaN where the formulas do, with
+    one part to a value or two, and leaves what it does not enter."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.shared import shared_ffn_backward, shared_ffn_train
+    d, fs, S = 256, 96, 2
+    x, w13, w2 = problem(T, d, fs, S, 190)
+    y, gu = shared_ffn_train(x, w13, w2)
+    dy = normal((T, d), 195, 0.1)
+    fine = shared_ffn_backward(x, gu, dy, w13, w2)
+    dy[2, 7] = float("inf")
+    dx, dw13, dw2 = shared_ffn_backward(x, gu, dy, w13, w2)
+    torch.cuda.synchronize()
+
+    def same_kind(got, want, name):
+        assert torch.equal(torch.isnan(got), torch.isnan(want)), name
+        inf = torch.isinf(want)
+        assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf].to(F8), want[inf]), name
+    keep = torch.arange(T) != 2
+    assert torch.equal(dx[keep], fine[0][keep]) and not torch.isfinite(dx[2]).any()
+    for j in range(S):
+        g, u = gu[:, j, :fs].to(F8).cpu(), gu[:, j, fs:].to(F8).cpu()
+        h = g * torch.sigmoid(g) * u
+        same_kind(dw2[j].cpu(), sum(dy[t].to(F8).cpu()[:, None] * h[t] for t in range(T)), "dw2")
+        assert torch.isinf(dw2[j][7]).all() and torch.isinf(dw13[j]).all()
+    w2[1, 9, 5] = float("-inf")
+    got = shared_ffn_train(x, w13, w2)[0]
+    torch.cuda.synchronize()
+    g, u = (x.to(F8) @ w.to(F8).t() for w in (w13[1, 5:6], w13[1, fs + 5:fs + 6]))
+    want = torch.where((g * u)[:, 0] > 0, -math.inf, math.inf)   # silu has its argument's sign
+    assert torch.equal(got[:, 9].to(F8), want)
+    others = torch.arange(d) != 9
+    assert torch.equal(got[:, others], y[:, others])
