@@ -99,5 +99,7 @@ class _SharedFFN(torch.autograd.Function):
 
 def shared_ffn(x, w13, w2):
     """The shared experts as a torch operation: y [T][d] bf16, differentiable once
-    in x, w13 and w2."""
+    in x, w13 and w2.  Capture its backward together with its forward, with no eager
+    graph of the same leaves alive (torch accumulates their gradients on the stream
+    that graph was recorded on), or capture the two halves above."""
     return _SharedFFN.apply(x, w13, w2)

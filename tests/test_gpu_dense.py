@@ -725,3 +725,13 @@ def test_shared_infinite_gradients_and_weights(T):
     assert torch.equal(got[:, 9].to(F8), want)
     others = torch.arange(d) != 9
     assert torch.equal(got[:, others], y[:, others])
+
+
+@pytest.mark.parametrize("xd", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,k,zero", [(1, 1280, True), (3, 4096, False), (7, 128, True), (12, 2176, True),
+                                      (30, 1152, False), (50, 1280, True), (90, 1152, True), (300, 640, False)])
+def test_w4_groups_of_32_in_whole_blocks(T, k, zero, xd):
+    """Contractions that are a multiple of 128, whose four scales a block are copied
+    together; and what the gated form's two halves read."""
+    require_gpu()
+    test_w4_products(T, 134, k, 32, zero, xd)
