@@ -620,8 +620,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile(DenseArgs g) {
   run_tiles<P, BM, BN, WM, WN, RING, SPLIT>(g, at, sA, sB);
 }
 
-// dx, dW13 and dW2 in one launch: none depends on another, and none's tiles fill
-// its last round of CUs.  kCUs workgroups for every n[p] rounds of product p, dx's
+// dx (on XM x XN tiles), dW13 and dW2 in one launch: none depends on another, and
+// none's tiles fill its last round of CUs.  kCUs workgroups for every n[p] rounds of product p, dx's
 // first (they are the longest); a CU that has no dx tile, or is done with it, takes
 // a workgroup of the next product.
 constexpr int kCUs = 256;
@@ -629,16 +629,18 @@ struct GradArgs {
   DenseArgs g[3];
   int n[3], wgs[3];
 };
-template <int BM, int BN, int WM, int WN, int RING>
+template <int XM, int XN, int XRING, int BM, int BN, int RING, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void dense_grads(GradArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t sA[RING * BM * 2 * kBK];
-  __shared__ __attribute__((aligned(16))) uint8_t sB[RING * BN * 2 * kBK];
+  constexpr int kA = XRING * XM > RING * BM ? XRING * XM : RING * BM;
+  constexpr int kB = XRING * XN > RING * BN ? XRING * XN : RING * BN;
+  __shared__ __attribute__((aligned(16))) uint8_t sA[kA * 2 * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sB[kB * 2 * kBK];
   int wg = blockIdx.x;   // (every product's first is a multiple of 8, so wg & 7 is the XCD)
   auto items = [&](int p) {
     const int w = wg >> 3, r = w / (kCUs / 8) * a.n[p];
     return Items{kCUs, wg & 7, w % (kCUs / 8), r, r + a.n[p]};
   };
-  if (wg < a.wgs[0]) return run_tiles<kDX, BM, BN, WM, WN, RING, false>(a.g[0], items(0), sA, sB);
+  if (wg < a.wgs[0]) return run_tiles<kDX, XM, XN, WM, WN, XRING, false>(a.g[0], items(0), sA, sB);
   wg -= a.wgs[0];
   if (wg < a.wgs[1]) return run_tiles<kDW13, BM, BN, WM, WN, RING, false>(a.g[1], items(1), sA, sB);
   wg -= a.wgs[1];
@@ -802,7 +804,7 @@ hipError_t launch_product(const k3moe_shape& s, DenseArgs g, float* part, hipStr
 // The three gradients in one launch (g.o0 NULL: not wanted).  A workgroup takes as
 // many of the short tiles as 48 stages make (16 on the smallest tiles, three to a
 // CU), so that its start weighs little.
-template <int BM, int BN, int WM, int WN, int RING>
+template <int XM, int XN, int XRING, int BM, int BN, int RING, int WM, int WN>
 hipError_t launch_grads_tile(const k3moe_shape& s, const DenseArgs (&g)[3], hipStream_t st) {
   GradArgs a;
   const int64_t F = (int64_t)s.n_shared * s.f_shared, T = s.T, d = s.d;
@@ -811,7 +813,8 @@ hipError_t launch_grads_tile(const k3moe_shape& s, const DenseArgs (&g)[3], hipS
   for (int p = 0; p < 3; ++p) {
     a.g[p] = g[p];
     const int64_t rows = p == 2 ? g[p].m_hi : M[p];
-    const int64_t items = (rows + BM - 1) / BM * ((N[p] + BN - 1) / BN);
+    const int bm = p == 0 ? XM : BM, bn = p == 0 ? XN : BN;
+    const int64_t items = (rows + bm - 1) / bm * ((N[p] + bn - 1) / bn);
     const int64_t rounds = (items + kCUs - 1) / kCUs, nst = (K[p] + kBK - 1) / kBK;
     const int64_t least = std::max<int64_t>((BM == 64 ? 16 : 48) / nst, 1);
     a.n[p] = (int)std::min(rounds, p == 0 ? rounds : p == 1 ? std::max(least, (rounds + 1) / 2) : least);
@@ -819,7 +822,7 @@ hipError_t launch_grads_tile(const k3moe_shape& s, const DenseArgs (&g)[3], hipS
     total += a.wgs[p];
   }
   if (total == 0) return hipSuccess;
-  dense_grads<BM, BN, WM, WN, RING><<<(unsigned)total, 64 * WM * WN, 0, st>>>(a);
+  dense_grads<XM, XN, XRING, BM, BN, RING, WM, WN><<<(unsigned)total, 64 * WM * WN, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -883,7 +886,7 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   grads[2].a = static_cast<const uint16_t*>(dy);
   grads[2].b = ws.h;
   grads[2].o0 = dw2;
-  // One launch for the three: backward 257 us at T = 517 (279 in three launches), 1158
+  // One launch for the three: backward 254 us at T = 517 (279 in three launches), 1158
   // at 4096 (1181).  From four rounds of dx on a partly filled last round weighs
   // less than what a workgroup saves by going from tile to tile: 4.53 ms in launches
   // of their own at T = 16384 (4.63 in one); and without dx there is nothing to fill
@@ -899,14 +902,23 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   const int64_t t64 = (s.T + 63) / 64, d64 = (s.d + 63) / 64,
                 f64 = ((int64_t)s.n_shared * s.f_shared + 31) / 32;   // of 2 F
   const int64_t tiles64 = t64 * d64 + f64 * d64 + (f64 + 1) / 2 * d64;
-  if (dx && tile == kTile256 && dx_tiles < 4 * kCUs) return launch_grads_tile<256, 256, 2, 4, 2>(s, grads, st);
-  if (dx && (tile == kTile128 || tile == kTile128x256)) return launch_grads_tile<128, 256, 2, 4, 3>(s, grads, st);
-  if (tile == kTile64 && tiles64 <= (dx ? 10240 : 4096)) return launch_grads_tile<64, 64, 2, 2, 3>(s, grads, st);
+  if (dx && tile == kTile256 && dx_tiles < 4 * kCUs)
+    return launch_grads_tile<256, 256, 2, 256, 256, 2, 2, 4>(s, grads, st);
+  if (dx && (tile == kTile128 || tile == kTile128x256)) {
+    // (the weight gradients on 256 x 256 tiles, where there are some: T = 517 254 us
+    // against 264 on dx's 128 x 256, 1000 358, 394; 2000 x 2048 x 1024, 96 tiles of
+    // theirs, 73, 85; 1061 x 3616 x 128, 22 tiles, 44, 37)
+    const int64_t d256 = (s.d + 255) / 256, f256 = ((int64_t)s.n_shared * s.f_shared + 127) / 128;
+    if (d256 * f256 * 3 / 2 >= 64) return launch_grads_tile<128, 256, 3, 256, 256, 2, 2, 4>(s, grads, st);
+    return launch_grads_tile<128, 256, 3, 128, 256, 3, 2, 4>(s, grads, st);
+  }
+  if (tile == kTile64 && tiles64 <= (dx ? 10240 : 4096))
+    return launch_grads_tile<64, 64, 3, 64, 64, 3, 2, 2>(s, grads, st);
   if (dx && (e = launch_product<kDX>(s, grads[0], ws.part, st)) != hipSuccess) return e;
   if (const int64_t rows = dw13 && dw2 ? tail_rows(s) : -1; rows >= 0) {
     grads[0].o0 = nullptr;
     grads[2].m_hi = s.d - (int)rows;
-    if ((e = launch_grads_tile<256, 256, 2, 4, 2>(s, grads, st)) != hipSuccess || rows == 0) return e;
+    if ((e = launch_grads_tile<256, 256, 2, 256, 256, 2, 2, 4>(s, grads, st)) != hipSuccess || rows == 0) return e;
     grads[2].m_lo = grads[2].m_hi;
     grads[2].m_hi = s.d;
     dense_tile<kDW2, 128, 128, 2, 4, 3><<<grouped_grid(), 512, 0, st>>>(grads[2]);

@@ -735,3 +735,11 @@ def test_w4_groups_of_32_in_whole_blocks(T, k, zero, xd):
     together; and what the gated form's two halves read."""
     require_gpu()
     test_w4_products(T, 134, k, 32, zero, xd)
+
+
+@pytest.mark.parametrize("T,d,fs,S", [(1101, 3520, 768, 2), (2500, 1536, 1024, 1), (7190, 1088, 128, 1),
+                                      (3001, 2560, 1600, 2)])
+def test_shared_gradients_in_one_launch(T, d, fs, S):
+    """Gradients whose tiles share a launch, with dx on smaller tiles than the
+    weights' and on the same; alone they come from launches of their own."""
+    test_shared_train_and_backward(T, d, fs, S)
