@@ -553,11 +553,11 @@ k3moe_status k3moe_grad_norm(const k3moe_tensor* tensors, int32_t n, float* norm
                              size_t workspace_bytes, void* stream);
 /* The same norm, and out = data * min(1, max_norm / norm) for every tensor,
  * rounded to out_dtype.  The factor comes from the fp64 norm (finite gradients
- * are clipped even where *norm is past fp32's range); a norm of infinities or
- * NaN scales nothing (out = data), and the caller sees it in *norm.  In place
- * (out == data) a step that needs no clipping is left untouched.  Errors: as above; EINVAL also for a max_norm
- * that is negative or NaN and for an out that overlaps any tensor but its own
- * data. */
+ * are clipped even where *norm is past fp32's range, and by factors below it);
+ * a norm of infinities or NaN scales nothing (out = data), and the caller sees
+ * it in *norm.  In place (out == data) a step that needs no clipping is left
+ * untouched.  Errors: as above; EINVAL also for a max_norm that is negative or
+ * NaN and for an out that overlaps any tensor but its own data. */
 k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_norm, float* norm,
                              void* workspace, size_t workspace_bytes, void* stream);
 

@@ -126,7 +126,13 @@ __global__ __launch_bounds__(256) void scale_all(Table t, const double* __restri
   if (n > 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
   // (a norm of infinities or NaN leaves the gradients as they are)
   const bool scaled = v < (double)INFINITY && v > (double)max_norm;
-  const float f = scaled ? (float)((double)max_norm / v) : 1.0f;
+  const double factor = scaled ? (double)max_norm / v : 1.0;
+  // Below fp32's normal range (a norm past max_norm 2^126) the factor has fewer bits in
+  // fp32 than its products with such gradients can hold: they are taken in fp64 there,
+  // and rounded once.
+  const bool tiny = factor < 0x1p-126;
+  const float f = (float)factor;
+  auto times = [&](float g) { return tiny ? (float)((double)g * factor) : g * f; };
   for (int w = blockIdx.x; w < t.units; w += gridDim.x) {
     const int u = t.units - 1 - w;
     const Entry& e = t.e[tensor_of(t, u)];
@@ -138,7 +144,7 @@ __global__ __launch_bounds__(256) void scale_all(Table t, const double* __restri
         load8(e, i, v);
         if (scaled)
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) v[j] *= f;
+          for (int j = 0; j < kVec; ++j) v[j] = times(v[j]);
         if (e.out_f32) {
           F32x8 w;
 #pragma unroll
@@ -153,7 +159,7 @@ __global__ __launch_bounds__(256) void scale_all(Table t, const double* __restri
         }
       } else {
         for (int64_t q = i; q < b; ++q) {
-          const float v = scaled ? load1(e, q) * f : load1(e, q);
+          const float v = scaled ? times(load1(e, q)) : load1(e, q);
           if (e.out_f32) static_cast<float*>(e.out)[q] = v;
           else static_cast<uint16_t*>(e.out)[q] = f32_to_bf16(v);
         }

@@ -1,0 +1,44 @@
+"""The dense operators on the GPU where a call is at the edge of what the header
+allows.  Tolerances as in test_gpu_dense: half a step of a type is eps / 2 of a
+value (bf16 2^-8, fp32 2^-24)."""
+import math
+
+import pytest
+import torch
+
+from gpu_util import log, require_gpu
+from test_gpu_dense import B, F8, S24
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value,count,max_norm", [
+    (3e38, 4, 1e-3), (3e38, 4, 1e-7), (3e38, 70_001, 1.0), (3e38, 16_411, 1e-30), (1e25, 9, 1e-14),
+    (2e38, 3, 1e-1)])
+def test_clip_by_a_factor_below_fp32s_normal_range(value, count, max_norm, dt, out):
+    """max_norm / norm under 2^-126 is no normal fp32 number, but the clipped gradients
+    are: each is off by its own rounding to fp32 (the factor is fp64, off by a few
+    2^-53), a bf16 one by bf16's on top, and by max_norm's, which enters the call as a C
+    float: m (1 + a) g / norm (1 + b) with |a|, |b| <= 2^-24."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.grads import clip_grads
+    g = torch.full((count,), value, device="cuda").to(dt)
+    g[1] = -g[1] / 3
+    g[2] = g[2] / 1024
+    norm = math.sqrt(math.fsum((g.to(F8) ** 2).tolist()))
+    factor = max_norm / norm
+    assert factor < 2.0 ** -126
+    want = g.to(F8) * factor
+    eps = 2 * S24 * 1.001 + (B if out == torch.bfloat16 else 0.0)
+    for name, outs in (("into", [torch.empty_like(g, dtype=out)]), ("in place", None)):
+        if outs is None and dt != out:
+            continue
+        clip_grads([g], max_norm, out=outs)
+        torch.cuda.synchronize()
+        got = (outs or [g])[0].to(F8)
+        worst = float(((got - want).abs() / want.abs()).max())
+        log(f"  {value:g} x {count}, max_norm {max_norm:g}, {dt} -> {out} {name}: factor {factor:.3g}, worst {worst:.3g}")
+        # (smallest outputs here: 1e-30 / sqrt(16411) / 1024 = 7.6e-36, normal)
+        assert worst <= eps
