@@ -467,8 +467,9 @@ k3moe_status k3moe_cache_stats_get(const k3moe_expert_cache* cache, k3moe_cache_
 /* x [T][d] bf16 -> gu [T][n_shared][2 f_shared] bf16, the pre-activations
  * (gate, then up, of every expert) for k3moe_shared_ffn_backward, and
  * y [T][d] in out_dtype.  Errors: EINVAL (no shared experts, NULL pointers,
- * bank not matching), EUNSUPPORTED (bank not BF16, x_dtype), ESHAPE, EALIGN,
- * EWORKSPACE.  Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_SHARED_TRAIN). */
+ * bank not matching; gu, y or the workspace overlapping the inputs or each
+ * other), EUNSUPPORTED (bank not BF16, x_dtype), ESHAPE, EALIGN, EWORKSPACE.
+ * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_SHARED_TRAIN). */
 k3moe_status k3moe_shared_ffn_train(const k3moe_shape* shape, const k3moe_expert_bank* bank,
                                     const void* x, void* gu, void* y, void* workspace,
                                     size_t workspace_bytes, void* stream);
@@ -477,8 +478,8 @@ k3moe_status k3moe_shared_ffn_train(const k3moe_shape* shape, const k3moe_expert
  * output that is NULL is not computed (all three NULL: nothing is enqueued).
  * The number of tokens can change the order of a sum, and so the last bits of a
  * token's values; the same call gives the same bits.
- * T = 0 writes zeros to dw13 and dw2.  The outputs must not overlap the inputs
- * or each other.  Errors: as for k3moe_shared_ffn_train.
+ * T = 0 writes zeros to dw13 and dw2.  The outputs and the workspace must not
+ * overlap the inputs or each other (EINVAL).  Errors: as for k3moe_shared_ffn_train.
  * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_SHARED_BACKWARD). */
 k3moe_status k3moe_shared_ffn_backward(const k3moe_shape* shape, const k3moe_expert_bank* bank,
                                        const void* x, const void* gu, const void* dy, void* dx,

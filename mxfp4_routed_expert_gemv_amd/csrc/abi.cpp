@@ -192,20 +192,38 @@ k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_
                     const void* x, void* out, void* workspace, size_t workspace_bytes, void* stream,
                     bool glu);
 
-// out must not touch what other workgroups still read.
+// An operand's bytes; NULL or empty ones overlap nothing.
+struct Region {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+// What a call writes must not touch what other workgroups still read or write.
+template <size_t W, size_t R>
+k3moe_status check_disjoint(const Region (&written)[W], const Region (&read)[R]) {
+  auto meet = [](const Region& a, const Region& b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes && b.bytes && p < q + b.bytes && q < p + a.bytes;
+  };
+  for (size_t i = 0; i < W; ++i) {
+    for (size_t j = 0; j < R; ++j)
+      if (meet(written[i], read[j]))
+        return fail(K3MOE_EINVAL, "%s overlaps %s", written[i].name, read[j].name);
+    for (size_t j = 0; j < i; ++j)
+      if (meet(written[i], written[j]))
+        return fail(K3MOE_EINVAL, "%s overlaps %s", written[i].name, written[j].name);
+  }
+  return K3MOE_OK;
+}
+
 k3moe_status check_w4_out(const k3moe_w4_matrix& w, size_t x_bytes, const void* x,
                           const void* out, size_t out_bytes) {
   const size_t scales = (size_t)w.n * (w.k / w.group);
-  const struct { const void* p; size_t bytes; const char* name; } in[] = {
-      {x, x_bytes, "x"}, {w.codes, (size_t)w.n * (w.k / 2), "codes"},
-      {w.scale, 2 * scales, "scale"}, {w.zero, w.zero ? scales : 0, "zero"}};
-  const uintptr_t o = reinterpret_cast<uintptr_t>(out);
-  for (const auto& i : in) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(i.p);
-    if (i.bytes && o < a + i.bytes && a < o + out_bytes)
-      return fail(K3MOE_EINVAL, "out overlaps %s", i.name);
-  }
-  return K3MOE_OK;
+  const Region written[] = {{out, out_bytes, "out"}};
+  const Region read[] = {{x, x_bytes, "x"}, {w.codes, (size_t)w.n * (w.k / 2), "codes"},
+                         {w.scale, 2 * scales, "scale"}, {w.zero, scales, "zero"}};
+  return check_disjoint(written, read);
 }
 
 constexpr int kMaxTensors = 1 << 20;
@@ -724,6 +742,12 @@ k3moe_status k3moe_shared_ffn_train(const k3moe_shape* shape, const k3moe_expert
   size_t need = 0;
   carve_shared_train(s, false, nullptr, &need);
   K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  const size_t td = (size_t)s.T * s.d, tf = (size_t)s.T * s.n_shared * s.f_shared;
+  const size_t w = (size_t)s.n_shared * s.f_shared * s.d * 2;
+  const Region written[] = {{gu, 4 * tf, "gu"}, {y, td * (s.out_dtype == K3MOE_F32 ? 4 : 2), "y"},
+                            {workspace, need, "workspace"}};
+  const Region read[] = {{x, 2 * td, "x"}, {bank->w13, 2 * w, "w13"}, {bank->w2, w, "w2"}};
+  K3_CHECK(check_disjoint(written, read));
   return hip_status(launch_shared_train(s, *bank, x, gu, y,
                                         carve_shared_train(s, false, workspace, nullptr),
                                         static_cast<hipStream_t>(stream)),
@@ -740,18 +764,26 @@ k3moe_status k3moe_shared_ffn_backward(const k3moe_shape* shape, const k3moe_exp
   K3_CHECK(opt_ptr(dx, "dx"));
   K3_CHECK(opt_ptr(dw13, "dw13"));
   K3_CHECK(opt_ptr(dw2, "dw2"));
+  const size_t w = (size_t)s.n_shared * s.f_shared * s.d * 2, td = (size_t)s.T * s.d * 2;
+  size_t need = 0;
+  if (s.T > 0) {
+    K3_CHECK(need_ptr(x, "x"));
+    K3_CHECK(need_ptr(gu, "gu"));
+    K3_CHECK(need_ptr(dy, "dy"));
+    carve_shared_train(s, true, nullptr, &need);
+    K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  }
+  // (without outputs the workspace is not used either)
+  const Region written[] = {{dx, td, "dx"}, {dw13, 2 * w, "dw13"}, {dw2, w, "dw2"},
+                            {workspace, dx || dw13 || dw2 ? need : 0, "workspace"}};
+  const Region read[] = {{x, td, "x"}, {gu, (size_t)s.T * s.n_shared * s.f_shared * 4, "gu"},
+                         {dy, td, "dy"}, {bank->w13, 2 * w, "w13"}, {bank->w2, w, "w2"}};
+  K3_CHECK(check_disjoint(written, read));
   if (s.T == 0) {
-    const size_t w = (size_t)s.n_shared * s.f_shared * s.d * 2;
     hipError_t e = launch_zero(dw13, 2 * w, st);
     if (e == hipSuccess) e = launch_zero(dw2, w, st);
     return hip_status(e, "k3moe_shared_ffn_backward launch");
   }
-  K3_CHECK(need_ptr(x, "x"));
-  K3_CHECK(need_ptr(gu, "gu"));
-  K3_CHECK(need_ptr(dy, "dy"));
-  size_t need = 0;
-  carve_shared_train(s, true, nullptr, &need);
-  K3_CHECK(check_ws(workspace, workspace_bytes, need));
   return hip_status(launch_shared_backward(s, *bank, x, gu, dy, dx, dw13, dw2,
                                            carve_shared_train(s, true, workspace, nullptr), st),
                     "k3moe_shared_ffn_backward launch");
