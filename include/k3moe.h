@@ -515,10 +515,10 @@ typedef struct k3moe_w4_matrix {
 /* Workspace of the two calls below (0, where NULL is accepted, up to 16 tokens,
  * and for invalid arguments); 256-byte aligned. */
 size_t k3moe_w4_workspace_bytes(const k3moe_w4_matrix* w, int64_t T);
-/* out [T][n] = x W^T.  Errors: EINVAL (NULL pointers, negative sizes, an out that
- * overlaps x or W), ESHAPE, EUNSUPPORTED, EALIGN (out is 16-byte aligned too),
- * EWORKSPACE.  The order of a token's sums, and so its last bits, can depend on T;
- * the same call gives the same bits. */
+/* out [T][n] = x W^T.  Errors: EINVAL (NULL pointers, negative sizes, an out or a
+ * workspace that overlaps x, W or the other), ESHAPE, EUNSUPPORTED, EALIGN (out is
+ * 16-byte aligned too), EWORKSPACE.  The order of a token's sums, and so its last
+ * bits, can depend on T; the same call gives the same bits. */
 k3moe_status k3moe_w4_linear(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype,
                              int32_t out_dtype, const void* x, void* out, void* workspace,
                              size_t workspace_bytes, void* stream);

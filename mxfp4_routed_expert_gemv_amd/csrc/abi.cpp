@@ -217,10 +217,11 @@ k3moe_status check_disjoint(const Region (&written)[W], const Region (&read)[R])
   return K3MOE_OK;
 }
 
-k3moe_status check_w4_out(const k3moe_w4_matrix& w, size_t x_bytes, const void* x,
-                          const void* out, size_t out_bytes) {
+k3moe_status check_w4_regions(const k3moe_w4_matrix& w, size_t x_bytes, const void* x,
+                              const void* out, size_t out_bytes, const void* workspace,
+                              size_t ws_bytes) {
   const size_t scales = (size_t)w.n * (w.k / w.group);
-  const Region written[] = {{out, out_bytes, "out"}};
+  const Region written[] = {{out, out_bytes, "out"}, {workspace, ws_bytes, "workspace"}};
   const Region read[] = {{x, x_bytes, "x"}, {w.codes, (size_t)w.n * (w.k / 2), "codes"},
                          {w.scale, 2 * scales, "scale"}, {w.zero, scales, "zero"}};
   return check_disjoint(written, read);
@@ -423,9 +424,11 @@ k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_
   K3_CHECK(opt_ptr(w->zero, "zero"));
   K3_CHECK(need_ptr(x, "x"));
   K3_CHECK(need_ptr(out, "out"));
-  K3_CHECK(check_ws(workspace, workspace_bytes, align256(w4_part_floats(*w, T) * sizeof(float))));
-  K3_CHECK(check_w4_out(*w, (size_t)T * w->k * (x_dtype == K3MOE_F32 ? 4 : 2), x, out,
-                        (size_t)T * (glu ? w->n / 2 : w->n) * (out_dtype == K3MOE_F32 ? 4 : 2)));
+  const size_t need = align256(w4_part_floats(*w, T) * sizeof(float));
+  K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  K3_CHECK(check_w4_regions(*w, (size_t)T * w->k * (x_dtype == K3MOE_F32 ? 4 : 2), x, out,
+                            (size_t)T * (glu ? w->n / 2 : w->n) * (out_dtype == K3MOE_F32 ? 4 : 2),
+                            workspace, need));
   return hip_status(launch_w4(*w, T, x_dtype == K3MOE_F32, out_dtype == K3MOE_F32, glu, x, out,
                               static_cast<float*>(workspace), static_cast<hipStream_t>(stream)),
                     glu ? "k3moe_w4_glu launch" : "k3moe_w4_linear launch");

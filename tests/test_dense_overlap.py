@@ -81,3 +81,21 @@ def test_training_backward_of_an_empty_batch():
         return k3.lib.k3moe_shared_ffn_backward(ctypes.byref(sh), ctypes.byref(b), None, None, None, None,
                                                 p["dw13"], p["dw2"], None, 0, None)
     each_overlap(sizes, ("dw13", "dw2"), call)
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_w4_workspace(glu):
+    """Above 16 tokens the workspace holds partial sums that workgroups write while
+    others still read the operands."""
+    fn = k3.lib.k3moe_w4_glu if glu else k3.lib.k3moe_w4_linear
+    n, k, group = 64, 512, 128
+    scales = n * (k // group)
+
+    def call(p):
+        w = k3.make_w4(n, k, group, p["codes"], p["scale"], p["zero"])
+        return fn(ctypes.byref(w), T, k3.F32, k3.BF16, p["x"], p["out"], p["workspace"], need, None)
+    need = k3.k3moe_w4_workspace_bytes(k3.make_w4(n, k, group, BASE, BASE, BASE), T)
+    assert need > 0
+    sizes = {"x": T * k * 4, "codes": n * k // 2, "scale": 2 * scales, "zero": scales,
+             "out": T * (n // 2 if glu else n) * 2, "workspace": need}
+    each_overlap(sizes, ("out", "workspace"), call)
