@@ -548,8 +548,8 @@ size_t k3moe_grad_workspace_bytes(int32_t n);
 /* *norm (device fp32) = sqrt(sum over the tensors of the squares of their
  * elements), summed in fp64 in a fixed order.  tensors is a HOST array (read
  * before the call returns), `out` fields ignored; n = 0 gives 0.  The same
- * tensor twice counts twice.  Errors: EINVAL (NULL, n < 0 or n > 2^20, sizes),
- * EUNSUPPORTED (dtypes), EALIGN, EWORKSPACE. */
+ * tensor twice counts twice.  Errors: EINVAL (NULL, n < 0 or n > 2^20, sizes, a
+ * workspace that overlaps a tensor or norm), EUNSUPPORTED (dtypes), EALIGN, EWORKSPACE. */
 k3moe_status k3moe_grad_norm(const k3moe_tensor* tensors, int32_t n, float* norm, void* workspace,
                              size_t workspace_bytes, void* stream);
 /* The same norm, and out = data * min(1, max_norm / norm) for every tensor,
@@ -558,7 +558,8 @@ k3moe_status k3moe_grad_norm(const k3moe_tensor* tensors, int32_t n, float* norm
  * a norm of infinities or NaN scales nothing (out = data), and the caller sees
  * it in *norm.  In place (out == data) a step that needs no clipping is left
  * untouched.  Errors: as above; EINVAL also for a max_norm that is negative or
- * NaN and for an out that overlaps any tensor but its own data. */
+ * NaN, for an out that overlaps any tensor but its own data, and for a norm or
+ * a workspace that overlaps a tensor's data or out. */
 k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_norm, float* norm,
                              void* workspace, size_t workspace_bytes, void* stream);
 

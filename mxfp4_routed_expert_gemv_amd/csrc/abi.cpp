@@ -199,13 +199,14 @@ struct Region {
   const char* name;
 };
 
+bool meet(const Region& a, const Region& b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && p < q + b.bytes && q < p + a.bytes;
+}
+
 // What a call writes must not touch what other workgroups still read or write.
 template <size_t W, size_t R>
 k3moe_status check_disjoint(const Region (&written)[W], const Region (&read)[R]) {
-  auto meet = [](const Region& a, const Region& b) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a.bytes && b.bytes && p < q + b.bytes && q < p + a.bytes;
-  };
   for (size_t i = 0; i < W; ++i) {
     for (size_t j = 0; j < R; ++j)
       if (meet(written[i], read[j]))
@@ -259,6 +260,26 @@ k3moe_status check_overlap(const k3moe_tensor* ts, int32_t n) {
                   s.out ? s.tensor : out_t, s.out ? any_t : s.tensor);
     if (s.hi > any) any = s.hi, any_t = s.tensor;
     if (s.out && s.hi > outs) outs = s.hi, out_t = s.tensor;
+  }
+  return K3MOE_OK;
+}
+
+// The workspace and, as the clipping writes it while tensors are still read, the
+// norm touch no tensor.  (k3moe_grad_norm writes it after the last read.)
+k3moe_status check_grad_regions(const k3moe_tensor* ts, int32_t n, bool clip, const float* norm,
+                                const void* workspace, size_t ws_bytes) {
+  const Region ws{workspace, ws_bytes, "workspace"}, nm{norm, sizeof(float), "norm"};
+  if (meet(ws, nm)) return fail(K3MOE_EINVAL, "workspace overlaps norm");
+  for (int32_t i = 0; i < n; ++i) {
+    const k3moe_tensor& t = ts[i];
+    const Region data{t.data, (size_t)t.numel * (t.dtype == K3MOE_F32 ? 4 : 2), "the data"};
+    const Region out{clip ? t.out : nullptr, (size_t)t.numel * (t.out_dtype == K3MOE_F32 ? 4 : 2),
+                     "the out"};
+    for (const Region* r : {&data, &out}) {
+      if (meet(ws, *r) || (clip && meet(nm, *r)))
+        return fail(K3MOE_EINVAL, "%s overlaps %s of tensor %d", meet(ws, *r) ? ws.name : nm.name,
+                    r->name, i);
+    }
   }
   return K3MOE_OK;
 }
@@ -444,6 +465,7 @@ k3moe_status run_grads(const k3moe_tensor* tensors, int32_t n, bool clip, float 
   size_t need = 0;
   carve_grads(n, nullptr, &need);
   K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  K3_CHECK(check_grad_regions(tensors, n, clip, norm, workspace, need));
   return hip_status(launch_grads(tensors, n, clip, max_norm, norm,
                                  carve_grads(n, workspace, nullptr),
                                  static_cast<hipStream_t>(stream)),

@@ -99,3 +99,42 @@ def test_w4_workspace(glu):
     sizes = {"x": T * k * 4, "codes": n * k // 2, "scale": 2 * scales, "zero": scales,
              "out": T * (n // 2 if glu else n) * 2, "workspace": need}
     each_overlap(sizes, ("out", "workspace"), call)
+
+
+def grads(*rows):
+    ts = (k3.Tensor * len(rows))()
+    for t, r in zip(ts, rows):
+        t.data, t.out, t.numel, t.dtype, t.out_dtype = r
+    return ts
+
+
+def test_clip_norm_and_workspace():
+    """*norm and the partial sums are written while tensors are still read or
+    written: neither may lie in a tensor, in an out or in the other."""
+    n = 1000
+    need = k3.k3moe_grad_workspace_bytes(3)
+    sizes = {"data": 2 * n, "out": 4 * n, "second": 4 * n, "norm": 4, "workspace": need}
+
+    def call(p):
+        ts = grads((p["data"], p["out"], n, k3.BF16, k3.F32), (p["second"], p["second"], n, k3.F32, k3.F32),
+                   (None, None, 0, k3.F32, k3.F32))
+        return k3.lib.k3moe_grad_clip(ts, 3, 1.0, p["norm"], p["workspace"], need, None)
+    each_overlap(sizes, ("norm", "workspace"), call)
+    # the norm's every place inside a tensor
+    for at in (0, 4, 2 * n - 4, 4 * n - 4):
+        p = places(sizes)
+        p["norm"] = p["out"] + at
+        refused(call(p), "norm", "out")
+
+
+def test_norm_and_workspace_of_the_norm_alone():
+    """grad_norm writes *norm after everything is read, so it may replace an element;
+    its partial sums may not."""
+    n = 1000
+    need = k3.k3moe_grad_workspace_bytes(1)
+    sizes = {"data": 2 * n, "norm": 4, "workspace": need}
+
+    def call(p):
+        return k3.lib.k3moe_grad_norm(grads((p["data"], None, n, k3.BF16, 7)), 1, p["norm"], p["workspace"],
+                                      need, None)
+    each_overlap(sizes, ("workspace",), call)
