@@ -6,6 +6,7 @@ from operator import attrgetter
 from struct import pack
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import (BF16, F32, current_stream, k3moe_grad_clip, k3moe_grad_norm,
                k3moe_grad_workspace_bytes, on_device)
@@ -22,7 +23,7 @@ def _types(tensors):
     return types
 
 
-def _call(run, tensors, outs, stream):
+def _call(run, tensors, outs, stream, clip):
     tensors = list(tensors)
     if not tensors:
         raise ValueError("no tensors")
@@ -51,13 +52,15 @@ def _call(run, tensors, outs, stream):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         ws = torch.empty(k3moe_grad_workspace_bytes(n), dtype=torch.uint8, device=dev)
         run(words, n, norm, ws, current_stream(dev))
+    if clip:   # autograd has to know what was overwritten
+        increment_version(outs or tensors)
     return norm
 
 
 def grad_norm(tensors, stream=None):
     """The 2-norm over all elements of all tensors (fp32 or bf16, contiguous, on
     one device), a device fp32 scalar; the host does not wait."""
-    return _call(k3moe_grad_norm, tensors, None, stream)
+    return _call(k3moe_grad_norm, tensors, None, stream, False)
 
 
 def clip_grads(tensors, max_norm, out=None, stream=None):
@@ -65,4 +68,4 @@ def clip_grads(tensors, max_norm, out=None, stream=None):
     `out` (fp32 or bf16 each, of the same shapes), and returns the norm as
     grad_norm does.  A norm of infinities or NaN scales nothing."""
     return _call(lambda ts, n, norm, ws, st: k3moe_grad_clip(ts, n, float(max_norm), norm, ws, st),
-                 tensors, out, stream)
+                 tensors, out, stream, True)

@@ -4,6 +4,7 @@ kernels; this file only marshals."""
 import ctypes
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import BF16, F32, K3moeError, W4Matrix, check_workspace, lib, on_device
 
@@ -40,6 +41,7 @@ def _run(call, half, x, codes, scale, zero, out_dtype, out, workspace, stream):
             not (zero is None or (zero.get_device() == index and zero.is_contiguous())) or \
             not (out is None or (out.get_device() == index and out.is_contiguous())):
         raise ValueError("the tensors must be contiguous and on one GPU")
+    given = out
     w = W4Matrix(n, k, k // groups, codes.data_ptr(), scale.data_ptr(),
                  None if zero is None else zero.data_ptr())
     if stream is None and torch.cuda.current_device() == index:
@@ -50,6 +52,8 @@ def _run(call, half, x, codes, scale, zero, out_dtype, out, workspace, stream):
                                   index)
     if status:
         raise K3moeError(status, lib.k3moe_last_error().decode())
+    if given is not None:   # autograd has to know what was overwritten
+        increment_version(given)
     return out
 
 

@@ -42,3 +42,36 @@ def test_clip_by_a_factor_below_fp32s_normal_range(value, count, max_norm, dt, o
         log(f"  {value:g} x {count}, max_norm {max_norm:g}, {dt} -> {out} {name}: factor {factor:.3g}, worst {worst:.3g}")
         # (smallest outputs here: 1e-30 / sqrt(16411) / 1024 = 7.6e-36, normal)
         assert worst <= eps
+
+
+def test_results_written_in_place_are_seen_by_autograd():
+    """A tensor that a pending backward saved and one of these calls then overwrote is
+    reported, as for torch's own operations in place."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.grads import clip_grads, grad_norm
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_glu, w4_linear
+    x = torch.ones((2, 64), dtype=torch.bfloat16, device="cuda")
+    codes = torch.full((64, 32), 0x9A, dtype=torch.uint8, device="cuda")
+    scale = torch.ones((64, 2), dtype=torch.bfloat16, device="cuda")
+    other = torch.ones((2, 64), device="cuda")
+    calls = [("clip", lambda t: clip_grads([other, t], 1e-3)),
+             ("clip into", lambda t: clip_grads([other], 1e-3, out=[t])),
+             ("clip into, from an iterator", lambda t: clip_grads(iter([other]), 1e-3, out=iter([t]))),
+             ("linear", lambda t: w4_linear(x, codes, scale, out=t)),
+             ("gated", lambda t: w4_glu(x, codes, scale, out=t))]
+    for name, call in calls:
+        p = torch.ones((2, 32 if name == "gated" else 64), device="cuda", requires_grad=True)
+        saved = p * 1.0
+        loss = (saved * saved).sum()
+        call(saved.detach())
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+        assert p.grad is None, name
+    # what is only read is not
+    p = torch.ones(64, device="cuda", requires_grad=True)
+    saved = p * 1.0
+    loss = (saved * saved).sum()
+    grad_norm([saved.detach()])
+    clip_grads([saved.detach()], 1e-3, out=[torch.empty_like(other[0])])
+    loss.backward()
+    assert (p.grad == 2).all()
