@@ -842,16 +842,19 @@ hipError_t launch_tile(const W4Args& g, hipStream_t st) {
 // tokens at a time (so that its partial sums stay bounded).
 constexpr int kFew = 16, kChunk = 256;
 
+// Tokens of a workgroup of the tiled kernel.
+int tile_tokens(int T, bool x_f32) { return x_f32 || T <= 32 ? 32 : 64; }
 // Blocks of a piece of the contraction for a chunk of T tokens, a whole number of
 // steps: at most one workgroup a CU (a second round of a few workgroups costs as
 // much as the first).
-int tile_piece(int n, int k, int T) {
-  const int64_t wgs = (int64_t)((n + 127) / 128) * ((T + 63) / 64);
+int tile_piece(int n, int k, int T, bool x_f32) {
+  const int tt = tile_tokens(T, x_f32);
+  const int64_t wgs = (int64_t)((n + 127) / 128) * ((T + tt - 1) / tt);
   const int64_t pairs = (k + 2 * kBlk - 1) / (2 * kBlk), s = std::max<int64_t>(256 / wgs, 1);
   return (int)((pairs + s - 1) / s * 2);
 }
-int tile_splits(int n, int k, int T) {
-  const int per = tile_piece(n, k, T) * kBlk;
+int tile_splits(int n, int k, int T, bool x_f32) {
+  const int per = tile_piece(n, k, T, x_f32) * kBlk;
   return (k + per - 1) / per;
 }
 
@@ -883,10 +886,10 @@ hipError_t launch_t(W4Args g, hipStream_t st) {
     c.T = std::min(kChunk, T - t);
     c.x = static_cast<const uint8_t*>(g.x) + (size_t)t * g.k * (F32X ? 4 : 2);
     c.out = static_cast<uint8_t*>(g.out) + (size_t)t * out;
-    c.splits = tile_splits(g.n, g.k, c.T);
-    c.per_split = tile_piece(g.n, g.k, c.T);
-    const hipError_t e = F32X || c.T <= 32 ? launch_tile<2, F32X, GLU>(c, st)
-                                           : launch_tile<F32X ? 2 : 4, F32X, GLU>(c, st);
+    c.splits = tile_splits(g.n, g.k, c.T, F32X);
+    c.per_split = tile_piece(g.n, g.k, c.T, F32X);
+    const hipError_t e = tile_tokens(c.T, F32X) == 32 ? launch_tile<2, F32X, GLU>(c, st)
+                                                      : launch_tile<F32X ? 2 : 4, F32X, GLU>(c, st);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -895,10 +898,11 @@ hipError_t launch_t(W4Args g, hipStream_t st) {
 }  // namespace
 
 // Floats of the partial sums: the largest of a chunk's and the last, smaller
-// chunk's.
+// chunk's, for bf16 x (fp32's workgroups of fewer tokens are no fewer, and so their
+// pieces no more).
 size_t w4_part_floats(const k3moe_w4_matrix& w, int64_t T) {
   if (T <= kFew) return 0;
-  auto floats = [&](int64_t t) { return (size_t)tile_splits(w.n, w.k, (int)t) * t * w.n; };
+  auto floats = [&](int64_t t) { return (size_t)tile_splits(w.n, w.k, (int)t, false) * t * w.n; };
   const int64_t rest = T % kChunk;
   return T < kChunk ? floats(T) : std::max(floats(kChunk), rest ? floats(rest) : 0);
 }

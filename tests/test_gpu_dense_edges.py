@@ -75,3 +75,30 @@ def test_results_written_in_place_are_seen_by_autograd():
     clip_grads([saved.detach()], 1e-3, out=[torch.empty_like(other[0])])
     loss.backward()
     assert (p.grad == 2).all()
+
+
+@pytest.mark.parametrize("xd", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,n,k", [(40, 4096, 7168), (64, 4096, 7168), (100, 2048, 2048), (200, 512, 4096)])
+def test_w4_pieces_of_the_contraction_fill_one_round(T, n, k, xd):
+    """The contraction is cut so that its workgroups (128 weight rows x 32 tokens of
+    fp32 x, 64 of bf16, x the pieces) make one round of the 256 CUs, which the partial
+    sums that a call leaves in its workspace show."""
+    require_gpu()
+    from test_gpu_dense import rounded, w4_bounds, w4_problem, within
+    from mxfp4_routed_expert_gemv_amd import k3moe_w4_workspace_bytes, make_w4
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_linear
+    x, codes, scale, z = w4_problem(T, n, k, 128, True, xd, 200)
+    nbytes = k3moe_w4_workspace_bytes(make_w4(n, k, 128, codes, scale, z), T)
+    ws = torch.full((nbytes + 1024,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = w4_linear(x, codes, scale, z, out_dtype=torch.float32, workspace=ws)
+    torch.cuda.synchronize()
+    sums = ws[:nbytes].view(torch.float32)
+    used = int((~torch.isnan(sums)).sum())
+    pieces = used // (T * n)
+    log(f"  T={T} n={n} k={k} {xd}: {pieces} pieces")
+    assert used == pieces * T * n and not torch.isnan(sums[:used]).any()
+    tokens = 32 if xd == torch.float32 else 64
+    assert pieces >= 1 and pieces * -(-n // 128) * -(-T // tokens) <= 256
+    assert (ws[nbytes:] == 0xFF).all()
+    want, tol = w4_bounds(x, codes, scale, z)
+    within(out, want, rounded(want, tol, torch.float32), 0, "linear")
