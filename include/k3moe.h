@@ -499,6 +499,9 @@ k3moe_status k3moe_shared_ffn_backward(const k3moe_shape* shape, const k3moe_exp
  * nothing.
  * x [T][k] and the output in F32 or BF16 each (EUNSUPPORTED otherwise).  The
  * sums are fp32 and follow IEEE rules for infinities and NaN in x and scale.
+ * With F32 on both sides their error is that of an fp32 product of W (0.8 to 1.7
+ * times); with bf16 on either side, up to 8 times that where x has a mean (2e-6
+ * of the output for 4096 terms).
  * The pages' engines run 4-bit weights without a dense copy (kimi-k3-in-c
  * review page, "KDA/MLA/MoE" table); integer codes with group scales beside
  * their MXFP4 are this library's.

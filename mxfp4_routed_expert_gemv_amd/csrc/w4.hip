@@ -9,7 +9,13 @@
 //   sum (q - z) x = sum (16 + q) x - (16 + z) sum x,
 // with sum x from the same instruction against ones.  All products are exact
 // and the sums fp32; the subtraction amplifies their rounding by about
-// 24 / 4.6 (the offset over the codes' spread).  An infinity or NaN among a
+// 24 / 4.6 (the offset over the codes' spread), and more where x has a mean.  With
+// fp32 x and outputs it is therefore taken after every 32 weights, before the sums
+// have grown: the error is 0.8 to 1.7 times that of a plain fp32 product (4096 terms,
+// x of spread 1 and mean 0 to 20), against 1.6 to 7.5 with one subtraction per group of
+// 128, for 3 to 12 % of the time (5 tokens gated 2 x 2049 x 7168 13.0 -> 13.5 us, 64
+// tokens 8192 x 4096 30.3 -> 33.3).  With bf16 x or outputs, whose own rounding is
+// 2^-8, it is taken once per scale of a block.  An infinity or NaN among a
 // group's terms would come out of that difference as NaN whatever its sign, so
 // a wave whose sums are not finite repeats its slice with the weights (q - z) s
 // themselves, as two exact bf16 parts, which follows the definition.
@@ -290,8 +296,9 @@ __device__ __forceinline__ void wide_values(const uint8_t* scale, const uint8_t*
 __device__ __forceinline__ int code_swz(int r) { return ((r >> 1) & 2) ^ ((r >> 3) & 1) * 3; }
 
 // Workgroup blockIdx.x: 16 NF weight rows (gated form: 8 NF gate
-// rows and the matching up rows) x RC tokens.
-template <int W, int D, int RC, int NF, int SG, bool F32X, bool WIDE, bool GLU>
+// rows and the matching up rows) x RC tokens.  The offset is taken off after every FS
+// steps of 32.
+template <int W, int D, int RC, int NF, int SG, int FS, bool F32X, bool WIDE, bool GLU>
 __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
   using L = Slot<RC, NF, SG, F32X, WIDE>;
   constexpr int NB = GLU ? 8 * NF : 16 * NF;   // outputs per token
@@ -433,8 +440,8 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
 #pragma unroll
     for (int f = 0; f < NF; ++f) transpose4(c[f]);
 #pragma unroll
-    for (int s = 0; s < 4 / SG; ++s) {
-      if (blk * kBlk + s * SG * 32 >= g.k) break;
+    for (int s = 0; s < 4 / FS; ++s) {
+      if (blk * kBlk + s * FS * 32 >= g.k) break;
       f32x4_t sum[MB], dot[MB][NF];
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
@@ -443,7 +450,7 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
         for (int f = 0; f < NF; ++f) dot[m][f] = nil;
       }
 #pragma unroll
-      for (int j = s * SG; j < (s + 1) * SG; ++j) {
+      for (int j = s * FS; j < (s + 1) * FS; ++j) {
         bf16x8_t w[NF];
 #pragma unroll
         for (int f = 0; f < NF; ++f) w[f] = codes_biased(c[f][j]);
@@ -466,7 +473,8 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args g) {
         for (int f = 0; f < NF; ++f)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[m][f][r] = __builtin_fmaf(sc[f][s], __builtin_fmaf(off[f][s], sum[m][r], dot[m][f][r]),
+            acc[m][f][r] = __builtin_fmaf(sc[f][s * FS / SG],
+                                          __builtin_fmaf(off[f][s * FS / SG], sum[m][r], dot[m][f][r]),
                                           acc[m][f][r]);
     }
   }
@@ -548,7 +556,7 @@ struct TileSlot {
   static_assert(XC * 8192 == 16 * MB * kRow && kStages >= 2, "whole copies, two steps in LDS");
 };
 
-template <int MB, int SG, bool F32X, bool WIDE>
+template <int MB, int SG, int FS, bool F32X, bool WIDE>
 __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
   using L = TileSlot<MB, SG, F32X, WIDE>;
   constexpr int XP = F32X ? 3 : 1, kStages = L::kStages;
@@ -663,8 +671,8 @@ __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
       }
     }
 #pragma unroll
-    for (int s = 0; s < 4 / SG; ++s) {
-      if (blk * kBlk + s * SG * 32 >= g.k) break;
+    for (int s = 0; s < 4 / FS; ++s) {
+      if (blk * kBlk + s * FS * 32 >= g.k) break;
       float sc[2], off[2];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
@@ -673,7 +681,7 @@ __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
           off[f] = woff[f][s];
           continue;
         }
-        const int i = ((wk * (4 / SG) + s) * 128 + wn * 32 + f * 16 + ln) * 4;
+        const int i = ((wk * (4 / SG) + s * FS / SG) * 128 + wn * 32 + f * 16 + ln) * 4;
         sc[f] = bf16_lo(*reinterpret_cast<const uint32_t*>(vals + L::kS + i));
         off[f] = -(float)(16 + (g.zero ? *reinterpret_cast<const int*>(vals + L::kZ + i) : 8));
       }
@@ -681,7 +689,7 @@ __global__ __launch_bounds__(512) void w4_tile(W4Args g) {
 #pragma unroll
       for (int m = 0; m < MB; ++m) sum[m] = dot[0][m] = dot[1][m] = nil;
 #pragma unroll
-      for (int j = s * SG; j < (s + 1) * SG; ++j) {
+      for (int j = s * FS; j < (s + 1) * FS; ++j) {
         const bf16x8_t w[2] = {codes_biased(c[0][j]), codes_biased(c[1][j])};
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
@@ -803,12 +811,19 @@ constexpr int ring_depth() {
   return n < 4 ? n : 4;
 }
 
-template <int W, int RC, int NF, int SG, bool F32X, bool WIDE, bool GLU>
-hipError_t launch_sg(const W4Args& g, hipStream_t st) {
+template <int W, int RC, int NF, int SG, int FS, bool F32X, bool WIDE, bool GLU>
+hipError_t launch_fs(const W4Args& g, hipStream_t st) {
   constexpr int NB = GLU ? 8 * NF : 16 * NF;
-  w4_kernel<W, ring_depth<W, RC, NF, SG, F32X, WIDE>(), RC, NF, SG, F32X, WIDE, GLU>
+  w4_kernel<W, ring_depth<W, RC, NF, SG, F32X, WIDE>(), RC, NF, SG, FS, F32X, WIDE, GLU>
       <<<((GLU ? g.f : g.n) + NB - 1) / NB, 64 * W, 0, st>>>(g);
   return hipGetLastError();
+}
+// (FS 1 for fp32 x and outputs: what it costs and brings is at the top)
+template <int W, int RC, int NF, int SG, bool F32X, bool WIDE, bool GLU>
+hipError_t launch_sg(const W4Args& g, hipStream_t st) {
+  if constexpr (F32X && SG > 1)
+    if (g.out_f32) return launch_fs<W, RC, NF, SG, 1, F32X, WIDE, GLU>(g, st);
+  return launch_fs<W, RC, NF, SG, SG, F32X, WIDE, GLU>(g, st);
 }
 template <int W, int RC, int NF, bool F32X, bool GLU>
 hipError_t launch(const W4Args& g, hipStream_t st) {
@@ -818,16 +833,25 @@ hipError_t launch(const W4Args& g, hipStream_t st) {
   if (group == 64) return launch_sg<W, RC, NF, 2, F32X, false, GLU>(g, st);
   return launch_sg<W, RC, NF, 4, F32X, false, GLU>(g, st);   // a multiple of 128
 }
+template <int MB, int SG, bool F32X, bool WIDE>
+void launch_tile_sg(const W4Args& g, dim3 grid, hipStream_t st) {
+  if constexpr (F32X && SG > 1)
+    if (g.out_f32) {
+      w4_tile<MB, SG, 1, F32X, WIDE><<<grid, 512, 0, st>>>(g);
+      return;
+    }
+  w4_tile<MB, SG, SG, F32X, WIDE><<<grid, 512, 0, st>>>(g);
+}
 template <int MB, bool F32X, bool GLU>
 hipError_t launch_tile(const W4Args& g, hipStream_t st) {
   // (a multiple of 8 along the weights: the token blocks of one set of rows run
   // on the same XCD, whose L2 then serves the codes)
   const dim3 grid(((g.n + 127) / 128 + 7) / 8 * 8, g.splits, (g.T + 16 * MB - 1) / (16 * MB));
   const int group = g.k / g.groups;
-  if (group == 32 && g.groups % 4 == 0) w4_tile<MB, 1, F32X, true><<<grid, 512, 0, st>>>(g);
-  else if (group == 32) w4_tile<MB, 1, F32X, false><<<grid, 512, 0, st>>>(g);
-  else if (group == 64) w4_tile<MB, 2, F32X, false><<<grid, 512, 0, st>>>(g);
-  else w4_tile<MB, 4, F32X, false><<<grid, 512, 0, st>>>(g);
+  if (group == 32 && g.groups % 4 == 0) launch_tile_sg<MB, 1, F32X, true>(g, grid, st);
+  else if (group == 32) launch_tile_sg<MB, 1, F32X, false>(g, grid, st);
+  else if (group == 64) launch_tile_sg<MB, 2, F32X, false>(g, grid, st);
+  else launch_tile_sg<MB, 4, F32X, false>(g, grid, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int n_out = GLU ? g.f : g.n;

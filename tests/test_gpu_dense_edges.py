@@ -102,3 +102,109 @@ def test_w4_pieces_of_the_contraction_fill_one_round(T, n, k, xd):
     assert (ws[nbytes:] == 0xFF).all()
     want, tol = w4_bounds(x, codes, scale, z)
     within(out, want, rounded(want, tol, torch.float32), 0, "linear")
+
+
+def offset_sums(x, codes, scale, zero):
+    """x W^T in 64 bits, and the square of what fp32 roundings leave of it, per output.
+    The kernels take a step of 32 weights as sum (16 + q) x - (16 + z) sum x, either sum
+    by three matrix instructions, one for each 8 bits of x.  An instruction adds 32
+    products to what is there, with a rounding each at most: the first has the partial
+    sums, the other two move the full one by 2^-8 of it or less, so that each of their
+    64 roundings is of the full sum.  Then the difference is rounded, and the running
+    sum of the steps.  A rounding to the nearest is off by at most 2^-24 of its value,
+    evenly spread a third of that squared on average, and independent roundings add up
+    as their squares."""
+    n, half = codes.shape
+    k, T = 2 * half, x.shape[0]
+    q = torch.stack([codes & 15, codes >> 4], -1).view(n, k).to(F8)
+    z = (torch.full_like(scale, 8.0) if zero is None else zero).to(F8).repeat_interleave(k // scale.shape[1], 1)
+    s = scale.to(F8).repeat_interleave(k // scale.shape[1], 1)
+    xs = x.to(F8).view(T, k // 32, 32).transpose(0, 1).contiguous()     # [steps][T][32]
+    qs = (16 + q).view(n, k // 32, 32).permute(1, 2, 0).contiguous()    # [steps][32][n]
+    zs = (16 + z)[:, ::32].t()[:, None, :]
+    dot = off = squares = 0
+    for i in range(32):
+        dot = dot + xs[:, :, i:i + 1] * qs[:, i:i + 1]
+        off = off + xs[:, :, i:i + 1] * zs
+        squares = squares + dot ** 2 + off ** 2
+    squares = squares + 64 * (dot ** 2 + off ** 2)
+    ss = s[:, ::32].t()[:, None, :]
+    term = (dot - off) * ss
+    run = term.cumsum(0)
+    return run[-1], (S24 ** 2 / 3) * (squares * ss ** 2 + term ** 2 + run ** 2).sum(0)
+
+
+FP32_X = [(1, 96, 1024, 128), (3, 500, 4096, 128), (8, 130, 2048, 256), (13, 66, 1536, 512), (16, 40, 640, 64),
+          (30, 200, 1024, 128), (48, 258, 2048, 64), (200, 70, 1024, 128), (5, 514, 4096, 32), (70, 100, 1120, 32)]
+
+
+@pytest.mark.parametrize("mean", [0.0, 0.5, 20.0])
+@pytest.mark.parametrize("T,n,k,group", FP32_X)
+def test_w4_fp32_values_keep_fp32s_bits(T, n, k, group, mean):
+    """fp32 x into fp32 outputs: the error of all outputs together is that of fp32
+    roundings, for x with a mean too (where the offset's sums are far larger than their
+    difference), for zero points past 15 and for scales of either sign.  An x without
+    its lowest 8 bits is off by more, without its lower 16 by hundreds of times."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_linear
+    g = torch.Generator().manual_seed(300 + T)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, dtype=torch.uint8).cuda()
+    shape = (n, k // group)
+    sign = torch.randint(0, 2, shape, generator=g) * 2 - 1
+    scale = ((torch.rand(shape, generator=g) * 0.1 + 0.01) * sign).bfloat16().cuda()
+    x = (torch.randn((T, k), generator=g) + mean).cuda()
+    for hi in (None, 16, 256):
+        zero = None if hi is None else torch.randint(hi // 2, hi, shape, generator=g, dtype=torch.int64).to(torch.uint8).cuda()
+        want, square = offset_sums(x, codes, scale, zero)
+        got = w4_linear(x, codes, scale, zero, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        # (and the waves' and pieces' sums, 64 at most, a rounding of about the output each)
+        allowed = float((square + 64 / 3 * (S24 * want) ** 2).sum()) ** 0.5
+        err = float((got.to(F8) - want).norm())
+        log(f"  T={T} n={n} k={k} group={group} mean={mean} zero<{hi}: {err:.3e} of {allowed:.3e}, "
+            f"relative {err / float(want.norm()):.2e}")
+        assert err <= allowed
+
+
+@pytest.mark.parametrize("T,n,k,group", FP32_X[:8])
+def test_w4_fp32_values_do_not_depend_on_how_scales_are_grouped(T, n, k, group):
+    """A longer group is groups of 32 with one scale: fp32 x into fp32 outputs takes the
+    offset off after every 32 weights, before its sums grow, whatever the group, so the
+    bits are the same."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_glu, w4_linear
+    from test_gpu_dense import w4_problem
+    x, codes, scale, zero = w4_problem(T, n, k, group, True, torch.float32, 320)
+    fine = [t.repeat_interleave(group // 32, 1).contiguous() for t in (scale, zero)]
+    x += 3.0
+    for call in (w4_linear, w4_glu):
+        got, want = call(x, codes, scale, zero), call(x, codes, *fine)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), call.__name__
+
+
+@pytest.mark.parametrize("part", [9, 17, 18])
+@pytest.mark.parametrize("group", [32, 64, 128, 512])
+@pytest.mark.parametrize("T", [1, 2, 7, 16, 25, 33, 70, 260])
+def test_w4_low_bits_of_fp32_values(T, group, part):
+    """Outputs that the low bits of x alone make up: in every 128 weights one pair of x, 1
+    and 1 + 2^-part, meets weights 7 and -7, the rest of x is zero.  31 + 17 (1 + 2^-18)
+    has 24 bits, so every sum here is exact in fp32, and the output -7 (k / 128) 2^-part."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_glu, w4_linear
+    n, k = 48, 1536
+    codes = torch.full((n, k // 2), 0x1F, dtype=torch.uint8, device="cuda")   # 15, 1, 15, 1, ...
+    scale = torch.ones((n, k // group), dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros((T, k), device="cuda")
+    for b in range(k // 128):   # (another place of the block in every block and token)
+        for t in range(T):
+            at = 128 * b + 2 * ((5 * b + 7 * t) % 64)
+            x[t, at], x[t, at + 1] = 1.0, 1.0 + 2.0 ** -part
+    want = -7.0 * (k // 128) * 2.0 ** -part
+    got = w4_linear(x, codes, scale)
+    both = w4_glu(x, codes, scale)
+    torch.cuda.synchronize()
+    assert got.dtype == torch.float32 and (got == want).all()
+    # silu(g) u with g = u = want, small: the sigmoid's and two products' roundings
+    h = want * want / (1 + math.exp(-want))
+    assert ((both.to(F8) - h).abs() <= 16 * S24 * h).all()
