@@ -208,3 +208,56 @@ def test_w4_low_bits_of_fp32_values(T, group, part):
     # silu(g) u with g = u = want, small: the sigmoid's and two products' roundings
     h = want * want / (1 + math.exp(-want))
     assert ((both.to(F8) - h).abs() <= 16 * S24 * h).all()
+
+
+@pytest.mark.parametrize("T", [1, 16, 200])
+def test_shared_full_size_layer_with_few_tokens(T, monkeypatch):
+    """The sizes whose dx is split over the contraction (of two parts a value up to 16
+    tokens) and whose weight gradients run on tiles of their own, or share a launch."""
+    import test_gpu_dense as dense
+    dense.test_shared_train_and_backward(T, 7168, 2048, 2)
+    if T <= 16:
+        dense.test_shared_values_of_few_tokens_keep_16_bits(T, 7168, 2048, 2, monkeypatch)
+
+
+@pytest.mark.parametrize("T", [2500, 4096, 16384])
+def test_shared_full_size_layer_with_many_tokens(T):
+    """256 x 256 tiles over several rounds, full ones and not, and dx in a launch of its
+    own: sampled tokens of y, gu and dx and sampled features of the weights' gradients
+    against the formulas."""
+    require_gpu()
+    from mxfp4_routed_expert_gemv_amd.shared import shared_ffn_backward, shared_ffn_train
+    from test_gpu_dense import Ref, normal, problem, rounded, within
+    d, fs, S = 7168, 2048, 2
+    x, w13, w2 = problem(T, d, fs, S, 400)
+    y, gu = shared_ffn_train(x, w13, w2)
+    dy = normal((T, d), 405, 0.1)
+    dx, dw13, dw2 = shared_ffn_backward(x, gu, dy, w13, w2)
+    torch.cuda.synchronize()
+    # tokens: of every tile of 256 rows one, at another place in each, and the last
+    rows = torch.tensor(sorted({min(256 * i + 37 * i % 256, T - 1) for i in range(-(-T // 256))} | {0, T - 1})).cuda()
+    ref = Ref(x[rows], w13, w2)
+    y_want, y_tol, gu_want, gu_tol = ref.forward()
+    within(y[rows], y_want, rounded(y_want, y_tol), 2, "y")
+    within(gu[rows], gu_want, gu_tol, 1, "gu")
+    want, tol = ref.backward(gu[rows], dy[rows])[0]
+    within(dx[rows], want, rounded(want, tol), 2, "dx")
+    # features: one of every 128, and the last
+    cols = torch.tensor(sorted({128 * i + 29 * i % 128 for i in range(fs // 128)} | {0, fs - 1})).cuda()
+    few, xa, dya = T * S24, x.to(F8).abs(), dy.to(F8).abs()
+    for j in range(S):
+        g, u, w = gu[:, j, cols].to(F8), gu[:, j, fs + cols].to(F8), w2[j].to(F8)[:, cols]
+        s = torch.sigmoid(g)
+        dh, dh_e = dy.to(F8) @ w, d * S24 * (dya @ w.abs())
+        sil, ds, ds_m = g * s, s * (1 + g * (1 - s)), s + (g * s * (1 - s)).abs()
+        for name, at, v, e in (("gate", cols, dh * u * ds, (dh_e * ds.abs() + 16 * S24 * (dh.abs() + dh_e) * ds_m) * u.abs()),
+                               ("up", fs + cols, dh * sil, (dh_e + 16 * S24 * (dh.abs() + dh_e)) * sil.abs())):
+            e = e + B * (v.abs() + e)   # the rounding of dg or du
+            want = v.t() @ x.to(F8)
+            tol = e.t() @ xa + few * ((v.abs() + e).t() @ xa)
+            within(dw13[j][at], want, rounded(want, tol), 2, f"dw13 ({name}) of expert {j}")
+        h = sil * u
+        want = dy.to(F8).t() @ h
+        h_e = (B + 16 * S24) * h.abs()
+        within(dw2[j][:, cols], want, rounded(want, dya.t() @ h_e + few * (dya.t() @ (h.abs() + h_e))), 2,
+               f"dw2 of expert {j}")
