@@ -188,10 +188,6 @@ k3moe_status check_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int3
   return K3MOE_OK;
 }
 
-k3moe_status run_w4(const k3moe_w4_matrix* w, int64_t T, int32_t x_dtype, int32_t out_dtype,
-                    const void* x, void* out, void* workspace, size_t workspace_bytes, void* stream,
-                    bool glu);
-
 // An operand's bytes; NULL or empty ones overlap nothing.
 struct Region {
   const void* p;

@@ -791,12 +791,11 @@ hipError_t launch_product(const k3moe_shape& s, DenseArgs g, float* part, hipStr
     }
   } else if (p.tile == kTile256) {
     dense_tile<P, 256, 256, 2, 4, 2><<<cus, 512, 0, st>>>(g);
-  } else if (p.tile == kTile128x256) {
-    dense_tile<P, 128, 256, 2, 4, 3><<<cus, 512, 0, st>>>(g);
-  } else if (p.tile == kTile128) {
-    dense_tile<P, 128, 128, 2, 4, 3><<<cus, 512, 0, st>>>(g);
-  } else {
+  } else if (p.tile == kTile64) {
     dense_tile<P, 64, 64, 2, 2, 3><<<cus * 3, 256, 0, st>>>(g);
+  } else if constexpr (P != kDX) {   // (dx on these tiles shares the weight gradients' launch)
+    if (p.tile == kTile128x256) dense_tile<P, 128, 256, 2, 4, 3><<<cus, 512, 0, st>>>(g);
+    else dense_tile<P, 128, 128, 2, 4, 3><<<cus, 512, 0, st>>>(g);
   }
   return hipGetLastError();
 }
