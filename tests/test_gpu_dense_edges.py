@@ -261,3 +261,44 @@ def test_shared_full_size_layer_with_many_tokens(T):
         h_e = (B + 16 * S24) * h.abs()
         within(dw2[j][:, cols], want, rounded(want, dya.t() @ h_e + few * (dya.t() @ (h.abs() + h_e))), 2,
                f"dw2 of expert {j}")
+
+
+@pytest.mark.parametrize("on_side", [False, True])
+def test_the_calls_of_the_c_interface_from_python(on_side):
+    """k3moe_* with buffers of the caller's own, on torch's current stream and on one
+    given as an object and as a raw handle, against the torch-facing calls."""
+    require_gpu()
+    import mxfp4_routed_expert_gemv_amd as k3
+    from mxfp4_routed_expert_gemv_amd.grads import clip_grads, grad_norm
+    from mxfp4_routed_expert_gemv_amd.w4 import w4_glu, w4_linear
+    from test_gpu_dense import w4_problem
+    T, n, k, group = 40, 96, 512, 64
+    x, codes, scale, z = w4_problem(T, n, k, group, True, torch.bfloat16, 500)
+    w = k3.make_w4(n, k, group, codes, scale, z)
+    need = k3.k3moe_w4_workspace_bytes(w, T)
+    linear, gated = w4_linear(x, codes, scale, z), w4_glu(x, codes, scale, z)
+    grads = [linear.float(), gated.float()]
+    norm, outs = grad_norm(grads), [torch.empty_like(g) for g in grads]
+    clip_grads(grads, 0.5, out=outs)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream() if on_side else None
+    for stream in (side, side.cuda_stream if on_side else None):
+        a, b = torch.full_like(linear, 7), torch.full_like(gated, 7)
+        ws = torch.empty(max(need, k3.k3moe_grad_workspace_bytes(2)), dtype=torch.uint8, device="cuda")
+        mine, got = [torch.full_like(g, 7) for g in grads], torch.full((2,), 7.0, device="cuda")
+        ts = (k3.Tensor * 2)()
+        for t, g, o in zip(ts, grads, mine):
+            t.data, t.out, t.numel, t.dtype, t.out_dtype = g.data_ptr(), o.data_ptr(), g.numel(), k3.F32, k3.F32
+        torch.cuda.synchronize()
+        k3.k3moe_w4_linear(w, T, k3.BF16, k3.BF16, x, a, ws, stream)
+        k3.k3moe_w4_glu(w, T, k3.BF16, k3.BF16, x, b, (ws.data_ptr(), need), stream)
+        k3.k3moe_grad_norm(ts, 2, got[:1], ws, stream)
+        k3.k3moe_grad_clip(ts, 2, 0.5, got[1:], ws, stream)
+        torch.cuda.synchronize()
+        assert torch.equal(a, linear) and torch.equal(b, gated)
+        assert torch.equal(got, torch.stack([norm, norm]))
+        assert all(torch.equal(p, q) for p, q in zip(mine, outs))
+    with pytest.raises(k3.K3moeError, match="workspace"):
+        k3.k3moe_w4_linear(w, T, k3.BF16, k3.BF16, x, linear, None, None)
+    with pytest.raises(k3.K3moeError, match="overlaps"):
+        k3.k3moe_w4_glu(w, T, k3.BF16, k3.BF16, x, x, ws, None)
