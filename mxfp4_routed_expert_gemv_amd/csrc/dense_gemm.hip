@@ -16,16 +16,18 @@
 // products read the weights' every byte whatever the rows, and a rounding to 8 bits
 // of so few values does not average out (an output's error of sqrt(2) of its own
 // rounding alone, but up to twice that for one token of a small layer).  That costs
-// nothing (T = 16 forward 46.5, backward 118 us; T = 17 46.3, 117).  Where the
+// nothing (T = 16 forward 46.7, backward 117 us; T = 17 46.6, 116).  Where the
 // parts are rows of a product, its sums of a row and of the one kRows further are
 // added; where they are contracted over, the other operand's rows are taken twice.
 // From about 2000 tokens the matrix cores bound all six (d 7168, two experts of 2048,
-// T = 16384: dx 1.36 ms = 1.41 PFLOP/s, dW13 and dW2 2.21 ms = 1.31, dh 0.85 ms =
-// 1.13, whose epilogue moves 670 MB; the library's product of such sizes reaches 1.4
+// T = 16384: dx 1.37 ms = 1.40 PFLOP/s, dW13 and dW2 2.27 ms = 1.27, dh 0.86 ms =
+// 1.12, whose epilogue moves 670 MB; the library's product of such sizes reaches 1.4
 // to 1.5): they are busy 60 to 65 % of the time at the 1.95 GHz that this load
-// leaves, what is missing being LDS reads and copies between them.  Below about 300
+// leaves, what is missing being LDS reads and copies between them.  That is where the
+// tiles fill whole rounds of the CUs; a last round of a few tiles takes as long as a
+// full one (forward at T = 4096 539 us, 4097 654, 2500 447).  Below about 300
 // tokens reading the weights (backward: and writing their gradients) bounds them:
-// T = 1 forward 46 us for 176 MB, backward 116 us for 352 MB.
+// T = 1 forward 45 us for 176 MB, backward 115 us for 352 MB.
 #include <algorithm>
 
 #include "internal.h"
@@ -176,8 +178,8 @@ __device__ __forceinline__ int gate_col(int n, int fs) { return n + n / fs * fs;
 // ---- epilogues.  A fragment's sums give a lane four consecutive columns of a row;
 // two fragments side by side, their odd and even groups of 16 lanes exchanged, give
 // it eight: lane group lg then has columns 8 (lg / 2) .. + 8 of fragment lg mod 2,
-// a store is 16 bytes and a row's part of it 64 (against stores of 8 and 32: the
-// backward at T = 64 131 us, 142; at 16384 4.54 ms, 4.67).
+// a store is 16 bytes and a row's part of it 64 (with stores of 8 and 32 the
+// backward took 8 % longer at T = 64 and 3 % at 16384).
 __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
   const auto t = __builtin_amdgcn_permlane16_swap(a, b, false, false);
   a = t[0];
@@ -691,8 +693,8 @@ struct Plan {
 //     gate/up 57 us at T = 200 (66 on 128 x 128; 92 with 2 slots)
 // Where the outputs are few, the contraction is split, so that every CU loads a part
 // of the weights: on 64 x 64 tiles below about 100 tokens, on the larger ones up to
-// about 800 (forward at T = 128 60 us against 77 without a split on larger tiles,
-// T = 256 81, 109; backward at T = 512 237, 267).  The sums of a piece then cost
+// about 800 (forward at T = 128 59 us against 76 without a split on larger tiles,
+// T = 256 80, 107; backward at T = 512 225, 247).  The sums of a piece then cost
 // their way to memory and back, and a second kernel 5 us.
 // A weight gradient's contraction can be a few tokens: there a tile's way out counts
 // (us a round: 9, 4.6, 2.7, 1.9; both gradients at T = 64 65, 61, 63, 71).
@@ -746,7 +748,7 @@ Plan plan_product(int P, const k3moe_shape& s) {
 // the rows of dW2 that do not fit go to 128 x 128 tiles, four times as many, in a
 // launch of their own.  -1: two launches take no longer.  (T = 16384, d 7168, two
 // experts of 2048: 896 and 448 tiles, 4 and 2 rounds; here 5 and 1024 rows of dW2 in
-// one round of the small tiles: backward 4.44 ms against 4.55.)
+// one round of the small tiles: backward 4.31 ms against 4.39.)
 int64_t tail_rows(const k3moe_shape& s) {
   if (plan_product(kDW13, s).tile != kTile256 || plan_product(kDW2, s).tile != kTile256) return -1;
   const int64_t F = (int64_t)s.n_shared * s.f_shared;
@@ -885,14 +887,14 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   grads[2].a = static_cast<const uint16_t*>(dy);
   grads[2].b = ws.h;
   grads[2].o0 = dw2;
-  // One launch for the three: backward 254 us at T = 517 (279 in three launches), 1158
-  // at 4096 (1181).  From four rounds of dx on a partly filled last round weighs
-  // less than what a workgroup saves by going from tile to tile: 4.53 ms in launches
-  // of their own at T = 16384 (4.63 in one); and without dx there is nothing to fill
-  // the gaps with (T = 517 190 us against 201).
+  // One launch for the three: backward 244 us at T = 517 (275 in three launches), 1150
+  // at 4096 (1175).  From four rounds of dx on a partly filled last round weighs
+  // less than what a workgroup saves by going from tile to tile: 4.31 ms in launches
+  // of their own at T = 16384 (4.50 in one); and without dx there is nothing to fill
+  // the gaps with (T = 517 174 us against 179).
   // On 64 x 64 tiles one launch is worth it for smaller layers (tokens x d x fs x
-  // experts: 4 x 256 x 128 16 us against 25; 128 x 4096 x 512 x 3, 4700 tiles: 44, 57;
-  // 64 x 4096 x 1024 x 3, 9300 tiles: 57, 63; without dx, 16 x 4096 x 512 x 3: 35, 34);
+  // experts: 4 x 256 x 128 16 us against 22; 128 x 4096 x 512 x 3, 4700 tiles: 42, 56;
+  // 64 x 4096 x 1024 x 3, 9300 tiles: 55, 62; without dx, 16 x 4096 x 512 x 3: 33, 33);
   // where the weight gradients alone fill the chip they are faster on their own tiles,
   // beside a dx whose contraction is split (64 x 7168 x 2048 x 2, 21600 tiles: 127 us
   // against 140).
@@ -904,9 +906,9 @@ hipError_t launch_shared_backward(const k3moe_shape& s, const k3moe_expert_bank&
   if (dx && tile == kTile256 && dx_tiles < 4 * kCUs)
     return launch_grads_tile<256, 256, 2, 256, 256, 2, 2, 4>(s, grads, st);
   if (dx && (tile == kTile128 || tile == kTile128x256)) {
-    // (the weight gradients on 256 x 256 tiles, where there are some: T = 517 254 us
-    // against 264 on dx's 128 x 256, 1000 358, 394; 2000 x 2048 x 1024, 96 tiles of
-    // theirs, 73, 85; 1061 x 3616 x 128, 22 tiles, 44, 37)
+    // (the weight gradients on 256 x 256 tiles, where there are some: T = 517 244 us
+    // against 252 on dx's 128 x 256, 1000 357, 389; 2000 x 2048 x 1024, 96 tiles of
+    // theirs, 70, 82; 1061 x 3616 x 128, 22 tiles, 43, 35)
     const int64_t d256 = (s.d + 255) / 256, f256 = ((int64_t)s.n_shared * s.f_shared + 127) / 128;
     if (d256 * f256 * 3 / 2 >= 64) return launch_grads_tile<128, 256, 3, 256, 256, 2, 2, 4>(s, grads, st);
     return launch_grads_tile<128, 256, 3, 128, 256, 3, 2, 4>(s, grads, st);

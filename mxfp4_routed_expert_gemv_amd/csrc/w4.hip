@@ -20,9 +20,9 @@
 // a wave whose sums are not finite repeats its slice with the weights (q - z) s
 // themselves, as two exact bf16 parts, which follows the definition.
 //
-// What bounds them, at one token 7168 x 4096, group 128 (15 MB): 6.7 us, of which a
-// launch is 2.3 and the codes at a large copy's rate 3.2; 16384 x 16384 (134 MB and
-// scales) 40.5 us, 3.4 TB/s.  From about 32 tokens on what a CU has to bring of x
+// What bounds them, at one token 7168 x 4096, group 128 (15 MB from HBM): 7.0 us, of
+// which a launch is 2.3 and the codes at a large copy's rate 3.2; 16384 x 16384
+// (134 MB and scales) 38.8 us, 3.6 TB/s.  From about 32 tokens on what a CU has to bring of x
 // into LDS weighs more than the weights.
 //
 // fp32 activations enter as three exact bf16 parts (the top 8 significant bits,
@@ -270,7 +270,7 @@ __device__ __forceinline__ void dma_u8(const void* base, uint32_t off, uint32_t 
 //   scale  [4 / SG][16 NF] dwords, then zero the same; WIDE (groups of 32, four of
 //     them a block at a time, whose addresses are then whole dwords): scale [16 NF]
 //     [4] bf16, then zero [16 NF][4] bytes, half of the copies or less (64 tokens
-//     7168 x 4096: 16.9 us against 19.0; 32 tokens 16384 x 4096: 24.5, 27.3)
+//     7168 x 4096: 18.4 us against 20.8; 32 tokens 16384 x 4096: 26.1, 30.0)
 // The permutations spread the 16 rows of a fragment read over the LDS banks.
 template <int RC, int NF, int SG, bool F32X, bool WIDE>
 struct Slot {
@@ -797,13 +797,13 @@ __global__ __launch_bounds__(256) void w4_finish(W4Args g) {
 
 // Slots of a wave's ring: as many as the 160 KB of a CU hold, at most 4.  What
 // counts is how many bytes a CU has in flight: one workgroup of 16 waves with a
-// slot or two each reads faster than 8 waves with up to four (n x k, group, us:
-// one token 7168 x 4096, 128: 6.7 against 7.4; gated 2 x 4096 x 7168: 10.5
-// against 11.4; 16 tokens 7168 x 4096, 64: 8.5 against 9.3; 5 fp32 tokens gated
-// 2 x 2049 x 7168, 64: 15.6 against 18.0), fp32 too, where the 16 waves' bound of
+// slot or two each reads faster than 8 waves with up to four (n x k, group, us from HBM:
+// one token 7168 x 4096, 128: 7.0 against 7.8; gated 2 x 4096 x 7168: 11.0
+// against 12.0; 16 tokens 7168 x 4096, 64: 9.1 against 9.8; 5 fp32 tokens gated
+// 2 x 2049 x 7168, 64: 16.3 against 19.1), fp32 too, where the 16 waves' bound of
 // 128 registers puts five to nine of them in scratch; only 32 workgroups of a
-// short contraction lose (2 fp32 tokens 1024 x 1024, 32: 5.1 against 4.8).  16
-// fp32 tokens do not fit with 16 waves; 8 there against 4: 17.7, 22.2
+// short contraction lose (2 fp32 tokens 1024 x 1024, 32: 4.6 against 4.5).  16
+// fp32 tokens do not fit with 16 waves; 8 there against 4: 19.3, 25.5
 // (7168 x 7168).
 template <int W, int RC, int NF, int SG, bool F32X, bool WIDE>
 constexpr int ring_depth() {
@@ -886,9 +886,9 @@ int tile_splits(int n, int k, int T, bool x_f32) {
 // partial sums and second launch cost 5 us: 32 weight rows a workgroup, which reads
 // all of x.  It pays where those workgroups run in one round of the 256 CUs and x
 // is short against what the split form writes, some n T sums (us, this form against
-// the split one; 32 tokens x 4096: n 512 7.7, 7.8; 8192 10.2, 14.1; 8448 17.6, 16.1;
-// 64 x 4096: n 512 11.6, 9.5; 3584 12.4, 14.1; 8192 15.2, 19.7; 64 x 7168: n 1024
-// 16.9, 13.2; 8192 23.3, 24.1; 32 fp32 x 4096: n 2048 15.1, 11.4; 8192 18.2, 21.0).
+// the split one; 32 tokens x 4096: n 512 8.4, 8.9; 8192 11.2, 15.0; 8448 18.8, 17.1;
+// 64 x 4096: n 512 12.6, 11.0; 3584 15.0, 15.7; 8192 16.6, 20.7; 64 x 7168: n 1024
+// 18.8, 14.4; 8192 25.3, 24.5; 32 fp32 x 4096: n 2048 16.7, 12.7; 8192 20.7, 23.4).
 bool one_round(const W4Args& g, bool x_f32) {
   const int64_t T = g.T <= 32 ? 32 : 64, x = T * g.k * (x_f32 ? 4 : 2);
   return g.T <= (x_f32 ? 32 : 64) && g.n <= 256 * 32 && x <= (256 << 10) + 64 * (int64_t)g.n;
