@@ -78,7 +78,8 @@ def w4_linear(x, codes, scale, zero=None, out_dtype=None, out=None, workspace=No
     x [T][k] (bf16 or fp32), codes [n][k / 2] uint8 (low nibble = even element),
     scale [n][k / g] bf16, zero [n][k / g] uint8 (None: 8 everywhere).
     out_dtype: bf16 or fp32, x's by default.  workspace: a uint8 tensor of
-    k3moe_w4_workspace_bytes (made when needed, above 16 tokens, if not given)."""
+    k3moe_w4_workspace_bytes (made when needed, above 16 tokens, if not given).
+    The result carries no gradient."""
     return _run(lib.k3moe_w4_linear, False, x, codes, scale, zero, out_dtype, out, workspace, stream)
 
 
