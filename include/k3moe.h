@@ -71,7 +71,9 @@ enum {
   K3MOE_OP_LAYER = 5,
   K3MOE_OP_EXPERT_GATEUP = 6,
   K3MOE_OP_SHARED_TRAIN = 7,
-  K3MOE_OP_SHARED_BACKWARD = 8
+  K3MOE_OP_SHARED_BACKWARD = 8,
+  K3MOE_OP_DISPATCH = 9,
+  K3MOE_OP_ROUTE_BACKWARD = 10
 };
 /* Router modes (k3moe_shape.router).
  *   SOFTMAX:      S_t = k largest logits; w = softmax of the chosen logits.
@@ -565,6 +567,70 @@ k3moe_status k3moe_grad_norm(const k3moe_tensor* tensors, int32_t n, float* norm
  * a workspace that overlaps a tensor's data or out. */
 k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_norm, float* norm,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Training through the routing: rows moved to the experts' order and back, with
+ * the gradients of both and of the router.  The (token, slot) pairs are those of
+ * k3moe_permute, pair p = t*k + s at sorted position pair_pos[p]; a dropped pair
+ * (pair_pos -1) has no row and no part in any sum.  Only T, d, E, k, the types
+ * and, for the router, `router` of the shape are used beside its checks.  x_dtype
+ * is the type of x and of the sorted rows, out_dtype that of y and dy.  Sums are
+ * fp32 in a fixed order (slots ascending), rounded once.  A position or id
+ * outside its range is taken as dropped.  Outputs must not overlap inputs or each
+ * other (EINVAL).
+ * The reference pages only run their model; this pass is the library's, for
+ * experts of the caller's own between the sorting and the combine.
+ * ------------------------------------------------------------------------- */
+/* k3moe_permute's outputs for topk_idx (the same values), and rows [T*k][d]:
+ *   rows[pair_pos[t*k+s]] = x[t], zeros behind the last pair's row.
+ * Errors: EINVAL, EALIGN, EWORKSPACE.
+ * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_DISPATCH). */
+k3moe_status k3moe_dispatch(const k3moe_shape* shape, const void* x, const int32_t* topk_idx,
+                            void* rows, int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
+                            int32_t* pair_pos, int32_t* diag, void* workspace,
+                            size_t workspace_bytes, void* stream);
+/* Its backward: dx [T][d] (out_dtype), dx[t] = sum over the slots of
+ * drows[pair_pos[t*k+s]], drows [T*k][d] (x_dtype).  Errors: EINVAL, EALIGN. */
+k3moe_status k3moe_dispatch_backward(const k3moe_shape* shape, const void* drows,
+                                     const int32_t* pair_pos, void* dx, void* stream);
+/* Rows back at their tokens, with the weights applied:
+ *   y[t] = add[t] (0 when add is NULL) + sum over the slots with topk_w[t][s] != 0
+ *          of topk_w[t][s] * rows[pair_pos[t*k+s]],
+ * rows [T*k][d] (x_dtype), topk_w [T][k] fp32, add and y [T][d] (out_dtype).
+ * k3moe_combine with 16-bit rows or an add of y's own type.
+ * Errors: EINVAL, EALIGN. */
+k3moe_status k3moe_collect(const k3moe_shape* shape, const void* rows, const int32_t* pair_pos,
+                           const float* topk_w, const void* add, void* y, void* stream);
+/* Its backward, from dy [T][d] (out_dtype):
+ *   drows[pair_pos[t*k+s]] = topk_w[t][s] * dy[t] (x_dtype), zeros from row
+ *     offsets[E] on,
+ *   dw[t][s] = sum over the columns of dy[t] * rows[pair_pos[t*k+s]] (fp32), 0 for
+ *     a dropped pair.
+ * (add's gradient is dy.)  An output that is NULL is not computed; rows is read
+ * for dw only, topk_w and offsets for drows only (NULL where not read).
+ * Errors: EINVAL, EALIGN. */
+k3moe_status k3moe_collect_backward(const k3moe_shape* shape, const void* dy, const void* rows,
+                                    const int32_t* pair_pos, const float* topk_w,
+                                    const int32_t* offsets, void* drows, float* dw, void* stream);
+/* The router's gradient, from that of the weights: dw [T][k] fp32 ->
+ *   dx [T][d] (x_dtype) = sum over the slots of dl[t][s] * w_router[topk_idx[t][s]],
+ *   dw_router [E][d] (out_dtype) = sum over the tokens of each expert of dl x,
+ * with dl the gradient of the chosen experts' logits (the choice itself has none):
+ *   softmax       dl_s = w_s (dw_s - sum of w dw)
+ *   sigmoid       dl_s = dw_s w_s (1 - w_s)
+ *   renormalised  dl_s = w_s (1 - sigmoid(logit_s)) (dw_s - sum of w dw)
+ * Terms whose dl is 0 are skipped.  logits [T][E] fp32 as k3moe_route writes them
+ * (renormalised sigmoid only, else NULL).  offsets, sorted_pair and pair_pos as
+ * k3moe_permute or k3moe_dispatch write them.  An output that is NULL is not
+ * computed; T = 0 writes zeros to dw_router.
+ * Errors: EINVAL, EALIGN, EWORKSPACE.
+ * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_ROUTE_BACKWARD). */
+k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const void* w_router,
+                                  const int32_t* topk_idx, const float* topk_w, const float* dw,
+                                  const float* logits, const int32_t* offsets,
+                                  const int32_t* sorted_pair, const int32_t* pair_pos, void* dx,
+                                  void* dw_router, void* workspace, size_t workspace_bytes,
+                                  void* stream);
 
 /* Static description of a status code. */
 const char* k3moe_status_str(k3moe_status status);

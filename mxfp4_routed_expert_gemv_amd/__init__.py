@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(HERE, "libk3moe.so")
 F32, BF16 = 0, 1
 FMT_MXFP4, FMT_BF16, FMT_RVQ3 = 0, 1, 2
 (OP_ROUTE, OP_PERMUTE, OP_EXPERT_FFN, OP_SHARED_FFN, OP_COMBINE, OP_LAYER,
- OP_EXPERT_GATEUP, OP_SHARED_TRAIN, OP_SHARED_BACKWARD) = range(9)
+ OP_EXPERT_GATEUP, OP_SHARED_TRAIN, OP_SHARED_BACKWARD, OP_DISPATCH, OP_ROUTE_BACKWARD) = range(11)
 PATH_GEMV, PATH_MFMA = 0, 1
 ROUTER_SOFTMAX, ROUTER_SIGMOID, ROUTER_SIGMOID_NORM = 0, 1, 2
 ROUTERS = {"softmax": ROUTER_SOFTMAX, "sigmoid": ROUTER_SIGMOID,
@@ -41,7 +41,9 @@ EXPORTS = ["k3moe_workspace_bytes", "k3moe_mxfp4_bytes", "k3moe_path_class", "k3
            "k3moe_cache_workspace_bytes", "k3moe_cache_layer", "k3moe_cache_prefetch",
            "k3moe_cache_plan", "k3moe_cache_stats_get", "k3moe_shared_ffn_train",
            "k3moe_shared_ffn_backward", "k3moe_w4_workspace_bytes", "k3moe_w4_linear", "k3moe_w4_glu",
-           "k3moe_grad_workspace_bytes", "k3moe_grad_norm", "k3moe_grad_clip"]
+           "k3moe_grad_workspace_bytes", "k3moe_grad_norm", "k3moe_grad_clip", "k3moe_dispatch",
+           "k3moe_dispatch_backward", "k3moe_collect", "k3moe_collect_backward",
+           "k3moe_route_backward"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -152,6 +154,16 @@ def _load():
     lib.k3moe_grad_norm.argtypes = [P, I32, P, P, S, P]
     lib.k3moe_grad_clip.restype = ctypes.c_int
     lib.k3moe_grad_clip.argtypes = [P, I32, ctypes.c_float, P, P, S, P]
+    lib.k3moe_dispatch.restype = ctypes.c_int
+    lib.k3moe_dispatch.argtypes = [SP, P, P, P, P, P, P, P, P, P, S, P]
+    lib.k3moe_dispatch_backward.restype = ctypes.c_int
+    lib.k3moe_dispatch_backward.argtypes = [SP, P, P, P, P]
+    lib.k3moe_collect.restype = ctypes.c_int
+    lib.k3moe_collect.argtypes = [SP, P, P, P, P, P, P]
+    lib.k3moe_collect_backward.restype = ctypes.c_int
+    lib.k3moe_collect_backward.argtypes = [SP, P, P, P, P, P, P, P, P]
+    lib.k3moe_route_backward.restype = ctypes.c_int
+    lib.k3moe_route_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, P, P, S, P]
     lib.k3moe_status_str.restype = ctypes.c_char_p
     lib.k3moe_status_str.argtypes = [ctypes.c_int]
     lib.k3moe_last_error.restype = ctypes.c_char_p
@@ -337,6 +349,39 @@ def k3moe_grad_norm(tensors, n, norm, workspace=None, stream=None):
 def k3moe_grad_clip(tensors, n, max_norm, norm, workspace=None, stream=None):
     wp, wb = _ws(workspace)
     _check(lib.k3moe_grad_clip(tensors, n, max_norm, _addr(norm), wp, wb, _stream(stream)))
+
+
+def k3moe_dispatch(shape, x, topk_idx, rows, counts, offsets, sorted_pair, pair_pos, diag=None,
+                   workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_dispatch(ctypes.byref(shape), _addr(x), _addr(topk_idx), _addr(rows),
+                              _addr(counts), _addr(offsets), _addr(sorted_pair), _addr(pair_pos),
+                              _addr(diag), wp, wb, _stream(stream)))
+
+
+def k3moe_dispatch_backward(shape, drows, pair_pos, dx, stream=None):
+    _check(lib.k3moe_dispatch_backward(ctypes.byref(shape), _addr(drows), _addr(pair_pos),
+                                       _addr(dx), _stream(stream)))
+
+
+def k3moe_collect(shape, rows, pair_pos, topk_w, add, y, stream=None):
+    _check(lib.k3moe_collect(ctypes.byref(shape), _addr(rows), _addr(pair_pos), _addr(topk_w),
+                             _addr(add), _addr(y), _stream(stream)))
+
+
+def k3moe_collect_backward(shape, dy, rows, pair_pos, topk_w, offsets, drows, dw, stream=None):
+    _check(lib.k3moe_collect_backward(ctypes.byref(shape), _addr(dy), _addr(rows),
+                                      _addr(pair_pos), _addr(topk_w), _addr(offsets), _addr(drows),
+                                      _addr(dw), _stream(stream)))
+
+
+def k3moe_route_backward(shape, x, w_router, topk_idx, topk_w, dw, logits, offsets, sorted_pair,
+                         pair_pos, dx, dw_router, workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_route_backward(ctypes.byref(shape), _addr(x), _addr(w_router),
+                                    _addr(topk_idx), _addr(topk_w), _addr(dw), _addr(logits),
+                                    _addr(offsets), _addr(sorted_pair), _addr(pair_pos), _addr(dx),
+                                    _addr(dw_router), wp, wb, _stream(stream)))
 
 
 class ExpertCache:

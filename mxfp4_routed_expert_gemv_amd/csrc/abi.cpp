@@ -214,6 +214,19 @@ k3moe_status check_disjoint(const Region (&written)[W], const Region (&read)[R])
   return K3MOE_OK;
 }
 
+// Bytes of the operands that move between the tokens' and the experts' order.
+struct RowBytes {
+  size_t out, x, y, rows, pairs;   // one output element; x, y, the rows, a word per pair
+  explicit RowBytes(const k3moe_shape& s) {
+    const size_t in = s.x_dtype == K3MOE_F32 ? 4 : 2, P = (size_t)s.T * s.k;
+    out = s.out_dtype == K3MOE_F32 ? 4 : 2;
+    x = (size_t)s.T * s.d * in;
+    y = (size_t)s.T * s.d * out;
+    rows = P * s.d * in;
+    pairs = 4 * P;
+  }
+};
+
 k3moe_status check_w4_regions(const k3moe_w4_matrix& w, size_t x_bytes, const void* x,
                               const void* out, size_t out_bytes, const void* workspace,
                               size_t ws_bytes) {
@@ -582,6 +595,8 @@ size_t k3moe_workspace_bytes(const k3moe_shape* shape, int op) {
     case K3MOE_OP_LAYER: carve_layer(*shape, nullptr, &n); break;
     case K3MOE_OP_SHARED_TRAIN: carve_shared_train(*shape, false, nullptr, &n); break;
     case K3MOE_OP_SHARED_BACKWARD: carve_shared_train(*shape, true, nullptr, &n); break;
+    case K3MOE_OP_DISPATCH: carve_permute(*shape, nullptr, &n); break;
+    case K3MOE_OP_ROUTE_BACKWARD: carve_route_back(*shape, nullptr, &n); break;
     default: return 0;
   }
   return n;
@@ -845,6 +860,144 @@ k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_n
   if (!(max_norm >= 0.0f)) return fail(K3MOE_EINVAL, "max_norm is negative or NaN");
   return run_grads(tensors, n, true, max_norm, norm, workspace, workspace_bytes, stream,
                    "k3moe_grad_clip launch");
+}
+
+k3moe_status k3moe_dispatch(const k3moe_shape* shape, const void* x, const int32_t* topk_idx,
+                            void* rows, int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
+                            int32_t* pair_pos, int32_t* diag, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  K3_CHECK(check_shape(shape));
+  const k3moe_shape& s = *shape;
+  if (s.T == 0) return ok();
+  K3_CHECK(need_ptr(x, "x"));
+  K3_CHECK(need_ptr(topk_idx, "topk_idx"));
+  K3_CHECK(need_ptr(rows, "rows"));
+  K3_CHECK(need_ptr(counts, "counts"));
+  K3_CHECK(need_ptr(offsets, "offsets"));
+  K3_CHECK(need_ptr(sorted_pair, "sorted_pair"));
+  K3_CHECK(need_ptr(pair_pos, "pair_pos"));
+  K3_CHECK(opt_ptr(diag, "diag"));
+  size_t need = 0;
+  carve_permute(s, nullptr, &need);
+  K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  const RowBytes b(s);
+  const Region written[] = {{rows, b.rows, "rows"}, {counts, 4 * (size_t)s.E, "counts"},
+                            {offsets, 4 * (size_t)s.E + 4, "offsets"}, {sorted_pair, b.pairs, "sorted_pair"},
+                            {pair_pos, b.pairs, "pair_pos"}, {diag, 4 * K3MOE_DIAG_COUNT, "diag"},
+                            {workspace, need, "workspace"}};
+  const Region read[] = {{x, b.x, "x"}, {topk_idx, b.pairs, "topk_idx"}};
+  K3_CHECK(check_disjoint(written, read));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e = launch_permute(s, topk_idx, counts, offsets, sorted_pair, pair_pos, diag,
+                                carve_permute(s, workspace, nullptr), st);
+  if (e == hipSuccess) e = launch_dispatch_rows(s, x, pair_pos, offsets, rows, st);
+  return hip_status(e, "k3moe_dispatch launch");
+}
+
+k3moe_status k3moe_dispatch_backward(const k3moe_shape* shape, const void* drows,
+                                     const int32_t* pair_pos, void* dx, void* stream) {
+  K3_CHECK(check_shape(shape));
+  const k3moe_shape& s = *shape;
+  if (s.T == 0) return ok();
+  K3_CHECK(need_ptr(drows, "drows"));
+  K3_CHECK(need_ptr(pair_pos, "pair_pos"));
+  K3_CHECK(need_ptr(dx, "dx"));
+  const RowBytes b(s);
+  const Region written[] = {{dx, b.y, "dx"}};
+  const Region read[] = {{drows, b.rows, "drows"}, {pair_pos, b.pairs, "pair_pos"}};
+  K3_CHECK(check_disjoint(written, read));
+  return hip_status(launch_collect(s, drows, pair_pos, nullptr, nullptr, dx,
+                                   static_cast<hipStream_t>(stream)),
+                    "k3moe_dispatch_backward launch");
+}
+
+k3moe_status k3moe_collect(const k3moe_shape* shape, const void* rows, const int32_t* pair_pos,
+                           const float* topk_w, const void* add, void* y, void* stream) {
+  K3_CHECK(check_shape(shape));
+  const k3moe_shape& s = *shape;
+  if (s.T == 0) return ok();
+  K3_CHECK(need_ptr(rows, "rows"));
+  K3_CHECK(need_ptr(pair_pos, "pair_pos"));
+  K3_CHECK(need_ptr(topk_w, "topk_w"));
+  K3_CHECK(opt_ptr(add, "add"));
+  K3_CHECK(need_ptr(y, "y"));
+  const RowBytes b(s);
+  const Region written[] = {{y, b.y, "y"}};
+  const Region read[] = {{rows, b.rows, "rows"}, {pair_pos, b.pairs, "pair_pos"},
+                         {topk_w, b.pairs, "topk_w"}, {add, b.y, "add"}};
+  K3_CHECK(check_disjoint(written, read));
+  return hip_status(launch_collect(s, rows, pair_pos, topk_w, add, y,
+                                   static_cast<hipStream_t>(stream)),
+                    "k3moe_collect launch");
+}
+
+k3moe_status k3moe_collect_backward(const k3moe_shape* shape, const void* dy, const void* rows,
+                                    const int32_t* pair_pos, const float* topk_w,
+                                    const int32_t* offsets, void* drows, float* dw, void* stream) {
+  K3_CHECK(check_shape(shape));
+  const k3moe_shape& s = *shape;
+  if (s.T == 0 || (!drows && !dw)) return ok();
+  K3_CHECK(need_ptr(dy, "dy"));
+  K3_CHECK(need_ptr(pair_pos, "pair_pos"));
+  K3_CHECK(opt_ptr(drows, "drows"));
+  K3_CHECK(opt_ptr(dw, "dw"));
+  if (dw) K3_CHECK(need_ptr(rows, "rows"));
+  if (drows) {
+    K3_CHECK(need_ptr(topk_w, "topk_w"));
+    K3_CHECK(need_ptr(offsets, "offsets"));
+  }
+  const RowBytes b(s);
+  const Region written[] = {{drows, b.rows, "drows"}, {dw, b.pairs, "dw"}};
+  const Region read[] = {{dy, b.y, "dy"}, {dw ? rows : nullptr, b.rows, "rows"},
+                         {pair_pos, b.pairs, "pair_pos"}, {drows ? topk_w : nullptr, b.pairs, "topk_w"},
+                         {drows ? offsets : nullptr, 4 * (size_t)s.E + 4, "offsets"}};
+  K3_CHECK(check_disjoint(written, read));
+  return hip_status(launch_collect_back(s, dy, rows, pair_pos, topk_w, offsets, drows, dw,
+                                        static_cast<hipStream_t>(stream)),
+                    "k3moe_collect_backward launch");
+}
+
+k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const void* w_router,
+                                  const int32_t* topk_idx, const float* topk_w, const float* dw,
+                                  const float* logits, const int32_t* offsets,
+                                  const int32_t* sorted_pair, const int32_t* pair_pos, void* dx,
+                                  void* dw_router, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  K3_CHECK(check_shape(shape));
+  const k3moe_shape& s = *shape;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  K3_CHECK(opt_ptr(dx, "dx"));
+  K3_CHECK(opt_ptr(dw_router, "dw_router"));
+  const RowBytes b(s);
+  const size_t weights = (size_t)s.E * s.d;
+  if (s.T == 0)
+    return hip_status(launch_zero(dw_router, weights * b.out, st), "k3moe_route_backward launch");
+  if (!dx && !dw_router) return ok();
+  K3_CHECK(need_ptr(x, "x"));
+  K3_CHECK(need_ptr(w_router, "w_router"));
+  K3_CHECK(need_ptr(topk_idx, "topk_idx"));
+  K3_CHECK(need_ptr(topk_w, "topk_w"));
+  K3_CHECK(need_ptr(dw, "dw"));
+  if (s.router == K3MOE_ROUTER_SIGMOID_NORM) K3_CHECK(need_ptr(logits, "logits"));
+  else if (logits) return fail(K3MOE_EINVAL, "logits are given but this router's gradient takes none");
+  K3_CHECK(need_ptr(offsets, "offsets"));
+  K3_CHECK(need_ptr(sorted_pair, "sorted_pair"));
+  K3_CHECK(need_ptr(pair_pos, "pair_pos"));
+  size_t need = 0;
+  carve_route_back(s, nullptr, &need);
+  K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  const Region written[] = {{dx, b.x, "dx"}, {dw_router, weights * b.out, "dw_router"},
+                            {workspace, need, "workspace"}};
+  const Region read[] = {{x, b.x, "x"}, {w_router, 2 * weights, "w_router"},
+                         {topk_idx, b.pairs, "topk_idx"}, {topk_w, b.pairs, "topk_w"},
+                         {dw, b.pairs, "dw"}, {logits, 4 * (size_t)s.T * s.E, "logits"},
+                         {offsets, 4 * (size_t)s.E + 4, "offsets"},
+                         {sorted_pair, b.pairs, "sorted_pair"}, {pair_pos, b.pairs, "pair_pos"}};
+  K3_CHECK(check_disjoint(written, read));
+  return hip_status(launch_route_back(s, x, static_cast<const uint16_t*>(w_router), topk_idx, topk_w,
+                                      dw, logits, offsets, sorted_pair, pair_pos, dx, dw_router,
+                                      carve_route_back(s, workspace, nullptr), st),
+                    "k3moe_route_backward launch");
 }
 
 const char* k3moe_status_str(k3moe_status status) {

@@ -202,6 +202,27 @@ GradWs carve_grads(int n, void* ws, size_t* bytes);
 hipError_t launch_grads(const k3moe_tensor* ts, int n, bool clip, float max_norm, float* norm,
                         const GradWs& ws, hipStream_t st);
 
+// Rows to and from the experts' order and the router's gradient (rows.hip).
+struct RouteBackWs {
+  float* dl;         // [T][k] gradient of the chosen experts' logits
+  int32_t* chunks;   // the experts' pairs in chunks, four words each
+  int32_t* joins;    // [E] first row and number of the rows of `part`, two words each
+  float* part;       // [..][d] sums of chunks
+};
+RouteBackWs carve_route_back(const k3moe_shape& s, void* ws, size_t* bytes);
+hipError_t launch_dispatch_rows(const k3moe_shape& s, const void* x, const int32_t* pair_pos,
+                                const int32_t* offsets, void* rows, hipStream_t st);
+hipError_t launch_collect(const k3moe_shape& s, const void* rows, const int32_t* pair_pos,
+                          const float* w, const void* add, void* out, hipStream_t st);
+hipError_t launch_collect_back(const k3moe_shape& s, const void* dy, const void* rows,
+                               const int32_t* pair_pos, const float* w, const int32_t* offsets,
+                               void* drows, float* dw, hipStream_t st);
+hipError_t launch_route_back(const k3moe_shape& s, const void* x, const uint16_t* w_router,
+                             const int32_t* idx, const float* w, const float* dw, const float* logits,
+                             const int32_t* offsets, const int32_t* sorted_pair,
+                             const int32_t* pair_pos, void* dx, void* dw_router,
+                             const RouteBackWs& ws, hipStream_t st);
+
 // Whole-layer entry points: the host-side validation (nothing enqueued; *need
 // = workspace bytes, 0 for an empty batch), the status of a workspace that is
 // too small, and the stages of a validated call on a workspace of at least
