@@ -632,6 +632,37 @@ k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const
                                   void* dw_router, void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The orthogonalised update of a weight matrix (what a Muon step adds, times its
+ * learning rate): Newton-Schulz steps that move every singular value of the
+ * gradient or momentum towards 1 and leave its singular vectors.  For each of
+ * `batch` matrices G [m][n], with X taken wide (G, or its transpose when m > n):
+ *   X = G / |G| (Frobenius; a matrix of zeros stays zero), `steps` times
+ *   X = a X + b (X X^T) X + c (X X^T)^2 X,  out = scale X  (rounded to bf16)
+ * The norm is fp64; the products' operands are rounded to fp16 (11 bits), a X is
+ * not (22 bits), sums are fp32.  The result is within 3e-3 of the exact one in
+ * norm, 1.7e-3 of it the rounding to bf16.  A non-finite G gives non-finite values.
+ * (The reference pages do not train; this belongs to k3moe_shared_ffn_backward,
+ * k3moe_route_backward and k3moe_grad_clip.)
+ * ------------------------------------------------------------------------- */
+typedef struct k3moe_ortho {
+  int32_t batch;               /* 1 .. 65535 */
+  int32_t m, n;                /* 1 .. 32768 each; batch m n <= 2^34 */
+  int32_t dtype;               /* of g: K3MOE_F32 or K3MOE_BF16 */
+  int32_t steps;               /* 1 .. 64 */
+  const float* coefficients;   /* HOST [steps][3]: a, b, c of each step */
+  float scale;                 /* finite */
+} k3moe_ortho;
+/* Workspace of the call below (0 for invalid arguments); 256-byte aligned. */
+size_t k3moe_orthogonalize_workspace_bytes(const k3moe_ortho* p);
+/* g [batch][m][n] -> out [batch][m][n] bf16; out may be g itself when that is bf16.
+ * Errors: EINVAL (NULL pointers, steps, scale, coefficients that let a singular
+ * value pass 1.4 before the last step or that are not finite, an out that overlaps g
+ * otherwise, a workspace that overlaps either), ESHAPE, EUNSUPPORTED, EALIGN,
+ * EWORKSPACE. */
+k3moe_status k3moe_orthogonalize(const k3moe_ortho* p, const void* g, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* k3moe_status_str(k3moe_status status);
 /* Detail of the last non-OK status returned on the calling thread. */

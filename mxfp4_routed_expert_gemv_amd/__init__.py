@@ -43,7 +43,7 @@ EXPORTS = ["k3moe_workspace_bytes", "k3moe_mxfp4_bytes", "k3moe_path_class", "k3
            "k3moe_shared_ffn_backward", "k3moe_w4_workspace_bytes", "k3moe_w4_linear", "k3moe_w4_glu",
            "k3moe_grad_workspace_bytes", "k3moe_grad_norm", "k3moe_grad_clip", "k3moe_dispatch",
            "k3moe_dispatch_backward", "k3moe_collect", "k3moe_collect_backward",
-           "k3moe_route_backward"]
+           "k3moe_route_backward", "k3moe_orthogonalize_workspace_bytes", "k3moe_orthogonalize"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -80,6 +80,12 @@ class W4Matrix(ctypes.Structure):
 class Tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class Ortho(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("m", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("coefficients", ctypes.POINTER(ctypes.c_float)), ("scale", ctypes.c_float)]
 
 
 class K3moeError(RuntimeError):
@@ -164,6 +170,10 @@ def _load():
     lib.k3moe_collect_backward.argtypes = [SP, P, P, P, P, P, P, P, P]
     lib.k3moe_route_backward.restype = ctypes.c_int
     lib.k3moe_route_backward.argtypes = [SP, P, P, P, P, P, P, P, P, P, P, P, P, S, P]
+    lib.k3moe_orthogonalize_workspace_bytes.restype = S
+    lib.k3moe_orthogonalize_workspace_bytes.argtypes = [ctypes.POINTER(Ortho)]
+    lib.k3moe_orthogonalize.restype = ctypes.c_int
+    lib.k3moe_orthogonalize.argtypes = [ctypes.POINTER(Ortho), P, P, P, S, P]
     lib.k3moe_status_str.restype = ctypes.c_char_p
     lib.k3moe_status_str.argtypes = [ctypes.c_int]
     lib.k3moe_last_error.restype = ctypes.c_char_p
@@ -382,6 +392,15 @@ def k3moe_route_backward(shape, x, w_router, topk_idx, topk_w, dw, logits, offse
                                     _addr(topk_idx), _addr(topk_w), _addr(dw), _addr(logits),
                                     _addr(offsets), _addr(sorted_pair), _addr(pair_pos), _addr(dx),
                                     _addr(dw_router), wp, wb, _stream(stream)))
+
+
+def k3moe_orthogonalize_workspace_bytes(p: Ortho) -> int:
+    return lib.k3moe_orthogonalize_workspace_bytes(ctypes.byref(p))
+
+
+def k3moe_orthogonalize(p: Ortho, g, out, workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(lib.k3moe_orthogonalize(ctypes.byref(p), _addr(g), _addr(out), wp, wb, _stream(stream)))
 
 
 class ExpertCache:

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <new>
 #include <string>
 #include <vector>
@@ -313,6 +314,22 @@ k3moe_status check_grads(const k3moe_tensor* ts, int32_t n, const float* norm, b
       return fail(K3MOE_EALIGN, "tensor %d is not aligned to its elements", i);
   }
   return clip ? check_overlap(ts, n) : K3MOE_OK;
+}
+
+k3moe_status check_ortho(const k3moe_ortho* p) {
+  if (!p) return fail(K3MOE_EINVAL, "the problem is NULL");
+  if (p->batch < 1 || p->batch > 65535 || p->m < 1 || p->m > 32768 || p->n < 1 || p->n > 32768 ||
+      (int64_t)p->batch * p->m * p->n > (int64_t(1) << 34))
+    return fail(K3MOE_ESHAPE, "batch = %d, m = %d, n = %d: need 1 <= batch <= 65535, 1 <= m, n <= 32768, "
+                "batch * m * n <= 2^34", p->batch, p->m, p->n);
+  if (p->dtype != K3MOE_F32 && p->dtype != K3MOE_BF16)
+    return fail(K3MOE_EUNSUPPORTED, "dtype %d is not F32 or BF16", p->dtype);
+  if (p->steps < 1 || p->steps > 64) return fail(K3MOE_EINVAL, "steps = %d: need 1 <= steps <= 64", p->steps);
+  if (!p->coefficients) return fail(K3MOE_EINVAL, "coefficients is NULL");
+  if (!std::isfinite(p->scale)) return fail(K3MOE_EINVAL, "scale is not finite");
+  if (!ortho_bounded(*p))
+    return fail(K3MOE_EINVAL, "the coefficients let a singular value pass 1.4 before the last step");
+  return K3MOE_OK;
 }
 
 k3moe_status hip_status(hipError_t e, const char* what) {
@@ -998,6 +1015,31 @@ k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const
                                       dw, logits, offsets, sorted_pair, pair_pos, dx, dw_router,
                                       carve_route_back(s, workspace, nullptr), st),
                     "k3moe_route_backward launch");
+}
+
+size_t k3moe_orthogonalize_workspace_bytes(const k3moe_ortho* p) {
+  if (check_ortho(p) != K3MOE_OK) return 0;
+  size_t need = 0;
+  carve_ortho(*p, nullptr, &need);
+  return need;
+}
+
+k3moe_status k3moe_orthogonalize(const k3moe_ortho* p, const void* g, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  K3_CHECK(check_ortho(p));
+  K3_CHECK(need_ptr(g, "g"));
+  K3_CHECK(need_ptr(out, "out"));
+  size_t need = 0;
+  carve_ortho(*p, nullptr, &need);
+  K3_CHECK(check_ws(workspace, workspace_bytes, need));
+  const size_t n = (size_t)p->batch * p->m * p->n, size = p->dtype == K3MOE_F32 ? 4 : 2;
+  const bool in_place = g == out && p->dtype == K3MOE_BF16;
+  const Region written[] = {{out, 2 * n, "out"}, {workspace, need, "workspace"}};
+  const Region read[] = {{in_place ? nullptr : g, size * n, "g"}};
+  K3_CHECK(check_disjoint(written, read));
+  return hip_status(launch_ortho(*p, g, out, carve_ortho(*p, workspace, nullptr),
+                                 static_cast<hipStream_t>(stream)),
+                    "k3moe_orthogonalize launch");
 }
 
 const char* k3moe_status_str(k3moe_status status) {

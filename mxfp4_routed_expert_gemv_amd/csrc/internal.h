@@ -223,6 +223,20 @@ hipError_t launch_route_back(const k3moe_shape& s, const void* x, const uint16_t
                              const int32_t* pair_pos, void* dx, void* dw_router,
                              const RouteBackWs& ws, hipStream_t st);
 
+// The orthogonalised update (ortho.hip), on checked arguments.
+struct OrthoWs {
+  double* sums;      // sums of squares of pieces of each matrix
+  uint16_t* x[2];    // X's first parts, of this step and the next
+  uint16_t* lo;      // its second parts
+  uint16_t* A;       // X X^T
+  uint16_t* B;       // b A + c A A
+  float* part;       // partial sums of products whose contraction is split
+};
+OrthoWs carve_ortho(const k3moe_ortho& p, void* ws, size_t* bytes);
+bool ortho_bounded(const k3moe_ortho& p);
+hipError_t launch_ortho(const k3moe_ortho& p, const void* g, void* out, const OrthoWs& ws,
+                        hipStream_t st);
+
 // Whole-layer entry points: the host-side validation (nothing enqueued; *need
 // = workspace bytes, 0 for an empty batch), the status of a workspace that is
 // too small, and the stages of a validated call on a workspace of at least
