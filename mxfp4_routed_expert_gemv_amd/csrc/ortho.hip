@@ -49,10 +49,12 @@ struct OrthoArgs {
   uint16_t* A;            // [batch][s][s]
   uint16_t* B;
   void* out;              // kLast: [batch][rows][cols], kLastT: [batch][cols][rows], bf16
-  float* part;            // split contraction: sums of [tile][split] in the waves' own order
+  float* part;            // sums of the split tiles' pieces, in the waves' own order
   int s, l, batch;        // s and l in whole 64
   int rows, cols;         // the matrix's own
-  int splits, k_split;    // contraction elements per split (a multiple of kBK)
+  int whole;              // tiles that one workgroup computes; the contraction of the others
+  int pieces, k_piece;    // is split into pieces of k_piece elements (a multiple of kBK)
+  int keep_lo;            // kStep: the next step takes second parts (the last does not)
   float ca, cb, cc, scale;
 };
 
@@ -131,11 +133,32 @@ __device__ __forceinline__ At tile_at(const OrthoArgs& g, int it) {
   return At{b, (first + q - j * gsz) * C::BM, j * C::BN};
 }
 
-// ---- epilogue: row block i (16 rows) of a wave's fragments.  Two fragments side by
-// side, their odd and even groups of 16 lanes exchanged, give a lane eight
-// consecutive columns of its row (and of B and X, which it reads there, 16 bytes).
+// ---- epilogue of a wave's fragments.  Two fragments side by side, their odd and even
+// groups of 16 lanes exchanged, give a lane eight consecutive columns of its row; it
+// reads A or X's two parts there, 16 bytes each (outside the matrix: at the origin).
+struct Old {
+  uint4 h, l;   // A, or X's parts
+};
+template <int P>
+__device__ __forceinline__ Old load_old(const OrthoArgs& g, int b, int m16, int n_wave, int f) {
+  const int lane = threadIdx.x & 63, lg = lane >> 4, m = m16 + (lane & 15);
+  const int n = n_wave + (f + (lg & 1)) * 16 + (lg >> 1) * 8;
+  Old o{};
+  if (P == kPoly) {
+    const uint32_t at = m < g.s && n < g.s ? (uint32_t)m * g.s + n : 0;
+    o.h = *reinterpret_cast<const uint4*>(g.A + (size_t)b * g.s * g.s + at);
+  } else if (P > kPoly) {
+    const uint32_t at = m < g.s && n < g.l ? (uint32_t)m * g.l + n : 0;
+    o.h = *reinterpret_cast<const uint4*>(g.x + (size_t)b * g.s * g.l + at);
+    if (P == kStep) o.l = *reinterpret_cast<const uint4*>(g.lo + (size_t)b * g.s * g.l + at);
+  }
+  return o;
+}
+
+// Row block i (16 rows).
 template <int P, int NF>
-__device__ __forceinline__ void finish_row(const OrthoArgs& g, int b, int m16, int n_wave, f32x4_t (&acc)[NF]) {
+__device__ __forceinline__ void finish_row(const OrthoArgs& g, int b, int m16, int n_wave, f32x4_t (&acc)[NF],
+                                           const Old (&old)[NF / 2]) {
   const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4, m = m16 + ln;
   const size_t ss = (size_t)g.s * g.s, sl = (size_t)g.s * g.l;
 #pragma unroll
@@ -158,7 +181,7 @@ __device__ __forceinline__ void finish_row(const OrthoArgs& g, int b, int m16, i
 #pragma unroll
         for (int r = 0; r < 8; ++r) v[r] *= 1.0f / kScaleX;
       } else {
-        const uint4 a = in ? *reinterpret_cast<const uint4*>(g.A + at) : make_uint4(0, 0, 0, 0);
+        const uint4 a = old[f / 2].h;
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
         const float hb = 0.5f * g.cb, hc = g.cc * (0.5f / kScaleX);
 #pragma unroll
@@ -178,15 +201,12 @@ __device__ __forceinline__ void finish_row(const OrthoArgs& g, int b, int m16, i
     } else {
       const bool in = m < g.s && n < g.l;
       const size_t at = b * sl + (size_t)m * g.l + n;
-      uint4 h{}, l{};
-      if (in) {
-        h = *reinterpret_cast<const uint4*>(g.x + at);
-        l = *reinterpret_cast<const uint4*>(g.lo + at);
-      }
+      const uint4 h = old[f / 2].h, l = old[f / 2].l;
       const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        const float x = r & 1 ? f16_hi(hw[r / 2]) + f16_hi(lw[r / 2]) : f16_lo(hw[r / 2]) + f16_lo(lw[r / 2]);
+        float x = r & 1 ? f16_hi(hw[r / 2]) : f16_lo(hw[r / 2]);
+        if (P == kStep) x += r & 1 ? f16_hi(lw[r / 2]) : f16_lo(lw[r / 2]);
         v[r] = __builtin_fmaf(g.ca, x, v[r] * (2.0f / kScaleX));
       }
       if (P == kStep) {
@@ -198,7 +218,7 @@ __device__ __forceinline__ void finish_row(const OrthoArgs& g, int b, int m16, i
         }
         if (in) {
           *reinterpret_cast<uint4*>(g.xo + at) = make_uint4(ho[0], ho[1], ho[2], ho[3]);
-          *reinterpret_cast<uint4*>(g.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (g.keep_lo) *reinterpret_cast<uint4*>(g.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         continue;
       }
@@ -242,9 +262,10 @@ __device__ __forceinline__ void finish_row(const OrthoArgs& g, int b, int m16, i
   }
 }
 
-// ---- the products.  SPLIT: an item is a tile and one of g.splits pieces of the
-// contraction; its sums go to g.part, and ortho_finish adds the pieces in order.
-template <int P, int BM, int BN, int WM, int WN, int RING, bool SPLIT>
+// ---- the products.  The first g.whole items are tiles, the others pieces of the
+// contraction of a tile each: their sums go to g.part, and ortho_finish adds them in
+// order.
+template <int P, int BM, int BN, int WM, int WN, int RING>
 __global__ __launch_bounds__(64 * WM * WN) void ortho_tile(OrthoArgs g) {
   using C = Tile<P, BM, BN, WM, WN>;
   using OA = typename C::A;
@@ -257,22 +278,34 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_tile(OrthoArgs g) {
   const int ln = lane & 15, lg = lane >> 4;
   const int N = C::kSym ? g.s : g.l, K = P == kGram ? g.l : g.s;
   const int mt = (g.s + BM - 1) / BM, nt = (N + BN - 1) / BN;
-  const int splits = SPLIT ? g.splits : 1;
-  const int n_items = g.batch * (C::kSym ? sym_tiles(mt) : mt * nt) * splits;
+  const int n_tiles = g.batch * (C::kSym ? sym_tiles(mt) : mt * nt);
+  const int n_items = g.whole + (n_tiles - g.whole) * g.pieces;
   // A round takes the next gridDim.x items, its 8 contiguous pieces one to an XCD.
+  // Every other workgroup takes the split tiles' round first, the others last, so that
+  // half of them work on a tile while the tiles of the other half go to memory.
   const int G = gridDim.x, xcd = blockIdx.x & 7, wi = blockIdx.x >> 3;
+  const int full = g.whole / G;
+  bool early = false;
   auto item_of = [&](int r) {
+    if (early && r <= full) r = r == 0 ? full : r - 1;
     const int64_t first = (int64_t)r * G;
     if (first >= n_items) return n_items;
     const int end = (int)min(first + G, (int64_t)n_items), piece = (end - (int)first + 7) >> 3;
     const int it = (int)first + xcd * piece + wi;
     return wi < piece && it < end ? it : n_items;
   };
+  // (where it has an item of that round)
+  early = (wi & 1) && g.whole % G == 0 && n_items - g.whole <= G && item_of(full) < n_items;
   auto span = [&](int it, int& k0, int& k1) {   // the item's tile
-    const int t = SPLIT ? it / splits : it, sp = SPLIT ? it - t * splits : 0;
-    k0 = SPLIT ? sp * g.k_split : 0;
-    k1 = SPLIT ? min(k0 + g.k_split, K) : K;
-    return tile_at<C>(g, t);
+    if (it < g.whole) {
+      k0 = 0;
+      k1 = K;
+      return tile_at<C>(g, it);
+    }
+    const int j = it - g.whole, t = j / g.pieces;
+    k0 = (j - t * g.pieces) * g.k_piece;
+    k1 = min(k0 + g.k_piece, K);
+    return tile_at<C>(g, g.whole + t);
   };
 
   // ---- copies, as in the shared experts' products (K is a multiple of kBK)
@@ -398,14 +431,28 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_tile(OrthoArgs g) {
       advance();
       slot = next;
     }
+    if (it >= g.whole) {
+      f32x4_t* p = reinterpret_cast<f32x4_t*>(g.part) + (size_t)(it - g.whole) * MF * NF * (64 * WM * WN);
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      if constexpr (SPLIT) {
-        f32x4_t* p = reinterpret_cast<f32x4_t*>(g.part) + (size_t)it * MF * NF * (64 * WM * WN);
+      for (int i = 0; i < MF; ++i)
 #pragma unroll
         for (int f = 0; f < NF; ++f) p[(i * NF + f) * (64 * WM * WN) + threadIdx.x] = acc[i][f];
-      } else {
-        finish_row<P, NF>(g, t.b, t.m0 + (wm * MF + i) * 16, t.n0 + wn * NF * 16, acc[i]);
+    } else {
+      // (what the next row block needs is on its way while one is finished, or a
+      // tile's way out is one wait for memory after the other)
+      Old old[2][NF / 2];
+      auto load = [&](int i) {
+#pragma unroll
+        for (int f = 0; f < NF; f += 2)
+          old[i & 1][f / 2] = load_old<P>(g, t.b, t.m0 + (wm * MF + i) * 16, t.n0 + wn * NF * 16, f);
+      };
+      load(0);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        if (i + 1 < MF) load(i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        finish_row<P, NF>(g, t.b, t.m0 + (wm * MF + i) * 16, t.n0 + wn * NF * 16, acc[i], old[i & 1]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -418,17 +465,21 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_finish(OrthoArgs g) {
   using C = Tile<P, BM, BN, WM, WN>;
   constexpr int MF = C::MF, NF = C::NF, kT = 64 * WM * WN;
   const int i = blockIdx.x % MF, tile = blockIdx.x / MF, wv = threadIdx.x >> 6;
-  const At t = tile_at<C>(g, tile);
+  const At t = tile_at<C>(g, g.whole + tile);
   const f32x4_t* p = reinterpret_cast<const f32x4_t*>(g.part) +
-                     ((size_t)tile * g.splits * MF + i) * NF * kT + threadIdx.x;
+                     ((size_t)tile * g.pieces * MF + i) * NF * kT + threadIdx.x;
   f32x4_t acc[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < g.splits; ++s, p += (size_t)MF * NF * kT) {
+  for (int s = 0; s < g.pieces; ++s, p += (size_t)MF * NF * kT) {
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[f] += p[f * kT];
   }
-  finish_row<P, NF>(g, t.b, t.m0 + (wv / WN * MF + i) * 16, t.n0 + wv % WN * NF * 16, acc);
+  const int m16 = t.m0 + (wv / WN * MF + i) * 16, n_wave = t.n0 + wv % WN * NF * 16;
+  Old old[NF / 2];
+#pragma unroll
+  for (int f = 0; f < NF; f += 2) old[f / 2] = load_old<P>(g, t.b, m16, n_wave, f);
+  finish_row<P, NF>(g, t.b, m16, n_wave, acc, old);
 }
 
 // ---- the matrix on its way in.  Sums of squares, in fp64, of equal pieces of a
@@ -538,10 +589,12 @@ __global__ __launch_bounds__(256) void scale_in(const void* __restrict__ g, cons
   }
 }
 
-// How a product runs: its tile and the pieces its contraction is split into.
-enum { kTile256, kTile128, kTile64 };
+// How a product runs: its tile, and how many of them are whole; the others are split
+// into pieces of the contraction.
+enum { kTile256, kTile128x256, kTile128, kTile64 };
 struct Plan {
-  int tile, splits, k_split;
+  int tile, whole, pieces, k_piece;
+  size_t part;   // floats of the pieces' sums
 };
 
 struct Dims {
@@ -557,34 +610,74 @@ struct Dims {
   }
 };
 
-int64_t tiles_of(int P, const Dims& d, int edge) {
-  const int64_t mt = (d.s + edge - 1) / edge, nt = (d.l + edge - 1) / edge;
+int64_t tiles_of(int P, const Dims& d, int bm, int bn) {
+  const int64_t mt = (d.s + bm - 1) / bm, nt = (d.l + bn - 1) / bn;
   return d.batch * (P <= kPoly ? mt * (mt + 1) / 2 : mt * nt);
 }
 
+// The tile and split that cost least, by what a 64-element stage and a tile's way out
+// take (us).  A last round of a few tiles takes as long as a full one, so the tiles
+// behind the last full round may be split: their pieces' sums go to memory and back
+// (at 4.5 TB/s) and a second kernel adds them, 4 us.
 Plan plan_product(int P, const Dims& d) {
-  const int nst = (P == kGram ? d.l : d.s) / kBK;
-  auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
-  const int64_t t64 = tiles_of(P, d, 64);
-  double best = t64 <= 256 ? 0.43 * nst : t64 <= 512 ? 0.5 * nst : rounds(t64, 768) * 0.64 * nst;
-  Plan p{kTile64, 1, 0};
-  auto consider = [&](int tile, int64_t t, double stage) {
-    const double c = rounds(t, 256) * stage * nst;
-    if (c < best) best = c, p = Plan{tile, 1, 0};
+  struct Kind {
+    int bm, bn, slots;
+    double stage, out;
   };
-  consider(kTile128, tiles_of(P, d, 128), 0.65);
-  consider(kTile256, tiles_of(P, d, 256), 1.6);
-  return p;
+  constexpr Kind kinds[4] = {{256, 256, 256, 1.6, 9.0}, {128, 256, 256, 0.95, 4.6},
+                             {128, 128, 256, 0.65, 2.7}, {64, 64, 768, 0.64, 1.9}};
+  const int64_t nst = (P == kGram ? d.l : d.s) / kBK;
+  double best = 1e30;
+  Plan plan{};
+  for (int k = 0; k < 4; ++k) {
+    const Kind& c = kinds[k];
+    if (P <= kPoly && c.bm != c.bn) continue;
+    const int64_t n = tiles_of(P, d, c.bm, c.bn);
+    // a round of `items` tiles or pieces of st stages; three 64 x 64 tiles share a CU
+    auto round = [&](int64_t items, int64_t st) {
+      const int64_t last = items % c.slots, full = items / c.slots;
+      const double tail = k != 3 ? c.stage : last <= 256 ? 0.43 : last <= 512 ? 0.5 : 0.64;
+      return full * (c.stage * st + c.out) + (last ? tail * st + c.out : 0.0);
+    };
+    double cost = round(n, nst);
+    if (cost < best) best = cost, plan = Plan{k, (int)n, 1, 0, 0};
+    const int64_t rest = n % c.slots, whole = n - rest;
+    for (int64_t p = 2; rest && p <= 32 && 2 * p <= nst; ++p) {
+      const int64_t per = (nst + p - 1) / p;
+      if ((p - 1) * per >= nst || rest * p > 2 * c.slots) continue;
+      const double bytes = 4.0 * rest * p * c.bm * c.bn;
+      cost = round(whole, nst) + round(rest * p, per) + 4.0 + 2 * bytes / 4.5e6;
+      if (cost < best)
+        best = cost, plan = Plan{k, (int)whole, (int)p, (int)per * kBK, (size_t)rest * p * c.bm * c.bn};
+    }
+  }
+  return plan;
+}
+
+template <int P, int BM, int BN, int WM, int WN, int RING>
+hipError_t launch_tiles(const OrthoArgs& g, int64_t tiles, int grid, hipStream_t st) {
+  constexpr int kT = 64 * WM * WN, MF = BM / 16 / WM;
+  ortho_tile<P, BM, BN, WM, WN, RING><<<grid, kT, 0, st>>>(g);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || tiles == g.whole) return e;
+  ortho_finish<P, BM, BN, WM, WN><<<(unsigned)((tiles - g.whole) * MF), kT, 0, st>>>(g);
+  return hipGetLastError();
 }
 
 template <int P>
 hipError_t launch_product(const Dims& d, OrthoArgs g, hipStream_t st) {
   const Plan p = plan_product(P, d);
   const int cus = grouped_grid();
-  if (p.tile == kTile256) ortho_tile<P, 256, 256, 2, 4, 2, false><<<cus, 512, 0, st>>>(g);
-  else if (p.tile == kTile128) ortho_tile<P, 128, 128, 2, 4, 3, false><<<cus, 512, 0, st>>>(g);
-  else ortho_tile<P, 64, 64, 2, 2, 3, false><<<cus * 3, 256, 0, st>>>(g);
-  return hipGetLastError();
+  g.whole = p.whole;
+  g.pieces = p.pieces;
+  g.k_piece = p.k_piece;
+  switch (p.tile) {
+    case kTile256: return launch_tiles<P, 256, 256, 2, 4, 2>(g, tiles_of(P, d, 256, 256), cus, st);
+    case kTile128: return launch_tiles<P, 128, 128, 2, 4, 3>(g, tiles_of(P, d, 128, 128), cus, st);
+    case kTile64: return launch_tiles<P, 64, 64, 2, 2, 3>(g, tiles_of(P, d, 64, 64), cus * 3, st);
+  }
+  if constexpr (P > kPoly) return launch_tiles<P, 128, 256, 2, 4, 3>(g, tiles_of(P, d, 128, 256), cus, st);
+  return hipSuccess;   // (no plan of a symmetric product)
 }
 
 int pieces_of(const Dims& d) {
@@ -605,7 +698,9 @@ OrthoWs carve_ortho(const k3moe_ortho& p, void* ws, size_t* bytes) {
   w.lo = c.take<uint16_t>(sl);
   w.A = c.take<uint16_t>(ss);
   w.B = c.take<uint16_t>(ss);
-  w.part = c.take<float>(0);
+  size_t part = 0;
+  for (int P : {kGram, kPoly, kStep}) part = std::max(part, plan_product(P, d).part);
+  w.part = c.take<float>(part);
   if (bytes) *bytes = c.off;
   return w;
 }
@@ -674,6 +769,7 @@ hipError_t launch_ortho(const k3moe_ortho& p, const void* g, void* out, const Or
     a.ca = p.coefficients[3 * i];
     a.cb = p.coefficients[3 * i + 1];
     a.cc = p.coefficients[3 * i + 2];
+    a.keep_lo = i + 2 < p.steps;
     if ((e = launch_product<kGram>(d, a, st)) != hipSuccess) return e;
     if ((e = launch_product<kPoly>(d, a, st)) != hipSuccess) return e;
     if (i + 1 < p.steps) e = launch_product<kStep>(d, a, st);
