@@ -639,9 +639,11 @@ k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const
  * `batch` matrices G [m][n], with X taken wide (G, or its transpose when m > n):
  *   X = G / |G| (Frobenius; a matrix of zeros stays zero), `steps` times
  *   X = a X + b (X X^T) X + c (X X^T)^2 X,  out = scale X  (rounded to bf16)
- * The norm is fp64; the products' operands are rounded to fp16 (11 bits), a X is
- * not (22 bits), sums are fp32.  The result is within 3e-3 of the exact one in
- * norm, 1.7e-3 of it the rounding to bf16.  A non-finite G gives non-finite values.
+ * Sums are fp32, the norm's fp32 or more.  Where the short side is at most 128 and
+ * the product of the a^2 of all steps but the last at most 2^15, the products'
+ * operands keep 22 bits; otherwise they are rounded to fp16 (11 bits, but 22 for the
+ * term a X of every step but the last), and the result is within 3e-3 of the exact one
+ * in norm, 1.7e-3 of it the rounding to bf16.  A non-finite G gives non-finite values.
  * (The reference pages do not train; this belongs to k3moe_shared_ffn_backward,
  * k3moe_route_backward and k3moe_grad_clip.)
  * ------------------------------------------------------------------------- */

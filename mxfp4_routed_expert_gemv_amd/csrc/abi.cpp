@@ -332,6 +332,13 @@ k3moe_status check_ortho(const k3moe_ortho* p) {
   return K3MOE_OK;
 }
 
+size_t ortho_workspace(const k3moe_ortho& p) {
+  size_t need = 0;
+  if (ortho_small_ok(p)) carve_ortho_small(p, nullptr, &need);
+  else carve_ortho(p, nullptr, &need);
+  return need;
+}
+
 k3moe_status hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return ok();
   return fail(K3MOE_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
@@ -1018,10 +1025,7 @@ k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const
 }
 
 size_t k3moe_orthogonalize_workspace_bytes(const k3moe_ortho* p) {
-  if (check_ortho(p) != K3MOE_OK) return 0;
-  size_t need = 0;
-  carve_ortho(*p, nullptr, &need);
-  return need;
+  return check_ortho(p) == K3MOE_OK ? ortho_workspace(*p) : 0;
 }
 
 k3moe_status k3moe_orthogonalize(const k3moe_ortho* p, const void* g, void* out, void* workspace,
@@ -1029,16 +1033,17 @@ k3moe_status k3moe_orthogonalize(const k3moe_ortho* p, const void* g, void* out,
   K3_CHECK(check_ortho(p));
   K3_CHECK(need_ptr(g, "g"));
   K3_CHECK(need_ptr(out, "out"));
-  size_t need = 0;
-  carve_ortho(*p, nullptr, &need);
+  const size_t need = ortho_workspace(*p);
   K3_CHECK(check_ws(workspace, workspace_bytes, need));
   const size_t n = (size_t)p->batch * p->m * p->n, size = p->dtype == K3MOE_F32 ? 4 : 2;
   const bool in_place = g == out && p->dtype == K3MOE_BF16;
   const Region written[] = {{out, 2 * n, "out"}, {workspace, need, "workspace"}};
   const Region read[] = {{in_place ? nullptr : g, size * n, "g"}};
   K3_CHECK(check_disjoint(written, read));
-  return hip_status(launch_ortho(*p, g, out, carve_ortho(*p, workspace, nullptr),
-                                 static_cast<hipStream_t>(stream)),
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  return hip_status(ortho_small_ok(*p)
+                        ? launch_ortho_small(*p, g, out, carve_ortho_small(*p, workspace, nullptr), st)
+                        : launch_ortho(*p, g, out, carve_ortho(*p, workspace, nullptr), st),
                     "k3moe_orthogonalize launch");
 }
 

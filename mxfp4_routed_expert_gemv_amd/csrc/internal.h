@@ -234,6 +234,17 @@ struct OrthoWs {
 };
 OrthoWs carve_ortho(const k3moe_ortho& p, void* ws, size_t* bytes);
 bool ortho_bounded(const k3moe_ortho& p);
+// Matrices whose short side is at most 128 (ortho_small.hip).
+struct OrthoSmallWs {
+  float* part;       // sums of A's pieces
+  int* exps;         // the power of two that each piece was divided by
+  uint16_t* poly;    // the polynomials of every step, two parts
+  float* norm;       // each matrix's scale
+};
+bool ortho_small_ok(const k3moe_ortho& p);
+OrthoSmallWs carve_ortho_small(const k3moe_ortho& p, void* ws, size_t* bytes);
+hipError_t launch_ortho_small(const k3moe_ortho& p, const void* g, void* out, const OrthoSmallWs& ws,
+                              hipStream_t st);
 hipError_t launch_ortho(const k3moe_ortho& p, const void* g, void* out, const OrthoWs& ws,
                         hipStream_t st);
 

@@ -13,10 +13,12 @@
 // the term a X: a step multiplies a small singular value by a (3.4 for the usual
 // coefficients), and what rounding X adds in directions where the update has little
 // would grow along (relative error of the result for a gradient with sixteen
-// directions ten times its noise, 512 x 1024: 1e-2 with one part, 2e-4 with two;
-// for noise alone 1.6e-3, as much as the bf16 output's own rounding).  The roundings
-// inside the products do not need it: they are relative to A and B, which are small
-// where X is.
+// directions ten times its noise, 512 x 1024: 1e-2 with one part, 3e-4 with two;
+// for noise alone 1.5e-3, as much as the bf16 output's own rounding).  The last step,
+// whose error nothing multiplies any more, does without.  The roundings inside the
+// products do not need it: they are relative to A and B, which are small where X is.
+//
+// Matrices whose short side is at most 128 take the kernels of ortho_small.hip.
 #include <algorithm>
 #include <cmath>
 
@@ -64,8 +66,14 @@ __device__ __forceinline__ float f16_lo(uint32_t w) {
 __device__ __forceinline__ float f16_hi(uint32_t w) {
   return (float)__builtin_bit_cast(f16x2_t, w)[1];
 }
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {   // to nearest even
-  return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
+// To nearest even.  (The bits are opaque from here on: where the compiler sees a
+// product in `a`, it may round it to fp16 in one step for one use of the result and
+// through fp32 for another, and a second part taken from the one would not fit the
+// other.)
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t w = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
+  asm volatile("" : "+v"(w));
+  return w;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));

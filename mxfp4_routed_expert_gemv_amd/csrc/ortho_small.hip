@@ -1,0 +1,497 @@
+// The orthogonalised update (ortho.hip) of matrices whose short side is at most 128.
+// The products of such a matrix fill no tiles, and a launch for each of them costs
+// more than it computes.  Every step multiplies X by a polynomial of its own A = X X^T
+// from the left, and A's next value follows from A alone, so X is needed only at both
+// ends:
+//   gram_parts   A_0 = X X^T, a piece of X's columns to a workgroup
+//   iterate      P_k = a + b A_k + c A_k A_k,  A_k+1 = P_k A_k P_k, one workgroup a matrix
+//   apply        P_4 ( .. P_1 (P_0 X)), 64 or 128 columns to a workgroup
+// A holds squares of singular values: what A_0 lacks in bits a small one lacks twice,
+// and a step multiplies it by a^2.  So every operand here has two fp16 parts (22 bits,
+// three products each), and the host takes this path only while the product of the a^2
+// is at most 2^15 (five of the usual steps: 19800); then a gradient with sixteen
+// directions a hundred times its noise comes out 4e-4 off in norm, noise alone 1e-6.
+// 256 x 128: three launches for seventeen.
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "kern_common.h"
+#include "dense_tile.h"
+
+namespace k3 {
+namespace {
+
+using namespace dense;
+
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+
+constexpr float kScaleX = 32768.0f;   // 2^15, of X (at most 1.4)
+constexpr float kScaleA = 16384.0f;   // 2^14, of A and P A (at most 1.96)
+
+struct SmallArgs {
+  const void* g;          // [batch][m][n]
+  float* part;            // [batch][chunks][S][S] sums, in the tiles' lane order
+  int* exps;              // [batch][chunks] the sums are of g / 2^exps
+  uint16_t* poly;         // [batch][steps][2][S][S] both parts of every P
+  float* norm;            // [batch][2] 1 / |g / 2^e| and e
+  void* out;
+  int rows, cols, tr;     // of X, the matrix taken wide; tr: g is its transpose
+  int f32, chunks, panels, steps;   // panels of a chunk
+  float scale;
+  float c[64][3];
+};
+
+// A power of two that takes P, at most |a| + 3.9, below 2^15.
+__device__ __forceinline__ float poly_scale(float a) {
+  const int q = (int)((__float_as_uint(fabsf(a) + 3.9f) >> 23) & 255) - 127;
+  return ldexpf(1.0f, 14 - q);
+}
+// To nearest even.  (The bits are opaque from here on: where the compiler sees a
+// product in `a`, it may round it to fp16 in one step for one use of the result and
+// through fp32 for another, and a second part taken from the one would not fit the
+// other.)
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t w = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
+  asm volatile("" : "+v"(w));
+  return w;
+}
+__device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t hi) {
+  const f16x2_t h = __builtin_bit_cast(f16x2_t, hi);
+  return pack_f16(a - (float)h[0], b - (float)h[1]);
+}
+
+// A matrix of R rows x K columns in LDS, two parts of R K halves: panels of 64
+// columns, each as an operand tile with the contraction along the rows of memory.
+template <int R, int K>
+struct Parts {
+  static constexpr int kPart = R * K * 2, kBytes = 2 * kPart;
+  using O = Operand<true, R>;
+  __device__ static __forceinline__ void frags(const uint8_t* p, int rb, int k32, int ln, int lg, f16x8_t (&f)[2]) {
+    const uint8_t* panel = p + (k32 >> 1) * O::kSlot;
+    f[0] = __builtin_bit_cast(f16x8_t, O::frag(panel, rb, k32 & 1, ln, lg));
+    f[1] = __builtin_bit_cast(f16x8_t, O::frag(panel + kPart, rb, k32 & 1, ln, lg));
+  }
+  // four columns c .. of row r (c % 4 == 0)
+  __device__ static __forceinline__ void put4(uint8_t* p, int r, int c, const float (&v)[4]) {
+    uint8_t* at = p + (c >> 6) * O::kSlot + r * 128 + ((((c >> 3) & 7) ^ ((r >> 1) & 7)) << 4) + (c & 4) * 2;
+    const uint2 h = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+    *reinterpret_cast<uint2*>(at) = h;
+    *reinterpret_cast<uint2*>(at + kPart) = make_uint2(rest_f16(v[0], v[1], h.x), rest_f16(v[2], v[3], h.y));
+  }
+  // eight columns (c % 8 == 0)
+  __device__ static __forceinline__ void put8(uint8_t* p, int r, int c, const float (&v)[8]) {
+    uint8_t* at = p + (c >> 6) * O::kSlot + r * 128 + ((((c >> 3) & 7) ^ ((r >> 1) & 7)) << 4);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = pack_f16(v[2 * j], v[2 * j + 1]);
+      l[j] = rest_f16(v[2 * j], v[2 * j + 1], h[j]);
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(at + kPart) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+};
+
+__device__ __forceinline__ f32x4_t mfma3(const f16x8_t (&a)[2], const f16x8_t (&b)[2], f32x4_t c) {
+  c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1], b[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[1], c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[0], c, 0, 0, 0);
+}
+
+// acc += A B^T over K columns: MB x NB blocks of 16 x 16 from row blocks ra of A and
+// rb of B; a lane holds row ln of A's block, columns 4 lg .. of B's.
+template <typename M, int MB, int NB, int K>
+__device__ __forceinline__ void multiply(const uint8_t* a, const uint8_t* b, int ra, int rb, f32x4_t (&acc)[MB][NB]) {
+  const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+#pragma unroll
+  for (int k = 0; k < K / 32; ++k) {
+    f16x8_t fa[MB][2], fb[NB][2];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) M::frags(a, ra + i, k, ln, lg, fa[i]);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) M::frags(b, rb + j, k, ln, lg, fb[j]);
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = mfma3(fb[j], fa[i], acc[i][j]);
+  }
+}
+
+__device__ __forceinline__ float load_g(const void* g, size_t i, int f32) {
+  return f32 ? static_cast<const float*>(g)[i] : bf16_lo(static_cast<const uint16_t*>(g)[i]);
+}
+// Eight elements i, i + step, ..; the last of them `in`, the others 0.
+__device__ __forceinline__ void load8_g(const void* g, size_t i, size_t step, int in, int f32, float (&v)[8]) {
+  if (step == 1 && in >= 8 && i % 8 == 0) {
+    if (f32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(g) + i);
+      const float4 a = p[0], b = p[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + i);
+      v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+      v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < in ? load_g(g, i + j * step, f32) : 0.0f;
+}
+
+// Workgroups of 1024 threads take 8192 elements of X at a time: kW columns.
+template <int S>
+struct Panel {
+  static constexpr int kW = 8192 / S;
+};
+
+// ---- A's part of `panels` panels of X
+template <int S>
+__global__ __launch_bounds__(1024) void gram_parts(SmallArgs g) {
+  constexpr int kW = Panel<S>::kW, NB = S / 64;   // 4 x 4 waves, NB x NB blocks each
+  using M = Parts<S, kW>;
+  __shared__ __attribute__((aligned(16))) uint8_t x[M::kBytes];
+  __shared__ float top[16];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const size_t first = (size_t)blockIdx.y * g.rows * g.cols;
+  // row r of X and eight columns from u on; a row of memory to neighbouring lanes
+  const int r = g.tr ? tid % S : tid / (kW / 8), u = (g.tr ? tid / S : tid % (kW / 8)) * 8;
+  auto load = [&](int panel, float (&v)[8]) {
+    const int c = panel * kW + u;
+    const int in = r < g.rows ? g.cols - c : 0;
+    if (g.tr) load8_g(g.g, first + (size_t)c * g.rows + r, g.rows, in, g.f32, v);
+    else load8_g(g.g, first + (size_t)r * g.cols + c, 1, in, g.f32, v);
+  };
+  const int p0 = blockIdx.x * g.panels, p1 = min(p0 + g.panels, (g.cols + kW - 1) / kW);
+  float v[8], w[8], most = 0.0f;
+  load(p0, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
+  for (int p = p0 + 1; p < p1; ++p) {
+    load(p, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(w[j]));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+  if (lane == 0) top[wv] = most;
+  __syncthreads();
+  most = top[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) most = fmaxf(most, top[i]);
+  // most < 2^e (zeros have the least e of all, an infinity goes on as it is)
+  int e = most > 0.0f ? 0 : -1000;
+  if (most > 0.0f && most < INFINITY) (void)frexpf(most, &e);
+  f32x4_t acc[NB][NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int p = p0; p < p1; ++p) {
+    if (p > p0) load(p, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = ldexpf(v[j], 15 - e);
+    if (p > p0) __syncthreads();
+    M::put8(x, r, u, v);
+    __syncthreads();
+    multiply<M, NB, NB, kW>(x, x, (wv >> 2) * NB, (wv & 3) * NB, acc);
+  }
+  const size_t chunk = (size_t)blockIdx.y * g.chunks + blockIdx.x;
+  if (tid == 0) g.exps[chunk] = e;
+  f32x4_t* part = reinterpret_cast<f32x4_t*>(g.part) + chunk * (S * S / 4);
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int tile = ((wv >> 2) * NB + i) * (S / 16) + (wv & 3) * NB + j;
+      part[tile * 64 + lane] = acc[i][j] * (1.0f / (kScaleX * kScaleX));
+    }
+}
+
+// ---- the polynomials.  64: 4 x 4 waves of one block; 128: 2 x 4 waves of 4 x 2
+// blocks, so that a product's LDS reads take no longer than its matrix instructions.
+template <int S>
+struct Waves {
+  static constexpr int MB = S == 64 ? 1 : 4, NB = S == 64 ? 1 : 2;
+  static constexpr int N = S / 16 / MB * (S / 16 / NB), kThreads = 64 * N;
+};
+template <int S>
+__global__ __launch_bounds__(Waves<S>::kThreads) void iterate(SmallArgs g) {
+  constexpr int MB = Waves<S>::MB, NB = Waves<S>::NB, N = Waves<S>::N;
+  using M = Parts<S, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t sA[M::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sP[M::kBytes];
+  __shared__ float sums[N];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
+  const int ra = wv / (S / 16 / NB) * MB, rb = wv % (S / 16 / NB) * NB;
+  f32x4_t A[MB][NB], acc[MB][NB];
+  auto zero = [&]() {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  auto put = [&](uint8_t* to, float f, f32x4_t (&v)[MB][NB]) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const float q[4] = {v[i][j][0] * f, v[i][j][1] * f, v[i][j][2] * f, v[i][j][3] * f};
+        M::put4(to, (ra + i) * 16 + ln, (rb + j) * 16 + lg * 4, q);
+      }
+  };
+  // A_0: the parts in order, as multiples of the largest one's power of two
+  const int* exps = g.exps + (size_t)blockIdx.x * g.chunks;
+  int e = exps[0];
+  for (int c = 1; c < g.chunks; ++c) e = max(e, exps[c]);
+  const f32x4_t* part = reinterpret_cast<const f32x4_t*>(g.part) + (size_t)blockIdx.x * g.chunks * (S * S / 4);
+  zero();
+  for (int c = 0; c < g.chunks; ++c) {
+    const float f = ldexpf(1.0f, 2 * (exps[c] - e));
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[i][j] += f * part[(size_t)c * (S * S / 4) + ((ra + i) * (S / 16) + rb + j) * 64 + lane];
+  }
+  float trace = 0.0f;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) trace += ra + i == rb + j && ln == lg * 4 + q ? acc[i][j][q] : 0.0f;
+  trace = wave_sum(trace);
+  if (lane == 0) sums[wv] = trace;
+  __syncthreads();
+  trace = sums[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) trace += sums[i];
+  const float f = trace == 0.0f ? 0.0f : 1.0f / trace;
+  if (threadIdx.x == 0) {
+    g.norm[2 * blockIdx.x] = trace == 0.0f ? 0.0f : 1.0f / sqrtf(trace);
+    g.norm[2 * blockIdx.x + 1] = (float)e;
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) A[i][j] = acc[i][j] * f;
+  put(sA, kScaleA, A);
+  __syncthreads();
+  uint16_t* poly = g.poly + (size_t)blockIdx.x * g.steps * 2 * S * S;
+  for (int s = 0; s < g.steps; ++s, poly += 2 * S * S) {
+    const float ca = g.c[s][0], cb = g.c[s][1], cc = g.c[s][2] * (1.0f / (kScaleA * kScaleA));
+    const float scale = poly_scale(ca);
+    zero();
+    multiply<M, MB, NB, S>(sA, sA, ra, rb, acc);
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        float q[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool diagonal = ra + i == rb + j && ln == lg * 4 + r;
+          q[r] = __builtin_fmaf(cc, acc[i][j][r], __builtin_fmaf(cb, A[i][j][r], diagonal ? ca : 0.0f)) * scale;
+        }
+        const int m = (ra + i) * 16 + ln, n = (rb + j) * 16 + lg * 4;
+        M::put4(sP, m, n, q);
+        const uint2 h = make_uint2(pack_f16(q[0], q[1]), pack_f16(q[2], q[3]));
+        uint16_t* p = poly + m * S + n;
+        *reinterpret_cast<uint2*>(p) = h;
+        *reinterpret_cast<uint2*>(p + S * S) = make_uint2(rest_f16(q[0], q[1], h.x), rest_f16(q[2], q[3], h.y));
+      }
+    if (s + 1 == g.steps) break;
+    __syncthreads();
+    const float back = 1.0f / scale;   // (a product of P and A has their scales)
+    zero();
+    multiply<M, MB, NB, S>(sP, sA, ra, rb, acc);
+    __syncthreads();
+    put(sA, back, acc);                // P A, in A's place
+    __syncthreads();
+    zero();
+    multiply<M, MB, NB, S>(sP, sA, ra, rb, acc);
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) A[i][j] = acc[i][j] * (back / kScaleA);
+    __syncthreads();
+    put(sA, kScaleA, A);
+    __syncthreads();
+  }
+}
+
+// 4 x 4 values of 16 bits transposed between four neighbouring lanes (as in ortho.hip).
+__device__ __forceinline__ uint2 transpose4(uint2 v, int lane) {
+  const bool odd = lane & 1, upper = lane & 2;
+  const uint32_t px = __builtin_amdgcn_mov_dpp((int)v.x, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+  const uint32_t py = __builtin_amdgcn_mov_dpp((int)v.y, 0xB1, 0xF, 0xF, true);
+  const uint32_t x = odd ? (px >> 16) | (v.x & 0xFFFF0000u) : (v.x & 0xFFFFu) | (px << 16);
+  const uint32_t y = odd ? (py >> 16) | (v.y & 0xFFFF0000u) : (v.y & 0xFFFFu) | (py << 16);
+  const uint32_t qx = __builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);     // lane ^ 2
+  const uint32_t qy = __builtin_amdgcn_mov_dpp((int)y, 0x4E, 0xF, 0xF, true);
+  return upper ? make_uint2(qy, y) : make_uint2(x, qx);
+}
+
+// ---- kW columns of X through all polynomials.  X is kept transposed, [kW][S], as the
+// products need it; a wave has 16 rows of P and two blocks of columns, and reads P's
+// fragments from memory, the next step's while it multiplies.
+template <int S>
+__global__ __launch_bounds__(1024) void apply(SmallArgs g) {
+  constexpr int kW = Panel<S>::kW, K = S / 32;
+  using M = Parts<kW, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t x[M::kBytes];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, ln = lane & 15, lg = lane >> 4;
+  const size_t first = (size_t)blockIdx.y * g.rows * g.cols;
+  const int n0 = blockIdx.x * kW;
+  const int mb = wv % (S / 16), nb = wv / (S / 16) * 2;
+  const uint16_t* poly = g.poly + (size_t)blockIdx.y * g.steps * 2 * S * S + (mb * 16 + ln) * S + lg * 8;
+  auto load_p = [&](int s, f16x8_t (&f)[K][2]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        f[k][h] = *reinterpret_cast<const f16x8_t*>(poly + ((size_t)s * 2 + h) * S * S + k * 32);
+  };
+  f16x8_t fp[K][2], next[K][2];
+  load_p(0, fp);
+  {
+    // column c of X and eight rows from u on
+    const int c = g.tr ? tid / (S / 8) : tid % kW, u = (g.tr ? tid % (S / 8) : tid / kW) * 8;
+    const int in = n0 + c < g.cols ? g.rows - u : 0;
+    float v[8];
+    if (g.tr) load8_g(g.g, first + (size_t)(n0 + c) * g.rows + u, 1, in, g.f32, v);
+    else load8_g(g.g, first + (size_t)u * g.cols + n0 + c, g.cols, in, g.f32, v);
+    const float f = g.norm[2 * blockIdx.y] * kScaleX;
+    const int e = (int)g.norm[2 * blockIdx.y + 1];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = ldexpf(v[j], -e) * f;
+    M::put8(x, c, u, v);
+  }
+  __syncthreads();
+  for (int s = 0; s < g.steps; ++s) {
+    if (s + 1 < g.steps) load_p(s + 1, next);
+    const float back = 1.0f / poly_scale(g.c[s][0]);
+    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f16x8_t fx[2];
+        M::frags(x, nb + j, k, ln, lg, fx);
+        acc[j] = mfma3(fp[k], fx, acc[j]);   // a lane: column ln of the block, rows 4 lg ..
+      }
+    if (s + 1 == g.steps) {
+      const float f = back / kScaleX * g.scale;
+      uint16_t* o = static_cast<uint16_t*>(g.out) + first;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        typedef __attribute__((ext_vector_type(2))) float f2;
+        const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{acc[j][0] * f, acc[j][1] * f}, bf16x2_t));
+        const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{acc[j][2] * f, acc[j][3] * f}, bf16x2_t));
+        uint2 q = make_uint2(a, b);
+        // four values of one row of memory: rows of X there when it is g's transpose
+        int row = n0 + (nb + j) * 16 + ln, col = mb * 16 + lg * 4;
+        if (!g.tr) {
+          q = transpose4(q, lane);
+          row = mb * 16 + lg * 4 + (ln & 3);
+          col = n0 + (nb + j) * 16 + (ln & ~3);
+        }
+        const int nr = g.tr ? g.cols : g.rows, nc = g.tr ? g.rows : g.cols;
+        if (row >= nr || col >= nc) continue;
+        uint16_t* p = o + (size_t)row * nc + col;
+        if (nc % 4 == 0) {
+          *reinterpret_cast<uint2*>(p) = q;
+        } else {
+          const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (col + r < nc) p[r] = (uint16_t)(w[r / 2] >> (r & 1 ? 16 : 0));
+        }
+      }
+      break;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float q[4] = {acc[j][0] * back, acc[j][1] * back, acc[j][2] * back, acc[j][3] * back};
+      M::put4(x, (nb + j) * 16 + ln, mb * 16 + lg * 4, q);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fp[k][h] = next[k][h];
+  }
+}
+
+int side(const k3moe_ortho& p) { return std::min(p.m, p.n) <= 64 ? 64 : 128; }
+
+// Pieces of X's columns: one more costs `iterate` about half of what a panel costs
+// `gram_parts`.
+void split(const k3moe_ortho& p, int* chunks, int* panels) {
+  const int n = (std::max(p.m, p.n) + 8192 / side(p) - 1) / (8192 / side(p));
+  const int want = std::max(1, std::min(64, (int)std::ceil(std::sqrt(2.0 * n))));
+  *panels = (n + want - 1) / want;
+  *chunks = (n + *panels - 1) / *panels;
+}
+
+template <int S>
+hipError_t launch(const SmallArgs& a, int batch, hipStream_t st) {
+  gram_parts<S><<<dim3(a.chunks, batch), 1024, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  iterate<S><<<batch, Waves<S>::kThreads, 0, st>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  apply<S><<<dim3((a.cols + Panel<S>::kW - 1) / Panel<S>::kW, batch), 1024, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool ortho_small_ok(const k3moe_ortho& p) {
+  if (std::min(p.m, p.n) > 128) return false;
+  double grown = 1.0;
+  for (int i = 0; i + 1 < p.steps; ++i) {
+    const double a = p.coefficients[3 * i];
+    grown *= std::max(1.0, a * a);
+  }
+  return grown <= 32768.0;
+}
+
+OrthoSmallWs carve_ortho_small(const k3moe_ortho& p, void* ws, size_t* bytes) {
+  int chunks, panels;
+  split(p, &chunks, &panels);
+  const size_t ss = (size_t)side(p) * side(p), b = p.batch;
+  Carver c(ws);
+  OrthoSmallWs w;
+  w.part = c.take<float>(b * chunks * ss);
+  w.exps = c.take<int>(b * chunks);
+  w.poly = c.take<uint16_t>(b * p.steps * 2 * ss);
+  w.norm = c.take<float>(2 * b);
+  if (bytes) *bytes = c.off;
+  return w;
+}
+
+hipError_t launch_ortho_small(const k3moe_ortho& p, const void* g, void* out, const OrthoSmallWs& ws, hipStream_t st) {
+  SmallArgs a{};
+  a.g = g;
+  a.part = ws.part;
+  a.exps = ws.exps;
+  a.poly = ws.poly;
+  a.norm = ws.norm;
+  a.out = out;
+  a.rows = std::min(p.m, p.n);
+  a.cols = std::max(p.m, p.n);
+  a.tr = p.m > p.n;
+  a.f32 = p.dtype == K3MOE_F32;
+  split(p, &a.chunks, &a.panels);
+  a.steps = p.steps;
+  a.scale = p.scale;
+  for (int i = 0; i < p.steps; ++i)
+    for (int j = 0; j < 3; ++j) a.c[i][j] = p.coefficients[3 * i + j];
+  return side(p) == 64 ? launch<64>(a, p.batch, st) : launch<128>(a, p.batch, st);
+}
+
+}  // namespace k3

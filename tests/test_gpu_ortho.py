@@ -2,7 +2,7 @@
 
 Tolerances.  The library's header names what is rounded: the products' operands to
 fp16 (X, A = X X^T and B = b A + c A A, each scaled by a power of two), a X to two
-fp16 parts, the result to bf16.  `rounded` takes exactly these roundings in 64 bits,
+fp16 parts (to one in the last step), the result to bf16.  `rounded` takes exactly these roundings in 64 bits,
 so its distance E from the definition is what they cost on this input; the kernels
 add fp32 sums (2^-24 a term) that move some of them by one step.  The result may be
 1.25 E away in norm, and each value by its bf16 rounding, 2^-8 of it, and 8 times
@@ -73,9 +73,9 @@ def rounded(g, steps=5, coefficients=MUON, scale=1.0):
         x = x / norm if float(norm) else x
         wide = x.shape[0] <= x.shape[1]
         x = x if wide else x.t().contiguous()
-        for a, b, c in schedule(steps, coefficients):
+        for i, (a, b, c) in enumerate(schedule(steps, coefficients)):
             hi = part(x, S)
-            x = hi + part(x - hi, S)
+            x = hi + (part(x - hi, S) if i + 1 < steps else 0.0)
             A = part(hi @ hi.t(), S)
             B = part(b * A + c * A @ A, S / 2)
             x = a * x + B @ hi
@@ -127,6 +127,44 @@ def test_against_the_definition(batch, m, n, dtype):
     check(call(g), g, f"{batch} x {m} x {n}")
 
 
+# (of six of these steps the squares of the first coefficients grow past 2^15: the
+# tiled products take matrices of every size then)
+@pytest.mark.parametrize("batch,m,n", [s for s in SIZES if min(s[1:]) <= 128])
+def test_small_matrices_on_the_tiled_products(batch, m, n):
+    g = gradient(batch, m, n, torch.float32, 1)
+    check(call(g, steps=6), g, f"{batch} x {m} x {n}", steps=6)
+
+
+@pytest.mark.parametrize("batch,m,n", [s for s in SIZES if min(s[1:]) <= 128] + [
+    (1, 128, 128), (2, 128, 4099), (3, 61, 33), (1, 65, 32768), (1, 9000, 5)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_small_matrices_keep_more_bits(batch, m, n, dtype):
+    """Short sides up to 128: every operand has 22 bits.  What rounding A = X X^T costs
+    is at most 2^-22 of its largest eigenvalue, 1, times what five steps multiply a
+    small one by, 3.4445^8 = 19800, so 5e-3 of an eigenvalue in the directions where
+    the gradient has least, and those are a small part of it: in norm a tenth of that,
+    beside the rounding to bf16 of every value."""
+    g = gradient(batch, m, n, dtype, 14)
+    want = exact(g)
+    err = (call(g).to(F8) - want).abs()
+    half = torch.ldexp(torch.ones_like(want), torch.frexp(want).exponent - 9)   # half a step of bf16
+    rest = (err - half).clamp(min=0.0)
+    rel = float((rest.flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)).max())
+    log(f"  {batch} x {m} x {n}: {rel:.1e} beside the rounding")
+    assert rel <= 5e-4
+
+
+def test_pieces_of_different_size():
+    """Columns of zeros, of tiny and of large values in different pieces of one matrix."""
+    g = gradient(2, 40, 3000, torch.float32, 15)
+    g[:, :, :700] = 0
+    g[:, :, 900:1500] *= 2.0 ** -40
+    g[0, :, 1500:] *= 2.0 ** -70
+    check(call(g), g, "pieces")
+    t = g.transpose(1, 2).contiguous()
+    check(call(t), t, "pieces of rows")
+
+
 def test_largest_tiles():
     """More than a round of 256 x 256 tiles in every product, rows and columns that do
     not fill the last ones, a tall matrix."""
@@ -142,10 +180,11 @@ def test_few_strong_directions(noise):
     check(call(g), g, f"noise {noise}")
 
 
+@pytest.mark.parametrize("m,n", [(150, 260), (33, 90), (120, 77)])
 @pytest.mark.parametrize("steps,coefficients", [(1, MUON), (2, CUBIC), (12, CUBIC), (8, QUINTIC),
                                                 (3, (MUON, QUINTIC, CUBIC))])
-def test_steps_and_coefficients(steps, coefficients):
-    g = gradient(2, 150, 260, torch.float32, 4)
+def test_steps_and_coefficients(steps, coefficients, m, n):
+    g = gradient(2, m, n, torch.float32, 4)
     check(call(g, steps=steps, coefficients=coefficients, scale=0.2), g, f"{steps} steps",
           steps=steps, coefficients=coefficients, scale=0.2)
 
