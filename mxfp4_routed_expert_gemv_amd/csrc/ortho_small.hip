@@ -14,6 +14,7 @@
 // 256 x 128: three launches for seventeen.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "kern_common.h"
@@ -34,11 +35,11 @@ struct SmallArgs {
   const void* g;          // [batch][m][n]
   float* part;            // [batch][chunks][S][S] sums, in the tiles' lane order
   int* exps;              // [batch][chunks] the sums are of g / 2^exps
-  uint16_t* poly;         // [batch][steps][2][S][S] both parts of every P
+  uint16_t* poly;         // [batch][steps] both parts of every P, see poly_at
   float* norm;            // [batch][2] 1 / |g / 2^e| and e
   void* out;
   int rows, cols, tr;     // of X, the matrix taken wide; tr: g is its transpose
-  int f32, chunks, panels, steps;   // panels of a chunk
+  int chunks, panels, steps;   // panels of a chunk
   float scale;
   float c[64][3];
 };
@@ -56,6 +57,12 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   uint32_t w = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
   asm volatile("" : "+v"(w));
   return w;
+}
+// Where a P's part h has columns c .. of row r (c % 4 == 0): in the order of the
+// fragments that apply reads, 1 KB each, [row block][32 columns][part][lane].
+template <int S>
+__device__ __forceinline__ int poly_at(int r, int c, int h) {
+  return (((r >> 4) * (S / 32) + (c >> 5)) * 2 + h) * 512 + ((r & 15) + ((c >> 3) & 3) * 16) * 8 + (c & 4);
 }
 __device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t hi) {
   const f16x2_t h = __builtin_bit_cast(f16x2_t, hi);
@@ -94,51 +101,76 @@ struct Parts {
   }
 };
 
-__device__ __forceinline__ f32x4_t mfma3(const f16x8_t (&a)[2], const f16x8_t (&b)[2], f32x4_t c) {
-  c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1], b[0], c, 0, 0, 0);
-  c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[1], c, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[0], c, 0, 0, 0);
+// Product q of the parts of a and b added to c (the least first; that of both second
+// parts is left out).
+template <int q>
+__device__ __forceinline__ f32x4_t mfma(const f16x8_t (&a)[2], const f16x8_t (&b)[2], f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q == 0], b[q == 1], c, 0, 0, 0);
 }
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 // acc += A B^T over K columns: MB x NB blocks of 16 x 16 from row blocks ra of A and
 // rb of B; a lane holds row ln of A's block, columns 4 lg .. of B's.
 template <typename M, int MB, int NB, int K>
 __device__ __forceinline__ void multiply(const uint8_t* a, const uint8_t* b, int ra, int rb, f32x4_t (&acc)[MB][NB]) {
   const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  f16x8_t fa[2][MB][2], fb[2][NB][2];   // (the next 32 columns' fragments on their way)
+  auto load = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) M::frags(a, ra + i, k, ln, lg, fa[k & 1][i]);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) M::frags(b, rb + j, k, ln, lg, fb[k & 1][j]);
+  };
+  load(0);
 #pragma unroll
   for (int k = 0; k < K / 32; ++k) {
-    f16x8_t fa[MB][2], fb[NB][2];
+    if (k + 1 < K / 32) load(k + 1);
+    auto add = [&](auto q) {   // (of all blocks in turn: the next into the same sums has to wait)
 #pragma unroll
-    for (int i = 0; i < MB; ++i) M::frags(a, ra + i, k, ln, lg, fa[i]);
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) M::frags(b, rb + j, k, ln, lg, fb[j]);
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = mfma3(fb[j], fa[i], acc[i][j]);
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma<q>(fb[k & 1][j], fa[k & 1][i], acc[i][j]);
+    };
+    add(Int<0>());
+    add(Int<1>());
+    add(Int<2>());
   }
 }
 
-__device__ __forceinline__ float load_g(const void* g, size_t i, int f32) {
-  return f32 ? static_cast<const float*>(g)[i] : bf16_lo(static_cast<const uint16_t*>(g)[i]);
-}
-// Eight elements i, i + step, ..; the last of them `in`, the others 0.
-__device__ __forceinline__ void load8_g(const void* g, size_t i, size_t step, int in, int f32, float (&v)[8]) {
-  if (step == 1 && in >= 8 && i % 8 == 0) {
-    if (f32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(g) + i);
-      const float4 a = p[0], b = p[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + i);
-      v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
-      v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
-    }
-    return;
-  }
+// Eight elements i, i + step, .. of g, `in` of them (the others 0).  VEC: they are
+// neighbours at 32 (bf16: 16) bytes, all of them in or none.  Every load is issued, of
+// the first element where there is none, and nothing waits before get(): behind
+// branches each would be waited for by itself.
+template <bool F32, bool VEC>
+struct Eight {
+  static constexpr int kWords = !F32 && VEC ? 4 : 8;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* g, size_t i, size_t step, int in) {
+    if (VEC) {
+      const size_t at = in >= 8 ? i : 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < in ? load_g(g, i + j * step, f32) : 0.0f;
-}
+      for (int q = 0; q < kWords / 4; ++q) {
+        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const char*>(g) + at * (F32 ? 4 : 2) + 16 * q);
+        w[4 * q] = a.x; w[4 * q + 1] = a.y; w[4 * q + 2] = a.z; w[4 * q + 3] = a.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const size_t at = j < in ? i + j * step : 0;
+        w[j] = F32 ? static_cast<const uint32_t*>(g)[at] : static_cast<const uint16_t*>(g)[at];
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int in, float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = F32 ? __uint_as_float(w[j]) : VEC ? (j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2])) : bf16_lo(w[j]);
+      v[j] = j < in ? x : 0.0f;
+    }
+  }
+};
 
 // Workgroups of 1024 threads take 8192 elements of X at a time: kW columns.
 template <int S>
@@ -147,7 +179,7 @@ struct Panel {
 };
 
 // ---- A's part of `panels` panels of X
-template <int S>
+template <int S, bool F32, bool VEC>
 __global__ __launch_bounds__(1024) void gram_parts(SmallArgs g) {
   constexpr int kW = Panel<S>::kW, NB = S / 64;   // 4 x 4 waves, NB x NB blocks each
   using M = Parts<S, kW>;
@@ -157,19 +189,22 @@ __global__ __launch_bounds__(1024) void gram_parts(SmallArgs g) {
   const size_t first = (size_t)blockIdx.y * g.rows * g.cols;
   // row r of X and eight columns from u on; a row of memory to neighbouring lanes
   const int r = g.tr ? tid % S : tid / (kW / 8), u = (g.tr ? tid / S : tid % (kW / 8)) * 8;
-  auto load = [&](int panel, float (&v)[8]) {
+  const size_t step = g.tr ? g.rows : 1;
+  auto inside = [&](int panel) { return r < g.rows ? g.cols - (panel * kW + u) : 0; };
+  auto load = [&](int panel, Eight<F32, VEC>& x8) {
     const int c = panel * kW + u;
-    const int in = r < g.rows ? g.cols - c : 0;
-    if (g.tr) load8_g(g.g, first + (size_t)c * g.rows + r, g.rows, in, g.f32, v);
-    else load8_g(g.g, first + (size_t)r * g.cols + c, 1, in, g.f32, v);
+    x8.load(g.g, first + (g.tr ? (size_t)c * g.rows + r : (size_t)r * g.cols + c), step, inside(panel));
   };
   const int p0 = blockIdx.x * g.panels, p1 = min(p0 + g.panels, (g.cols + kW - 1) / kW);
+  Eight<F32, VEC> raw;
   float v[8], w[8], most = 0.0f;
-  load(p0, v);
+  load(p0, raw);
+  raw.get(inside(p0), v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
   for (int p = p0 + 1; p < p1; ++p) {
-    load(p, w);
+    load(p, raw);
+    raw.get(inside(p), w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(w[j]));
   }
@@ -189,7 +224,10 @@ __global__ __launch_bounds__(1024) void gram_parts(SmallArgs g) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int p = p0; p < p1; ++p) {
-    if (p > p0) load(p, v);
+    if (p > p0) {
+      load(p, raw);
+      raw.get(inside(p), v);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = ldexpf(v[j], 15 - e);
     if (p > p0) __syncthreads();
@@ -209,8 +247,8 @@ __global__ __launch_bounds__(1024) void gram_parts(SmallArgs g) {
     }
 }
 
-// ---- the polynomials.  64: 4 x 4 waves of one block; 128: 2 x 4 waves of 4 x 2
-// blocks, so that a product's LDS reads take no longer than its matrix instructions.
+// ---- the polynomials.  64: 4 x 4 waves of one block; 128: 2 x 2 waves of 4 x 4
+// blocks, so that a product's LDS reads take less time than its matrix instructions.
 template <int S>
 struct Waves {
   static constexpr int MB = S == 64 ? 1 : 4, NB = S == 64 ? 1 : 2;
@@ -223,6 +261,9 @@ __global__ __launch_bounds__(Waves<S>::kThreads) void iterate(SmallArgs g) {
   __shared__ __attribute__((aligned(16))) uint8_t sA[M::kBytes];
   __shared__ __attribute__((aligned(16))) uint8_t sP[M::kBytes];
   __shared__ float sums[N];
+  __shared__ float coef[64][3];
+  // (read at once and early: an argument of a kernel is far away)
+  if (threadIdx.x < 3 * g.steps) (&coef[0][0])[threadIdx.x] = (&g.c[0][0])[threadIdx.x];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
   const int ra = wv / (S / 16 / NB) * MB, rb = wv % (S / 16 / NB) * NB;
   f32x4_t A[MB][NB], acc[MB][NB];
@@ -281,7 +322,7 @@ __global__ __launch_bounds__(Waves<S>::kThreads) void iterate(SmallArgs g) {
   __syncthreads();
   uint16_t* poly = g.poly + (size_t)blockIdx.x * g.steps * 2 * S * S;
   for (int s = 0; s < g.steps; ++s, poly += 2 * S * S) {
-    const float ca = g.c[s][0], cb = g.c[s][1], cc = g.c[s][2] * (1.0f / (kScaleA * kScaleA));
+    const float ca = coef[s][0], cb = coef[s][1], cc = coef[s][2] * (1.0f / (kScaleA * kScaleA));
     const float scale = poly_scale(ca);
     zero();
     multiply<M, MB, NB, S>(sA, sA, ra, rb, acc);
@@ -298,9 +339,9 @@ __global__ __launch_bounds__(Waves<S>::kThreads) void iterate(SmallArgs g) {
         const int m = (ra + i) * 16 + ln, n = (rb + j) * 16 + lg * 4;
         M::put4(sP, m, n, q);
         const uint2 h = make_uint2(pack_f16(q[0], q[1]), pack_f16(q[2], q[3]));
-        uint16_t* p = poly + m * S + n;
-        *reinterpret_cast<uint2*>(p) = h;
-        *reinterpret_cast<uint2*>(p + S * S) = make_uint2(rest_f16(q[0], q[1], h.x), rest_f16(q[2], q[3], h.y));
+        *reinterpret_cast<uint2*>(poly + poly_at<S>(m, n, 0)) = h;
+        *reinterpret_cast<uint2*>(poly + poly_at<S>(m, n, 1)) =
+            make_uint2(rest_f16(q[0], q[1], h.x), rest_f16(q[2], q[3], h.y));
       }
     if (s + 1 == g.steps) break;
     __syncthreads();
@@ -335,94 +376,116 @@ __device__ __forceinline__ uint2 transpose4(uint2 v, int lane) {
 }
 
 // ---- kW columns of X through all polynomials.  X is kept transposed, [kW][S], as the
-// products need it; a wave has 16 rows of P and two blocks of columns, and reads P's
-// fragments from memory, the next step's while it multiplies.
-template <int S>
-__global__ __launch_bounds__(1024) void apply(SmallArgs g) {
-  constexpr int kW = Panel<S>::kW, K = S / 32;
+// products need it; a wave has 16 rows of P and four blocks of columns, and reads P's
+// fragments from memory, kAhead steps before it needs them: the reads take longer than
+// a step.
+template <int S, bool F32, bool VEC>
+__global__ __launch_bounds__(512) void apply(SmallArgs g) {
+  constexpr int kW = Panel<S>::kW, K = S / 32, kAhead = 4, NB = 4;
   using M = Parts<kW, S>;
   __shared__ __attribute__((aligned(16))) uint8_t x[M::kBytes];
+  __shared__ float unscale[64];   // of every step's P
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, ln = lane & 15, lg = lane >> 4;
   const size_t first = (size_t)blockIdx.y * g.rows * g.cols;
   const int n0 = blockIdx.x * kW;
-  const int mb = wv % (S / 16), nb = wv / (S / 16) * 2;
-  const uint16_t* poly = g.poly + (size_t)blockIdx.y * g.steps * 2 * S * S + (mb * 16 + ln) * S + lg * 8;
+  const int mb = wv % (S / 16), nb = wv / (S / 16) * NB;
+  const uint16_t* poly = g.poly + (size_t)blockIdx.y * g.steps * 2 * S * S + mb * K * 1024 + lane * 8;
+  f16x8_t fp[kAhead][K][2];
   auto load_p = [&](int s, f16x8_t (&f)[K][2]) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        f[k][h] = *reinterpret_cast<const f16x8_t*>(poly + ((size_t)s * 2 + h) * S * S + k * 32);
+        f[k][h] = *reinterpret_cast<const f16x8_t*>(poly + (size_t)s * 2 * S * S + (k * 2 + h) * 512);
   };
-  f16x8_t fp[K][2], next[K][2];
-  load_p(0, fp);
-  {
-    // column c of X and eight rows from u on
-    const int c = g.tr ? tid / (S / 8) : tid % kW, u = (g.tr ? tid % (S / 8) : tid / kW) * 8;
-    const int in = n0 + c < g.cols ? g.rows - u : 0;
-    float v[8];
-    if (g.tr) load8_g(g.g, first + (size_t)(n0 + c) * g.rows + u, 1, in, g.f32, v);
-    else load8_g(g.g, first + (size_t)u * g.cols + n0 + c, g.cols, in, g.f32, v);
-    const float f = g.norm[2 * blockIdx.y] * kScaleX;
-    const int e = (int)g.norm[2 * blockIdx.y + 1];
+  const float norm = g.norm[2 * blockIdx.y], power = g.norm[2 * blockIdx.y + 1];
+  // column c of X and eight rows from u on
+  Eight<F32, VEC> raw[2];
+  auto place = [&](int q, int& c, int& u) {
+    const int i = tid + 512 * q;
+    c = g.tr ? i / (S / 8) : i % kW;
+    u = (g.tr ? i % (S / 8) : i / kW) * 8;
+    return n0 + c < g.cols ? g.rows - u : 0;
+  };
+  const size_t stride = g.tr ? 1 : g.cols;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = ldexpf(v[j], -e) * f;
+  for (int q = 0; q < 2; ++q) {
+    int c, u;
+    const int in = place(q, c, u);
+    raw[q].load(g.g, first + (g.tr ? (size_t)(n0 + c) * g.rows + u : (size_t)u * g.cols + n0 + c), stride, in);
+  }
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) load_p(min(j, g.steps - 1), fp[j]);
+  if (tid < g.steps) unscale[tid] = 1.0f / poly_scale(g.c[tid][0]);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    int c, u;
+    float v[8];
+    const int in = place(q, c, u);
+    raw[q].get(in, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = ldexpf(v[j], -(int)power) * (norm * kScaleX);
     M::put8(x, c, u, v);
   }
   __syncthreads();
-  for (int s = 0; s < g.steps; ++s) {
-    if (s + 1 < g.steps) load_p(s + 1, next);
-    const float back = 1.0f / poly_scale(g.c[s][0]);
-    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  f32x4_t acc[NB];
+  auto step = [&](int s, f16x8_t (&p)[K][2]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int j = 0; j < NB; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        f16x8_t fx[2];
-        M::frags(x, nb + j, k, ln, lg, fx);
-        acc[j] = mfma3(fp[k], fx, acc[j]);   // a lane: column ln of the block, rows 4 lg ..
-      }
-    if (s + 1 == g.steps) {
-      const float f = back / kScaleX * g.scale;
-      uint16_t* o = static_cast<uint16_t*>(g.out) + first;
+    for (int k = 0; k < K; ++k) {
+      f16x8_t fx[NB][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        typedef __attribute__((ext_vector_type(2))) float f2;
-        const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{acc[j][0] * f, acc[j][1] * f}, bf16x2_t));
-        const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{acc[j][2] * f, acc[j][3] * f}, bf16x2_t));
-        uint2 q = make_uint2(a, b);
-        // four values of one row of memory: rows of X there when it is g's transpose
-        int row = n0 + (nb + j) * 16 + ln, col = mb * 16 + lg * 4;
-        if (!g.tr) {
-          q = transpose4(q, lane);
-          row = mb * 16 + lg * 4 + (ln & 3);
-          col = n0 + (nb + j) * 16 + (ln & ~3);
-        }
-        const int nr = g.tr ? g.cols : g.rows, nc = g.tr ? g.rows : g.cols;
-        if (row >= nr || col >= nc) continue;
-        uint16_t* p = o + (size_t)row * nc + col;
-        if (nc % 4 == 0) {
-          *reinterpret_cast<uint2*>(p) = q;
-        } else {
-          const uint32_t w[2] = {q.x, q.y};
+      for (int j = 0; j < NB; ++j) M::frags(x, nb + j, k, ln, lg, fx[j]);
+      auto add = [&](auto q) {   // a lane: column ln of the block, rows 4 lg ..
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (col + r < nc) p[r] = (uint16_t)(w[r / 2] >> (r & 1 ? 16 : 0));
-        }
-      }
-      break;
+        for (int j = 0; j < NB; ++j) acc[j] = mfma<q>(p[k], fx[j], acc[j]);
+      };
+      add(Int<0>());
+      add(Int<1>());
+      add(Int<2>());
     }
+    if (s + kAhead < g.steps) load_p(s + kAhead, p);
+    if (s + 1 == g.steps) return;
+    const float back = unscale[s];
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NB; ++j) {
       const float q[4] = {acc[j][0] * back, acc[j][1] * back, acc[j][2] * back, acc[j][3] * back};
       M::put4(x, (nb + j) * 16 + ln, mb * 16 + lg * 4, q);
     }
     __syncthreads();
+  };
+  for (int s = 0; s < g.steps; s += kAhead) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int j = 0; j < kAhead; ++j)
+      if (s + j < g.steps) step(s + j, fp[j]);
+  }
+  const float f = g.scale * (1.0f / kScaleX) * unscale[g.steps - 1];
+  uint16_t* o = static_cast<uint16_t*>(g.out) + first;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) fp[k][h] = next[k][h];
+  for (int j = 0; j < NB; ++j) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{acc[j][0] * f, acc[j][1] * f}, bf16x2_t));
+    const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{acc[j][2] * f, acc[j][3] * f}, bf16x2_t));
+    uint2 q = make_uint2(a, b);
+    // four values of one row of memory: rows of X there when it is g's transpose
+    int row = n0 + (nb + j) * 16 + ln, col = mb * 16 + lg * 4;
+    if (!g.tr) {
+      q = transpose4(q, lane);
+      row = mb * 16 + lg * 4 + (ln & 3);
+      col = n0 + (nb + j) * 16 + (ln & ~3);
+    }
+    const int nr = g.tr ? g.cols : g.rows, nc = g.tr ? g.rows : g.cols;
+    if (row >= nr || col >= nc) continue;
+    uint16_t* p = o + (size_t)row * nc + col;
+    if (nc % 4 == 0) {
+      *reinterpret_cast<uint2*>(p) = q;
+    } else {
+      const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (col + r < nc) p[r] = (uint16_t)(w[r / 2] >> (r & 1 ? 16 : 0));
+    }
   }
 }
 
@@ -437,14 +500,19 @@ void split(const k3moe_ortho& p, int* chunks, int* panels) {
   *chunks = (n + *panels - 1) / *panels;
 }
 
-template <int S>
+template <int S, bool F32>
 hipError_t launch(const SmallArgs& a, int batch, hipStream_t st) {
-  gram_parts<S><<<dim3(a.chunks, batch), 1024, 0, st>>>(a);
+  // gram_parts reads along X's rows, apply along its columns: one of them along memory
+  const bool whole = (a.tr ? a.rows : a.cols) % 8 == 0;
+  const dim3 parts(a.chunks, batch), panels((a.cols + Panel<S>::kW - 1) / Panel<S>::kW, batch);
+  if (whole && !a.tr) gram_parts<S, F32, true><<<parts, 1024, 0, st>>>(a);
+  else gram_parts<S, F32, false><<<parts, 1024, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   iterate<S><<<batch, Waves<S>::kThreads, 0, st>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  apply<S><<<dim3((a.cols + Panel<S>::kW - 1) / Panel<S>::kW, batch), 1024, 0, st>>>(a);
+  if (whole && a.tr) apply<S, F32, true><<<panels, 512, 0, st>>>(a);
+  else apply<S, F32, false><<<panels, 512, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -485,13 +553,13 @@ hipError_t launch_ortho_small(const k3moe_ortho& p, const void* g, void* out, co
   a.rows = std::min(p.m, p.n);
   a.cols = std::max(p.m, p.n);
   a.tr = p.m > p.n;
-  a.f32 = p.dtype == K3MOE_F32;
   split(p, &a.chunks, &a.panels);
   a.steps = p.steps;
   a.scale = p.scale;
   for (int i = 0; i < p.steps; ++i)
     for (int j = 0; j < 3; ++j) a.c[i][j] = p.coefficients[3 * i + j];
-  return side(p) == 64 ? launch<64>(a, p.batch, st) : launch<128>(a, p.batch, st);
+  if (p.dtype == K3MOE_F32) return side(p) == 64 ? launch<64, true>(a, p.batch, st) : launch<128, true>(a, p.batch, st);
+  return side(p) == 64 ? launch<64, false>(a, p.batch, st) : launch<128, false>(a, p.batch, st);
 }
 
 }  // namespace k3
