@@ -360,7 +360,7 @@ RouteWs carve_route(const k3moe_shape& s, void* ws, size_t* bytes) {
 PermuteWs carve_permute(const k3moe_shape& s, void* ws, size_t* bytes) {
   Carver c(ws);
   PermuteWs r;
-  const int ch = permute_chunk_tokens(s.k);
+  const int ch = permute_chunk_tokens(s.T, s.k);
   const size_t nchunks = (size_t)((s.T + ch - 1) / ch);
   r.chunk_base = c.take<int32_t>(nchunks * s.E);
   if (bytes) *bytes = c.off;

@@ -23,7 +23,7 @@ inline bool routed_scaled(const k3moe_shape& s) {
   return mfma_shape_ok(s) && s.routed_format == K3MOE_FMT_MXFP4;
 }
 // Tokens per chunk of the large-batch permute (one bit per token in LDS masks).
-int permute_chunk_tokens(int k);
+int permute_chunk_tokens(int64_t T, int k);
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -205,6 +205,7 @@ hipError_t launch_grads(const k3moe_tensor* ts, int n, bool clip, float max_norm
 // Rows to and from the experts' order and the router's gradient (rows.hip).
 struct RouteBackWs {
   float* dl;         // [T][k] gradient of the chosen experts' logits
+  float* dl_sorted;  // [T k] the same at the pairs' positions
   int32_t* chunks;   // the experts' pairs in chunks, four words each
   int32_t* joins;    // [E] first row and number of the rows of `part`, two words each
   float* part;       // [..][d] sums of chunks

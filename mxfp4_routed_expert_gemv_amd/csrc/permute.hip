@@ -9,12 +9,14 @@
 // expert".
 //
 // Small batches (T <= 256, T*k <= 4096): one workgroup does everything in LDS.
-// Larger batches, three launches over chunks of CH tokens:
+// Larger batches, three launches over chunks of CH tokens, a thread to a pair:
 //   chunk_hist    per-chunk, per-expert pair counts (LDS atomics);
-//   chunk_scan    per expert, exclusive scan over chunks; exclusive scan over
-//                 experts gives offsets; chunk bases become offsets[e] + pairs
-//                 of e in earlier chunks;
-//   chunk_scatter per chunk, positions = chunk base + rank from the masks.
+//   chunk_scan    per expert, exclusive scan over chunks (64 experts and 16 groups
+//                 of chunks to a workgroup), and the counts;
+//   chunk_scatter per chunk, the experts' offsets from the counts, positions =
+//                 offset + pairs of the expert in earlier chunks + rank from the masks.
+// All latency: 12 us at T = 4096, top 16 of 896 (54 with a thread to a token, chunks
+// of 256 and one workgroup for the scan).
 #include "internal.h"
 #include "kern_common.h"
 
@@ -105,8 +107,8 @@ __global__ __launch_bounds__(1024) void permute_small(const int32_t* __restrict_
   for (int q = total + tid; q < P; q += 1024) sorted_pair[q] = -1;
 }
 
-// Chunked path.  CH tokens per chunk (one thread per token); the chunk's id
-// rows are staged in LDS with coalesced loads.
+// Chunked path.  CH tokens per chunk; the chunk's id rows are staged in LDS with
+// coalesced loads.
 template <int CH>
 __global__ __launch_bounds__(256) void chunk_hist(const int32_t* __restrict__ idx,
                                                   int32_t* __restrict__ chunk_base,
@@ -115,95 +117,128 @@ __global__ __launch_bounds__(256) void chunk_hist(const int32_t* __restrict__ id
   __shared__ int rows[kSmallPairs];  // CH * k <= 4096
   __shared__ int cnt[1024];
   const int64_t t0 = (int64_t)blockIdx.x * CH;
-  const int nt = (int)((T - t0) < CH ? (T - t0) : CH);
-  for (int i = threadIdx.x; i < nt * k; i += 256) rows[i] = idx[t0 * k + i];
+  const int np = (int)((T - t0) < CH ? (T - t0) : CH) * k;
+  for (int i = threadIdx.x; i < np; i += 256) rows[i] = idx[t0 * k + i];
   for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
   __syncthreads();
   int bad = 0;
-  if ((int)threadIdx.x < nt)
-    for (int s = 0; s < k; ++s) {
-      if (valid_slot(rows + threadIdx.x * k, s, E)) atomicAdd(&cnt[rows[threadIdx.x * k + s]], 1);
-      else ++bad;
-    }
+  for (int p = threadIdx.x; p < np; p += 256) {
+    const int t = p / k;
+    if (valid_slot(rows + t * k, p - t * k, E)) atomicAdd(&cnt[rows[p]], 1);
+    else ++bad;
+  }
   if (bad && diag) atomicAdd(&diag[K3MOE_DIAG_BAD_EXPERT_IDS], bad);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += 256) chunk_base[(size_t)blockIdx.x * E + e] = cnt[e];
 }
 
-// One workgroup of 1024 threads: thread e owns expert e (E <= 1024).
+// Lane l of wave g: expert 64 blockIdx + l, the g-th of 16 groups of chunks.
 __global__ __launch_bounds__(1024) void chunk_scan(int32_t* __restrict__ chunk_base,
-                                                   int32_t* __restrict__ counts,
-                                                   int32_t* __restrict__ offsets, int nchunks,
+                                                   int32_t* __restrict__ counts, int nchunks,
                                                    int E) {
-  __shared__ int sums[1024];
-  constexpr int B = 16;
-  const int e = threadIdx.x;
+  __shared__ int sums[16][64];
+  constexpr int B = 8;   // loads in flight
+  const int l = threadIdx.x & 63, g = threadIdx.x >> 6, e = blockIdx.x * 64 + l;
+  const int per = (nchunks + 15) / 16, c0 = g * per, c1 = min(c0 + per, nchunks);
+  const bool in = e < E;
+  const int32_t* at = chunk_base + (in ? e : 0);
+  int sum = 0;
+  for (int c = c0; c < c1; c += B) {
+    int v[B];
+#pragma unroll
+    for (int u = 0; u < B; ++u) v[u] = at[(size_t)min(c + u, c1 - 1) * E];
+#pragma unroll
+    for (int u = 0; u < B; ++u) sum += c + u < c1 ? v[u] : 0;
+  }
+  sums[g][l] = sum;
+  __syncthreads();
   int run = 0;
-  if (e < E) {
-    for (int c0 = 0; c0 < nchunks; c0 += B) {
-      int v[B];
+  for (int q = 0; q < g; ++q) run += sums[q][l];
+  if (!in) return;
+  if (g == 15) counts[e] = run + sum;
+  for (int c = c0; c < c1; c += B) {
+    int v[B];
 #pragma unroll
-      for (int u = 0; u < B; ++u) v[u] = (c0 + u < nchunks) ? chunk_base[(size_t)(c0 + u) * E + e] : 0;
+    for (int u = 0; u < B; ++u) v[u] = at[(size_t)min(c + u, c1 - 1) * E];
 #pragma unroll
-      for (int u = 0; u < B; ++u)
-        if (c0 + u < nchunks) {
-          chunk_base[(size_t)(c0 + u) * E + e] = run;
-          run += v[u];
-        }
-    }
+    for (int u = 0; u < B; ++u)
+      if (c + u < c1) {
+        chunk_base[(size_t)(c + u) * E + e] = run;
+        run += v[u];
+      }
   }
-  int total;
-  const int excl = block_excl_scan_1024(e < E ? run : 0, sums, &total);
-  if (e < E) {
-    counts[e] = run;
-    offsets[e] = excl;
-    for (int c = 0; c < nchunks; ++c) chunk_base[(size_t)c * E + e] += excl;
-  }
-  if (e == 0) offsets[E] = total;
 }
 
 template <int CH>
 __global__ __launch_bounds__(256) void chunk_scatter(const int32_t* __restrict__ idx,
                                                      const int32_t* __restrict__ chunk_base,
-                                                     const int32_t* __restrict__ offsets,
+                                                     const int32_t* __restrict__ counts,
+                                                     int32_t* __restrict__ offsets,
                                                      int32_t* __restrict__ sorted_pair,
                                                      int32_t* __restrict__ pair_pos, int64_t T,
                                                      int E, int k) {
   constexpr int NW = CH / 64;
   __shared__ int rows[kSmallPairs];  // CH * k <= 4096
   __shared__ int base[1024];
+  __shared__ int wave[4];
   __shared__ unsigned long long mask[1024][NW];
+  const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * CH;
-  const int nt = (int)((T - t0) < CH ? (T - t0) : CH);
-  for (int i = threadIdx.x; i < nt * k; i += 256) rows[i] = idx[t0 * k + i];
-  for (int e = threadIdx.x; e < E; e += 256) base[e] = chunk_base[(size_t)blockIdx.x * E + e];
-  for (int i = threadIdx.x; i < E * NW; i += 256) (&mask[0][0])[i] = 0ull;
+  const int np = (int)((T - t0) < CH ? (T - t0) : CH) * k;
+  for (int i = tid; i < np; i += 256) rows[i] = idx[t0 * k + i];
+  for (int i = tid; i < E * NW; i += 256) (&mask[0][0])[i] = 0ull;
+  // the experts' offsets: thread i has experts 4 i .. 4 i + 3
+  int c[4], before[4], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = tid * 4 + j;
+    c[j] = e < E ? counts[e] : 0;
+    before[j] = e < E ? chunk_base[(size_t)blockIdx.x * E + e] : 0;
+    sum += c[j];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(incl, o, 64);
+    if ((tid & 63) >= o) incl += v;
+  }
+  if ((tid & 63) == 63) wave[tid >> 6] = incl;
   __syncthreads();
-  const int lt = threadIdx.x;
-  const int word = lt >> 6;
-  const unsigned long long bit = 1ull << (lt & 63);
-  if (lt < nt)
-    for (int s = 0; s < k; ++s)
-      if (valid_slot(rows + lt * k, s, E)) atomicOr(&mask[rows[lt * k + s]][word], bit);
-  __syncthreads();
-  if (lt < nt)
-    for (int s = 0; s < k; ++s) {
-      const int64_t p = (t0 + lt) * k + s;
-      if (valid_slot(rows + lt * k, s, E)) {
-        const int e = rows[lt * k + s];
-        int rank = __popcll(mask[e][word] & (bit - 1ull));
-        for (int w = 0; w < word; ++w) rank += __popcll(mask[e][w]);
-        const int pos = base[e] + rank;
-        sorted_pair[pos] = (int32_t)p;
-        pair_pos[p] = pos;
-      } else {
-        pair_pos[p] = -1;
-      }
+  int off = incl - sum;
+  for (int w = 0; w < (tid >> 6); ++w) off += wave[w];
+  const int valid = wave[0] + wave[1] + wave[2] + wave[3];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = tid * 4 + j;
+    if (e < E) {
+      base[e] = off + before[j];
+      if (blockIdx.x == 0) offsets[e] = off;
     }
+    off += c[j];
+  }
+  if (blockIdx.x == 0 && tid == 0) offsets[E] = valid;
+  for (int p = tid; p < np; p += 256) {
+    const int t = p / k;
+    if (valid_slot(rows + t * k, p - t * k, E)) atomicOr(&mask[rows[p]][t >> 6], 1ull << (t & 63));
+  }
+  __syncthreads();
+  for (int p = tid; p < np; p += 256) {
+    const int t = p / k, word = t >> 6;
+    const int64_t pair = t0 * k + p;
+    if (valid_slot(rows + t * k, p - t * k, E)) {
+      const int e = rows[p];
+      int rank = __popcll(mask[e][word] & ((1ull << (t & 63)) - 1ull));
+      for (int w = 0; w < word; ++w) rank += __popcll(mask[e][w]);
+      const int pos = base[e] + rank;
+      sorted_pair[pos] = (int32_t)pair;
+      pair_pos[pair] = pos;
+    } else {
+      pair_pos[pair] = -1;
+    }
+  }
   // Positions past the last valid pair (only when ids were dropped) get -1.
   const int64_t P = T * k;
-  const int valid = offsets[E];
-  for (int64_t q = valid + (int64_t)blockIdx.x * 256 + lt; q < P; q += (int64_t)gridDim.x * 256)
+  for (int64_t q = valid + (int64_t)blockIdx.x * 256 + tid; q < P; q += (int64_t)gridDim.x * 256)
     sorted_pair[q] = -1;
 }
 
@@ -215,16 +250,18 @@ hipError_t chunked(const k3moe_shape& s, const int32_t* idx, int32_t* counts, in
   chunk_hist<CH><<<nchunks, 256, 0, st>>>(idx, ws.chunk_base, diag, s.T, s.E, s.k);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  chunk_scan<<<1, 1024, 0, st>>>(ws.chunk_base, counts, offsets, nchunks, s.E);
+  chunk_scan<<<(s.E + 63) / 64, 1024, 0, st>>>(ws.chunk_base, counts, nchunks, s.E);
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  chunk_scatter<CH><<<nchunks, 256, 0, st>>>(idx, ws.chunk_base, offsets, sorted_pair, pair_pos,
-                                             s.T, s.E, s.k);
+  chunk_scatter<CH><<<nchunks, 256, 0, st>>>(idx, ws.chunk_base, counts, offsets, sorted_pair,
+                                             pair_pos, s.T, s.E, s.k);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int permute_chunk_tokens(int k) { return k <= 16 ? 256 : 64; }
+// Small chunks fill the chip; from 2^17 tokens there are enough of the larger ones,
+// whose counts take a quarter of the memory.
+int permute_chunk_tokens(int64_t T, int k) { return k <= 16 && T >= (1 << 17) ? 256 : 64; }
 
 hipError_t launch_permute(const k3moe_shape& s, const int32_t* idx, int32_t* counts,
                           int32_t* offsets, int32_t* sorted_pair, int32_t* pair_pos,
@@ -234,7 +271,8 @@ hipError_t launch_permute(const k3moe_shape& s, const int32_t* idx, int32_t* cou
                                       (int)s.T, s.E, s.k);
     return hipGetLastError();
   }
-  if (s.k <= 16) return chunked<256>(s, idx, counts, offsets, sorted_pair, pair_pos, diag, ws, st);
+  if (permute_chunk_tokens(s.T, s.k) == 256)
+    return chunked<256>(s, idx, counts, offsets, sorted_pair, pair_pos, diag, ws, st);
   return chunked<64>(s, idx, counts, offsets, sorted_pair, pair_pos, diag, ws, st);
 }
 

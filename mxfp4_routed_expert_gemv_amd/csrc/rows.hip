@@ -88,59 +88,28 @@ __global__ __launch_bounds__(512) void dispatch_rows(const uint4* __restrict__ x
 
 // ---- a token's rows, weighted and summed
 struct GatherArgs {
-  const void* rows;          // [P][d] or, of the router's gradient, W [E][d] bf16
-  const int32_t* pair_pos;   // [T][k]
-  const float* w;            // [T][k], NULL: 1 everywhere
-  const void* add;           // [T][d] in the output's type, or NULL
-  void* out;                 // [T][d]
-  int64_t T;
-  int units, k, out_f32;     // units of 8 elements a row
-  // the router's gradient
-  const int32_t* idx;        // [T][k]
-  const float* dw;           // [T][k]
-  const float* logits;       // [T][E], for the renormalised sigmoid
-  float* dl;                 // [T][k], written
-  int E, router;
+  const void* rows;     // [limit][d]
+  const int32_t* pos;   // [T][k] the rows
+  const float* w;       // [T][k], NULL: 1 everywhere
+  const void* add;      // [T][d] in the output's type, or NULL
+  void* out;            // [T][d]
+  int64_t T, limit;     // positions outside 0 .. limit are dropped
+  int units, k;         // units of 8 elements a row
+  int out_f32;
 };
 
-// The chosen experts' dL/dlogit from dL/dw, lane s for slot s (0 for a dropped
-// pair, whose dw does not count).  With sig = sigmoid(logit):
-//   softmax       w = e^l / sum e^l       dl_s = w_s (dw_s - sum w dw)
-//   sigmoid       w = sig                 dl_s = dw_s w_s (1 - w_s)
-//   renormalised  w = sig / sum sig       dl_s = w_s (1 - sig_s) (dw_s - sum w dw)
-// 1 - sig is taken as sigmoid(-l), which keeps its bits where sig is near 1.
-__device__ __forceinline__ float dlogit(const GatherArgs& g, int64_t t, int s, int e, bool there) {
-  const float w = s < g.k ? g.w[t * g.k + s] : 0.0f;
-  const float dw = there ? g.dw[t * g.k + s] : 0.0f;
-  if (g.router == K3MOE_ROUTER_SIGMOID) return there ? dw * w * (1.0f - w) : 0.0f;
-  const float mean = wave_sum(there ? w * dw : 0.0f);
-  float v = w * (dw - mean);
-  if (g.router == K3MOE_ROUTER_SIGMOID_NORM && there) v *= 1.0f / (1.0f + expf(g.logits[t * g.E + e]));
-  return there ? v : 0.0f;
-}
-
-// G rows' loads are in flight at a time.  ROUTE: the router's gradient.
-template <bool ROWS_F32, int G, bool ROUTE>
+// G rows' loads are in flight at a time.  Grid (pieces of a row, tokens in strides);
+// BY_PIECE: (tokens in strides of one to a wave, pieces of 512 columns), so that the
+// chip works on one piece of the rows at a time: the router's weights, which many
+// tokens read, then come from the L2s (T = 16384, 896 x 7168: 3.8 GB).
+template <bool ROWS_F32, int G, bool BY_PIECE>
 __global__ __launch_bounds__(512) void gather_sum(GatherArgs g) {
-  const int u = blockIdx.x * blockDim.x + threadIdx.x;
-  const int lane = threadIdx.x & 63;
-  const int64_t P = g.T * g.k;
-  const int64_t limit = ROUTE ? g.E : P;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int u = BY_PIECE ? blockIdx.y * 64 + (threadIdx.x & 63) : blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t step = BY_PIECE ? gridDim.x * 4 : gridDim.y;
   const bool in = u < g.units;
   const int uc = in ? u : g.units - 1;
-  for (int64_t t = blockIdx.y; t < g.T; t += gridDim.y) {
-    float dl = 0.0f;
-    int e = -1;
-    if (ROUTE) {
-      const bool slot = lane < g.k;
-      e = slot ? g.idx[t * g.k + lane] : -1;
-      const int p = slot ? g.pair_pos[t * g.k + lane] : -1;
-      const bool there = p >= 0 && e >= 0 && e < g.E;
-      dl = dlogit(g, t, lane, e, there);
-      e = there ? e : -1;
-      if (u < 64 && slot) g.dl[t * g.k + lane] = dl;
-      if (!g.out) continue;
-    }
+  for (int64_t t = BY_PIECE ? blockIdx.x * 4 + wv : blockIdx.y; t < g.T; t += step) {
     f8 acc{};
     if (g.add) acc = load8(g.add, t * g.units + uc, g.out_f32);
     for (int s0 = 0; s0 < g.k; s0 += G) {
@@ -150,14 +119,9 @@ __global__ __launch_bounds__(512) void gather_sum(GatherArgs g) {
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         const int s = s0 + j < g.k ? s0 + j : g.k - 1;
-        if (ROUTE) {
-          at[j] = __builtin_amdgcn_readlane(e, s);
-          w[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(dl), s));
-        } else {
-          at[j] = g.pair_pos[t * g.k + s];
-          w[j] = g.w ? g.w[t * g.k + s] : 1.0f;
-        }
-        if (s0 + j >= g.k || at[j] >= limit) at[j] = -1;
+        at[j] = g.pos[t * g.k + s];
+        w[j] = g.w ? g.w[t * g.k + s] : 1.0f;
+        if (s0 + j >= g.k || at[j] >= g.limit) at[j] = -1;
       }
 #pragma unroll
       for (int j = 0; j < G; ++j)
@@ -248,96 +212,166 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
   }
 }
 
-// ---- the router's weight gradient.  An expert's pairs are cut into chunks of
-// kChunk; a wave has 512 columns of a chunk.  An expert of one chunk is done with
-// it, the chunks of others leave fp32 sums that dw_join adds in order.
-constexpr int kChunk = 256;
-struct Chunk {
-  int e, q0, q1, part;   // pairs q0 .. q1 of expert e; part: row of its sums, -1: none
+// ---- the router's gradient: first that of the chosen experts' logits, from dL/dw (0
+// for a dropped pair, whose dw does not count).  With sig = sigmoid(logit):
+//   softmax       w = e^l / sum e^l       dl_s = w_s (dw_s - sum w dw)
+//   sigmoid       w = sig                 dl_s = dw_s w_s (1 - w_s)
+//   renormalised  w = sig / sum sig       dl_s = w_s (1 - sig_s) (dw_s - sum w dw)
+// 1 - sig is taken as sigmoid(-l), which keeps its bits where sig is near 1.
+struct RouteArgs {
+  const int32_t* idx;        // [T][k]
+  const int32_t* pair_pos;   // [T][k]
+  const float* w;            // [T][k]
+  const float* dw;           // [T][k]
+  const float* logits;       // [T][E], for the renormalised sigmoid
+  const int32_t* offsets;    // [E + 1]
+  float* dl;                 // [T][k]
+  float* dl_sorted;          // [T k] at the pairs' positions
+  int4* list;                // the chunks: expert, pairs q0 .. q1, row of the sums or -1
+  int2* joins;               // [E] first row and number of the rows of an expert's sums
+  int64_t T;
+  int E, k, router, max_chunks;
 };
 
-// The list of chunks, at least one for every expert, by one workgroup: thread e
-// places expert e's.
-__global__ __launch_bounds__(1024) void plan_chunks(const int32_t* __restrict__ offsets, Chunk* list,
-                                                    int2* joins, int E, int64_t P, int max_chunks) {
-  __shared__ int sums[2][1024];
-  const int e = threadIdx.x;
+// The router's weight gradient goes by chunks: an expert's pairs, kChunk to a chunk and
+// a chunk at least.  An expert of one chunk is done with it, the chunks of others leave
+// fp32 sums that dw_join adds in order.  The list is made by one workgroup, thread i
+// placing experts 4 i .. 4 i + 3.
+constexpr int kChunk = 256;
+__device__ void plan_chunks(const RouteArgs& g) {
+  __shared__ int wave[2][4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t P = g.T * g.k;
   auto at = [&](int i) {
-    const int64_t o = offsets[i];
+    const int64_t o = g.offsets[i];
     return (int)(o < 0 ? 0 : o > P ? P : o);
   };
-  int q0 = 0, n = 0;
-  if (e < E) {
-    q0 = at(e);
-    n = at(e + 1) - q0;
-    n = n < 0 ? 0 : n;
+  int q0[4], n[4], c[4], sum[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = tid * 4 + j;
+    q0[j] = e < g.E ? at(e) : 0;
+    n[j] = e < g.E ? max(at(e + 1) - q0[j], 0) : 0;
+    c[j] = e < g.E ? max((n[j] + kChunk - 1) / kChunk, 1) : 0;
+    sum[0] += c[j];
+    sum[1] += c[j] > 1 ? c[j] : 0;
   }
-  const int chunks = e < E ? (n > kChunk ? (n + kChunk - 1) / kChunk : 1) : 0;
-  const int parts = chunks > 1 ? chunks : 0;
-  sums[0][e] = chunks;
-  sums[1][e] = parts;
+  int first[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int incl = sum[h];
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 63) wave[h][tid >> 6] = incl;
+    first[h] = incl - sum[h];
+  }
   __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {
-    const int a = e >= o ? sums[0][e - o] : 0, b = e >= o ? sums[1][e - o] : 0;
-    __syncthreads();
-    sums[0][e] += a;
-    sums[1][e] += b;
-    __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    for (int w = 0; w < (tid >> 6); ++w) first[h] += wave[h][w];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = tid * 4 + j;
+    if (e >= g.E) break;
+    const int parts = c[j] > 1 ? c[j] : 0;
+    for (int i = 0; i < c[j] && first[0] + i < g.max_chunks; ++i)
+      g.list[first[0] + i] = make_int4(e, q0[j] + i * kChunk, min(q0[j] + (i + 1) * kChunk, q0[j] + n[j]),
+                                       parts ? first[1] + i : -1);
+    g.joins[e] = make_int2(first[1], parts);
+    first[0] += c[j];
+    first[1] += parts;
   }
-  const int first = sums[0][e] - chunks, part = sums[1][e] - parts;
-  for (int c = 0; c < chunks && first + c < max_chunks; ++c)
-    list[first + c] = Chunk{e, q0 + c * kChunk, min(q0 + (c + 1) * kChunk, q0 + n),
-                            parts ? part + c : -1};
-  if (e < E) joins[e] = make_int2(part, parts);
-  for (int c = sums[0][1023] + e; c < max_chunks; c += 1024) list[c] = Chunk{-1, 0, 0, -1};
+  const int all = wave[0][0] + wave[0][1] + wave[0][2] + wave[0][3];
+  for (int i = all + tid; i < g.max_chunks; i += 256) g.list[i] = make_int4(-1, 0, 0, -1);
 }
 
-template <bool X_F32>
+// A wave a token, and one workgroup for the list of chunks.
+__global__ __launch_bounds__(256) void route_logits(RouteArgs g) {
+  if (blockIdx.x == 0) return plan_chunks(g);
+  const int s = threadIdx.x & 63;
+  const int64_t P = g.T * g.k, step = (int64_t)(gridDim.x - 1) * 4;
+  for (int64_t t = (int64_t)(blockIdx.x - 1) * 4 + (threadIdx.x >> 6); t < g.T; t += step) {
+    const bool slot = s < g.k;
+    const int64_t p = t * g.k + s;
+    const int e = slot ? g.idx[p] : -1, pos = slot ? g.pair_pos[p] : -1;
+    const bool there = pos >= 0 && pos < P && e >= 0 && e < g.E;
+    const float w = there ? g.w[p] : 0.0f, dw = there ? g.dw[p] : 0.0f;
+    float v;
+    if (g.router == K3MOE_ROUTER_SIGMOID) {
+      v = dw * w * (1.0f - w);
+    } else {
+      v = w * (dw - wave_sum(w * dw));
+      if (g.router == K3MOE_ROUTER_SIGMOID_NORM && there) v *= 1.0f / (1.0f + expf(g.logits[t * g.E + e]));
+    }
+    if (slot) g.dl[p] = there ? v : 0.0f;
+    if (there) g.dl_sorted[pos] = v;
+  }
+}
+
+// dW of a chunk's C columns by a wave, C / 8 lanes to a row, so 512 / C pairs at a time.
+//   512: a row's loads are 1 KB; for few tokens, whose x the L2s hold.
+//    64: workgroups go by slices of 64 columns, XCD x through slices x, x + 8, ..,
+//        so that an XCD works on one slice of x at a time, which its L2 holds.
+// (16384 tokens, d 7168, 896 experts, 16 a token: 555 us on 512 columns; 64 tokens:
+// 8 us there.)
+template <bool X_F32, int C>
 __global__ __launch_bounds__(256) void dw_chunks(const void* __restrict__ x,
                                                  const int32_t* __restrict__ sorted_pair,
-                                                 const float* __restrict__ dl,
-                                                 const Chunk* __restrict__ list,
+                                                 const float* __restrict__ dl_sorted,
+                                                 const int4* __restrict__ list,
                                                  float* __restrict__ part, void* __restrict__ dw,
-                                                 int64_t T, int units, int k, int out_f32, int max_parts) {
-  constexpr int G = 8;
-  const int u = blockIdx.x * blockDim.x + threadIdx.x, lane = threadIdx.x & 63;
-  const Chunk c = list[blockIdx.y];
-  if (c.e < 0) return;
+                                                 int64_t T, int units, int k, int out_f32, int chunks,
+                                                 int max_parts) {
+  constexpr int L = C / 8, R = 64 / L, G = C == 512 ? 8 : 64 / R;   // lanes to a row, rows, loads in flight
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, row = lane / L;
+  const int n_slices = (units + L - 1) / L, blocks = (chunks + 3) / 4;
+  const int j = blockIdx.x >> 3;
+  const int slice = (blockIdx.x & 7) + 8 * (j / blocks), at = j % blocks * 4 + wv;
+  if (slice >= n_slices || at >= chunks) return;
+  const int4 c = list[at];   // expert, first and last pair, row of the sums
+  if (c.x < 0) return;
+  const int u = slice * L + lane % L;
   const int64_t P = T * k;
   const int uc = u < units ? u : units - 1;
   f8 acc{};
-  for (int b = c.q0; b < c.q1; b += 64) {
+  for (int b = c.y; b < c.z; b += 64) {
     // lane i has the token and weight of pair b + i
     int tok = 0;
     float w = 0.0f;
-    if (b + lane < c.q1) {
+    if (b + lane < c.z) {
       const int p = sorted_pair[b + lane];
       if (p >= 0 && p < P) {
         tok = (unsigned)p / (unsigned)k;
-        w = dl[p];
+        w = dl_sorted[b + lane];
       }
     }
-    const int n = min(64, c.q1 - b);
-    for (int i = 0; i < n; i += G) {
+    const int n = min(64, c.z - b);
+    for (int i = 0; i < n; i += G * R) {
       f8 v[G];
       float wi[G];
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
-        const int a = i + j < n ? i + j : n - 1;
-        wi[j] = i + j < n ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), a)) : 0.0f;
-        v[j] = load8<X_F32>(x, (size_t)__builtin_amdgcn_readlane(tok, a) * units + uc);
+      for (int q = 0; q < G; ++q) {
+        const int a = i + q * R + row;   // (those behind the last pair have weight 0)
+        wi[q] = __shfl(w, a, 64);
+        v[q] = load8<X_F32>(x, (size_t)__shfl(tok, a, 64) * units + uc);
       }
 #pragma unroll
-      for (int j = 0; j < G; ++j)
-        if (wi[j] != 0.0f) {
+      for (int q = 0; q < G; ++q)
+        if (wi[q] != 0.0f) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) acc.v[q] = __builtin_fmaf(wi[j], v[j].v[q], acc.v[q]);
+          for (int h = 0; h < 8; ++h) acc.v[h] = __builtin_fmaf(wi[q], v[q].v[h], acc.v[h]);
         }
     }
   }
-  if (u >= units) return;
-  if (c.part < 0) store8(dw, (size_t)c.e * units + u, acc, out_f32);
-  else if (c.part < max_parts) store8<true>(part, (size_t)c.part * units + u, acc);
+#pragma unroll
+  for (int o = L; o < 64; o <<= 1)
+#pragma unroll
+    for (int h = 0; h < 8; ++h) acc.v[h] += __shfl_xor(acc.v[h], o, 64);
+  if (u >= units || row != 0) return;
+  if (c.w < 0) store8(dw, (size_t)c.x * units + u, acc, out_f32);
+  else if (c.w < max_parts) store8<true>(part, (size_t)c.w * units + u, acc);
 }
 
 __global__ __launch_bounds__(256) void dw_join(const float* __restrict__ part,
@@ -346,11 +380,19 @@ __global__ __launch_bounds__(256) void dw_join(const float* __restrict__ part,
   const int u = blockIdx.x * blockDim.x + threadIdx.x, e = blockIdx.y;
   const int2 j = joins[e];
   if (u >= units || j.y == 0) return;
+  constexpr int B = 4;   // loads in flight
+  const int end = min(j.x + j.y, max_parts);
   f8 acc{};
-  for (int c = j.x; c < j.x + j.y && c < max_parts; ++c) {
-    const f8 v = load8<true>(part, (size_t)c * units + u);
+  for (int c = j.x; c < end; c += B) {
+    f8 v[B];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc.v[q] += v.v[q];
+    for (int q = 0; q < B; ++q) v[q] = load8<true>(part, (size_t)min(c + q, end - 1) * units + u);
+#pragma unroll
+    for (int q = 0; q < B; ++q)
+      if (c + q < end) {
+#pragma unroll
+        for (int h = 0; h < 8; ++h) acc.v[h] += v[q].v[h];
+      }
   }
   store8(dw, (size_t)e * units + u, acc, out_f32);
 }
@@ -363,16 +405,44 @@ void cover(int n, int most, unsigned* pieces, unsigned* threads) {
 }
 unsigned token_blocks(int64_t T) { return (unsigned)std::min<int64_t>(T, 65535); }
 
-template <bool ROWS_F32, bool ROUTE>
+template <bool ROWS_F32, bool BY_PIECE>
 hipError_t launch_gather(const GatherArgs& g, hipStream_t st) {
   unsigned pieces, threads;
   cover(g.units, 8, &pieces, &threads);
-  const dim3 grid(pieces, token_blocks(g.T));
-  if (g.k <= 2) gather_sum<ROWS_F32, 2, ROUTE><<<grid, threads, 0, st>>>(g);
-  else if (g.k <= 4) gather_sum<ROWS_F32, 4, ROUTE><<<grid, threads, 0, st>>>(g);
-  else if (g.k <= 8 || ROWS_F32) gather_sum<ROWS_F32, 8, ROUTE><<<grid, threads, 0, st>>>(g);
-  else gather_sum<ROWS_F32, 16, ROUTE><<<grid, threads, 0, st>>>(g);
+  dim3 grid(pieces, token_blocks(g.T));
+  if (BY_PIECE) {
+    grid = dim3((unsigned)std::min<int64_t>((g.T + 3) / 4, 1 << 20), (g.units + 63) / 64);
+    threads = 256;
+  }
+  if (g.k <= 2) gather_sum<ROWS_F32, 2, BY_PIECE><<<grid, threads, 0, st>>>(g);
+  else if (g.k <= 4) gather_sum<ROWS_F32, 4, BY_PIECE><<<grid, threads, 0, st>>>(g);
+  else if (g.k <= 8 || ROWS_F32) gather_sum<ROWS_F32, 8, BY_PIECE><<<grid, threads, 0, st>>>(g);
+  else gather_sum<ROWS_F32, 16, BY_PIECE><<<grid, threads, 0, st>>>(g);
   return hipGetLastError();
+}
+
+// By the size of x: slices of 64 columns from 8 MB on.
+template <bool X_F32>
+hipError_t launch_dw(const k3moe_shape& s, const void* x, const int32_t* sorted_pair, const RouteBackWs& ws,
+                     int chunks, int parts, void* dw, hipStream_t st) {
+  const int units = s.d / 8, of32 = s.out_dtype == K3MOE_F32;
+  const int4* list = reinterpret_cast<const int4*>(ws.chunks);
+  const int64_t bytes = s.T * s.d * (X_F32 ? 4 : 2);
+  const int lanes = bytes >= (8 << 20) ? 8 : 64;
+  const int slices = ((units + lanes - 1) / lanes + 7) / 8;   // of an XCD
+  const int most = (1 << 20) / slices * 4;                      // chunks of a launch (2^23 workgroups)
+  for (int c0 = 0; c0 < chunks; c0 += most) {
+    const int n = std::min(chunks - c0, most);
+    auto run = [&](auto kernel) {
+      kernel<<<8u * slices * ((n + 3) / 4), 256, 0, st>>>(x, sorted_pair, ws.dl_sorted, list + c0, ws.part, dw, s.T,
+                                                          units, s.k, of32, n, parts);
+    };
+    if (lanes == 8) run(dw_chunks<X_F32, 64>);
+    else run(dw_chunks<X_F32, 512>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 int max_chunks(const k3moe_shape& s) { return (int)(s.E + s.T * s.k / kChunk); }
@@ -385,6 +455,7 @@ RouteBackWs carve_route_back(const k3moe_shape& s, void* ws, size_t* bytes) {
   Carver c(ws);
   RouteBackWs w;
   w.dl = c.take<float>((size_t)s.T * s.k);
+  w.dl_sorted = c.take<float>((size_t)s.T * s.k);
   w.chunks = c.take<int32_t>(4 * (size_t)max_chunks(s));
   w.joins = c.take<int32_t>(2 * (size_t)s.E);
   w.part = c.take<float>((size_t)max_parts(s) * s.d);
@@ -406,11 +477,12 @@ hipError_t launch_collect(const k3moe_shape& s, const void* rows, const int32_t*
                           const float* w, const void* add, void* out, hipStream_t st) {
   GatherArgs g{};
   g.rows = rows;
-  g.pair_pos = pair_pos;
+  g.pos = pair_pos;
   g.w = w;
   g.add = add;
   g.out = out;
   g.T = s.T;
+  g.limit = s.T * s.k;
   g.units = s.d / 8;
   g.k = s.k;
   g.out_f32 = s.out_dtype == K3MOE_F32;
@@ -437,46 +509,47 @@ hipError_t launch_route_back(const k3moe_shape& s, const void* x, const uint16_t
                              const int32_t* pair_pos, void* dx, void* dw_router,
                              const RouteBackWs& ws, hipStream_t st) {
   if (!dx && !dw_router) return hipSuccess;
-  GatherArgs g{};
-  g.rows = w_router;
-  g.pair_pos = pair_pos;
-  g.w = w;
-  g.out = dx;
-  g.T = s.T;
-  g.units = s.d / 8;
-  g.k = s.k;
-  g.out_f32 = s.x_dtype == K3MOE_F32;
-  g.idx = idx;
-  g.dw = dw;
-  g.logits = logits;
-  g.dl = ws.dl;
-  g.E = s.E;
-  g.router = s.router;
-  hipError_t e = launch_gather<false, true>(g, st);
-  if (e != hipSuccess || !dw_router) return e;
-  Chunk* list = reinterpret_cast<Chunk*>(ws.chunks);
-  int2* joins = reinterpret_cast<int2*>(ws.joins);
-  const int chunks = max_chunks(s), parts = max_parts(s);
-  plan_chunks<<<1, 1024, 0, st>>>(offsets, list, joins, s.E, s.T * s.k, chunks);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  RouteArgs a{};
+  a.idx = idx;
+  a.pair_pos = pair_pos;
+  a.w = w;
+  a.dw = dw;
+  a.logits = logits;
+  a.offsets = offsets;
+  a.dl = ws.dl;
+  a.dl_sorted = ws.dl_sorted;
+  a.list = reinterpret_cast<int4*>(ws.chunks);
+  a.joins = reinterpret_cast<int2*>(ws.joins);
+  a.T = s.T;
+  a.E = s.E;
+  a.k = s.k;
+  a.router = s.router;
+  const int chunks = a.max_chunks = max_chunks(s), parts = max_parts(s);
+  route_logits<<<1 + (unsigned)std::min<int64_t>((s.T + 3) / 4, 1 << 20), 256, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (dx) {
+    GatherArgs g{};
+    g.rows = w_router;
+    g.pos = idx;
+    g.w = ws.dl;
+    g.out = dx;
+    g.T = s.T;
+    g.limit = s.E;
+    g.units = s.d / 8;
+    g.k = s.k;
+    g.out_f32 = s.x_dtype == K3MOE_F32;
+    if ((e = launch_gather<false, true>(g, st)) != hipSuccess) return e;
+  }
+  if (!dw_router) return hipSuccess;
+  e = s.x_dtype == K3MOE_F32 ? launch_dw<true>(s, x, sorted_pair, ws, chunks, parts, dw_router, st)
+                             : launch_dw<false>(s, x, sorted_pair, ws, chunks, parts, dw_router, st);
+  if (e != hipSuccess || parts == 0) return e;
   unsigned pieces, threads;
-  cover(g.units, 4, &pieces, &threads);
-  const int of32 = s.out_dtype == K3MOE_F32;
-  for (int c0 = 0; c0 < chunks; c0 += 65535) {
-    const dim3 grid(pieces, std::min(chunks - c0, 65535));
-    if (s.x_dtype == K3MOE_F32)
-      dw_chunks<true><<<grid, threads, 0, st>>>(x, sorted_pair, ws.dl, list + c0, ws.part, dw_router,
-                                                s.T, g.units, s.k, of32, parts);
-    else
-      dw_chunks<false><<<grid, threads, 0, st>>>(x, sorted_pair, ws.dl, list + c0, ws.part, dw_router,
-                                                 s.T, g.units, s.k, of32, parts);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (parts > 0) {
-    dw_join<<<dim3(pieces, s.E), threads, 0, st>>>(ws.part, joins, dw_router, g.units, of32, parts);
-    e = hipGetLastError();
-  }
-  return e;
+  cover(s.d / 8, 4, &pieces, &threads);
+  dw_join<<<dim3(pieces, s.E), threads, 0, st>>>(ws.part, a.joins, dw_router, s.d / 8,
+                                                 s.out_dtype == K3MOE_F32, parts);
+  return hipGetLastError();
 }
 
 }  // namespace k3

@@ -85,7 +85,8 @@ def gathered(rows, pos):
     return r * (pos >= 0)[:, :, None]
 
 
-@pytest.mark.parametrize("T,d,E,k", SIZES)
+# (and batches of several chunks of the sort, the last with more tokens to a chunk)
+@pytest.mark.parametrize("T,d,E,k", SIZES + [(4097, 32, 896, 16), (131149, 32, 77, 2)])
 @pytest.mark.parametrize("dtype", DTS)
 @pytest.mark.parametrize("bad", [False, True])
 def test_dispatch(T, d, E, k, dtype, bad):
@@ -224,14 +225,14 @@ def route_reference(x, wr, idx, w, dw, logits, pos, router, T, d, E, k):
     return dx, dx_tol, dwr, (n + 1) * S24 * mag + err
 
 
-@pytest.mark.parametrize("T,d,E,k", SIZES + [(3000, 96, 12, 4)])
+@pytest.mark.parametrize("T,d,E,k", SIZES + [(3000, 96, 12, 4), (9000, 608, 30, 3)])
 @pytest.mark.parametrize("router", ["softmax", "sigmoid", "sigmoid_norm"])
 @pytest.mark.parametrize("dtype,out,bad", [(torch.bfloat16, torch.bfloat16, False),
                                            (torch.float32, torch.float32, True),
                                            (torch.bfloat16, torch.float32, True)])
 def test_route_backward(T, d, E, k, router, dtype, out, bad):
     r = routing()
-    x, wr, idx, w, dw, logits = route_case(T, d, E, k, router, dtype, bad, skew=T == 3000)
+    x, wr, idx, w, dw, logits = route_case(T, d, E, k, router, dtype, bad, skew=T >= 3000)
     order = r.sort_pairs(idx, E)
     lg = logits if router == "sigmoid_norm" else None
     if bad:   # the weight gradient of a dropped pair does not count
