@@ -584,7 +584,8 @@ k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_n
 /* k3moe_permute's outputs for topk_idx (the same values), and rows [T*k][d]:
  *   rows[pair_pos[t*k+s]] = x[t], zeros behind the last pair's row.
  * Errors: EINVAL, EALIGN, EWORKSPACE.
- * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_DISPATCH). */
+ * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_DISPATCH) (0, where NULL is
+ * accepted, up to 256 tokens and 4096 pairs). */
 k3moe_status k3moe_dispatch(const k3moe_shape* shape, const void* x, const int32_t* topk_idx,
                             void* rows, int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
                             int32_t* pair_pos, int32_t* diag, void* workspace,
@@ -624,7 +625,8 @@ k3moe_status k3moe_collect_backward(const k3moe_shape* shape, const void* dy, co
  * k3moe_permute or k3moe_dispatch write them.  An output that is NULL is not
  * computed; T = 0 writes zeros to dw_router.
  * Errors: EINVAL, EALIGN, EWORKSPACE.
- * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_ROUTE_BACKWARD). */
+ * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_ROUTE_BACKWARD) (0, where NULL is
+ * accepted, up to 64 tokens). */
 k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const void* w_router,
                                   const int32_t* topk_idx, const float* topk_w, const float* dw,
                                   const float* logits, const int32_t* offsets,

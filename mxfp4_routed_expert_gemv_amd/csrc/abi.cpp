@@ -215,6 +215,12 @@ k3moe_status check_disjoint(const Region (&written)[W], const Region (&read)[R])
   return K3MOE_OK;
 }
 
+size_t dispatch_workspace(const k3moe_shape& s) {
+  size_t need = 0;
+  if (!dispatch_small_ok(s)) carve_permute(s, nullptr, &need);
+  return need;
+}
+
 // Bytes of the operands that move between the tokens' and the experts' order.
 struct RowBytes {
   size_t out, x, y, rows, pairs;   // one output element; x, y, the rows, a word per pair
@@ -619,7 +625,7 @@ size_t k3moe_workspace_bytes(const k3moe_shape* shape, int op) {
     case K3MOE_OP_LAYER: carve_layer(*shape, nullptr, &n); break;
     case K3MOE_OP_SHARED_TRAIN: carve_shared_train(*shape, false, nullptr, &n); break;
     case K3MOE_OP_SHARED_BACKWARD: carve_shared_train(*shape, true, nullptr, &n); break;
-    case K3MOE_OP_DISPATCH: carve_permute(*shape, nullptr, &n); break;
+    case K3MOE_OP_DISPATCH: n = dispatch_workspace(*shape); break;
     case K3MOE_OP_ROUTE_BACKWARD: carve_route_back(*shape, nullptr, &n); break;
     default: return 0;
   }
@@ -901,8 +907,7 @@ k3moe_status k3moe_dispatch(const k3moe_shape* shape, const void* x, const int32
   K3_CHECK(need_ptr(sorted_pair, "sorted_pair"));
   K3_CHECK(need_ptr(pair_pos, "pair_pos"));
   K3_CHECK(opt_ptr(diag, "diag"));
-  size_t need = 0;
-  carve_permute(s, nullptr, &need);
+  const size_t need = dispatch_workspace(s);
   K3_CHECK(check_ws(workspace, workspace_bytes, need));
   const RowBytes b(s);
   const Region written[] = {{rows, b.rows, "rows"}, {counts, 4 * (size_t)s.E, "counts"},
@@ -912,6 +917,10 @@ k3moe_status k3moe_dispatch(const k3moe_shape* shape, const void* x, const int32
   const Region read[] = {{x, b.x, "x"}, {topk_idx, b.pairs, "topk_idx"}};
   K3_CHECK(check_disjoint(written, read));
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (dispatch_small_ok(s))
+    return hip_status(launch_dispatch_small(s, x, topk_idx, rows, counts, offsets, sorted_pair, pair_pos,
+                                            diag, st),
+                      "k3moe_dispatch launch");
   hipError_t e = launch_permute(s, topk_idx, counts, offsets, sorted_pair, pair_pos, diag,
                                 carve_permute(s, workspace, nullptr), st);
   if (e == hipSuccess) e = launch_dispatch_rows(s, x, pair_pos, offsets, rows, st);

@@ -211,6 +211,11 @@ struct RouteBackWs {
   float* part;       // [..][d] sums of chunks
 };
 RouteBackWs carve_route_back(const k3moe_shape& s, void* ws, size_t* bytes);
+// The sort and the rows in one launch, for batches of the sort's one workgroup.
+bool dispatch_small_ok(const k3moe_shape& s);
+hipError_t launch_dispatch_small(const k3moe_shape& s, const void* x, const int32_t* idx, void* rows,
+                                 int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
+                                 int32_t* pair_pos, int32_t* diag, hipStream_t st);
 hipError_t launch_dispatch_rows(const k3moe_shape& s, const void* x, const int32_t* pair_pos,
                                 const int32_t* offsets, void* rows, hipStream_t st);
 hipError_t launch_collect(const k3moe_shape& s, const void* rows, const int32_t* pair_pos,

@@ -50,13 +50,11 @@ __device__ __forceinline__ int block_excl_scan_1024(int v, int* sums, int* total
   return incl - v;
 }
 
-__global__ __launch_bounds__(1024) void permute_small(const int32_t* __restrict__ idx,
-                                                      int32_t* __restrict__ counts,
-                                                      int32_t* __restrict__ offsets,
-                                                      int32_t* __restrict__ sorted_pair,
-                                                      int32_t* __restrict__ pair_pos,
-                                                      int32_t* __restrict__ diag, int T, int E,
-                                                      int k) {
+__device__ __forceinline__ void small_sort(const int32_t* __restrict__ idx, int32_t* __restrict__ counts,
+                                           int32_t* __restrict__ offsets,
+                                           int32_t* __restrict__ sorted_pair,
+                                           int32_t* __restrict__ pair_pos, int32_t* __restrict__ diag,
+                                           int T, int E, int k) {
   __shared__ int ids[kSmallPairs];
   __shared__ unsigned char valid[kSmallPairs];
   __shared__ int cnt[1024];
@@ -105,6 +103,63 @@ __global__ __launch_bounds__(1024) void permute_small(const int32_t* __restrict_
     }
   }
   for (int q = total + tid; q < P; q += 1024) sorted_pair[q] = -1;
+}
+
+__global__ __launch_bounds__(1024) void permute_small(const int32_t* __restrict__ idx,
+                                                      int32_t* __restrict__ counts,
+                                                      int32_t* __restrict__ offsets,
+                                                      int32_t* __restrict__ sorted_pair,
+                                                      int32_t* __restrict__ pair_pos,
+                                                      int32_t* __restrict__ diag, int T, int E,
+                                                      int k) {
+  small_sort(idx, counts, offsets, sorted_pair, pair_pos, diag, T, E, k);
+}
+
+// The same, and the tokens' rows moved, in one launch: workgroup 0 sorts, workgroup
+// t + 1 moves token t's row (its 16-byte words) and finds the places of its pairs by
+// itself, as the valid pairs of lower experts and those of the same one in tokens
+// before.  (4 tokens of 1 KB: 4.0 and 2.6 us and a launch between in two.)
+__global__ __launch_bounds__(1024) void dispatch_small(const int32_t* __restrict__ idx,
+                                                       const uint4* __restrict__ x,
+                                                       uint4* __restrict__ rows,
+                                                       int32_t* __restrict__ counts,
+                                                       int32_t* __restrict__ offsets,
+                                                       int32_t* __restrict__ sorted_pair,
+                                                       int32_t* __restrict__ pair_pos,
+                                                       int32_t* __restrict__ diag, int T, int E, int k,
+                                                       int words) {
+  if (blockIdx.x == 0) return small_sort(idx, counts, offsets, sorted_pair, pair_pos, diag, T, E, k);
+  __shared__ int raw[kSmallPairs], ids[kSmallPairs];
+  __shared__ int place[64], total;
+  const int tid = threadIdx.x, lane = tid & 63, t0 = (int)blockIdx.x - 1, P = T * k;
+  for (int p = tid; p < P; p += 1024) raw[p] = idx[p];
+  if (tid < 64) place[tid] = 0;
+  if (tid == 0) total = 0;
+  __syncthreads();
+  for (int p = tid; p < P; p += 1024) {
+    const int t = p / k;
+    ids[p] = valid_slot(raw + t * k, p - t * k, E) ? raw[p] : -1;
+  }
+  __syncthreads();
+  // a wave counts for one slot at a time
+  for (int s = tid >> 6; s <= k; s += 16) {   // (s == k: all valid pairs)
+    const int e = s < k ? ids[t0 * k + s] : E;
+    int n = 0;
+    for (int p = lane; p < P; p += 64) {
+      const int id = ids[p];
+      n += id >= 0 && (id < e || (id == e && p < t0 * k));
+    }
+    n = wave_sum(n);
+    if (lane == 0) (s < k ? place[s] : total) = e < 0 ? -1 : n;
+  }
+  __syncthreads();
+  for (int u = tid; u < words; u += 1024) {
+    const uint4 v = x[(size_t)t0 * words + u];
+    for (int s = 0; s < k; ++s)
+      if (place[s] >= 0) rows[(size_t)place[s] * words + u] = v;
+  }
+  for (int q = total + t0; q < P; q += T)   // behind the last pair's row
+    for (int u = tid; u < words; u += 1024) rows[(size_t)q * words + u] = make_uint4(0, 0, 0, 0);
 }
 
 // Chunked path.  CH tokens per chunk; the chunk's id rows are staged in LDS with
@@ -262,6 +317,17 @@ hipError_t chunked(const k3moe_shape& s, const int32_t* idx, int32_t* counts, in
 // Small chunks fill the chip; from 2^17 tokens there are enough of the larger ones,
 // whose counts take a quarter of the memory.
 int permute_chunk_tokens(int64_t T, int k) { return k <= 16 && T >= (1 << 17) ? 256 : 64; }
+
+bool dispatch_small_ok(const k3moe_shape& s) { return s.T <= kSmallT && s.T * s.k <= kSmallPairs; }
+
+hipError_t launch_dispatch_small(const k3moe_shape& s, const void* x, const int32_t* idx, void* rows,
+                                 int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
+                                 int32_t* pair_pos, int32_t* diag, hipStream_t st) {
+  dispatch_small<<<1 + (unsigned)s.T, 1024, 0, st>>>(
+      idx, static_cast<const uint4*>(x), static_cast<uint4*>(rows), counts, offsets, sorted_pair,
+      pair_pos, diag, (int)s.T, s.E, s.k, s.d / (s.x_dtype == K3MOE_F32 ? 4 : 8));
+  return hipGetLastError();
+}
 
 hipError_t launch_permute(const k3moe_shape& s, const int32_t* idx, int32_t* counts,
                           int32_t* offsets, int32_t* sorted_pair, int32_t* pair_pos,

@@ -287,26 +287,183 @@ __device__ void plan_chunks(const RouteArgs& g) {
   for (int i = all + tid; i < g.max_chunks; i += 256) g.list[i] = make_int4(-1, 0, 0, -1);
 }
 
+// The slots' dl of token t, lane s for slot s.
+__device__ __forceinline__ float token_dl(const RouteArgs& g, int64_t t, int& e, int& pos, bool& there) {
+  const int s = threadIdx.x & 63;
+  const bool slot = s < g.k;
+  const int64_t p = t * g.k + (slot ? s : 0);
+  e = g.idx[p];
+  pos = g.pair_pos[p];
+  there = slot && pos >= 0 && pos < g.T * g.k && e >= 0 && e < g.E;
+  const float w = there ? g.w[p] : 0.0f, dw = there ? g.dw[p] : 0.0f;
+  if (g.router == K3MOE_ROUTER_SIGMOID) return there ? dw * w * (1.0f - w) : 0.0f;
+  float v = w * (dw - wave_sum(w * dw));
+  if (g.router == K3MOE_ROUTER_SIGMOID_NORM && there) v *= 1.0f / (1.0f + expf(g.logits[t * g.E + e]));
+  return there ? v : 0.0f;
+}
+
 // A wave a token, and one workgroup for the list of chunks.
 __global__ __launch_bounds__(256) void route_logits(RouteArgs g) {
   if (blockIdx.x == 0) return plan_chunks(g);
   const int s = threadIdx.x & 63;
-  const int64_t P = g.T * g.k, step = (int64_t)(gridDim.x - 1) * 4;
+  const int64_t step = (int64_t)(gridDim.x - 1) * 4;
   for (int64_t t = (int64_t)(blockIdx.x - 1) * 4 + (threadIdx.x >> 6); t < g.T; t += step) {
-    const bool slot = s < g.k;
-    const int64_t p = t * g.k + s;
-    const int e = slot ? g.idx[p] : -1, pos = slot ? g.pair_pos[p] : -1;
-    const bool there = pos >= 0 && pos < P && e >= 0 && e < g.E;
-    const float w = there ? g.w[p] : 0.0f, dw = there ? g.dw[p] : 0.0f;
-    float v;
-    if (g.router == K3MOE_ROUTER_SIGMOID) {
-      v = dw * w * (1.0f - w);
-    } else {
-      v = w * (dw - wave_sum(w * dw));
-      if (g.router == K3MOE_ROUTER_SIGMOID_NORM && there) v *= 1.0f / (1.0f + expf(g.logits[t * g.E + e]));
-    }
-    if (slot) g.dl[p] = there ? v : 0.0f;
+    int e, pos;
+    bool there;
+    const float v = token_dl(g, t, e, pos, there);
+    if (s < g.k) g.dl[t * g.k + s] = v;
     if (there) g.dl_sorted[pos] = v;
+  }
+}
+
+// Up to kFew tokens: everything in one launch, as each launch costs more than its work
+// (of more tokens an expert may have too many pairs for one workgroup).  The first nx workgroups take a token's dx
+// each, the others an expert's dW, whose pairs' dl they take from the tokens' weights
+// again, a lane to a pair.  A wave has every fourth piece of 512 columns, kP at a time.
+// (64 tokens, d 7168, 896 experts: 20 us in three launches; with a wave to a piece,
+// which takes each dl 14 times, 18.6; here 12.)
+constexpr int kFew = 64;
+template <bool X_F32>
+__global__ __launch_bounds__(256) void route_few(RouteArgs g, const void* __restrict__ x,
+                                                 const void* __restrict__ w_router,
+                                                 const int32_t* __restrict__ sorted_pair, void* __restrict__ dx,
+                                                 void* __restrict__ dw_router, int units, int out_f32, int nx) {
+  constexpr int G = 4, kP = 4;
+  __shared__ float s_dl[kFew];
+  __shared__ int s_row[kFew];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const bool tokens = (int)blockIdx.x < nx;
+  const int at = tokens ? blockIdx.x : (int)blockIdx.x - nx;   // token or expert
+  const int64_t P = g.T * g.k;
+  int n;   // rows to add up, in s_row, times s_dl
+  if (tokens) {
+    n = g.k;
+    if (wv == 0) {
+      int e, pos;
+      bool there;
+      const float dl = token_dl(g, at, e, pos, there);
+      s_dl[lane] = dl;
+      s_row[lane] = there ? e : 0;
+    }
+  } else {
+    auto offset = [&](int i) {
+      const int64_t o = g.offsets[i];
+      return (int)(o < 0 ? 0 : o > P ? P : o);
+    };
+    const int q0 = offset(at);
+    n = min(max(offset(at + 1) - q0, 0), kFew);
+    const int p = tid < n ? sorted_pair[q0 + tid] : -1;
+    const bool in = p >= 0 && p < P;
+    const int tok = in ? (unsigned)p / (unsigned)g.k : 0, pc = in ? p : 0;
+    if (wv == 0) {
+      const float w = g.w[pc], dw = g.dw[pc];
+      float dl = dw * w * (1.0f - w);
+      if (g.router != K3MOE_ROUTER_SIGMOID) {
+        // (the sum in the order of slots: wave_sum's differs, and so may the last bits
+        // of dl from dx's)
+        constexpr int B = 8;
+        float mean = 0.0f;
+        for (int s0 = 0; s0 < g.k; s0 += B) {
+          int e[B], pos[B];
+          float ws[B], dws[B];
+#pragma unroll
+          for (int j = 0; j < B; ++j) {
+            const int q = tok * g.k + min(s0 + j, g.k - 1);
+            e[j] = g.idx[q];
+            pos[j] = g.pair_pos[q];
+            ws[j] = g.w[q];
+            dws[j] = g.dw[q];
+          }
+#pragma unroll
+          for (int j = 0; j < B; ++j)
+            if (s0 + j < g.k && pos[j] >= 0 && pos[j] < P && e[j] >= 0 && e[j] < g.E)
+              mean = __builtin_fmaf(ws[j], dws[j], mean);
+        }
+        dl = w * (dw - mean);
+        if (g.router == K3MOE_ROUTER_SIGMOID_NORM) dl *= 1.0f / (1.0f + expf(g.logits[(size_t)tok * g.E + at]));
+      }
+      s_dl[tid] = in ? dl : 0.0f;
+      s_row[tid] = tok;
+    }
+  }
+  __syncthreads();
+  const void* from = tokens ? w_router : x;
+  const bool rows_f32 = X_F32 && !tokens;
+  for (int u0 = wv * 64 + lane; u0 - lane < units; u0 += 256 * kP) {
+    f8 acc[kP]{};
+    for (int i = 0; i < n; i += G) {
+      f8 v[G][kP];
+      float w[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const int a = min(i + j, n - 1);
+        w[j] = i + j < n ? s_dl[a] : 0.0f;
+        const size_t row = (size_t)s_row[a] * units;
+#pragma unroll
+        for (int c = 0; c < kP; ++c) v[j][c] = load8(from, row + min(u0 + 256 * c, units - 1), rows_f32);
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        if (w[j] != 0.0f) {
+#pragma unroll
+          for (int c = 0; c < kP; ++c)
+#pragma unroll
+            for (int h = 0; h < 8; ++h) acc[c].v[h] = __builtin_fmaf(w[j], v[j][c].v[h], acc[c].v[h]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kP; ++c) {
+      const int u = u0 + 256 * c;
+      if (u >= units) continue;
+      if (tokens) store8<X_F32>(dx, (size_t)at * units + u, acc[c]);
+      else store8(dw_router, (size_t)at * units + u, acc[c], out_f32);
+    }
+  }
+}
+
+// dx for many tokens: a workgroup holds 64 columns of all of W in LDS (128 bytes an
+// expert) and takes every gridDim.y-th group of tokens, eight to a wave, eight lanes to
+// a token; a lane has one of the token's slots and eight of its columns.  (T = 16384,
+// d 7168, 896 experts, 16 a token: from the L2s, row by row, 324 us.)
+constexpr int kDxWaves = 16;
+__global__ __launch_bounds__(64 * kDxWaves) void dx_columns(const uint4* __restrict__ w_router,
+                                                            const int32_t* __restrict__ idx,
+                                                            const float* __restrict__ dl,
+                                                            void* __restrict__ dx, int64_t T, int units,
+                                                            int E, int k, int out_f32) {
+  constexpr int kZero = 1024;   // a row of zeros, for the slots whose dl is 0
+  __shared__ uint4 sW[(kZero + 1) * 8];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, c = lane & 7;
+  const int u = blockIdx.x * 8 + c;
+  for (int i = threadIdx.x; i < E * 8; i += 64 * kDxWaves)
+    sW[i] = w_router[(size_t)(i >> 3) * units + min((int)blockIdx.x * 8 + (i & 7), units - 1)];
+  if (threadIdx.x < 8) sW[kZero * 8 + threadIdx.x] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  constexpr int kTokens = 8 * kDxWaves;   // of a workgroup at a time
+  for (int64_t t0 = (int64_t)blockIdx.y * kTokens; t0 < T; t0 += (int64_t)gridDim.y * kTokens) {
+    const int64_t t = t0 + wv * 8 + (lane >> 3), tc = t < T ? t : T - 1;
+    f8 acc{};
+    for (int s0 = 0; s0 < k; s0 += 8) {
+      const bool slot = s0 + c < k;
+      const int64_t p = tc * k + (slot ? s0 + c : 0);
+      const int id = idx[p];
+      const float v = dl[p];
+      const float w = slot && id >= 0 && id < E ? v : 0.0f;
+      const int e = w != 0.0f ? id : kZero;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int from = (lane & 56) + j;
+        const float wj = __shfl(w, from, 64);
+        const uint4 a = sW[__shfl(e, from, 64) * 8 + c];
+        const uint32_t q[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          acc.v[2 * h] = __builtin_fmaf(wj, bf16_lo(q[h]), acc.v[2 * h]);
+          acc.v[2 * h + 1] = __builtin_fmaf(wj, bf16_hi(q[h]), acc.v[2 * h + 1]);
+        }
+      }
+    }
+    if (t < T && u < units) store8(dx, t * units + u, acc, out_f32);
   }
 }
 
@@ -314,8 +471,7 @@ __global__ __launch_bounds__(256) void route_logits(RouteArgs g) {
 //   512: a row's loads are 1 KB; for few tokens, whose x the L2s hold.
 //    64: workgroups go by slices of 64 columns, XCD x through slices x, x + 8, ..,
 //        so that an XCD works on one slice of x at a time, which its L2 holds.
-// (16384 tokens, d 7168, 896 experts, 16 a token: 555 us on 512 columns; 64 tokens:
-// 8 us there.)
+// (16384 tokens, d 7168, 896 experts, 16 a token: 314 us on 64 columns, 555 on 512.)
 template <bool X_F32, int C>
 __global__ __launch_bounds__(256) void dw_chunks(const void* __restrict__ x,
                                                  const int32_t* __restrict__ sorted_pair,
@@ -453,7 +609,11 @@ int max_parts(const k3moe_shape& s) { return s.T > kChunk ? (int)(2 * (s.T * s.k
 
 RouteBackWs carve_route_back(const k3moe_shape& s, void* ws, size_t* bytes) {
   Carver c(ws);
-  RouteBackWs w;
+  RouteBackWs w{};
+  if (s.T <= kFew) {   // (one launch, nothing kept)
+    if (bytes) *bytes = 0;
+    return w;
+  }
   w.dl = c.take<float>((size_t)s.T * s.k);
   w.dl_sorted = c.take<float>((size_t)s.T * s.k);
   w.chunks = c.take<int32_t>(4 * (size_t)max_chunks(s));
@@ -524,11 +684,29 @@ hipError_t launch_route_back(const k3moe_shape& s, const void* x, const uint16_t
   a.E = s.E;
   a.k = s.k;
   a.router = s.router;
+  if (s.T <= kFew) {
+    const int units = s.d / 8, nx = dx ? (int)s.T : 0, nw = dw_router ? s.E : 0;
+    if (s.x_dtype == K3MOE_F32)
+      route_few<true><<<nx + nw, 256, 0, st>>>(a, x, w_router, sorted_pair, dx, dw_router, units,
+                                               s.out_dtype == K3MOE_F32, nx);
+    else
+      route_few<false><<<nx + nw, 256, 0, st>>>(a, x, w_router, sorted_pair, dx, dw_router, units,
+                                                s.out_dtype == K3MOE_F32, nx);
+    return hipGetLastError();
+  }
   const int chunks = a.max_chunks = max_chunks(s), parts = max_parts(s);
   route_logits<<<1 + (unsigned)std::min<int64_t>((s.T + 3) / 4, 1 << 20), 256, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (dx) {
+  // (a workgroup of dx_columns reads E rows once, 3 us, and then T k of them from LDS)
+  if (dx && s.T * s.k >= 16 * (int64_t)s.E && s.T >= 1024) {
+    const int units = s.d / 8, slices = (units + 7) / 8;
+    const int64_t groups = (s.T + 8 * kDxWaves - 1) / (8 * kDxWaves);
+    const unsigned y = (unsigned)std::min<int64_t>(groups, std::max(1, 256 / slices));
+    dx_columns<<<dim3(slices, y), 64 * kDxWaves, 0, st>>>(reinterpret_cast<const uint4*>(w_router), idx, ws.dl, dx,
+                                                        s.T, units, s.E, s.k, s.x_dtype == K3MOE_F32);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else if (dx) {
     GatherArgs g{};
     g.rows = w_router;
     g.pos = idx;

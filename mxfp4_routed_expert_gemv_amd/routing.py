@@ -26,7 +26,7 @@ Order = namedtuple("Order", "counts offsets sorted_pair pair_pos")
 def _shape_of(T, d, E, k, x_dtype, out_dtype, router=0, op=None):
     # the experts' own sizes are not used by these calls
     shape = make_shape(T, d, 32, E, k, 0, 0, _DT[x_dtype], _DT[out_dtype], router)
-    return shape, 0 if op is None else max(k3moe_workspace_bytes(shape, op), 256)
+    return shape, 0 if op is None else k3moe_workspace_bytes(shape, op)
 
 
 def _need(t, name, shape, dtypes, device):
@@ -53,7 +53,7 @@ def _out(dtype, name):
 
 def _scratch(workspace, nbytes, dev):
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     check_workspace(workspace, dev.index)
     return workspace
 
@@ -62,10 +62,12 @@ _I32, _F = (torch.int32,), (torch.float32,)
 
 
 def _empty_order(T, k, E, dev):
-    make = torch.empty if T else torch.zeros
-    return Order(make(E, dtype=torch.int32, device=dev), make(E + 1, dtype=torch.int32, device=dev),
-                 torch.empty(T * k, dtype=torch.int32, device=dev),
-                 torch.empty((T, k), dtype=torch.int32, device=dev))
+    # one allocation, every part at 16 bytes
+    P, e4, p4 = T * k, E + 3 & ~3, T * k + 3 & ~3
+    buf = (torch.empty if T else torch.zeros)(2 * e4 + 4 + 2 * p4, dtype=torch.int32, device=dev)
+    s = torch.as_strided
+    return Order(s(buf, (E,), (1,), 0), s(buf, (E + 1,), (1,), e4), s(buf, (P,), (1,), 2 * e4 + 4),
+                 s(buf, (T, k), (k, 1), 2 * e4 + 4 + p4))
 
 
 def _check_ids(idx, diag, dev):

@@ -18,7 +18,7 @@ DTS = [torch.bfloat16, torch.float32]
 # T, d, E, k: one token and one expert; toy; odd counts; more than the small sort takes;
 # one expert for many tokens; many slots; the full-size row
 SIZES = [(1, 32, 1, 1), (4, 256, 16, 4), (37, 96, 5, 5), (257, 544, 19, 3), (700, 64, 3, 1),
-         (65, 160, 130, 64), (23, 7168, 896, 16), (1100, 1056, 40, 10), (5, 16384, 7, 2)]
+         (65, 160, 130, 64), (64, 160, 130, 64), (23, 7168, 896, 16), (1100, 1056, 40, 10), (5, 16384, 7, 2)]
 
 
 def routing():

@@ -47,6 +47,8 @@ def call(op, s, ws_bytes=BIG, **kw):
 
 @pytest.mark.parametrize("op", NAMES)
 def test_refusals(op):
+    def shape(T=300, **kw):   # (a batch that needs the workspace)
+        return globals()["shape"](T=T, **kw)
     assert call(op, None) == EINVAL
     assert call(op, shape(T=-1)) == EINVAL
     assert call(op, shape(d=250)) == ESHAPE
@@ -95,8 +97,12 @@ def test_the_renormalised_router_needs_logits():
 
 
 def test_workspace():
-    need = k3.k3moe_workspace_bytes(shape(), k3.OP_DISPATCH)
-    assert need == k3.k3moe_workspace_bytes(shape(), k3.OP_PERMUTE)
+    assert k3.k3moe_workspace_bytes(shape(), k3.OP_DISPATCH) == 0   # (one launch)
+    for T, k in ((257, 4), (256, 16)):
+        s = shape(T=T, k=k)
+        need = 0 if T == 256 else k3.k3moe_workspace_bytes(s, k3.OP_PERMUTE)
+        assert k3.k3moe_workspace_bytes(s, k3.OP_DISPATCH) == need
+    assert k3.k3moe_workspace_bytes(shape(T=64), k3.OP_ROUTE_BACKWARD) == 0
     s = shape(T=3000)
     assert k3.k3moe_workspace_bytes(s, k3.OP_ROUTE_BACKWARD) >= 4 * 3000 * 4 + 2 * 46 * 256 * 4
     assert k3.k3moe_workspace_bytes(shape(T=0), k3.OP_ROUTE_BACKWARD) == 0
