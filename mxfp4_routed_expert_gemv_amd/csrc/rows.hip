@@ -22,15 +22,28 @@ struct f8 {
   float v[8];
 };
 
-template <bool F32>
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+// (NT: non-temporal, for rows that are read or written once)
+template <bool NT, typename V>
+__device__ __forceinline__ V ld(const V* p) {
+  return NT ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool NT, typename V>
+__device__ __forceinline__ void st(V* p, V v) {
+  if (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+template <bool F32, bool NT = false>
 __device__ __forceinline__ f8 load8(const void* base, size_t unit) {
   f8 r;
   if (F32) {
-    const float4* p = static_cast<const float4*>(base) + 2 * unit;
-    const float4 a = p[0], b = p[1];
+    const f32x4_t* p = static_cast<const f32x4_t*>(base) + 2 * unit;
+    const f32x4_t a = ld<NT>(p), b = ld<NT>(p + 1);
     r = f8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
   } else {
-    const uint4 a = static_cast<const uint4*>(base)[unit];
+    const u32x4_t a = ld<NT>(static_cast<const u32x4_t*>(base) + unit);
     r = f8{{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(a.z), bf16_hi(a.z),
             bf16_lo(a.w), bf16_hi(a.w)}};
   }
@@ -39,15 +52,15 @@ __device__ __forceinline__ f8 load8(const void* base, size_t unit) {
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
-template <bool F32>
+template <bool F32, bool NT = false>
 __device__ __forceinline__ void store8(void* base, size_t unit, const f8& r) {
   if (F32) {
-    float4* p = static_cast<float4*>(base) + 2 * unit;
-    p[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-    p[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+    f32x4_t* p = static_cast<f32x4_t*>(base) + 2 * unit;
+    st<NT>(p, f32x4_t{r.v[0], r.v[1], r.v[2], r.v[3]});
+    st<NT>(p + 1, f32x4_t{r.v[4], r.v[5], r.v[6], r.v[7]});
   } else {
-    static_cast<uint4*>(base)[unit] = make_uint4(pack2(r.v[0], r.v[1]), pack2(r.v[2], r.v[3]),
-                                                 pack2(r.v[4], r.v[5]), pack2(r.v[6], r.v[7]));
+    st<NT>(static_cast<u32x4_t*>(base) + unit, u32x4_t{pack2(r.v[0], r.v[1]), pack2(r.v[2], r.v[3]),
+                                                       pack2(r.v[4], r.v[5]), pack2(r.v[6], r.v[7])});
   }
 }
 __device__ __forceinline__ f8 load8(const void* base, size_t unit, bool f32) {
@@ -66,24 +79,24 @@ __device__ __forceinline__ int64_t used_rows(const int32_t* offsets, int E, int6
 
 // ---- dispatch: x's 16-byte words, whatever their type.  Grid (pieces of a row,
 // tokens in strides).
-__global__ __launch_bounds__(512) void dispatch_rows(const uint4* __restrict__ x,
+__global__ __launch_bounds__(512) void dispatch_rows(const u32x4_t* __restrict__ x,
                                                      const int32_t* __restrict__ pair_pos,
                                                      const int32_t* __restrict__ offsets,
-                                                     uint4* __restrict__ rows, int64_t T, int words,
+                                                     u32x4_t* __restrict__ rows, int64_t T, int words,
                                                      int E, int k) {
   const int u = blockIdx.x * blockDim.x + threadIdx.x;
   if (u >= words) return;
   const int64_t P = T * k;
   for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
-    const uint4 v = x[t * words + u];
+    const u32x4_t v = x[t * words + u];
     const int32_t* pos = pair_pos + t * k;
     for (int s = 0; s < k; ++s) {
       const int p = pos[s];
-      if (p >= 0 && p < P) rows[(size_t)p * words + u] = v;
+      if (p >= 0 && p < P) st<true>(rows + (size_t)p * words + u, v);
     }
   }
   for (int64_t q = used_rows(offsets, E, P) + blockIdx.y; q < P; q += gridDim.y)
-    rows[q * words + u] = make_uint4(0, 0, 0, 0);
+    st<true>(rows + q * words + u, u32x4_t{0, 0, 0, 0});
 }
 
 // ---- a token's rows, weighted and summed
@@ -178,7 +191,7 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
             f8 r;
 #pragma unroll
             for (int c = 0; c < 8; ++c) r.v[c] = w[j] * g.v[c];
-            store8<ROWS_F32>(drows, (size_t)at[j] * units + u, r);
+            store8<ROWS_F32, true>(drows, (size_t)at[j] * units + u, r);
           }
       }
       if (dw) {
@@ -629,7 +642,7 @@ hipError_t launch_dispatch_rows(const k3moe_shape& s, const void* x, const int32
   unsigned pieces, threads;
   cover(words, 8, &pieces, &threads);
   dispatch_rows<<<dim3(pieces, token_blocks(s.T)), threads, 0, st>>>(
-      static_cast<const uint4*>(x), pair_pos, offsets, static_cast<uint4*>(rows), s.T, words, s.E, s.k);
+      static_cast<const u32x4_t*>(x), pair_pos, offsets, static_cast<u32x4_t*>(rows), s.T, words, s.E, s.k);
   return hipGetLastError();
 }
 
