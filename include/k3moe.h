@@ -641,9 +641,9 @@ k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const
  * `batch` matrices G [m][n], with X taken wide (G, or its transpose when m > n):
  *   X = G / |G| (Frobenius; a matrix of zeros stays zero), `steps` times
  *   X = a X + b (X X^T) X + c (X X^T)^2 X,  out = scale X  (rounded to bf16)
- * Sums are fp32, the norm's fp32 or more.  Where the short side is at most 128 and
- * the product of the a^2 of all steps but the last at most 2^15, the products'
- * operands keep 22 bits; otherwise they are rounded to fp16 (11 bits, but 22 for the
+ * Sums are fp32, the norm's fp32 or more.  Where the short side is at most 64, or at
+ * most 128 beside a long one over 256, and the product of the a^2 of all steps but the
+ * last at most 2^15, the products' operands keep 22 bits; otherwise they are rounded to fp16 (11 bits, but 22 for the
  * term a X of every step but the last), and the result is within 3e-3 of the exact one
  * in norm, 1.7e-3 of it the rounding to bf16.  A non-finite G gives non-finite values.
  * (The reference pages do not train; this belongs to k3moe_shared_ffn_backward,
@@ -657,7 +657,8 @@ typedef struct k3moe_ortho {
   const float* coefficients;   /* HOST [steps][3]: a, b, c of each step */
   float scale;                 /* finite */
 } k3moe_ortho;
-/* Workspace of the call below (0 for invalid arguments); 256-byte aligned. */
+/* Workspace of the call below (0 for invalid arguments, and, where NULL is accepted, for
+ * short sides of 65 .. 128 beside long ones up to 256); 256-byte aligned. */
 size_t k3moe_orthogonalize_workspace_bytes(const k3moe_ortho* p);
 /* g [batch][m][n] -> out [batch][m][n] bf16; out may be g itself when that is bf16.
  * Errors: EINVAL (NULL pointers, steps, scale, coefficients that let a singular

@@ -375,6 +375,21 @@ __device__ __forceinline__ uint2 transpose4(uint2 v, int lane) {
   return upper ? make_uint2(qy, y) : make_uint2(x, qx);
 }
 
+// Four values of row `row` of memory from column `col` on (col % 4 == 0), those inside.
+__device__ __forceinline__ void put_row(uint16_t* o, int row, int col, const SmallArgs& g, uint2 q) {
+  const int nr = g.tr ? g.cols : g.rows, nc = g.tr ? g.rows : g.cols;
+  if (row >= nr || col >= nc) return;
+  uint16_t* p = o + (size_t)row * nc + col;
+  if (nc % 4 == 0) {
+    *reinterpret_cast<uint2*>(p) = q;
+  } else {
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (col + r < nc) p[r] = (uint16_t)(w[r / 2] >> (r & 1 ? 16 : 0));
+  }
+}
+
 // ---- kW columns of X through all polynomials.  X is kept transposed, [kW][S], as the
 // products need it; a wave has 16 rows of P and four blocks of columns, and reads P's
 // fragments from memory, kAhead steps before it needs them: the reads take longer than
@@ -475,21 +490,204 @@ __global__ __launch_bounds__(512) void apply(SmallArgs g) {
       row = mb * 16 + lg * 4 + (ln & 3);
       col = n0 + (nb + j) * 16 + (ln & ~3);
     }
-    const int nr = g.tr ? g.cols : g.rows, nc = g.tr ? g.rows : g.cols;
-    if (row >= nr || col >= nc) continue;
-    uint16_t* p = o + (size_t)row * nc + col;
-    if (nc % 4 == 0) {
-      *reinterpret_cast<uint2*>(p) = q;
-    } else {
-      const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (col + r < nc) p[r] = (uint16_t)(w[r / 2] >> (r & 1 ? 16 : 0));
-    }
+    put_row(o, row, col, g, q);
   }
 }
 
+// ---- matrices of 65 .. 128 by up to 256: all steps as ortho.hip takes them, by one
+// workgroup, X's first parts and A (then B) in LDS, X itself in fp32 in the registers
+// of the waves that compute it: 64 rows x 64 columns each of 2 x 4.  (256 x 128: one
+// launch of 33 us for three of 54, whose A alone takes 35: products of two parts
+// have three times the matrix instructions.)
+//
+// X [128][256] serves as both operands: a row's eight columns for X X^T, and, read
+// transposed, a column's eight rows for B X.  Row r's 32 bytes of columns 16 b .. are at
+// block b ^ key, key = r mod 4 | (r / 8 mod 2) << 2, their two halves swapped where r
+// has bit 2: eight rows' 16 bytes fall on distinct banks, and so do the eight lines of
+// half a wave's transposing read.
+constexpr int kBigL = 256;
+struct WholeX {
+  __device__ static __forceinline__ int at(int r, int c) {   // byte of column c of row r (c % 4 == 0)
+    const int key = (r & 3) | ((r >> 1) & 4);
+    return r * (2 * kBigL) + (((c >> 4) ^ key) << 5) + ((((c >> 3) ^ (r >> 2)) & 1) << 4) + (c & 7) * 2;
+  }
+  // rows 16 rb + ln, columns 32 k + 8 lg ..
+  __device__ static __forceinline__ f16x8_t rows(const uint8_t* x, int rb, int k, int ln, int lg) {
+    return *reinterpret_cast<const f16x8_t*>(x + at(rb * 16 + ln, 32 * k + 8 * lg));
+  }
+  // columns 16 cb + ln, rows 32 k + 8 lg ..
+  __device__ static __forceinline__ f16x8_t columns(const uint8_t* x, int cb, int k, int ln, int lg) {
+    const int r = 32 * k + 8 * lg + (ln >> 2);
+    union { s16x4_t h[2]; f16x8_t v; } f;
+    f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(x + at(r, cb * 16 + (ln & 3) * 4)));
+    f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(x + at(r + 4, cb * 16 + (ln & 3) * 4)));
+    return f.v;
+  }
+};
+
+template <bool F32>
+__global__ __launch_bounds__(512) void whole(SmallArgs g) {
+  constexpr int S = 128, MB = 4, NX = 4, NA = 2;   // blocks of a wave: rows, columns of X, of A
+  using O = Operand<true, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t sX[S * kBigL * 2];
+  __shared__ __attribute__((aligned(16))) uint8_t sA[S * S * 2];
+  __shared__ double sums[8];
+  __shared__ float coef[64][3];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, ln = lane & 15, lg = lane >> 4;
+  const int wr = wv >> 2, wc = wv & 3;
+  if (tid < 3 * g.steps) (&coef[0][0])[tid] = (&g.c[0][0])[tid];
+  const size_t first = (size_t)blockIdx.x * g.rows * g.cols;
+  // X, raw: rows 64 wr + 16 i + ln, columns 64 wc + 16 j + 4 lg + r
+  f32x4_t x[MB][NX];
+  const uint32_t down = g.tr ? 1 : g.cols, right = g.tr ? g.rows : 1;
+  const void* from = static_cast<const char*>(g.g) + first * (F32 ? 4 : 2);
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NX; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int m = (wr * MB + i) * 16 + ln, n = (wc * NX + j) * 16 + lg * 4 + r;
+        const uint32_t at = m < g.rows && n < g.cols ? m * down + n * right : 0;
+        x[i][j][r] = F32 ? static_cast<const float*>(from)[at] : bf16_lo(static_cast<const uint16_t*>(from)[at]);
+      }
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NX; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int m = (wr * MB + i) * 16 + ln, n = (wc * NX + j) * 16 + lg * 4 + r;
+        if (m >= g.rows || n >= g.cols) x[i][j][r] = 0.0f;
+        sum = fma((double)x[i][j][r], (double)x[i][j][r], sum);
+      }
+  sum = wave_sum(sum);
+  if (lane == 0) sums[wv] = sum;
+  __syncthreads();
+  sum = sums[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) sum += sums[w];
+  const double f = sum == 0.0 ? 0.0 : (double)kScaleX / sqrt(sum);
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NX; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[i][j][r] = (float)((double)x[i][j][r] * f);
+  // (X is 2^15 times itself, A too, B 2^14 times)
+  for (int s = 0;; ++s) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NX; ++j)
+        *reinterpret_cast<uint2*>(sX + WholeX::at((wr * MB + i) * 16 + ln, (wc * NX + j) * 16 + lg * 4)) =
+            make_uint2(pack_f16(x[i][j][0], x[i][j][1]), pack_f16(x[i][j][2], x[i][j][3]));
+    __syncthreads();
+    const float ca = coef[s][0], cb = coef[s][1], cc = coef[s][2];
+    // A, rows 64 wr + 16 i + ln, columns 32 wc + 16 j + 4 lg ..
+    f32x4_t a[MB][NA] = {};
+#pragma unroll
+    for (int k = 0; k < kBigL / 32; ++k) {
+      f16x8_t fa[MB], fb[NA];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) fa[i] = WholeX::rows(sX, wr * MB + i, k, ln, lg);
+#pragma unroll
+      for (int j = 0; j < NA; ++j) fb[j] = WholeX::rows(sX, wc * NA + j, k, ln, lg);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NA; ++j) a[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], a[i][j], 0, 0, 0);
+    }
+    auto put = [&](int i, int j, uint2 v) {
+      const int r = (wr * MB + i) * 16 + ln, c = (wc * NA + j) * 16 + lg * 4;
+      *reinterpret_cast<uint2*>(sA + (c >> 6) * O::kSlot + r * 128 + ((((c >> 3) & 7) ^ ((r >> 1) & 7)) << 4) +
+                                (c & 4) * 2) = v;
+    };
+    uint2 kept[MB][NA];   // A as it is rounded
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NA; ++j) {
+        a[i][j] *= 1.0f / kScaleX;
+        kept[i][j] = make_uint2(pack_f16(a[i][j][0], a[i][j][1]), pack_f16(a[i][j][2], a[i][j][3]));
+        put(i, j, kept[i][j]);
+        a[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    __syncthreads();
+    auto frag_a = [&](int rb, int k) {
+      return __builtin_bit_cast(f16x8_t, O::frag(sA + (k >> 1) * O::kSlot, rb, k & 1, ln, lg));
+    };
+#pragma unroll
+    for (int k = 0; k < S / 32; ++k) {
+      f16x8_t fa[MB], fb[NA];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) fa[i] = frag_a(wr * MB + i, k);
+#pragma unroll
+      for (int j = 0; j < NA; ++j) fb[j] = frag_a(wc * NA + j, k);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NA; ++j) a[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], a[i][j], 0, 0, 0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NA; ++j) {
+        const f16x2_t p = __builtin_bit_cast(f16x2_t, kept[i][j].x), q = __builtin_bit_cast(f16x2_t, kept[i][j].y);
+        const float old[4] = {(float)p[0], (float)p[1], (float)q[0], (float)q[1]};
+        float b[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) b[r] = __builtin_fmaf(cc * (0.5f / kScaleX), a[i][j][r], 0.5f * cb * old[r]);
+        put(i, j, make_uint2(pack_f16(b[0], b[1]), pack_f16(b[2], b[3])));
+      }
+    __syncthreads();
+    f32x4_t acc[MB][NX] = {};
+#pragma unroll
+    for (int k = 0; k < S / 32; ++k) {
+      f16x8_t fa[MB], fb[NX];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) fa[i] = frag_a(wr * MB + i, k);
+#pragma unroll
+      for (int j = 0; j < NX; ++j) fb[j] = WholeX::columns(sX, wc * NX + j, k, ln, lg);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NX; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NX; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[i][j][r] = __builtin_fmaf(ca, x[i][j][r], acc[i][j][r] * (2.0f / kScaleX));
+    if (s + 1 == g.steps) break;
+    __syncthreads();
+  }
+  const float scale = g.scale * (1.0f / kScaleX);
+  uint16_t* o = static_cast<uint16_t*>(g.out) + first;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+      const f32x4_t v = x[i][j] * scale;
+      uint2 q = make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[0], v[1]}, bf16x2_t)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[2], v[3]}, bf16x2_t)));
+      int row = (wr * MB + i) * 16 + ln, col = (wc * NX + j) * 16 + lg * 4;   // of memory
+      if (g.tr) {
+        q = transpose4(q, lane);
+        const int n = col + (ln & 3);
+        col = row - (ln & 3);
+        row = n;
+      }
+      put_row(o, row, col, g, q);
+    }
+}
+
 int side(const k3moe_ortho& p) { return std::min(p.m, p.n) <= 64 ? 64 : 128; }
+
+bool in_one(const k3moe_ortho& p) { return side(p) == 128 && std::max(p.m, p.n) <= kBigL; }
 
 // Pieces of X's columns: one more costs `iterate` about half of what a panel costs
 // `gram_parts`.
@@ -520,6 +718,7 @@ hipError_t launch(const SmallArgs& a, int batch, hipStream_t st) {
 
 bool ortho_small_ok(const k3moe_ortho& p) {
   if (std::min(p.m, p.n) > 128) return false;
+  if (in_one(p)) return true;
   double grown = 1.0;
   for (int i = 0; i + 1 < p.steps; ++i) {
     const double a = p.coefficients[3 * i];
@@ -529,6 +728,10 @@ bool ortho_small_ok(const k3moe_ortho& p) {
 }
 
 OrthoSmallWs carve_ortho_small(const k3moe_ortho& p, void* ws, size_t* bytes) {
+  if (in_one(p)) {
+    if (bytes) *bytes = 0;
+    return OrthoSmallWs{};
+  }
   int chunks, panels;
   split(p, &chunks, &panels);
   const size_t ss = (size_t)side(p) * side(p), b = p.batch;
@@ -558,6 +761,11 @@ hipError_t launch_ortho_small(const k3moe_ortho& p, const void* g, void* out, co
   a.scale = p.scale;
   for (int i = 0; i < p.steps; ++i)
     for (int j = 0; j < 3; ++j) a.c[i][j] = p.coefficients[3 * i + j];
+  if (in_one(p)) {
+    if (p.dtype == K3MOE_F32) whole<true><<<p.batch, 512, 0, st>>>(a);
+    else whole<false><<<p.batch, 512, 0, st>>>(a);
+    return hipGetLastError();
+  }
   if (p.dtype == K3MOE_F32) return side(p) == 64 ? launch<64, true>(a, p.batch, st) : launch<128, true>(a, p.batch, st);
   return side(p) == 64 ? launch<64, false>(a, p.batch, st) : launch<128, false>(a, p.batch, st);
 }

@@ -22,7 +22,7 @@ def _problem(batch, m, n, dtype, steps, coefficients, scale):
         raise ValueError(f"coefficients are (a, b, c), or one such triple for each of {steps} steps")
     flat = [float(v) for c in coefficients for v in c]
     p = Ortho(batch, m, n, _DT[dtype], steps, (ctypes.c_float * len(flat))(*flat), scale)
-    return p, max(k3moe_orthogonalize_workspace_bytes(p), 256)
+    return p, k3moe_orthogonalize_workspace_bytes(p)
 
 
 def orthogonalize(g, steps=5, coefficients=MUON, scale=1.0, out=None, workspace=None, stream=None):
@@ -53,7 +53,7 @@ def orthogonalize(g, steps=5, coefficients=MUON, scale=1.0, out=None, workspace=
         key = tuple(tuple(c) if hasattr(c, "__len__") else float(c) for c in coefficients)
         p, nbytes = _problem(g.numel() // (m * n), m, n, g.dtype, int(steps), key, float(scale))
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         else:
             check_workspace(workspace, dev.index)
         k3moe_orthogonalize(p, g, out, workspace, current_stream(dev))

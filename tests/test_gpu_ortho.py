@@ -117,7 +117,8 @@ def check(got, g, name, **kw):
 # what does not fill them; stacks
 SIZES = [(1, 1, 1), (1, 1, 5), (1, 9, 1), (1, 7, 3), (5, 33, 47), (3, 64, 64), (1, 65, 130), (2, 130, 65),
          (1, 256, 128), (1, 16, 256), (1, 200, 1000), (1, 1000, 201), (2, 513, 515), (1, 896, 7168),
-         (1, 1024, 1536), (3, 700, 340), (40, 100, 90), (1, 2200, 1900), (2, 64, 20000), (1, 20000, 70)]
+         (1, 1024, 1536), (3, 700, 340), (40, 100, 90), (3, 128, 256), (2, 255, 67), (1, 65, 65), (2, 77, 250),
+         (1, 2200, 1900), (2, 64, 20000), (1, 20000, 70)]
 
 
 @pytest.mark.parametrize("batch,m,n", SIZES)
@@ -135,8 +136,9 @@ def test_small_matrices_on_the_tiled_products(batch, m, n):
     check(call(g, steps=6), g, f"{batch} x {m} x {n}", steps=6)
 
 
-@pytest.mark.parametrize("batch,m,n", [s for s in SIZES if min(s[1:]) <= 128] + [
-    (1, 128, 128), (2, 128, 4099), (3, 61, 33), (1, 65, 32768), (1, 9000, 5)])
+# (a short side of 65 .. 128 beside a long one up to 256 takes the products' 11 bits)
+@pytest.mark.parametrize("batch,m,n", [s for s in SIZES if min(s[1:]) <= 64 or min(s[1:]) <= 128 and max(s[1:]) > 256] + [
+    (2, 64, 64), (2, 128, 4099), (3, 61, 33), (1, 65, 32768), (1, 9000, 5), (2, 257, 65), (1, 128, 257)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_small_matrices_keep_more_bits(batch, m, n, dtype):
     """Short sides up to 128: every operand has 22 bits.  What rounding A = X X^T costs

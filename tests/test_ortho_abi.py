@@ -86,6 +86,9 @@ def test_workspace():
     assert n(problem(m=128, n=64)) == n(problem(m=64, n=128))
     assert n(problem(batch=3)) > n(problem())
     assert n(problem(m=0)) == 0
+    # one launch that keeps nothing; and the first sizes past it
+    assert n(problem(m=256, n=128)) == 0 and n(problem(m=65, n=65)) == 0
+    assert n(problem(m=257, n=128)) and n(problem(m=256, n=129)) and n(problem(m=256, n=64))
 
 
 def test_python_call_refuses_what_is_not_on_a_gpu():
