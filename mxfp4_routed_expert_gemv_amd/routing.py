@@ -6,14 +6,14 @@ Tensors are torch device tensors, contiguous, all on one device; the work is
 enqueued on that device's current stream (or `stream`).  Every computation
 happens in libk3moe's kernels; this file only marshals."""
 from collections import namedtuple
+from ctypes import byref
 from functools import lru_cache
 
 import torch
 
-from . import (BF16, DIAG_COUNT, F32, OP_DISPATCH, OP_PERMUTE, OP_ROUTE, OP_ROUTE_BACKWARD, ROUTERS,
-               check_workspace, current_stream, k3moe_collect, k3moe_collect_backward,
-               k3moe_dispatch, k3moe_dispatch_backward, k3moe_permute, k3moe_route,
-               k3moe_route_backward, k3moe_workspace_bytes, make_shape, on_device)
+from . import (BF16, DIAG_COUNT, F32, K3moeError, OP_DISPATCH, OP_PERMUTE, OP_ROUTE,
+               OP_ROUTE_BACKWARD, ROUTERS, check_workspace, k3moe_permute, k3moe_route,
+               k3moe_workspace_bytes, lib, make_shape, on_device)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -29,13 +29,34 @@ def _shape_of(T, d, E, k, x_dtype, out_dtype, router=0, op=None):
     return shape, 0 if op is None else k3moe_workspace_bytes(shape, op)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_ptr = torch.Tensor.data_ptr
+
+
 def _need(t, name, shape, dtypes, device):
     if t.dtype not in dtypes:
         raise TypeError(f"{name} is {t.dtype}; {' or '.join(map(str, dtypes))} is needed")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}; {tuple(shape)} is needed")
-    if t.device != device or not t.is_cuda or not t.is_contiguous():
+    index = t.get_device()
+    if index < 0 or index != device.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on the operands' GPU")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(ws):
+    """Address and size of a workspace."""
+    if ws is None or isinstance(ws, tuple):
+        return ws or (None, 0)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _check(status):
+    if status:
+        raise K3moeError(status, lib.k3moe_last_error().decode())
 
 
 def _sizes(pair_pos, rows, name):
@@ -86,7 +107,7 @@ def sort_pairs(idx, n_experts, diag=None, workspace=None, stream=None):
     with on_device(dev, stream):
         order = _empty_order(T, k, E, dev)
         k3moe_permute(shape, idx, *order, diag, _scratch(workspace, nbytes, dev),
-                      current_stream(dev))
+                      _raw_stream(dev.index))
     return order
 
 
@@ -105,8 +126,9 @@ def dispatch(x, idx, n_experts, diag=None, workspace=None, stream=None):
     with on_device(dev, stream):
         rows = torch.empty((T * k, d), dtype=x.dtype, device=dev)
         order = _empty_order(T, k, E, dev)
-        k3moe_dispatch(shape, x, idx, rows, *order, diag, _scratch(workspace, nbytes, dev),
-                       current_stream(dev))
+        ws = _scratch(workspace, nbytes, dev)
+        _check(lib.k3moe_dispatch(byref(shape), _ptr(x), _ptr(idx), _ptr(rows), *map(_ptr, order),
+                                  _addr(diag), *_bytes(ws), _raw_stream(dev.index)))
     return rows, order
 
 
@@ -121,7 +143,8 @@ def dispatch_backward(drows, order, out_dtype=None, stream=None):
     shape, _ = _shape_of(T, d, k, k, drows.dtype, out_dtype)
     with on_device(dev, stream):
         dx = torch.empty((T, d), dtype=out_dtype, device=dev)
-        k3moe_dispatch_backward(shape, drows, pair_pos, dx, current_stream(dev))
+        _check(lib.k3moe_dispatch_backward(byref(shape), _ptr(drows), _ptr(pair_pos), _ptr(dx),
+                                           _raw_stream(dev.index)))
     return dx
 
 
@@ -141,7 +164,8 @@ def collect(rows, order, w, add=None, out_dtype=None, stream=None):
     shape, _ = _shape_of(T, d, k, k, rows.dtype, out_dtype)
     with on_device(dev, stream):
         y = torch.empty((T, d), dtype=out_dtype, device=dev)
-        k3moe_collect(shape, rows, pair_pos, w, add, y, current_stream(dev))
+        _check(lib.k3moe_collect(byref(shape), _ptr(rows), _ptr(pair_pos), _ptr(w), _addr(add),
+                                 _ptr(y), _raw_stream(dev.index)))
     return y
 
 
@@ -161,8 +185,9 @@ def collect_backward(dy, rows, order, w, need=(True, True), stream=None):
     with on_device(dev, stream):
         drows = torch.empty_like(rows) if need[0] else None
         dw = torch.empty((T, k), dtype=torch.float32, device=dev) if need[1] else None
-        k3moe_collect_backward(shape, dy, rows, pair_pos, w, offsets, drows, dw,
-                               current_stream(dev))
+        _check(lib.k3moe_collect_backward(byref(shape), _ptr(dy), _ptr(rows), _ptr(pair_pos),
+                                          _ptr(w), _ptr(offsets), _addr(drows), _addr(dw),
+                                          _raw_stream(dev.index)))
     return drows, dw
 
 
@@ -194,9 +219,11 @@ def route_backward(x, w_router, idx, w, dw, order, router="softmax", logits=None
         dx = torch.empty_like(x) if need[0] else None
         dwr = torch.empty((E, d), dtype=dw_dtype, device=dev) if need[1] else None
         # (an empty tensor's address may be NULL: for T = 0 nothing is read or written there)
-        k3moe_route_backward(shape, x, w_router, idx, w, dw, logits, offsets, sorted_pair, pair_pos,
-                             dx if T else None, dwr, _scratch(workspace, nbytes, dev),
-                             current_stream(dev))
+        ws = _scratch(workspace, nbytes, dev)
+        _check(lib.k3moe_route_backward(byref(shape), _ptr(x), _ptr(w_router), _ptr(idx), _ptr(w),
+                                        _ptr(dw), _addr(logits), _ptr(offsets), _ptr(sorted_pair),
+                                        _ptr(pair_pos), _addr(dx) if T else None, _addr(dwr),
+                                        *_bytes(ws), _raw_stream(dev.index)))
     return dx, dwr
 
 
@@ -241,7 +268,7 @@ class _Route(torch.autograd.Function):
             logits = (torch.empty((T, E), dtype=torch.float32, device=dev)
                       if router == "sigmoid_norm" else None)
             k3moe_route(shape, x, w_router, idx, w, logits, diag, _scratch(None, nbytes, dev),
-                        current_stream(dev), router_bias=bias)
+                        _raw_stream(dev.index), router_bias=bias)
         ctx.save_for_backward(x, w_router, idx, w, logits)
         ctx.router = router
         ctx.mark_non_differentiable(idx)
