@@ -164,27 +164,32 @@ __global__ __launch_bounds__(1024) void dispatch_small(const int32_t* __restrict
 
 // Chunked path.  CH tokens per chunk; the chunk's id rows are staged in LDS with
 // coalesced loads.
+// Threads of a chunk's workgroup: those of the larger chunks fit a launch of 2^31 tokens.
 template <int CH>
-__global__ __launch_bounds__(1024) void chunk_hist(const int32_t* __restrict__ idx,
+constexpr int chunk_threads() { return CH == 64 ? 1024 : 256; }
+
+template <int CH>
+__global__ __launch_bounds__(chunk_threads<CH>()) void chunk_hist(const int32_t* __restrict__ idx,
                                                   int32_t* __restrict__ chunk_base,
                                                   int32_t* __restrict__ diag, int64_t T, int E,
                                                   int k) {
+  constexpr int N = chunk_threads<CH>();
   __shared__ int rows[kSmallPairs];  // CH * k <= 4096
   __shared__ int cnt[1024];
   const int64_t t0 = (int64_t)blockIdx.x * CH;
   const int np = (int)((T - t0) < CH ? (T - t0) : CH) * k;
-  for (int i = threadIdx.x; i < np; i += 1024) rows[i] = idx[t0 * k + i];
-  for (int e = threadIdx.x; e < E; e += 1024) cnt[e] = 0;
+  for (int i = threadIdx.x; i < np; i += N) rows[i] = idx[t0 * k + i];
+  for (int e = threadIdx.x; e < E; e += N) cnt[e] = 0;
   __syncthreads();
   int bad = 0;
-  for (int p = threadIdx.x; p < np; p += 1024) {
+  for (int p = threadIdx.x; p < np; p += N) {
     const int t = p / k;
     if (valid_slot(rows + t * k, p - t * k, E)) atomicAdd(&cnt[rows[p]], 1);
     else ++bad;
   }
   if (bad && diag) atomicAdd(&diag[K3MOE_DIAG_BAD_EXPERT_IDS], bad);
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 1024) chunk_base[(size_t)blockIdx.x * E + e] = cnt[e];
+  for (int e = threadIdx.x; e < E; e += N) chunk_base[(size_t)blockIdx.x * E + e] = cnt[e];
 }
 
 // Lane l of wave g: expert 64 blockIdx + l, the g-th of 16 groups of chunks.
@@ -225,27 +230,33 @@ __global__ __launch_bounds__(1024) void chunk_scan(int32_t* __restrict__ chunk_b
 }
 
 template <int CH>
-__global__ __launch_bounds__(1024) void chunk_scatter(const int32_t* __restrict__ idx,
+__global__ __launch_bounds__(chunk_threads<CH>()) void chunk_scatter(const int32_t* __restrict__ idx,
                                                      const int32_t* __restrict__ chunk_base,
                                                      const int32_t* __restrict__ counts,
                                                      int32_t* __restrict__ offsets,
                                                      int32_t* __restrict__ sorted_pair,
                                                      int32_t* __restrict__ pair_pos, int64_t T,
                                                      int E, int k) {
-  constexpr int NW = CH / 64;
+  constexpr int NW = CH / 64, N = chunk_threads<CH>(), EPT = 1024 / N;   // experts of a thread
   __shared__ int rows[kSmallPairs];  // CH * k <= 4096
   __shared__ int base[1024];
-  __shared__ int wave[16];
+  __shared__ int wave[N / 64];
   __shared__ unsigned long long mask[1024][NW];
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * CH;
   const int np = (int)((T - t0) < CH ? (T - t0) : CH) * k;
-  for (int i = tid; i < np; i += 1024) rows[i] = idx[t0 * k + i];
-  for (int i = tid; i < E * NW; i += 1024) (&mask[0][0])[i] = 0ull;
-  // the experts' offsets: thread e has expert e
-  const int c = tid < E ? counts[tid] : 0;
-  const int before = tid < E ? chunk_base[(size_t)blockIdx.x * E + tid] : 0;
-  int incl = c;
+  for (int i = tid; i < np; i += N) rows[i] = idx[t0 * k + i];
+  for (int i = tid; i < E * NW; i += N) (&mask[0][0])[i] = 0ull;
+  // the experts' offsets: thread i has experts EPT i ..
+  int c[EPT], before[EPT], sum = 0;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int e = tid * EPT + j;
+    c[j] = e < E ? counts[e] : 0;
+    before[j] = e < E ? chunk_base[(size_t)blockIdx.x * E + e] : 0;
+    sum += c[j];
+  }
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int v = __shfl_up(incl, o, 64);
@@ -253,23 +264,28 @@ __global__ __launch_bounds__(1024) void chunk_scatter(const int32_t* __restrict_
   }
   if ((tid & 63) == 63) wave[tid >> 6] = incl;
   __syncthreads();
-  int off = incl - c, valid = 0;
+  int off = incl - sum, valid = 0;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) {
+  for (int w = 0; w < N / 64; ++w) {
     off += w < (tid >> 6) ? wave[w] : 0;
     valid += wave[w];
   }
-  if (tid < E) {
-    base[tid] = off + before;
-    if (blockIdx.x == 0) offsets[tid] = off;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int e = tid * EPT + j;
+    if (e < E) {
+      base[e] = off + before[j];
+      if (blockIdx.x == 0) offsets[e] = off;
+    }
+    off += c[j];
   }
   if (blockIdx.x == 0 && tid == 0) offsets[E] = valid;
-  for (int p = tid; p < np; p += 1024) {
+  for (int p = tid; p < np; p += N) {
     const int t = p / k;
     if (valid_slot(rows + t * k, p - t * k, E)) atomicOr(&mask[rows[p]][t >> 6], 1ull << (t & 63));
   }
   __syncthreads();
-  for (int p = tid; p < np; p += 1024) {
+  for (int p = tid; p < np; p += N) {
     const int t = p / k, word = t >> 6;
     const int64_t pair = t0 * k + p;
     if (valid_slot(rows + t * k, p - t * k, E)) {
@@ -285,7 +301,7 @@ __global__ __launch_bounds__(1024) void chunk_scatter(const int32_t* __restrict_
   }
   // Positions past the last valid pair (only when ids were dropped) get -1.
   const int64_t P = T * k;
-  for (int64_t q = valid + (int64_t)blockIdx.x * 1024 + tid; q < P; q += (int64_t)gridDim.x * 1024)
+  for (int64_t q = valid + (int64_t)blockIdx.x * N + tid; q < P; q += (int64_t)gridDim.x * N)
     sorted_pair[q] = -1;
 }
 
@@ -294,12 +310,12 @@ hipError_t chunked(const k3moe_shape& s, const int32_t* idx, int32_t* counts, in
                    int32_t* sorted_pair, int32_t* pair_pos, int32_t* diag, const PermuteWs& ws,
                    hipStream_t st) {
   const int nchunks = (int)((s.T + CH - 1) / CH);
-  chunk_hist<CH><<<nchunks, 1024, 0, st>>>(idx, ws.chunk_base, diag, s.T, s.E, s.k);
+  chunk_hist<CH><<<nchunks, chunk_threads<CH>(), 0, st>>>(idx, ws.chunk_base, diag, s.T, s.E, s.k);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   chunk_scan<<<(s.E + 63) / 64, 1024, 0, st>>>(ws.chunk_base, counts, nchunks, s.E);
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  chunk_scatter<CH><<<nchunks, 1024, 0, st>>>(idx, ws.chunk_base, counts, offsets, sorted_pair,
+  chunk_scatter<CH><<<nchunks, chunk_threads<CH>(), 0, st>>>(idx, ws.chunk_base, counts, offsets, sorted_pair,
                                              pair_pos, s.T, s.E, s.k);
   return hipGetLastError();
 }

@@ -290,7 +290,8 @@ __device__ void plan_chunks(const RouteArgs& g) {
     if (e >= g.E) break;
     const int parts = c[j] > 1 ? c[j] : 0;
     for (int i = 0; i < c[j] && first[0] + i < g.max_chunks; ++i)
-      g.list[first[0] + i] = make_int4(e, q0[j] + i * kChunk, min(q0[j] + (i + 1) * kChunk, q0[j] + n[j]),
+      g.list[first[0] + i] = make_int4(e, q0[j] + i * kChunk,
+                                       (int)min((int64_t)q0[j] + (i + 1) * kChunk, (int64_t)q0[j] + n[j]),
                                        parts ? first[1] + i : -1);
     g.joins[e] = make_int2(first[1], parts);
     first[0] += c[j];
@@ -505,18 +506,19 @@ __global__ __launch_bounds__(256) void dw_chunks(const void* __restrict__ x,
   const int64_t P = T * k;
   const int uc = u < units ? u : units - 1;
   f8 acc{};
-  for (int b = c.y; b < c.z; b += 64) {
+  const unsigned end = c.z;
+  for (unsigned b = c.y; b < end; b += 64) {   // (64 past the last pair may not fit an int)
     // lane i has the token and weight of pair b + i
     int tok = 0;
     float w = 0.0f;
-    if (b + lane < c.z) {
+    if (b + lane < end) {
       const int p = sorted_pair[b + lane];
       if (p >= 0 && p < P) {
         tok = (unsigned)p / (unsigned)k;
         w = dl_sorted[b + lane];
       }
     }
-    const int n = min(64, c.z - b);
+    const int n = (int)min(64u, end - b);
     for (int i = 0; i < n; i += G * R) {
       f8 v[G];
       float wi[G];
