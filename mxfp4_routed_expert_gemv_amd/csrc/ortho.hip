@@ -523,9 +523,14 @@ __global__ __launch_bounds__(256) void square_sums(const void* __restrict__ g, d
       }
     }
   } else {
-    for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
-      const double v = (double)load_g(g, first + i, F32);
-      a = fma(v, v, a);
+    constexpr int U = 8;   // loads in flight
+    for (int64_t i = lo + threadIdx.x; i < hi; i += 256 * U) {
+      float v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = load_g(g, first + min(i + 256 * u, hi - 1), F32);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + 256 * u < hi) a = fma((double)v[u], (double)v[u], a);
     }
   }
   a = wave_sum(a);
@@ -537,10 +542,10 @@ __global__ __launch_bounds__(256) void square_sums(const void* __restrict__ g, d
 
 // A 64 x 64 tile of X's two parts from g / |g| (0 for a matrix of zeros), zeros
 // outside the matrix.  TR: X is g's transpose.
-template <bool TR>
+template <bool TR, bool F32>
 __global__ __launch_bounds__(256) void scale_in(const void* __restrict__ g, const double* __restrict__ sums,
                                                 uint16_t* __restrict__ hi, uint16_t* __restrict__ lo,
-                                                int s, int l, int rows, int cols, int pieces, int f32) {
+                                                int s, int l, int rows, int cols, int pieces) {
   __shared__ float t[64][65];
   __shared__ double wave[4];
   double a = wave_sum((int)threadIdx.x < pieces ? sums[(size_t)blockIdx.z * pieces + threadIdx.x] : 0.0);
@@ -552,31 +557,34 @@ __global__ __launch_bounds__(256) void scale_in(const void* __restrict__ g, cons
   const size_t first = (size_t)blockIdx.z * rows * cols;
   // a thread's 16 elements: of X's row m0 + i (or, transposed, column n0 + i)
   const int c = (threadIdx.x & 15) * 4;
+  const int nr = TR ? cols : rows, nk = TR ? rows : cols;   // g's rows and columns
+  const int k = (TR ? m0 : n0) + c;
+  float v[4][4];
+  // (every load is issued, of the first element outside the matrix)
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int i = (threadIdx.x >> 4) + 16 * q;
-    const int r = (TR ? n0 : m0) + i, k = (TR ? m0 : n0) + c;
-    const int nr = TR ? cols : rows, nk = TR ? rows : cols;   // g's rows and columns
+    const int r = (TR ? n0 : m0) + (threadIdx.x >> 4) + 16 * q;
     const size_t at = first + (size_t)r * nk + k;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < nr && k < nk) {
-      if (nk % 4 == 0) {
-        if (f32) {
-          const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(g) + at);
-          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + at);
-          v[0] = bf16_lo(x.x); v[1] = bf16_hi(x.x); v[2] = bf16_lo(x.y); v[3] = bf16_hi(x.y);
-        }
+    if (nk % 4 == 0) {
+      const size_t p = r < nr && k < nk ? at : 0;
+      if (F32) {
+        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(g) + p);
+        v[q][0] = x.x; v[q][1] = x.y; v[q][2] = x.z; v[q][3] = x.w;
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (k + j < nk) v[j] = load_g(g, at + j, f32);
+        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + p);
+        v[q][0] = bf16_lo(x.x); v[q][1] = bf16_hi(x.x); v[q][2] = bf16_lo(x.y); v[q][3] = bf16_hi(x.y);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[q][j] = load_g(g, r < nr && k + j < nk ? at + j : 0, F32);
     }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int i = (threadIdx.x >> 4) + 16 * q, r = (TR ? n0 : m0) + i;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x = (float)((double)v[j] * f);
+      const float x = r < nr && k + j < nk ? (float)((double)v[q][j] * f) : 0.0f;
       if (TR) t[c + j][i] = x; else t[i][c + j] = x;
     }
   }
@@ -756,8 +764,11 @@ hipError_t launch_ortho(const k3moe_ortho& p, const void* g, void* out, const Or
   else square_sums<false><<<sums, 256, 0, st>>>(g, ws.sums, count, piece);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (d.tr) scale_in<true><<<tiles, 256, 0, st>>>(g, ws.sums, ws.x[0], ws.lo, d.s, d.l, d.rows, d.cols, pieces, f32);
-  else scale_in<false><<<tiles, 256, 0, st>>>(g, ws.sums, ws.x[0], ws.lo, d.s, d.l, d.rows, d.cols, pieces, f32);
+  auto scale = [&](auto kernel) {
+    kernel<<<tiles, 256, 0, st>>>(g, ws.sums, ws.x[0], ws.lo, d.s, d.l, d.rows, d.cols, pieces);
+  };
+  if (d.tr) f32 ? scale(scale_in<true, true>) : scale(scale_in<true, false>);
+  else f32 ? scale(scale_in<false, true>) : scale(scale_in<false, false>);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   OrthoArgs a{};
   a.lo = ws.lo;
