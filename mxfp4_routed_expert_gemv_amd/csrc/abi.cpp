@@ -217,7 +217,7 @@ k3moe_status check_disjoint(const Region (&written)[W], const Region (&read)[R])
 
 size_t dispatch_workspace(const k3moe_shape& s) {
   size_t need = 0;
-  if (!dispatch_small_ok(s)) carve_permute(s, nullptr, &need);
+  if (!permute_small_ok(s)) carve_permute(s, nullptr, &need);
   return need;
 }
 

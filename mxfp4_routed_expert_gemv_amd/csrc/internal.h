@@ -211,7 +211,9 @@ struct RouteBackWs {
   float* part;       // [..][d] sums of chunks
 };
 RouteBackWs carve_route_back(const k3moe_shape& s, void* ws, size_t* bytes);
-// The sort and the rows in one launch, for batches of the sort's one workgroup.
+// Batches that one workgroup sorts (without a workspace), and those whose rows move in the
+// same launch.
+bool permute_small_ok(const k3moe_shape& s);
 bool dispatch_small_ok(const k3moe_shape& s);
 hipError_t launch_dispatch_small(const k3moe_shape& s, const void* x, const int32_t* idx, void* rows,
                                  int32_t* counts, int32_t* offsets, int32_t* sorted_pair,

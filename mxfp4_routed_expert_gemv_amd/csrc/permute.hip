@@ -326,7 +326,10 @@ hipError_t chunked(const k3moe_shape& s, const int32_t* idx, int32_t* counts, in
 // whose counts take a quarter of the memory.
 int permute_chunk_tokens(int64_t T, int k) { return k <= 16 && T >= (1 << 17) ? 256 : 64; }
 
-bool dispatch_small_ok(const k3moe_shape& s) { return s.T <= kSmallT && s.T * s.k <= kSmallPairs; }
+bool permute_small_ok(const k3moe_shape& s) { return s.T <= kSmallT && s.T * s.k <= kSmallPairs; }
+// (each of the moving workgroups compares its token's ids with all: 4096 pairs of 256 x
+// 7168 take 38 us so, 28 in two launches; 1024 pairs 15, 18)
+bool dispatch_small_ok(const k3moe_shape& s) { return s.T <= kSmallT && s.T * s.k <= 1024; }
 
 hipError_t launch_dispatch_small(const k3moe_shape& s, const void* x, const int32_t* idx, void* rows,
                                  int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
@@ -340,7 +343,7 @@ hipError_t launch_dispatch_small(const k3moe_shape& s, const void* x, const int3
 hipError_t launch_permute(const k3moe_shape& s, const int32_t* idx, int32_t* counts,
                           int32_t* offsets, int32_t* sorted_pair, int32_t* pair_pos,
                           int32_t* diag, const PermuteWs& ws, hipStream_t st) {
-  if (s.T <= kSmallT && s.T * s.k <= kSmallPairs) {
+  if (permute_small_ok(s)) {
     permute_small<<<1, 1024, 0, st>>>(idx, counts, offsets, sorted_pair, pair_pos, diag,
                                       (int)s.T, s.E, s.k);
     return hipGetLastError();

@@ -9,7 +9,13 @@
 // All but dW go token by token: a wave has 64 units of 8 elements (512 columns) of
 // one token, so positions and weights are scalars, x or dy is read once, every
 // access of a row is 1 KB in one piece (fp32: 2 KB), and a sum has one order.
-// Nothing is reused but the token's own row: the bytes of the T k rows bound them.
+// Nothing is reused but the token's own row: the bytes of the T k rows bound them (d 7168,
+// 16 slots, bf16: dispatch of 4096 tokens 175 us for 1.0 GB, collect of 16384 810 us for
+// 4.2 GB, its backward at 4096 390 us for 1.9 GB, where a copy runs at 4.85 TB/s; fp32
+// rows: dispatch back of 1000 tokens 92 us for 0.49 GB).  A few tokens are latency: 8 us
+// for 37.  Moved rows are stored non-temporally (dispatch 200 us without, collect back
+// 395); read so, rows that the experts wrote last miss the last-level cache (collect of
+// 37 tokens 8 -> 12 us, dispatch back 92 -> 101).
 #include <algorithm>
 
 #include "internal.h"
