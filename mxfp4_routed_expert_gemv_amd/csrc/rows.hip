@@ -17,6 +17,7 @@
 // 395); read so, rows that the experts wrote last miss the last-level cache (collect of
 // 37 tokens 8 -> 12 us, dispatch back 92 -> 101).
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "kern_common.h"
@@ -158,9 +159,11 @@ __global__ __launch_bounds__(512) void gather_sum(GatherArgs g) {
 
 // ---- collect's backward: kSlots slots of a token to a workgroup of 4 waves, which
 // take the row's units in turn; the dot products' partial sums are added over the
-// lanes, then over the waves in order.
+// lanes, then over the waves in order.  WAVE: a wave to a token instead, for rows of up
+// to 1280 columns (5888 tokens, 6 slots, us so and with four waves: 192 columns 13, 27;
+// 1056 43, 47; 2048 86, 72).
 constexpr int kSlots = 4;
-template <bool ROWS_F32, bool DY_F32>
+template <bool ROWS_F32, bool DY_F32, bool WAVE>
 __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
                                                     const void* __restrict__ rows,
                                                     const int32_t* __restrict__ pair_pos,
@@ -170,8 +173,11 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
                                                     int64_t T, int units, int E, int k) {
   __shared__ float part[4][kSlots];
   const int64_t P = T * k;
-  const int s0 = blockIdx.x * kSlots, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+  constexpr int N = WAVE ? 64 : 256;   // threads to a token
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int s0 = blockIdx.x * kSlots, tid = WAVE ? lane : threadIdx.x;
+  const int64_t t0 = WAVE ? blockIdx.y * 4 + wv : blockIdx.y, step = WAVE ? gridDim.y * 4 : gridDim.y;
+  for (int64_t t = t0; t < T; t += step) {
     int at[kSlots];
     float w[kSlots], dot[kSlots];
 #pragma unroll
@@ -182,7 +188,7 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
       w[j] = slot ? topk_w[t * k + s0 + j] : 0.0f;
       dot[j] = 0.0f;
     }
-    for (int u = threadIdx.x; u < units; u += 256) {
+    for (int u = tid; u < units; u += N) {
       const f8 g = load8<DY_F32>(dy, t * units + u);
       f8 v[kSlots];
       if (dw) {
@@ -210,6 +216,12 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
     if (dw) {
 #pragma unroll
       for (int j = 0; j < kSlots; ++j) dot[j] = wave_sum(dot[j]);
+      if (WAVE) {
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+          if (lane == 0 && s0 + j < k) dw[t * k + s0 + j] = at[j] >= 0 ? dot[j] : 0.0f;
+        continue;
+      }
       if (lane == 0) {
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) part[wv][j] = dot[j];
@@ -226,8 +238,8 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
   }
   if (drows && blockIdx.x == 0) {
     const f8 zero{};
-    for (int64_t q = used_rows(offsets, E, P) + blockIdx.y; q < P; q += gridDim.y)
-      for (int u = threadIdx.x; u < units; u += 256) store8<ROWS_F32>(drows, q * units + u, zero);
+    for (int64_t q = used_rows(offsets, E, P) + t0; q < P; q += step)
+      for (int u = tid; u < units; u += N) store8<ROWS_F32>(drows, q * units + u, zero);
   }
 }
 
@@ -674,13 +686,20 @@ hipError_t launch_collect_back(const k3moe_shape& s, const void* dy, const void*
                                const int32_t* pair_pos, const float* w, const int32_t* offsets,
                                void* drows, float* dw, hipStream_t st) {
   if (!drows && !dw) return hipSuccess;
-  const dim3 grid((s.k + kSlots - 1) / kSlots, token_blocks(s.T));
+  const bool wave = s.d <= 1280;
+  const dim3 grid((s.k + kSlots - 1) / kSlots, token_blocks(wave ? (s.T + 3) / 4 : s.T));
   auto run = [&](auto kernel) {
     kernel<<<grid, 256, 0, st>>>(dy, rows, pair_pos, w, offsets, drows, dw, s.T, s.d / 8, s.E, s.k);
   };
   const bool f = s.out_dtype == K3MOE_F32;
-  if (s.x_dtype == K3MOE_F32) f ? run(collect_back<true, true>) : run(collect_back<true, false>);
-  else f ? run(collect_back<false, true>) : run(collect_back<false, false>);
+  auto pick = [&](auto rows_f32, auto dy_f32) {
+    if (wave) run(collect_back<rows_f32, dy_f32, true>);
+    else run(collect_back<rows_f32, dy_f32, false>);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (s.x_dtype == K3MOE_F32) f ? pick(Yes(), Yes()) : pick(Yes(), No());
+  else f ? pick(No(), Yes()) : pick(No(), No());
   return hipGetLastError();
 }
 
