@@ -228,6 +228,13 @@ def route_backward(x, w_router, idx, w, dw, order, router="softmax", logits=None
 
 
 # ------------------------------------------------------------- torch operations
+def _whole(grad):
+    """grad as the calls take it.  autograd may hand over a part of a larger tensor, which
+    is contiguous and still begins anywhere; the calls need 16 bytes."""
+    grad = grad.contiguous()
+    return grad.clone() if grad.data_ptr() % 16 else grad
+
+
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, idx, n_experts):
@@ -239,7 +246,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, drows, *_):
-        return dispatch_backward(drows.contiguous(), ctx.saved_tensors), None, None
+        return dispatch_backward(_whole(drows), ctx.saved_tensors), None, None
 
 
 class _Collect(torch.autograd.Function):
@@ -252,7 +259,7 @@ class _Collect(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         rows, w, *order = ctx.saved_tensors
-        dy = dy.contiguous()
+        dy = _whole(dy)
         drows, dw = collect_backward(dy, rows, order, w, need=ctx.needs_input_grad[:2])
         return (drows, dw, dy if ctx.needs_input_grad[2] else None, None, None, None, None)
 
@@ -280,7 +287,7 @@ class _Route(torch.autograd.Function):
         x, w_router, idx, w, logits = ctx.saved_tensors
         # the order of the pairs, sorted again from the ids rather than kept
         order = sort_pairs(idx, w_router.shape[0])
-        dx, dwr = route_backward(x, w_router, idx, w, dw.contiguous(), order, ctx.router, logits,
+        dx, dwr = route_backward(x, w_router, idx, w, _whole(dw), order, ctx.router, logits,
                                  need=ctx.needs_input_grad[:2])
         return dx, dwr, None, None, None, None
 

@@ -432,3 +432,38 @@ def test_captured_and_replayed():
         got = [o.clone() for o in outs]
         for a, b, name in zip(got, once(), ("y", "dx", "dw", "dx router", "dw_router")):
             assert torch.equal(a, b), (i, name)
+
+
+def test_gradients_that_begin_inside_another_tensor():
+    """What autograd hands a backward may be part of a larger tensor, at any element: the
+    second half of a concatenation's gradient begins at 5 * 3 * 4 = 60 bytes here, rows'
+    gradient at one element.  Moved, such a gradient gives the same bits."""
+    r = routing()
+    T, d, E, k = 5, 96, 7, 3
+    g, *_ = make(T, d, E, k, 41)
+    x = randn(g, T, d, dtype=torch.bfloat16).requires_grad_()
+    wr = randn(g, E, d, dtype=torch.bfloat16, std=0.1).requires_grad_()
+    dw = randn(g, 2 * T, k)
+    idx, w = r.route_tokens(x, wr, k)
+    want = torch.autograd.grad(w, (x, wr), dw[T:].clone(), retain_graph=True)
+    both = torch.cat([torch.zeros(T, k, device="cuda"), w])
+    got = torch.autograd.grad(both, (x, wr), dw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    def inside(t):   # t's values from the second element of a buffer on
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        at = buf[1:].view(t.shape)
+        at.copy_(t)
+        return at
+
+    rows, order = r.dispatch_tokens(x, idx, E)
+    up = randn(g, *rows.shape, dtype=rows.dtype)
+    want, = torch.autograd.grad(rows, x, up, retain_graph=True)
+    got, = torch.autograd.grad(rows, x, inside(up), retain_graph=True)
+    assert torch.equal(got, want)
+    leaf, wl = rows.detach().requires_grad_(), w.detach().requires_grad_()
+    y = r.collect_tokens(leaf, order, wl)
+    up = randn(g, T, d, dtype=y.dtype)
+    want = torch.autograd.grad(y, (leaf, wl), up, retain_graph=True)
+    got = torch.autograd.grad(y, (leaf, wl), inside(up))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
