@@ -247,8 +247,8 @@ __global__ __launch_bounds__(1024) void gram_parts(SmallArgs g) {
     }
 }
 
-// ---- the polynomials.  64: 4 x 4 waves of one block; 128: 2 x 2 waves of 4 x 4
-// blocks, so that a product's LDS reads take less time than its matrix instructions.
+// ---- the polynomials.  64: 4 x 4 waves of one block; 128: 2 x 4 waves of 4 x 2
+// blocks (43 us for five steps when that was chosen; four waves of 4 x 4 50).
 template <int S>
 struct Waves {
   static constexpr int MB = S == 64 ? 1 : 4, NB = S == 64 ? 1 : 2;
