@@ -185,7 +185,7 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
       const bool slot = s0 + j < k;
       at[j] = slot ? pair_pos[t * k + s0 + j] : -1;
       if (at[j] >= P) at[j] = -1;
-      w[j] = slot ? topk_w[t * k + s0 + j] : 0.0f;
+      w[j] = slot && drows ? topk_w[t * k + s0 + j] : 0.0f;   // (topk_w may be NULL for dw alone)
       dot[j] = 0.0f;
     }
     for (int u = tid; u < units; u += N) {
