@@ -260,7 +260,8 @@ k3moe_status k3moe_route(const k3moe_shape* shape, const void* x, const void* w_
  * token's row, is dropped (its pair_pos is -1, sorted positions past
  * offsets[E] hold -1) and counted in diag[K3MOE_DIAG_BAD_EXPERT_IDS].
  * Errors: EINVAL (a NULL output), EALIGN, EWORKSPACE.
- * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_PERMUTE). */
+ * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_PERMUTE), which does not fall as
+ * T grows. */
 k3moe_status k3moe_permute(const k3moe_shape* shape, const int32_t* topk_idx, int32_t* counts,
                            int32_t* offsets, int32_t* sorted_pair, int32_t* pair_pos,
                            int32_t* diag, void* workspace, size_t workspace_bytes, void* stream);
@@ -585,7 +586,7 @@ k3moe_status k3moe_grad_clip(const k3moe_tensor* tensors, int32_t n, float max_n
  *   rows[pair_pos[t*k+s]] = x[t], zeros behind the last pair's row.
  * Errors: EINVAL, EALIGN, EWORKSPACE.
  * Workspace: k3moe_workspace_bytes(shape, K3MOE_OP_DISPATCH) (0, where NULL is
- * accepted, up to 256 tokens and 4096 pairs). */
+ * accepted, up to 256 tokens and 4096 pairs), which does not fall as T grows. */
 k3moe_status k3moe_dispatch(const k3moe_shape* shape, const void* x, const int32_t* topk_idx,
                             void* rows, int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
                             int32_t* pair_pos, int32_t* diag, void* workspace,

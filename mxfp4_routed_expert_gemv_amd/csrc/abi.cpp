@@ -368,7 +368,8 @@ PermuteWs carve_permute(const k3moe_shape& s, void* ws, size_t* bytes) {
   PermuteWs r;
   const int ch = permute_chunk_tokens(s.T, s.k);
   const size_t nchunks = (size_t)((s.T + ch - 1) / ch);
-  r.chunk_base = c.take<int32_t>(nchunks * s.E);
+  // (what a batch needs serves a smaller one: larger chunks keep what the small ones take)
+  r.chunk_base = c.take<int32_t>(std::max(nchunks, permute_least_chunks(s.T, s.k)) * s.E);
   if (bytes) *bytes = c.off;
   return r;
 }

@@ -24,6 +24,8 @@ inline bool routed_scaled(const k3moe_shape& s) {
 }
 // Tokens per chunk of the large-batch permute (one bit per token in LDS masks).
 int permute_chunk_tokens(int64_t T, int k);
+// Chunks that the workspace has room for at least: those of every smaller batch.
+size_t permute_least_chunks(int64_t T, int k);
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 

@@ -323,8 +323,10 @@ hipError_t chunked(const k3moe_shape& s, const int32_t* idx, int32_t* counts, in
 }  // namespace
 
 // Small chunks fill the chip; from 2^17 tokens there are enough of the larger ones,
-// whose counts take a quarter of the memory.
-int permute_chunk_tokens(int64_t T, int k) { return k <= 16 && T >= (1 << 17) ? 256 : 64; }
+// whose counts take a quarter of the memory (the workspace is smaller from 2^19 tokens on).
+constexpr int64_t kLargeT = 1 << 17;
+int permute_chunk_tokens(int64_t T, int k) { return k <= 16 && T >= kLargeT ? 256 : 64; }
+size_t permute_least_chunks(int64_t T, int k) { return permute_chunk_tokens(T, k) == 256 ? kLargeT / 64 : 0; }
 
 bool permute_small_ok(const k3moe_shape& s) { return s.T <= kSmallT && s.T * s.k <= kSmallPairs; }
 // (each of the moving workgroups compares its token's ids with all: 4096 pairs of 256 x
