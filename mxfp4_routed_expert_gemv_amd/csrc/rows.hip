@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "chunk_plan.h"
 #include "internal.h"
 #include "kern_common.h"
 
@@ -268,7 +269,6 @@ struct RouteArgs {
 // a chunk at least.  An expert of one chunk is done with it, the chunks of others leave
 // fp32 sums that dw_join adds in order.  The list is made by one workgroup, thread i
 // placing experts 4 i .. 4 i + 3.
-constexpr int kChunk = 256;
 __device__ void plan_chunks(const RouteArgs& g) {
   __shared__ int wave[2][4];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -283,7 +283,7 @@ __device__ void plan_chunks(const RouteArgs& g) {
     const int e = tid * 4 + j;
     q0[j] = e < g.E ? at(e) : 0;
     n[j] = e < g.E ? max(at(e + 1) - q0[j], 0) : 0;
-    c[j] = e < g.E ? max((n[j] + kChunk - 1) / kChunk, 1) : 0;
+    c[j] = e < g.E ? chunks_of(n[j]) : 0;
     sum[0] += c[j];
     sum[1] += c[j] > 1 ? c[j] : 0;
   }
@@ -308,8 +308,7 @@ __device__ void plan_chunks(const RouteArgs& g) {
     if (e >= g.E) break;
     const int parts = c[j] > 1 ? c[j] : 0;
     for (int i = 0; i < c[j] && first[0] + i < g.max_chunks; ++i)
-      g.list[first[0] + i] = make_int4(e, q0[j] + i * kChunk,
-                                       (int)min((int64_t)q0[j] + (i + 1) * kChunk, (int64_t)q0[j] + n[j]),
+      g.list[first[0] + i] = make_int4(e, chunk_begin(q0[j], i), chunk_end(q0[j], n[j], i),
                                        parts ? first[1] + i : -1);
     g.joins[e] = make_int2(first[1], parts);
     first[0] += c[j];
@@ -634,9 +633,8 @@ hipError_t launch_dw(const k3moe_shape& s, const void* x, const int32_t* sorted_
   return hipSuccess;
 }
 
-int max_chunks(const k3moe_shape& s) { return (int)(s.E + s.T * s.k / kChunk); }
-// An expert of more than kChunk pairs has at most twice its pairs / kChunk chunks.
-int max_parts(const k3moe_shape& s) { return s.T > kChunk ? (int)(2 * (s.T * s.k / kChunk)) : 0; }
+int max_chunks(const k3moe_shape& s) { return most_chunks(s.E, s.T * s.k); }
+int max_parts(const k3moe_shape& s) { return most_parts(s.T, s.T * s.k); }
 
 }  // namespace
 
