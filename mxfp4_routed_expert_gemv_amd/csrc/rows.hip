@@ -268,7 +268,8 @@ struct RouteArgs {
 // The router's weight gradient goes by chunks: an expert's pairs, kChunk to a chunk and
 // a chunk at least.  An expert of one chunk is done with it, the chunks of others leave
 // fp32 sums that dw_join adds in order.  The list is made by one workgroup, thread i
-// placing experts 4 i .. 4 i + 3.
+// placing experts 4 i .. 4 i + 3.  Offsets that do not ascend give experts without pairs:
+// the chunks of others are at most max_chunks, whatever the offsets hold.
 __device__ void plan_chunks(const RouteArgs& g) {
   __shared__ int wave[2][4];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -278,11 +279,19 @@ __device__ void plan_chunks(const RouteArgs& g) {
     return (int)(o < 0 ? 0 : o > P ? P : o);
   };
   int q0[4], n[4], c[4], sum[2] = {0, 0};
+  bool falls = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int e = tid * 4 + j;
     q0[j] = e < g.E ? at(e) : 0;
-    n[j] = e < g.E ? max(at(e + 1) - q0[j], 0) : 0;
+    n[j] = e < g.E ? at(e + 1) - q0[j] : 0;
+    falls |= n[j] < 0;
+  }
+  const bool none = __syncthreads_or(falls);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = tid * 4 + j;
+    if (none) n[j] = 0;
     c[j] = e < g.E ? chunks_of(n[j]) : 0;
     sum[0] += c[j];
     sum[1] += c[j] > 1 ? c[j] : 0;

@@ -27,3 +27,20 @@ def test_one_gradient_of_collect_without_the_other_ones_operands(T, d, E, k, dty
     only = torch.full_like(drows, 7.0)
     k3moe_collect_backward(s, dy, None, order.pair_pos, w, order.offsets, only, None)
     assert torch.equal(only, drows)
+
+
+@pytest.mark.parametrize("T", [65, 300, 5000])
+def test_offsets_that_do_not_ascend_give_no_sums(T):
+    """As many chunks as the workspace has room for come only from offsets that ascend."""
+    r = routing()
+    E, k, d = 12, 4, 96
+    g, idx, w = make(T, d, E, k, 51)
+    x, wr = randn(g, T, d), randn(g, E, d, dtype=torch.bfloat16)
+    dw = randn(g, T, k)
+    order = r.sort_pairs(idx, E)
+    dx, dwr = r.route_backward(x, wr, idx, w, dw, order)
+    assert dwr.any(1).all()
+    P = T * k
+    for offsets in (order.offsets.flip(0), torch.tensor([0, P] * 6 + [0], dtype=torch.int32, device="cuda")):
+        dx2, none = r.route_backward(x, wr, idx, w, dw, order._replace(offsets=offsets.contiguous()))
+        assert torch.equal(dx2, dx) and not none.any()
