@@ -3,7 +3,8 @@ the weights applied, and the gradients of both and of the router; each as plain
 calls and as torch operations that autograd goes through.
 
 Tensors are torch device tensors, contiguous, all on one device; the work is
-enqueued on that device's current stream (or `stream`).  Every computation
+enqueued on that device's current stream (or `stream`).  An operand that begins
+inside another tensor, at other than 16 bytes, is copied first.  Every computation
 happens in libk3moe's kernels; this file only marshals."""
 from collections import namedtuple
 from ctypes import byref
@@ -45,6 +46,13 @@ def _need(t, name, shape, dtypes, device):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _whole(*operands):
+    """The operands at 16 bytes, as the calls need them: a contiguous part of a larger
+    tensor (a micro-batch's rows of w, a gradient that autograd hands over) may begin at
+    any element.  Called where the call's stream is current, which the copies belong to."""
+    return [t if t is None or not t.data_ptr() & 15 else t.clone() for t in operands]
 
 
 def _bytes(ws):
@@ -105,6 +113,7 @@ def sort_pairs(idx, n_experts, diag=None, workspace=None, stream=None):
     _check_ids(idx, diag, dev)
     shape, nbytes = _shape_of(T, 32, E, k, torch.bfloat16, torch.bfloat16, op=OP_PERMUTE)
     with on_device(dev, stream):
+        idx, = _whole(idx)
         order = _empty_order(T, k, E, dev)
         k3moe_permute(shape, idx, *order, diag, _scratch(workspace, nbytes, dev),
                       _raw_stream(dev.index))
@@ -124,6 +133,7 @@ def dispatch(x, idx, n_experts, diag=None, workspace=None, stream=None):
     _check_ids(idx, diag, dev)
     shape, nbytes = _shape_of(T, d, E, k, x.dtype, x.dtype, op=OP_DISPATCH)
     with on_device(dev, stream):
+        x, idx = _whole(x, idx)
         rows = torch.empty((T * k, d), dtype=x.dtype, device=dev)
         order = _empty_order(T, k, E, dev)
         ws = _scratch(workspace, nbytes, dev)
@@ -142,6 +152,7 @@ def dispatch_backward(drows, order, out_dtype=None, stream=None):
     _need(pair_pos, "pair_pos", (T, k), _I32, dev)
     shape, _ = _shape_of(T, d, k, k, drows.dtype, out_dtype)
     with on_device(dev, stream):
+        drows, pair_pos = _whole(drows, pair_pos)
         dx = torch.empty((T, d), dtype=out_dtype, device=dev)
         _check(lib.k3moe_dispatch_backward(byref(shape), _ptr(drows), _ptr(pair_pos), _ptr(dx),
                                            _raw_stream(dev.index)))
@@ -163,6 +174,7 @@ def collect(rows, order, w, add=None, out_dtype=None, stream=None):
         _need(add, "add", (T, d), (out_dtype,), dev)
     shape, _ = _shape_of(T, d, k, k, rows.dtype, out_dtype)
     with on_device(dev, stream):
+        rows, pair_pos, w, add = _whole(rows, pair_pos, w, add)
         y = torch.empty((T, d), dtype=out_dtype, device=dev)
         _check(lib.k3moe_collect(byref(shape), _ptr(rows), _ptr(pair_pos), _ptr(w), _addr(add),
                                  _ptr(y), _raw_stream(dev.index)))
@@ -183,6 +195,7 @@ def collect_backward(dy, rows, order, w, need=(True, True), stream=None):
     _need(w, "w", (T, k), _F, dev)
     shape, _ = _shape_of(T, d, E, k, rows.dtype, dy.dtype)
     with on_device(dev, stream):
+        dy, rows, pair_pos, w, offsets = _whole(dy, rows, pair_pos, w, offsets)
         drows = torch.empty_like(rows) if need[0] else None
         dw = torch.empty((T, k), dtype=torch.float32, device=dev) if need[1] else None
         _check(lib.k3moe_collect_backward(byref(shape), _ptr(dy), _ptr(rows), _ptr(pair_pos),
@@ -216,6 +229,8 @@ def route_backward(x, w_router, idx, w, dw, order, router="softmax", logits=None
     shape, nbytes = _shape_of(T, d, E, k, x.dtype, _out(dw_dtype, "dw_router"), ROUTERS[router],
                               OP_ROUTE_BACKWARD)
     with on_device(dev, stream):
+        x, w_router, idx, w, dw, logits, offsets, sorted_pair, pair_pos = _whole(
+            x, w_router, idx, w, dw, logits, offsets, sorted_pair, pair_pos)
         dx = torch.empty_like(x) if need[0] else None
         dwr = torch.empty((E, d), dtype=dw_dtype, device=dev) if need[1] else None
         # (an empty tensor's address may be NULL: for T = 0 nothing is read or written there)
@@ -228,13 +243,6 @@ def route_backward(x, w_router, idx, w, dw, order, router="softmax", logits=None
 
 
 # ------------------------------------------------------------- torch operations
-def _whole(grad):
-    """grad as the calls take it.  autograd may hand over a part of a larger tensor, which
-    is contiguous and still begins anywhere; the calls need 16 bytes."""
-    grad = grad.contiguous()
-    return grad.clone() if grad.data_ptr() % 16 else grad
-
-
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, idx, n_experts):
@@ -246,7 +254,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, drows, *_):
-        return dispatch_backward(_whole(drows), ctx.saved_tensors), None, None
+        return dispatch_backward(drows.contiguous(), ctx.saved_tensors), None, None
 
 
 class _Collect(torch.autograd.Function):
@@ -259,7 +267,7 @@ class _Collect(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         rows, w, *order = ctx.saved_tensors
-        dy = _whole(dy)
+        dy = dy.contiguous()
         drows, dw = collect_backward(dy, rows, order, w, need=ctx.needs_input_grad[:2])
         return (drows, dw, dy if ctx.needs_input_grad[2] else None, None, None, None, None)
 
@@ -274,7 +282,8 @@ class _Route(torch.autograd.Function):
             w = torch.empty((T, k), dtype=torch.float32, device=dev)
             logits = (torch.empty((T, E), dtype=torch.float32, device=dev)
                       if router == "sigmoid_norm" else None)
-            k3moe_route(shape, x, w_router, idx, w, logits, diag, _scratch(None, nbytes, dev),
+            at, wr, bias = _whole(x, w_router, bias)
+            k3moe_route(shape, at, wr, idx, w, logits, diag, _scratch(None, nbytes, dev),
                         _raw_stream(dev.index), router_bias=bias)
         ctx.save_for_backward(x, w_router, idx, w, logits)
         ctx.router = router
@@ -287,7 +296,7 @@ class _Route(torch.autograd.Function):
         x, w_router, idx, w, logits = ctx.saved_tensors
         # the order of the pairs, sorted again from the ids rather than kept
         order = sort_pairs(idx, w_router.shape[0])
-        dx, dwr = route_backward(x, w_router, idx, w, _whole(dw), order, ctx.router, logits,
+        dx, dwr = route_backward(x, w_router, idx, w, dw.contiguous(), order, ctx.router, logits,
                                  need=ctx.needs_input_grad[:2])
         return dx, dwr, None, None, None, None
 

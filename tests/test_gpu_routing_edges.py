@@ -44,3 +44,86 @@ def test_offsets_that_do_not_ascend_give_no_sums(T):
     for offsets in (order.offsets.flip(0), torch.tensor([0, P] * 6 + [0], dtype=torch.int32, device="cuda")):
         dx2, none = r.route_backward(x, wr, idx, w, dw, order._replace(offsets=offsets.contiguous()))
         assert torch.equal(dx2, dx) and not none.any()
+
+
+def inside(t):
+    """t's values from the second element of a buffer on, in one piece."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    at = buf[1:].view(t.shape)
+    at.copy_(t)
+    return at
+
+
+@pytest.mark.parametrize("T", [30, 300])
+def test_operands_that_begin_inside_another_tensor(T):
+    """Each operand of each call, alone and all of them, at one element of a buffer: the
+    same bits as at its beginning."""
+    r = routing()
+    E, k, d = 9, 3, 96
+    g, idx, w = make(T, d, E, k, 52)
+    x, wr = randn(g, T, d, dtype=torch.bfloat16), randn(g, E, d, dtype=torch.bfloat16)
+    dw, dy, logits = randn(g, T, k), randn(g, T, d, dtype=torch.bfloat16), randn(g, T, E)
+    rows, order = r.dispatch(x, idx, E)
+
+    def flat(out):
+        if isinstance(out, torch.Tensor):
+            return [out]
+        return [v for o in out for v in flat(o)]
+
+    def check(call, *operands):
+        want = flat(call(*operands))
+        for i in range(len(operands) + 1):
+            moved = [inside(t) if i in (j, len(operands)) else t for j, t in enumerate(operands)]
+            assert all(t.data_ptr() % 16 for t, o in zip(moved, operands) if t is not o)
+            assert all(torch.equal(a, b) for a, b in zip(flat(call(*moved)), want)), (call, i)
+
+    check(lambda x, idx: r.dispatch(x, idx, E), x, idx)
+    check(lambda idx: r.sort_pairs(idx, E), idx)
+    check(lambda rows, pos: r.dispatch_backward(rows, order._replace(pair_pos=pos)), rows, order.pair_pos)
+    check(lambda rows, pos, w, add: r.collect(rows, order._replace(pair_pos=pos), w, add=add),
+          rows, order.pair_pos, w, x)
+    check(lambda dy, rows, pos, w, off: r.collect_backward(dy, rows, order._replace(pair_pos=pos, offsets=off), w),
+          dy, rows, order.pair_pos, w, order.offsets)
+    check(lambda x, wr, idx, w, dw, lg, off, pairs, pos: r.route_backward(
+        x, wr, idx, w, dw, r.Order(order.counts, off, pairs, pos), "sigmoid_norm", lg),
+          x, wr, idx, w, dw, logits, order.offsets, order.sorted_pair, order.pair_pos)
+
+
+def test_micro_batches_of_one_choice():
+    """Tokens 5 .. of a routed batch: their weights begin at 5 * 3 * 4 = 60 bytes."""
+    r = routing()
+    T, d, E, k, at = 40, 96, 7, 3, 5
+    g, *_ = make(T, d, E, k, 53)
+    x = randn(g, T, d, dtype=torch.bfloat16).requires_grad_()
+    bias = inside(randn(g, E, std=0.1))
+    wr = inside(randn(g, E, d, dtype=torch.bfloat16, std=0.1)).requires_grad_()
+    idx, w = r.route_tokens(inside(x.detach()).requires_grad_(), wr, k, "sigmoid_norm", bias)
+    i2, w2 = r.route_tokens(x, wr.detach().clone().requires_grad_(), k, "sigmoid_norm", bias.clone())
+    assert torch.equal(idx, i2) and torch.equal(w, w2)
+    up = randn(g, T - at, d, dtype=torch.bfloat16)
+
+    def step(x, idx, w):
+        rows, order = r.dispatch_tokens(x, idx, E)
+        y = r.collect_tokens(rows, order, w, add=x)
+        return (y, *torch.autograd.grad(y, (x, w), up))
+    part = [t.detach()[at:] for t in (x, w)]
+    assert part[1].data_ptr() % 16
+    got = step(part[0].requires_grad_(), idx[at:], part[1].requires_grad_())
+    want = step(part[0].detach().clone().requires_grad_(), idx[at:].clone(), part[1].detach().clone().requires_grad_())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_operands_are_copied_on_the_calls_stream():
+    r = routing()
+    T, d, E, k = 300, 512, 24, 6
+    g, idx, w = make(T, d, E, k, 54)
+    x, off = randn(g, T, d, dtype=torch.bfloat16), inside(idx)
+    want, order = r.dispatch(x, idx, E)
+    y = r.collect(want, order, w)
+    st = torch.cuda.Stream()
+    w = inside(w)
+    st.wait_stream(torch.cuda.current_stream())
+    rows, o2 = r.dispatch(x, off, E, stream=st)
+    got = r.collect(rows, o2, w, stream=st)
+    st.synchronize()
+    assert torch.equal(rows, want) and torch.equal(got, y)
