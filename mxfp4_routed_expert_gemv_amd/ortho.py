@@ -43,20 +43,30 @@ def orthogonalize(g, steps=5, coefficients=MUON, scale=1.0, out=None, workspace=
             raise TypeError(f"out is {out.dtype}; torch.bfloat16 is needed")
         if out.shape != g.shape or out.device != g.device or not out.is_contiguous():
             raise ValueError("out must be a contiguous tensor of g's shape on its GPU")
+        a, b = g.data_ptr(), out.data_ptr()
+        if a < b + out.nbytes and b < a + g.nbytes and (a != b or g.dtype != out.dtype):
+            raise ValueError("out overlaps g, and is not g itself")
     m, n = g.shape[-2:]
     dev, given = g.device, out
     with on_device(dev, stream):
-        if out is None:
+        # the call takes its tensors at 16 bytes: a part of a larger one (a bucket of
+        # gradients) that begins elsewhere is copied, and its result too
+        if out is None or out.data_ptr() & 15:
             out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
         if out.numel() == 0:
-            return out
+            return out if given is None else given
         key = tuple(tuple(c) if hasattr(c, "__len__") else float(c) for c in coefficients)
         p, nbytes = _problem(g.numel() // (m * n), m, n, g.dtype, int(steps), key, float(scale))
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         else:
             check_workspace(workspace, dev.index)
+        if g.data_ptr() & 15:
+            g = g.clone()
         k3moe_orthogonalize(p, g, out, workspace, current_stream(dev))
-    if given is not None:   # autograd has to know what was overwritten
-        increment_version(given)
-    return out
+        if given is not None and given is not out:
+            given.detach().copy_(out)
+    if given is None:
+        return out
+    increment_version(given)   # autograd has to know what was overwritten
+    return given
