@@ -16,7 +16,10 @@
 // directions ten times its noise, 512 x 1024: 1e-2 with one part, 3e-4 with two;
 // for noise alone 1.5e-3, as much as the bf16 output's own rounding).  The last step,
 // whose error nothing multiplies any more, does without.  The roundings inside the
-// products do not need it: they are relative to A and B, which are small where X is.
+// products do not need it for small singular values: they are relative to A and B, which
+// are small where X is.  They are added again in every step, though: five of the usual
+// steps end 1.7e-3 to 3.9e-3 off before the output's rounding, and only steps that settle
+// (1.5, -0.5, 0) keep that for long.  Two parts everywhere would be three products for one.
 //
 // Matrices whose short side is at most 128 take the kernels of ortho_small.hip.
 //
