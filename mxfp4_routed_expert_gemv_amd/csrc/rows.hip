@@ -10,12 +10,14 @@
 // one token, so positions and weights are scalars, x or dy is read once, every
 // access of a row is 1 KB in one piece (fp32: 2 KB), and a sum has one order.
 // Nothing is reused but the token's own row: the bytes of the T k rows bound them (d 7168,
-// 16 slots, bf16: dispatch of 4096 tokens 175 us for 1.0 GB, collect of 16384 810 us for
+// 16 slots, bf16: dispatch of 4096 tokens 188 us for 1.0 GB, collect of 16384 810 us for
 // 4.2 GB, its backward at 4096 390 us for 1.9 GB, where a copy runs at 4.85 TB/s; fp32
 // rows: dispatch back of 1000 tokens 92 us for 0.49 GB).  A few tokens are latency: 8 us
-// for 37.  Moved rows are stored non-temporally (dispatch 200 us without, collect back
-// 395); read so, rows that the experts wrote last miss the last-level cache (collect of
-// 37 tokens 8 -> 12 us, dispatch back 92 -> 101).
+// for 37.  Rows are stored and read through the caches: non-temporal stores take as long or
+// longer (fp32 rows of 517 tokens: dispatch 62 us for 53, collect back 111 for 100; bf16 of
+// 4096: 207 for 204, 393 for 391) and leave what reads the rows next to memory (dispatch
+// and collect of 1000 tokens 112 us for 93), and non-temporal loads miss what the experts
+// wrote last (collect of 37 tokens 12 us for 8, dispatch back 101 for 92).
 #include <algorithm>
 #include <type_traits>
 
@@ -32,26 +34,16 @@ struct f8 {
 
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
-// (NT: non-temporal, for rows that are read or written once)
-template <bool NT, typename V>
-__device__ __forceinline__ V ld(const V* p) {
-  return NT ? __builtin_nontemporal_load(p) : *p;
-}
-template <bool NT, typename V>
-__device__ __forceinline__ void st(V* p, V v) {
-  if (NT) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
 
-template <bool F32, bool NT = false>
+template <bool F32>
 __device__ __forceinline__ f8 load8(const void* base, size_t unit) {
   f8 r;
   if (F32) {
     const f32x4_t* p = static_cast<const f32x4_t*>(base) + 2 * unit;
-    const f32x4_t a = ld<NT>(p), b = ld<NT>(p + 1);
+    const f32x4_t a = p[0], b = p[1];
     r = f8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
   } else {
-    const u32x4_t a = ld<NT>(static_cast<const u32x4_t*>(base) + unit);
+    const u32x4_t a = static_cast<const u32x4_t*>(base)[unit];
     r = f8{{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(a.z), bf16_hi(a.z),
             bf16_lo(a.w), bf16_hi(a.w)}};
   }
@@ -60,15 +52,15 @@ __device__ __forceinline__ f8 load8(const void* base, size_t unit) {
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
-template <bool F32, bool NT = false>
+template <bool F32>
 __device__ __forceinline__ void store8(void* base, size_t unit, const f8& r) {
   if (F32) {
     f32x4_t* p = static_cast<f32x4_t*>(base) + 2 * unit;
-    st<NT>(p, f32x4_t{r.v[0], r.v[1], r.v[2], r.v[3]});
-    st<NT>(p + 1, f32x4_t{r.v[4], r.v[5], r.v[6], r.v[7]});
+    p[0] = f32x4_t{r.v[0], r.v[1], r.v[2], r.v[3]};
+    p[1] = f32x4_t{r.v[4], r.v[5], r.v[6], r.v[7]};
   } else {
-    st<NT>(static_cast<u32x4_t*>(base) + unit, u32x4_t{pack2(r.v[0], r.v[1]), pack2(r.v[2], r.v[3]),
-                                                       pack2(r.v[4], r.v[5]), pack2(r.v[6], r.v[7])});
+    static_cast<u32x4_t*>(base)[unit] = u32x4_t{pack2(r.v[0], r.v[1]), pack2(r.v[2], r.v[3]),
+                                                pack2(r.v[4], r.v[5]), pack2(r.v[6], r.v[7])};
   }
 }
 __device__ __forceinline__ f8 load8(const void* base, size_t unit, bool f32) {
@@ -100,11 +92,11 @@ __global__ __launch_bounds__(512) void dispatch_rows(const u32x4_t* __restrict__
     const int32_t* pos = pair_pos + t * k;
     for (int s = 0; s < k; ++s) {
       const int p = pos[s];
-      if (p >= 0 && p < P) st<true>(rows + (size_t)p * words + u, v);
+      if (p >= 0 && p < P) rows[(size_t)p * words + u] = v;
     }
   }
   for (int64_t q = used_rows(offsets, E, P) + blockIdx.y; q < P; q += gridDim.y)
-    st<true>(rows + q * words + u, u32x4_t{0, 0, 0, 0});
+    rows[q * words + u] = u32x4_t{0, 0, 0, 0};
 }
 
 // ---- a token's rows, weighted and summed
@@ -204,7 +196,7 @@ __global__ __launch_bounds__(256) void collect_back(const void* __restrict__ dy,
             f8 r;
 #pragma unroll
             for (int c = 0; c < 8; ++c) r.v[c] = w[j] * g.v[c];
-            store8<ROWS_F32, true>(drows, (size_t)at[j] * units + u, r);
+            store8<ROWS_F32>(drows, (size_t)at[j] * units + u, r);
           }
       }
       if (dw) {
