@@ -259,9 +259,9 @@ class _Dispatch(torch.autograd.Function):
 
 class _Collect(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rows, w, add, *order):
+    def forward(ctx, rows, w, add, out_dtype, *order):
         ctx.save_for_backward(rows, w, *order)
-        return collect(rows, order, w, add)
+        return collect(rows, order, w, add, out_dtype)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -269,7 +269,7 @@ class _Collect(torch.autograd.Function):
         rows, w, *order = ctx.saved_tensors
         dy = dy.contiguous()
         drows, dw = collect_backward(dy, rows, order, w, need=ctx.needs_input_grad[:2])
-        return (drows, dw, dy if ctx.needs_input_grad[2] else None, None, None, None, None)
+        return (drows, dw, dy if ctx.needs_input_grad[2] else None, None, None, None, None, None)
 
 
 class _Route(torch.autograd.Function):
@@ -324,6 +324,6 @@ def dispatch_tokens(x, idx, n_experts):
     return rows, Order(*order)
 
 
-def collect_tokens(rows, order, w, add=None):
+def collect_tokens(rows, order, w, add=None, out_dtype=None):
     """collect as a torch operation: y, differentiable once in rows, w and add."""
-    return _Collect.apply(rows, w, add, *order)
+    return _Collect.apply(rows, w, add, out_dtype, *order)

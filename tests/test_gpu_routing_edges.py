@@ -127,3 +127,22 @@ def test_operands_are_copied_on_the_calls_stream():
     got = r.collect(rows, o2, w, stream=st)
     st.synchronize()
     assert torch.equal(rows, want) and torch.equal(got, y)
+
+
+@pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)])
+def test_collect_as_an_operation_into_another_type(dtype, out):
+    """The bits of collect and of its backward with y and dy in the given type."""
+    r = routing()
+    T, d, E, k = 70, 96, 9, 3
+    g, idx, w = make(T, d, E, k, 55)
+    order = r.sort_pairs(idx, E)
+    rows, w = randn(g, T * k, d, dtype=dtype).requires_grad_(), w.requires_grad_()
+    y = r.collect_tokens(rows, order, w, out_dtype=out)
+    assert y.dtype == out and torch.equal(y, r.collect(rows.detach(), order, w.detach(), out_dtype=out))
+    up = randn(g, T, d, dtype=out)
+    got = torch.autograd.grad(y, (rows, w), up)
+    want = r.collect_backward(up, rows.detach(), order, w.detach())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    add = randn(g, T, d, dtype=out).requires_grad_()
+    y = r.collect_tokens(rows, order, w, add, out)
+    assert torch.equal(torch.autograd.grad(y, add, up)[0], up)
