@@ -146,3 +146,39 @@ def test_collect_as_an_operation_into_another_type(dtype, out):
     add = randn(g, T, d, dtype=out).requires_grad_()
     y = r.collect_tokens(rows, order, w, add, out)
     assert torch.equal(torch.autograd.grad(y, add, up)[0], up)
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_the_c_interfaces_own_wrappers(T):
+    """The package's k3moe_* functions of these calls, on the caller's buffers: what the
+    calls above return."""
+    r = routing()
+    import mxfp4_routed_expert_gemv_amd as k3
+    d, E, k = 96, 9, 3
+    g, idx, w = make(T, d, E, k, 56, bad=True)
+    x, wr = randn(g, T, d, dtype=torch.bfloat16), randn(g, E, d, dtype=torch.bfloat16)
+    dw, dy = randn(g, T, k), randn(g, T, d, dtype=torch.bfloat16)
+    s = k3.make_shape(T, d, 32, E, k, 0, 0, k3.BF16, k3.BF16)
+
+    def scratch(op):
+        return torch.empty(k3.k3moe_workspace_bytes(s, op), dtype=torch.uint8, device="cuda")
+
+    def new(*shape, dtype=torch.bfloat16):
+        return torch.full(shape, 7, dtype=dtype, device="cuda")
+    want, order = r.dispatch(x, idx, E)
+    rows, parts = new(T * k, d), [new(*o.shape, dtype=torch.int32) for o in order]
+    k3.k3moe_dispatch(s, x, idx, rows, *parts, None, scratch(k3.OP_DISPATCH))
+    assert torch.equal(rows, want) and all(torch.equal(a, b) for a, b in zip(parts, order))
+    dx = new(T, d)
+    k3.k3moe_dispatch_backward(s, rows, order.pair_pos, dx)
+    assert torch.equal(dx, r.dispatch_backward(rows, order))
+    y = new(T, d)
+    k3.k3moe_collect(s, rows, order.pair_pos, w, x, y)
+    assert torch.equal(y, r.collect(rows, order, w, add=x))
+    drows, dwc = new(T * k, d), new(T, k, dtype=torch.float32)
+    k3.k3moe_collect_backward(s, dy, rows, order.pair_pos, w, order.offsets, drows, dwc)
+    assert all(torch.equal(a, b) for a, b in zip((drows, dwc), r.collect_backward(dy, rows, order, w)))
+    dwr = new(E, d)
+    k3.k3moe_route_backward(s, x, wr, idx, w, dw, None, order.offsets, order.sorted_pair, order.pair_pos, dx, dwr,
+                            scratch(k3.OP_ROUTE_BACKWARD))
+    assert all(torch.equal(a, b) for a, b in zip((dx, dwr), r.route_backward(x, wr, idx, w, dw, order)))
