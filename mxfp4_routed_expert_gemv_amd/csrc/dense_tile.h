@@ -1,7 +1,8 @@
 // Parts of the tiled 16-bit matrix products with both operands in LDS rings: the
 // copies, the operand tiles' LDS layout and fragment reads, the lane exchange of
 // the epilogues.  Used by the shared experts' training pass (bf16) and by the
-// orthogonalised update (fp16): nothing here depends on the 16 bits' meaning.
+// orthogonalised update (fp16): but for pack_f16, nothing here depends on the 16 bits'
+// meaning.
 #pragma once
 
 #include "grouped.h"
@@ -11,6 +12,8 @@ namespace k3 {
 namespace dense {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
@@ -93,6 +96,29 @@ __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
   const auto t = __builtin_amdgcn_permlane16_swap(a, b, false, false);
   a = t[0];
   b = t[1];
+}
+
+// 4 x 4 values of 16 bits, a row of them to each of four neighbouring lanes,
+// transposed: lane j of the four gets the j-th value of every lane.
+__device__ __forceinline__ uint2 transpose4(uint2 v, int lane) {
+  const bool odd = lane & 1, upper = lane & 2;
+  const uint32_t px = __builtin_amdgcn_mov_dpp((int)v.x, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+  const uint32_t py = __builtin_amdgcn_mov_dpp((int)v.y, 0xB1, 0xF, 0xF, true);
+  const uint32_t x = odd ? (px >> 16) | (v.x & 0xFFFF0000u) : (v.x & 0xFFFFu) | (px << 16);
+  const uint32_t y = odd ? (py >> 16) | (v.y & 0xFFFF0000u) : (v.y & 0xFFFFu) | (py << 16);
+  const uint32_t qx = __builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);     // lane ^ 2
+  const uint32_t qy = __builtin_amdgcn_mov_dpp((int)y, 0x4E, 0xF, 0xF, true);
+  return upper ? make_uint2(qy, y) : make_uint2(x, qx);
+}
+
+// Two values as fp16, to nearest even.  (The bits are opaque from here on: where the
+// compiler sees a product in `a`, it may round it to fp16 in one step for one use of the
+// result and through fp32 for another, and a second part taken from the one would not
+// fit the other.)
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t w = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
+  asm volatile("" : "+v"(w));
+  return w;
 }
 
 }  // namespace dense

@@ -21,7 +21,8 @@
 // steps end 1.7e-3 to 3.9e-3 off before the output's rounding, and only steps that settle
 // (1.5, -0.5, 0) keep that for long.  Two parts everywhere would be three products for one.
 //
-// Matrices whose short side is at most 128 take the kernels of ortho_small.hip.
+// Matrices whose short side is at most 128 take the kernels of ortho_small.hip, but for
+// coefficients that multiply its A too far (ortho_small_ok).
 //
 // The matrix cores bound large matrices, at the clock that the card's power leaves (2 x
 // 4096 x 7168, us a step: A 214, with its finish 224 = 1.07 PFLOP/s of the half that is
@@ -43,9 +44,6 @@ namespace {
 
 using namespace grouped;
 using namespace dense;
-
-typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
-typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 
 constexpr float kScaleX = 32768.0f;   // 2^15, of X and of A; B has half of it
 
@@ -77,30 +75,8 @@ __device__ __forceinline__ float f16_lo(uint32_t w) {
 __device__ __forceinline__ float f16_hi(uint32_t w) {
   return (float)__builtin_bit_cast(f16x2_t, w)[1];
 }
-// To nearest even.  (The bits are opaque from here on: where the compiler sees a
-// product in `a`, it may round it to fp16 in one step for one use of the result and
-// through fp32 for another, and a second part taken from the one would not fit the
-// other.)
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  uint32_t w = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
-  asm volatile("" : "+v"(w));
-  return w;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-}
-
-// 4 x 4 values of 16 bits, a row of them to each of four neighbouring lanes,
-// transposed: lane j of the four gets the j-th value of every lane.
-__device__ __forceinline__ uint2 transpose4(uint2 v, int lane) {
-  const bool odd = lane & 1, upper = lane & 2;
-  const uint32_t px = __builtin_amdgcn_mov_dpp((int)v.x, 0xB1, 0xF, 0xF, true);   // lane ^ 1
-  const uint32_t py = __builtin_amdgcn_mov_dpp((int)v.y, 0xB1, 0xF, 0xF, true);
-  const uint32_t x = odd ? (px >> 16) | (v.x & 0xFFFF0000u) : (v.x & 0xFFFFu) | (px << 16);
-  const uint32_t y = odd ? (py >> 16) | (v.y & 0xFFFF0000u) : (v.y & 0xFFFFu) | (py << 16);
-  const uint32_t qx = __builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);     // lane ^ 2
-  const uint32_t qy = __builtin_amdgcn_mov_dpp((int)y, 0x4E, 0xF, 0xF, true);
-  return upper ? make_uint2(qy, y) : make_uint2(x, qx);
 }
 
 template <int P, int BM_, int BN_, int WM_, int WN_>
@@ -643,7 +619,7 @@ int64_t tiles_of(int P, const Dims& d, int bm, int bn) {
 }
 
 // The tile and split that cost least, by what a 64-element stage and a tile's way out
-// take (us).  A last round of a few tiles takes as long as a full one, so the tiles
+// take (us) on 256 CUs.  A last round of a few tiles takes as long as a full one, so the tiles
 // behind the last full round may be split: their pieces' sums go to memory and back
 // (at 4.5 TB/s) and a second kernel adds them, 4 us.
 Plan plan_product(int P, const Dims& d) {

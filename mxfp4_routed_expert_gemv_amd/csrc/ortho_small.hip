@@ -7,11 +7,15 @@
 //   iterate      P_k = a + b A_k + c A_k A_k,  A_k+1 = P_k A_k P_k, one workgroup a matrix
 //   apply        P_4 ( .. P_1 (P_0 X)), 64 or 128 columns to a workgroup
 // A holds squares of singular values: what A_0 lacks in bits a small one lacks twice,
-// and a step multiplies it by a^2.  So every operand here has two fp16 parts (22 bits,
-// three products each), and the host takes this path only while the product of the a^2
-// is at most 2^15 (five of the usual steps: 19800); then a gradient with sixteen
+// and a step multiplies it by a^2.  So every operand of these three has two fp16 parts
+// (22 bits, three products each), and the host takes them only while the product of the
+// a^2 is at most 2^15 (five of the usual steps: 19800); then a gradient with sixteen
 // directions a hundred times its noise comes out 4e-4 off in norm, noise alone 1e-6.
-// 256 x 128: three launches for seventeen.
+// 128 x 2048: three launches for seventeen.
+//
+// A short side of 65 .. 128 beside a long one up to 256 goes to one launch instead,
+// whatever the coefficients: `whole` takes the steps as ortho.hip does, the products'
+// operands in fp16 alone (11 bits; the result as far off as there).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -24,9 +28,6 @@ namespace k3 {
 namespace {
 
 using namespace dense;
-
-typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
-typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 
 constexpr float kScaleX = 32768.0f;   // 2^15, of X (at most 1.4)
 constexpr float kScaleA = 16384.0f;   // 2^14, of A and P A (at most 1.96)
@@ -48,15 +49,6 @@ struct SmallArgs {
 __device__ __forceinline__ float poly_scale(float a) {
   const int q = (int)((__float_as_uint(fabsf(a) + 3.9f) >> 23) & 255) - 127;
   return ldexpf(1.0f, 14 - q);
-}
-// To nearest even.  (The bits are opaque from here on: where the compiler sees a
-// product in `a`, it may round it to fp16 in one step for one use of the result and
-// through fp32 for another, and a second part taken from the one would not fit the
-// other.)
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  uint32_t w = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
-  asm volatile("" : "+v"(w));
-  return w;
 }
 // Where a P's part h has columns c .. of row r (c % 4 == 0): in the order of the
 // fragments that apply reads, 1 KB each, [row block][32 columns][part][lane].
@@ -361,18 +353,6 @@ __global__ __launch_bounds__(Waves<S>::kThreads) void iterate(SmallArgs g) {
     put(sA, kScaleA, A);
     __syncthreads();
   }
-}
-
-// 4 x 4 values of 16 bits transposed between four neighbouring lanes (as in ortho.hip).
-__device__ __forceinline__ uint2 transpose4(uint2 v, int lane) {
-  const bool odd = lane & 1, upper = lane & 2;
-  const uint32_t px = __builtin_amdgcn_mov_dpp((int)v.x, 0xB1, 0xF, 0xF, true);   // lane ^ 1
-  const uint32_t py = __builtin_amdgcn_mov_dpp((int)v.y, 0xB1, 0xF, 0xF, true);
-  const uint32_t x = odd ? (px >> 16) | (v.x & 0xFFFF0000u) : (v.x & 0xFFFFu) | (px << 16);
-  const uint32_t y = odd ? (py >> 16) | (v.y & 0xFFFF0000u) : (v.y & 0xFFFFu) | (py << 16);
-  const uint32_t qx = __builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true);     // lane ^ 2
-  const uint32_t qy = __builtin_amdgcn_mov_dpp((int)y, 0x4E, 0xF, 0xF, true);
-  return upper ? make_uint2(qy, y) : make_uint2(x, qx);
 }
 
 // Four values of row `row` of memory from column `col` on (col % 4 == 0), those inside.

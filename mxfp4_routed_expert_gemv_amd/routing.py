@@ -12,8 +12,8 @@ from functools import lru_cache
 
 import torch
 
-from . import (BF16, DIAG_COUNT, F32, K3moeError, OP_DISPATCH, OP_PERMUTE, OP_ROUTE,
-               OP_ROUTE_BACKWARD, ROUTERS, check_workspace, k3moe_permute, k3moe_route,
+from . import (BF16, DIAG_COUNT, F32, OP_DISPATCH, OP_PERMUTE, OP_ROUTE, OP_ROUTE_BACKWARD,
+               ROUTERS, _addr, _check, _ws, check_workspace, k3moe_permute, k3moe_route,
                k3moe_workspace_bytes, lib, make_shape, on_device)
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
@@ -44,27 +44,11 @@ def _need(t, name, shape, dtypes, device):
         raise ValueError(f"{name} must be a contiguous tensor on the operands' GPU")
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _whole(*operands):
     """The operands at 16 bytes, as the calls need them: a contiguous part of a larger
     tensor (a micro-batch's rows of w, a gradient that autograd hands over) may begin at
     any element.  Called where the call's stream is current, which the copies belong to."""
     return [t if t is None or not t.data_ptr() & 15 else t.clone() for t in operands]
-
-
-def _bytes(ws):
-    """Address and size of a workspace."""
-    if ws is None or isinstance(ws, tuple):
-        return ws or (None, 0)
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-def _check(status):
-    if status:
-        raise K3moeError(status, lib.k3moe_last_error().decode())
 
 
 def _sizes(pair_pos, rows, name):
@@ -138,7 +122,7 @@ def dispatch(x, idx, n_experts, diag=None, workspace=None, stream=None):
         order = _empty_order(T, k, E, dev)
         ws = _scratch(workspace, nbytes, dev)
         _check(lib.k3moe_dispatch(byref(shape), _ptr(x), _ptr(idx), _ptr(rows), *map(_ptr, order),
-                                  _addr(diag), *_bytes(ws), _raw_stream(dev.index)))
+                                  _addr(diag), *_ws(ws), _raw_stream(dev.index)))
     return rows, order
 
 
@@ -238,7 +222,7 @@ def route_backward(x, w_router, idx, w, dw, order, router="softmax", logits=None
         _check(lib.k3moe_route_backward(byref(shape), _ptr(x), _ptr(w_router), _ptr(idx), _ptr(w),
                                         _ptr(dw), _addr(logits), _ptr(offsets), _ptr(sorted_pair),
                                         _ptr(pair_pos), _addr(dx) if T else None, _addr(dwr),
-                                        *_bytes(ws), _raw_stream(dev.index)))
+                                        *_ws(ws), _raw_stream(dev.index)))
     return dx, dwr
 
 
