@@ -642,17 +642,19 @@ k3moe_status k3moe_route_backward(const k3moe_shape* shape, const void* x, const
  * `batch` matrices G [m][n], with X taken wide (G, or its transpose when m > n):
  *   X = G / |G| (Frobenius; a matrix of zeros stays zero), `steps` times
  *   X = a X + b (X X^T) X + c (X X^T)^2 X,  out = scale X  (rounded to bf16)
- * Sums are fp32, the norm's fp32 or more.  Where the short side is at most 64, or at
- * most 128 beside a long one over 256, and the product of the a^2 of all steps but the
- * last at most 2^15, the products' operands keep 22 bits.  Otherwise they are rounded to
- * fp16 (11 bits, but 22 for the term a X of every step but the last).  What that costs
- * depends on the steps and on G's singular values.  Five steps of the usual coefficients
- * (3.4445, -4.7750, 2.0315) end within 3e-3 of the exact result in norm, 1.7e-3 of it the
- * rounding to bf16, where the singular values are spread, as a gradient's are, and within
- * 5e-3 where all are equal; eight within 7e-3.  More steps of these coefficients go on
- * moving the values and multiply what the roundings left, in directions where G has
- * (almost) nothing most: there is no bound then.  Steps that settle do not: 64 of
- * (1.5, -0.5, 0) or (1.875, -1.25, 0.375) end within 2.5e-3 for G of full rank.
+ * Sums are fp32, the norm's fp32 or more.  Where the short side is at most 128 and the
+ * product of the a^2 of all steps but the last at most 2^15 (and, whatever that is, for
+ * short sides of 65 .. 128 beside long ones up to 256), the products' operands keep 22
+ * bits: five steps of the usual coefficients (3.4445, -4.7750, 2.0315) end within 5e-4 of
+ * the exact result in norm beside the rounding to bf16, which is 1.7e-3.
+ * Otherwise the operands are rounded to fp16 (11 bits, but 22 for the term a X of every
+ * step but the last).  What that costs depends on the steps and on G's singular values.
+ * Five of those steps end within 3e-3 in norm, the rounding to bf16 included, where the
+ * singular values are spread, as a gradient's are, and within 5e-3 where all are equal;
+ * eight within 7e-3.  More of them go on moving the values and multiply what the roundings
+ * left, in directions where G has (almost) nothing most: there is no bound then.  Steps
+ * that settle do not: 64 of (1.5, -0.5, 0) or (1.875, -1.25, 0.375) end within 2.5e-3 for
+ * G of full rank.
  * A non-finite G gives non-finite values.
  * (The reference pages do not train; this belongs to k3moe_shared_ffn_backward,
  * k3moe_route_backward and k3moe_grad_clip.)

@@ -14,8 +14,8 @@
 // 128 x 2048: three launches for seventeen.
 //
 // A short side of 65 .. 128 beside a long one up to 256 goes to one launch instead,
-// whatever the coefficients: `whole` takes the steps as ortho.hip does, the products'
-// operands in fp16 alone (11 bits; the result as far off as there).
+// whatever the coefficients: `whole` takes the steps as ortho.hip does, with two parts of
+// every operand here too.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -73,11 +73,14 @@ struct Parts {
     f[1] = __builtin_bit_cast(f16x8_t, O::frag(panel + kPart, rb, k32 & 1, ln, lg));
   }
   // four columns c .. of row r (c % 4 == 0)
-  __device__ static __forceinline__ void put4(uint8_t* p, int r, int c, const float (&v)[4]) {
+  __device__ static __forceinline__ void put_parts(uint8_t* p, int r, int c, uint2 h, uint2 l) {
     uint8_t* at = p + (c >> 6) * O::kSlot + r * 128 + ((((c >> 3) & 7) ^ ((r >> 1) & 7)) << 4) + (c & 4) * 2;
-    const uint2 h = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
     *reinterpret_cast<uint2*>(at) = h;
-    *reinterpret_cast<uint2*>(at + kPart) = make_uint2(rest_f16(v[0], v[1], h.x), rest_f16(v[2], v[3], h.y));
+    *reinterpret_cast<uint2*>(at + kPart) = l;
+  }
+  __device__ static __forceinline__ void put4(uint8_t* p, int r, int c, const float (&v)[4]) {
+    const uint2 h = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+    put_parts(p, r, c, h, make_uint2(rest_f16(v[0], v[1], h.x), rest_f16(v[2], v[3], h.y)));
   }
   // eight columns (c % 8 == 0)
   __device__ static __forceinline__ void put8(uint8_t* p, int r, int c, const float (&v)[8]) {
@@ -475,71 +478,182 @@ __global__ __launch_bounds__(512) void apply(SmallArgs g) {
 }
 
 // ---- matrices of 65 .. 128 by up to 256: all steps as ortho.hip takes them, by one
-// workgroup, X's first parts and A (then B) in LDS, X itself in fp32 in the registers
-// of the waves that compute it: 64 rows x 64 columns each of 2 x 4.  (256 x 128: one
-// launch of 33 us for three of 54, whose A alone takes 35: products of two parts
-// have three times the matrix instructions.)
+// workgroup, X itself in fp32 in the registers of the waves that compute it: 64 rows x 64
+// columns each of 2 x 4.  Every operand of a product has two fp16 parts: A's (then B's) in
+// LDS, and beside them those of one half of X, 128 columns, at a time, as both halves'
+// do not fit.  A wave has 32 columns of each half.  (256 x 128: 60 us, a step 10, of which
+// LDS is busy 6.0 and the matrix cores 4.7; what is left are the nine barriers of a step.
+// One part took 33 us and left the result 1.2e-3 off in norm beside its rounding to bf16,
+// two 2e-8; all 64 blocks of the symmetric products for 36, and loads of single values of
+// 128 x 256: 65 and 75 us.)
 //
-// X [128][256] serves as both operands: a row's eight columns for X X^T, and, read
-// transposed, a column's eight rows for B X.  Row r's 32 bytes of columns 16 b .. are at
-// block b ^ key, key = r mod 4 | (r / 8 mod 2) << 2, their two halves swapped where r
+// Half of X, [128][128], serves as both operands: a row's eight columns for X X^T, and,
+// read transposed, a column's eight rows for B X.  Row r's 32 bytes of columns 16 b .. are
+// at block b ^ key, key = r mod 4 | (r / 8 mod 2) << 2, their two halves swapped where r
 // has bit 2: eight rows' 16 bytes fall on distinct banks, and so do the eight lines of
 // half a wave's transposing read.
-constexpr int kBigL = 256;
-struct WholeX {
+constexpr int kBigL = 256, kHalf = 128;
+struct HalfX {
+  static constexpr int kPart = 128 * kHalf * 2, kBytes = 2 * kPart;
   __device__ static __forceinline__ int at(int r, int c) {   // byte of column c of row r (c % 4 == 0)
     const int key = (r & 3) | ((r >> 1) & 4);
-    return r * (2 * kBigL) + (((c >> 4) ^ key) << 5) + ((((c >> 3) ^ (r >> 2)) & 1) << 4) + (c & 7) * 2;
+    return r * (2 * kHalf) + (((c >> 4) ^ key) << 5) + ((((c >> 3) ^ (r >> 2)) & 1) << 4) + (c & 7) * 2;
+  }
+  __device__ static __forceinline__ void put4(uint8_t* x, int r, int c, f32x4_t v) {
+    const uint2 h = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+    *reinterpret_cast<uint2*>(x + at(r, c)) = h;
+    *reinterpret_cast<uint2*>(x + kPart + at(r, c)) = make_uint2(rest_f16(v[0], v[1], h.x), rest_f16(v[2], v[3], h.y));
   }
   // rows 16 rb + ln, columns 32 k + 8 lg ..
-  __device__ static __forceinline__ f16x8_t rows(const uint8_t* x, int rb, int k, int ln, int lg) {
-    return *reinterpret_cast<const f16x8_t*>(x + at(rb * 16 + ln, 32 * k + 8 * lg));
+  __device__ static __forceinline__ void rows(const uint8_t* x, int rb, int k, int ln, int lg, f16x8_t (&f)[2]) {
+    const uint8_t* p = x + at(rb * 16 + ln, 32 * k + 8 * lg);
+    f[0] = *reinterpret_cast<const f16x8_t*>(p);
+    f[1] = *reinterpret_cast<const f16x8_t*>(p + kPart);
   }
   // columns 16 cb + ln, rows 32 k + 8 lg ..
-  __device__ static __forceinline__ f16x8_t columns(const uint8_t* x, int cb, int k, int ln, int lg) {
+  __device__ static __forceinline__ void columns(const uint8_t* x, int cb, int k, int ln, int lg, f16x8_t (&f)[2]) {
     const int r = 32 * k + 8 * lg + (ln >> 2);
-    union { s16x4_t h[2]; f16x8_t v; } f;
-    f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(x + at(r, cb * 16 + (ln & 3) * 4)));
-    f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(x + at(r + 4, cb * 16 + (ln & 3) * 4)));
-    return f.v;
+    const uint8_t *p = x + at(r, cb * 16 + (ln & 3) * 4), *q = x + at(r + 4, cb * 16 + (ln & 3) * 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      union { s16x4_t w[2]; f16x8_t v; } u;
+      u.w[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + h * kPart));
+      u.w[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(q + h * kPart));
+      f[h] = u.v;
+    }
+  }
+};
+
+// acc += MB x NB blocks' products over 128 columns: load_a(i, k, f) and load_b(j, k, f)
+// give the two parts of row block i and column block j, elements 32 k ..
+template <int MB, int NB, int N, typename LA, typename LB>
+__device__ __forceinline__ void add_products(LA load_a, LB load_b, f32x4_t (&acc)[N]) {
+  static_assert(N >= MB * NB, "a sum for every block");
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f16x8_t fa[MB][2], fb[NB][2];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) load_a(i, k, fa[i]);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) load_b(j, k, fb[j]);
+    auto add = [&](auto q) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i * NB + j] = mfma<q>(fb[j], fa[i], acc[i * NB + j]);
+    };
+    add(Int<0>());
+    add(Int<1>());
+    add(Int<2>());
+  }
+}
+
+// The 36 blocks of a symmetric product of 128 x 128 that lie on and over the diagonal: six
+// waves have 2 x 2 of them over it, the last two the three of two squares of 2 x 2 on it
+// each (so a SIMD has 8 or 10 where all 64 would be 16).
+struct SymBlocks {
+  static constexpr int kMost = 6;
+  int wv;
+  // squares of waves 0 .. 5: (0, 1) (0, 2) (0, 3) (1, 2) (1, 3) (2, 3)
+  __device__ __forceinline__ int upper() const { return wv < 3 ? 0 : wv < 5 ? 1 : 2; }
+  __device__ __forceinline__ int right() const { return wv < 3 ? wv + 1 : wv < 5 ? wv - 1 : 3; }
+  // f(b, row block, column block, whether it lies over the diagonal) for the wave's blocks
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if (wv < 6) {
+      const int rb = 2 * upper(), cb = 2 * right();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) f(b, rb + (b >> 1), cb + (b & 1), std::true_type());
+      return;
+    }
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const int at = 4 * (wv - 6) + 2 * d;
+      f(3 * d, at, at, std::false_type());
+      f(3 * d + 1, at, at + 1, std::true_type());
+      f(3 * d + 2, at + 1, at + 1, std::false_type());
+    }
+  }
+  // acc += rows' products with themselves; rows(rb, k, f) gives the parts of row block rb
+  template <typename L>
+  __device__ __forceinline__ void add(L rows, f32x4_t (&acc)[kMost]) const {
+    if (wv < 6) {
+      const int ra = 2 * upper(), rb = 2 * right();
+      add_products<2, 2>([&](int i, int k, f16x8_t (&f)[2]) { rows(ra + i, k, f); },
+                         [&](int j, int k, f16x8_t (&f)[2]) { rows(rb + j, k, f); }, acc);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        f16x8_t f[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) rows(4 * (wv - 6) + 2 * d + i, k, f[i]);
+        auto add = [&](auto q) {
+          acc[3 * d] = mfma<q>(f[0], f[0], acc[3 * d]);
+          acc[3 * d + 1] = mfma<q>(f[1], f[0], acc[3 * d + 1]);
+          acc[3 * d + 2] = mfma<q>(f[1], f[1], acc[3 * d + 2]);
+        };
+        add(Int<0>());
+        add(Int<1>());
+        add(Int<2>());
+      }
   }
 };
 
 template <bool F32>
 __global__ __launch_bounds__(512) void whole(SmallArgs g) {
-  constexpr int S = 128, MB = 4, NX = 4, NA = 2;   // blocks of a wave: rows, columns of X, of A
-  using O = Operand<true, S>;
-  __shared__ __attribute__((aligned(16))) uint8_t sX[S * kBigL * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t sA[S * S * 2];
+  constexpr int S = 128, MB = 4, NX = 4, NB = 2;   // blocks of a wave: rows, columns of X, of a half or of A
+  using M = Parts<S, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t sX[HalfX::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sA[M::kBytes];
   __shared__ double sums[8];
   __shared__ float coef[64][3];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, ln = lane & 15, lg = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, lg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wv >> 2, wc = wv & 3;
   if (tid < 3 * g.steps) (&coef[0][0])[tid] = (&g.c[0][0])[tid];
   const size_t first = (size_t)blockIdx.x * g.rows * g.cols;
-  // X, raw: rows 64 wr + 16 i + ln, columns 64 wc + 16 j + 4 lg + r
+  // X, raw: rows 64 wr + 16 i + ln, columns 128 h + 32 wc + 16 j + 4 lg + r at j + 2 h
   f32x4_t x[MB][NX];
+  auto row = [&](int i) { return (wr * MB + i) * 16 + ln; };
+  auto column = [&](int j) { return (j >> 1) * kHalf + (wc * NB + (j & 1)) * 16 + lg * 4; };
   const uint32_t down = g.tr ? 1 : g.cols, right = g.tr ? g.rows : 1;
   const void* from = static_cast<const char*>(g.g) + first * (F32 ? 4 : 2);
   double sum = 0.0;
+  if (!g.tr && g.cols % 4 == 0) {   // (four columns are neighbours, all of them in or none)
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < NX; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int m = (wr * MB + i) * 16 + ln, n = (wc * NX + j) * 16 + lg * 4 + r;
-        const uint32_t at = m < g.rows && n < g.cols ? m * down + n * right : 0;
-        x[i][j][r] = F32 ? static_cast<const float*>(from)[at] : bf16_lo(static_cast<const uint16_t*>(from)[at]);
+      for (int j = 0; j < NX; ++j) {
+        const uint32_t at = row(i) < g.rows && column(j) < g.cols ? row(i) * down + column(j) : 0;
+        if (F32) {
+          x[i][j] = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(from) + at);
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(from) + at);
+          x[i][j] = f32x4_t{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+        }
       }
+  } else {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NX; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int m = row(i), n = column(j) + r;
+          const uint32_t at = m < g.rows && n < g.cols ? m * down + n * right : 0;
+          x[i][j][r] = F32 ? static_cast<const float*>(from)[at] : bf16_lo(static_cast<const uint16_t*>(from)[at]);
+        }
+  }
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NX; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int m = (wr * MB + i) * 16 + ln, n = (wc * NX + j) * 16 + lg * 4 + r;
-        if (m >= g.rows || n >= g.cols) x[i][j][r] = 0.0f;
+        if (row(i) >= g.rows || column(j) + r >= g.cols) x[i][j][r] = 0.0f;
         sum = fma((double)x[i][j][r], (double)x[i][j][r], sum);
       }
   sum = wave_sum(sum);
@@ -556,92 +670,70 @@ __global__ __launch_bounds__(512) void whole(SmallArgs g) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[i][j][r] = (float)((double)x[i][j][r] * f);
   // (X is 2^15 times itself, A too, B 2^14 times)
-  for (int s = 0;; ++s) {
+  const bool both = g.cols > kHalf;
+  auto put_x = [&](int h) {
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int j = 0; j < NX; ++j)
-        *reinterpret_cast<uint2*>(sX + WholeX::at((wr * MB + i) * 16 + ln, (wc * NX + j) * 16 + lg * 4)) =
-            make_uint2(pack_f16(x[i][j][0], x[i][j][1]), pack_f16(x[i][j][2], x[i][j][3]));
+      for (int j = 0; j < NB; ++j) HalfX::put4(sX, row(i), column(j), x[i][2 * h + j]);
+  };
+  const SymBlocks sym{wv};
+  auto put_a = [&](const f32x4_t (&v)[SymBlocks::kMost]) {   // those under the diagonal too
+    sym.each([&](int b, int rb, int cb, auto over) {
+      const uint2 h = make_uint2(pack_f16(v[b][0], v[b][1]), pack_f16(v[b][2], v[b][3]));
+      const uint2 l = make_uint2(rest_f16(v[b][0], v[b][1], h.x), rest_f16(v[b][2], v[b][3], h.y));
+      M::put_parts(sA, rb * 16 + ln, cb * 16 + lg * 4, h, l);
+      if (over)   // (four neighbouring lanes have the same columns)
+        M::put_parts(sA, cb * 16 + lg * 4 + (ln & 3), rb * 16 + (ln & ~3), transpose4(h, lane), transpose4(l, lane));
+    });
+  };
+  auto x_rows = [&](int rb, int k, f16x8_t (&f)[2]) { HalfX::rows(sX, rb, k, ln, lg, f); };
+  auto a_rows = [&](int rb, int k, f16x8_t (&f)[2]) { M::frags(sA, rb, k, ln, lg, f); };
+  for (int s = 0;; ++s) {
+    f32x4_t a[SymBlocks::kMost] = {};
+    put_x(0);
     __syncthreads();
     const float ca = coef[s][0], cb = coef[s][1], cc = coef[s][2];
-    // A, rows 64 wr + 16 i + ln, columns 32 wc + 16 j + 4 lg ..
-    f32x4_t a[MB][NA] = {};
+    sym.add(x_rows, a);
+    if (both) {
+      __syncthreads();
+      put_x(1);
+      __syncthreads();
+      sym.add(x_rows, a);
+    }
 #pragma unroll
-    for (int k = 0; k < kBigL / 32; ++k) {
-      f16x8_t fa[MB], fb[NA];
+    for (int b = 0; b < SymBlocks::kMost; ++b) a[b] *= 1.0f / kScaleX;
+    put_a(a);
+    __syncthreads();
+    f32x4_t aa[SymBlocks::kMost] = {};
+    sym.add(a_rows, aa);
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < MB; ++i) fa[i] = WholeX::rows(sX, wr * MB + i, k, ln, lg);
+    for (int b = 0; b < SymBlocks::kMost; ++b)
 #pragma unroll
-      for (int j = 0; j < NA; ++j) fb[j] = WholeX::rows(sX, wc * NA + j, k, ln, lg);
+      for (int r = 0; r < 4; ++r) a[b][r] = __builtin_fmaf(cc * (0.5f / kScaleX), aa[b][r], 0.5f * cb * a[b][r]);
+    put_a(a);   // B
+    __syncthreads();
+    // (the half of X that is in LDS first)
+    auto half_step = [&](int h) {
+      f32x4_t acc[MB * NB] = {};
+      add_products<MB, NB>([&](int i, int k, f16x8_t (&f)[2]) { a_rows(wr * MB + i, k, f); },
+                           [&](int j, int k, f16x8_t (&f)[2]) { HalfX::columns(sX, wc * NB + j, k, ln, lg, f); }, acc);
 #pragma unroll
       for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int j = 0; j < NA; ++j) a[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], a[i][j], 0, 0, 0);
-    }
-    auto put = [&](int i, int j, uint2 v) {
-      const int r = (wr * MB + i) * 16 + ln, c = (wc * NA + j) * 16 + lg * 4;
-      *reinterpret_cast<uint2*>(sA + (c >> 6) * O::kSlot + r * 128 + ((((c >> 3) & 7) ^ ((r >> 1) & 7)) << 4) +
-                                (c & 4) * 2) = v;
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            x[i][2 * h + j][r] = __builtin_fmaf(ca, x[i][2 * h + j][r], acc[i * NB + j][r] * (2.0f / kScaleX));
     };
-    uint2 kept[MB][NA];   // A as it is rounded
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NA; ++j) {
-        a[i][j] *= 1.0f / kScaleX;
-        kept[i][j] = make_uint2(pack_f16(a[i][j][0], a[i][j][1]), pack_f16(a[i][j][2], a[i][j][3]));
-        put(i, j, kept[i][j]);
-        a[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      }
-    __syncthreads();
-    auto frag_a = [&](int rb, int k) {
-      return __builtin_bit_cast(f16x8_t, O::frag(sA + (k >> 1) * O::kSlot, rb, k & 1, ln, lg));
-    };
-#pragma unroll
-    for (int k = 0; k < S / 32; ++k) {
-      f16x8_t fa[MB], fb[NA];
-#pragma unroll
-      for (int i = 0; i < MB; ++i) fa[i] = frag_a(wr * MB + i, k);
-#pragma unroll
-      for (int j = 0; j < NA; ++j) fb[j] = frag_a(wc * NA + j, k);
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NA; ++j) a[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], a[i][j], 0, 0, 0);
+    if (both) {
+      half_step(1);
+      __syncthreads();
+      put_x(0);
+      __syncthreads();
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NA; ++j) {
-        const f16x2_t p = __builtin_bit_cast(f16x2_t, kept[i][j].x), q = __builtin_bit_cast(f16x2_t, kept[i][j].y);
-        const float old[4] = {(float)p[0], (float)p[1], (float)q[0], (float)q[1]};
-        float b[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) b[r] = __builtin_fmaf(cc * (0.5f / kScaleX), a[i][j][r], 0.5f * cb * old[r]);
-        put(i, j, make_uint2(pack_f16(b[0], b[1]), pack_f16(b[2], b[3])));
-      }
-    __syncthreads();
-    f32x4_t acc[MB][NX] = {};
-#pragma unroll
-    for (int k = 0; k < S / 32; ++k) {
-      f16x8_t fa[MB], fb[NX];
-#pragma unroll
-      for (int i = 0; i < MB; ++i) fa[i] = frag_a(wr * MB + i, k);
-#pragma unroll
-      for (int j = 0; j < NX; ++j) fb[j] = WholeX::columns(sX, wc * NX + j, k, ln, lg);
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NX; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NX; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[i][j][r] = __builtin_fmaf(ca, x[i][j][r], acc[i][j][r] * (2.0f / kScaleX));
+    half_step(0);
     if (s + 1 == g.steps) break;
     __syncthreads();
   }
@@ -654,14 +746,14 @@ __global__ __launch_bounds__(512) void whole(SmallArgs g) {
       const f32x4_t v = x[i][j] * scale;
       uint2 q = make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[0], v[1]}, bf16x2_t)),
                            __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[2], v[3]}, bf16x2_t)));
-      int row = (wr * MB + i) * 16 + ln, col = (wc * NX + j) * 16 + lg * 4;   // of memory
+      int at = row(i), col = column(j);   // row and column of memory
       if (g.tr) {
         q = transpose4(q, lane);
         const int n = col + (ln & 3);
-        col = row - (ln & 3);
-        row = n;
+        col = at - (ln & 3);
+        at = n;
       }
-      put_row(o, row, col, g, q);
+      put_row(o, at, col, g, q);
     }
 }
 

@@ -31,10 +31,10 @@ def orthogonalize(g, steps=5, coefficients=MUON, scale=1.0, out=None, workspace=
     from X = g / |g|, in bf16.  g [m][n], or a stack [..][m][n], bf16 or fp32 (a stack
     of no matrices gives none); coefficients: (a, b, c), or such a triple for each step;
     out: a bf16 tensor of g's shape, g itself among them.  The result carries no
-    gradient.  Sums are fp32; matrices with a short side over 128, and those of 65 .. 128
-    by up to 256, enter the products in fp16, which five of MUON's steps end with within
-    3e-3 of the exact result in norm where the singular values are spread, 5e-3 where all
-    are equal (1.7e-3 of it the rounding to bf16); smaller ones keep 22 bits."""
+    gradient.  Sums are fp32; matrices with a short side over 128 enter the products in
+    fp16, which five of MUON's steps end with within 3e-3 of the exact result in norm where
+    the singular values are spread, 5e-3 where all are equal (1.7e-3 of it the rounding to
+    bf16); smaller ones keep 22 bits."""
     if g.dim() < 2:
         raise ValueError(f"g {tuple(g.shape)} is a matrix or a stack of them")
     if g.dtype not in _DT:

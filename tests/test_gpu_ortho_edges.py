@@ -104,3 +104,36 @@ def test_steps_that_settle_keep_what_they_have(m, n, coefficients):
         e = off(spectrum(kind, m, n, 44), steps=64, coefficients=coefficients)
         log(f"  {m} x {n}, {kind}: {e:.2e}")
         assert e <= 2.5e-3, kind
+
+
+def beside_rounding(got, want):
+    """The distance in norm, of what of every value's error half a step of bf16 does not
+    cover; the largest of a stack."""
+    half = torch.ldexp(torch.ones_like(want), torch.frexp(want).exponent - 9)
+    rest = ((got.to(F8) - want).abs() - half).clamp(min=0.0)
+    return float((rest.flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)).max())
+
+
+@pytest.mark.parametrize("batch,m,n", [(1, 65, 65), (1, 65, 130), (1, 128, 256), (1, 256, 128), (3, 128, 128),
+                                       (2, 100, 90), (2, 255, 67), (2, 77, 250), (1, 128, 129), (40, 129, 127)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_workgroups_matrices_keep_22_bits(batch, m, n, dtype):
+    """65 .. 128 by up to 256: as the other short sides up to 128, the result is within 5e-4
+    in norm beside the rounding to bf16.  The products' operands have 22 bits, off by 2^-23:
+    what that costs a value grows by 3.4445 a step at most, 3.4445^5 2^-23 = 6e-5 of the
+    largest, 1.2, for each of a step's three products."""
+    g = gradient(batch, m, n, dtype, 45)
+    want = exact(g)
+    rel = beside_rounding(call(g), want)
+    log(f"  {batch} x {m} x {n}: {rel:.1e} beside the rounding")
+    assert rel <= 5e-4
+
+
+@pytest.mark.parametrize("m,n", [(64, 64), (33, 700), (64, 3000), (257, 128), (128, 1500), (70, 300), (128, 256),
+                                 (128, 128), (65, 66)])
+def test_short_sides_up_to_128_on_every_spectrum(m, n):
+    for kind in SPREAD + ["equal"]:
+        g = spectrum(kind, m, n, 46)
+        rel = beside_rounding(call(g), exact(g))
+        log(f"  {m} x {n}, {kind}: {rel:.1e}")
+        assert rel <= 5e-4, kind
