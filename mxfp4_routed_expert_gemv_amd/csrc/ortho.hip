@@ -24,13 +24,14 @@
 // Matrices whose short side is at most 128 take the kernels of ortho_small.hip, but for
 // coefficients that multiply its A too far (ortho_small_ok).
 //
-// The matrix cores bound large matrices, at the clock that the card's power leaves (2 x
-// 4096 x 7168, us a step: A 214, with its finish 224 = 1.07 PFLOP/s of the half that is
-// computed; B 145; X 450 = 1.07, of which some 30 us a round of tiles are its way out, X's
-// two parts read and written at once by all CUs: the next row block's are requested ahead,
-// and every other workgroup starts with a shorter piece).  896 x 7168 takes 16 + 5, 9 and
-// 25 us a step, half of it the start and way out of tiles of 14 stages; matrices of a few
-// hundred rows 5 to 7 us a launch.
+// Large matrices are bound by the products (2 x 4096 x 7168, us a step: A 209 to 214, with
+// its finish 220 = 1.09 PFLOP/s of the half that is computed; B 131 to 145; X 406 to 450, of
+// which some 30 us a round of tiles are its way out, X's two parts read and written at once
+// by all CUs: the next row block's are requested ahead, and every other workgroup starts
+// with a shorter piece).  Their matrix cores are busy 59 to 70 % of the time at 1.97 to 2.08
+// GHz; the clock falls as they get busier (a library product of such values: 94 % at 1.67).
+// 896 x 7168 takes 16 + 5, 9 and 25 us a step, half of it the start and way out of tiles of
+// 14 stages; matrices of a few hundred rows 5 to 7 us a launch.
 #include <algorithm>
 #include <cmath>
 

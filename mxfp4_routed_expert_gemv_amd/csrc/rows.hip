@@ -10,14 +10,15 @@
 // one token, so positions and weights are scalars, x or dy is read once, every
 // access of a row is 1 KB in one piece (fp32: 2 KB), and a sum has one order.
 // Nothing is reused but the token's own row: the bytes of the T k rows bound them (d 7168,
-// 16 slots, bf16: dispatch of 4096 tokens 188 us for 1.0 GB, collect of 16384 810 us for
+// 16 slots, bf16: dispatch of 4096 tokens 195 us for 1.0 GB, collect of 16384 810 us for
 // 4.2 GB, its backward at 4096 390 us for 1.9 GB, where a copy runs at 4.85 TB/s; fp32
 // rows: dispatch back of 1000 tokens 92 us for 0.49 GB).  A few tokens are latency: 8 us
-// for 37.  Rows are stored and read through the caches: non-temporal stores take as long or
-// longer (fp32 rows of 517 tokens: dispatch 62 us for 53, collect back 111 for 100; bf16 of
-// 4096: 207 for 204, 393 for 391) and leave what reads the rows next to memory (dispatch
-// and collect of 1000 tokens 112 us for 93), and non-temporal loads miss what the experts
-// wrote last (collect of 37 tokens 12 us for 8, dispatch back 101 for 92).
+// for 37.  Rows are stored and read through the caches: non-temporal stores leave what
+// reads the rows next to memory (dispatch and collect of 1000 tokens 112 us for 93) and are
+// no faster by themselves while the rows fit the last-level cache (fp32 rows of 517 tokens:
+// dispatch 62 us for 53, collect back 111 for 100; bf16 of 4096: 195 to 207 for 204 to 214,
+// 393 for 391); non-temporal loads miss what the experts wrote last (collect of 37 tokens 12
+// us for 8, dispatch back 101 for 92).
 #include <algorithm>
 #include <type_traits>
 

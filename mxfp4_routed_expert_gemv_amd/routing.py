@@ -48,7 +48,10 @@ def _whole(*operands):
     """The operands at 16 bytes, as the calls need them: a contiguous part of a larger
     tensor (a micro-batch's rows of w, a gradient that autograd hands over) may begin at
     any element.  Called where the call's stream is current, which the copies belong to."""
-    return [t if t is None or not t.data_ptr() & 15 else t.clone() for t in operands]
+    for t in operands:
+        if t is not None and t.data_ptr() & 15:
+            return [t if t is None or not t.data_ptr() & 15 else t.clone() for t in operands]
+    return operands
 
 
 def _sizes(pair_pos, rows, name):
